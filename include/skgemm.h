@@ -495,6 +495,102 @@ skg_status_t skg_gemm_f64(int64_t m, int64_t n, int64_t k, double alpha, const d
                           int64_t ldc, const skg_opts_t* opts, void* workspace, size_t ws_bytes,
                           void* stream);
 
+/* ------------------------------------------------------------ microscaled operators
+ * Quantised matrices hold rows x k codes and one scale for every block of
+ * consecutive elements along k:
+ *   SKG_MXFP8  e4m3 codes, one byte each; blocks of 32 elements, scales 2^e
+ *              (e8m0: byte e + 127)
+ *   SKG_MXFP4  e2m1 codes, two to a byte (the even element in the low half);
+ *              blocks of 32, e8m0 scales
+ *   SKG_NVFP4  e2m1 codes; blocks of 16, scales in e4m3, and one fp32 scale g > 0
+ *              for the whole matrix (the "tensor scale", a device scalar)
+ * An element stands for code * scale (* g). A block's scale is, with amax the
+ * largest magnitude in the block,
+ *   SKG_MXFP8, SKG_MXFP4  the least power of two s >= 2^-127 with amax / s <= 448
+ *                         (or 6): no element saturates;
+ *   SKG_NVFP4             s = e4m3(min(amax / (6 g), 448)) in fp32; with
+ *                         g = max |X| / (448 * 6) no block scale saturates,
+ * and codes are x / s (SKG_NVFP4: x * (1 / (s g)) in fp32) rounded to nearest,
+ * ties to even. A block that holds an infinity or a NaN gets the NaN scale
+ * (0xFF, SKG_NVFP4 0x7F) and zero codes, so all of it stands for NaN.
+ *
+ * Codes: row-major, ldq BYTES from row to row (a multiple of 16, at least
+ * skg_mx_codes_ld), zeros from k up to the next multiple of 32 elements.
+ * Scales: tiles of 128 rows x 4 blocks of 512 bytes, the tiles of the same rows
+ * after one another; within a tile row 32 q + l (0 <= l < 32) and block b are
+ * byte 16 l + 4 q + b. skg_mx_scales_size bytes; the quantisers write zeros where
+ * the matrix ends inside a tile. Codes and scales are 16-byte aligned. */
+typedef enum { SKG_MXFP8 = 0, SKG_MXFP4 = 1, SKG_NVFP4 = 2 } skg_mx_t;
+
+/* Least ldq of a matrix with rows of k elements (a multiple of 16 bytes), and
+ * the bytes of its scales. 0 for invalid arguments. */
+int64_t skg_mx_codes_ld(int64_t k, int32_t format);
+size_t skg_mx_scales_size(int64_t rows, int64_t k, int32_t format);
+
+/* Quantise a matrix, asynchronous on `stream`.
+ *   X: device, `type` (skg_out_t: fp32, fp16 or bf16), row-major with ldx elements
+ *      from row to row: rows x k, or with transpose = 1 k x rows (the quantised
+ *      matrix is then X^T, its blocks along X's columns).
+ *   tensor_scale: SKG_NVFP4's g, a device scalar (NULL = 1); else not read.
+ *   codes, scales: as above. values: NULL, or device, `type`, rows x k with ldv
+ *      elements from row to row: what codes and scales stand for.
+ * Any ldx and ldv, any element alignment; 16-byte aligned rows are read and
+ * written in 16-byte pieces. rows or k of zero is valid. */
+skg_status_t skg_mx_quantize(int64_t rows, int64_t k, const void* X, int64_t ldx, int32_t type,
+                             int32_t transpose, int32_t format, const float* tensor_scale,
+                             void* codes, int64_t ldq, void* scales, void* values, int64_t ldv,
+                             void* stream);
+
+/* RMS norm of x + residual with a quantised output, asynchronous on `stream`:
+ *   h = X + residual;  rstd = 1 / sqrt(mean over the row of h^2 + eps);
+ *   codes, scales = quantised(h * rstd * weight), in fp32 up to the codes.
+ *   X, residual (NULL = none), weight (cols), sum: device, `type` (skg_in_t).
+ *   sum: NULL, or h rounded to `type`; may be X or residual themselves.
+ *   rstd: NULL, or device, rows floats (for the gradient).
+ * tensor_scale, codes, ldq and scales as in skg_mx_quantize. */
+skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                            const void* residual, int64_t ldr, const void* weight, int32_t type,
+                            float eps, void* sum, int64_t lds, float* rstd, int32_t format,
+                            const float* tensor_scale, void* codes, int64_t ldq, void* scales,
+                            void* stream);
+
+/* Gradient of skg_rmsnorm_mx (the quantisation counts as the identity),
+ * asynchronous on `stream`. With xhat = H * rstd and u = weight * dY:
+ *   dX = rstd * (u - xhat * mean over the row of (u * xhat)) + dresidual
+ *   dweight = sum over the rows of dY * xhat    (cols floats)
+ *   H: the sum that the norm was taken of; dresidual: NULL, or the gradient that
+ *   reaches it by another path. dX is the gradient of X and of residual; it may
+ *   be dY or dresidual themselves. dY, H, weight, dresidual, dX: `type`
+ *   (skg_in_t).
+ *   workspace: device, 256-byte aligned, skg_workspace_size_rmsnorm_backward
+ *   bytes, any contents. The sums run in a fixed order (no atomics). */
+size_t skg_workspace_size_rmsnorm_backward(int64_t rows, int64_t cols);
+skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, int64_t lddy,
+                                  const void* H, int64_t ldh, const void* weight,
+                                  const float* rstd, const void* dresidual, int64_t lddr,
+                                  int32_t type, void* dX, int64_t lddx, float* dweight,
+                                  void* workspace, size_t ws_bytes, void* stream);
+
+/* C = alpha * A B^T + beta * C of two quantised matrices of one format,
+ * asynchronous on `stream`: A m x k, B n x k (codes with lda, ldb bytes from row
+ * to row, scales, and SKG_NVFP4's tensor scales as device scalars, NULL = 1; the
+ * other formats take them too, as plain factors). Products and sums in fp32 on
+ * the block-scaled tensor cores, the same result every time.
+ *   C: device, out_dtype (skg_out_t), row-major, ldc >= n elements; any alignment
+ *      (rows with four elements aligned together are written in whole lines);
+ *      read only if beta != 0.
+ *   workspace: device, 256-byte aligned, skg_workspace_size_mx bytes, zeroed once
+ *      with skg_workspace_init; holds the report (skg_report_read) that a wait
+ *      which runs out is recorded in (SKG_ERR_PIPELINE_TIMEOUT). Nothing else is
+ *      kept there: calls may share it, also at the same time.
+ * m, n or k of zero is valid (k = 0 gives C = beta * C). */
+size_t skg_workspace_size_mx(int64_t m, int64_t n, int64_t k, int32_t format);
+skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const void* A, int64_t lda,
+                         const void* scales_a, const float* tensor_scale_a, const void* B,
+                         int64_t ldb, const void* scales_b, const float* tensor_scale_b,
+                         float beta, void* C, int64_t ldc, int32_t format, int32_t out_dtype,
+                         void* workspace, size_t ws_bytes, void* stream);
+
 /* Number of SMs of the current device (0 if there is no device). */
 int32_t skg_device_sm_count(void);
 

@@ -954,6 +954,19 @@ skg_status_t workspace_need(int64_t m, int64_t n, int64_t k, int32_t a_layout, i
 
 size_t fixed_header_bytes() { return kHeaderBytes + kFlagBytes; }
 
+CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes,
+                           const void* base, uint64_t inner, uint64_t outer,
+                           uint64_t row_stride_elems, uint32_t box_inner, uint32_t box_outer,
+                           CUtensorMapSwizzle swz) {
+  if (!tensor_map_encoder()) return CUDA_ERROR_NOT_SUPPORTED;
+  return make_map(map, dt, elem_bytes, base, inner, outer, row_stride_elems, box_inner, box_outer,
+                  swz);
+}
+
+skg_report_t* workspace_report(void* workspace) {
+  return reinterpret_cast<skg_report_t*>((uint8_t*)workspace + sizeof(WsHeader));
+}
+
 skg_status_t gemm_compact(int64_t m, int64_t n, int64_t k, float alpha, const void* A,
                           int64_t lda, const void* B, int64_t ldb, float beta, void* C,
                           int64_t ldc, int32_t in_dtype, int32_t out_dtype, int32_t a_layout,

@@ -131,6 +131,16 @@ skg_status_t gemm_compact(int64_t m, int64_t n, int64_t k, float alpha, const vo
                           int32_t b_layout, const skg_opts_t* opts, void* workspace,
                           size_t ws_bytes, void* stream);
 
+// A tensor map of a row-major matrix: `inner` elements of elem_bytes per row,
+// `outer` rows row_stride_elems apart, boxes of box_inner x box_outer.
+CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes,
+                           const void* base, uint64_t inner, uint64_t outer,
+                           uint64_t row_stride_elems, uint32_t box_inner, uint32_t box_outer,
+                           CUtensorMapSwizzle swz);
+
+// The report in a workspace's header.
+skg_report_t* workspace_report(void* workspace);
+
 // Bytes at the start of every workspace that must be zero before its first
 // use: the header with the report, and the flags (skg_workspace_init).
 size_t fixed_header_bytes();

@@ -1,0 +1,450 @@
+// skg_gemm_mx: C = alpha * A B^T + beta * C of two microscaled matrices (A m x k,
+// B n x k, codes and block scales as skgemm.h lays them out), fp32 accumulation,
+// on the block-scaled tensor-core instructions of sm_103a.
+//
+//   C[i][j] = sum over blocks b of sA[i][b] sB[j][b] (sum over l in b of a[i][l] b[j][l]),
+//
+// the scales applied by the MMA. A CTA runs one 128 x 128 tile of C over a range of
+// k: warp 0 fills a ring of stages by TMA (128 bytes of k for each of 128 rows of
+// A and of B, and their scale tiles), warp 1 copies each stage's scales to TMEM
+// (tcgen05.cp, in the order of the MMAs behind it) and issues four MMAs, warps 2-5
+// take the accumulator to C through shared memory.
+//
+// When the tiles are fewer than the CTAs that fit the GPU, the S CTAs of a
+// cluster share a tile, a range of k each: every one leaves its partial sums in
+// its own shared memory, and after a cluster barrier each adds the rows r, r + S,
+// ... of all of them in rank order through distributed shared memory. No
+// workspace, no atomics, the same result every time.
+//
+// Every wait is bounded; when one runs out the CTA records
+// SKG_ERR_PIPELINE_TIMEOUT in the report, waits for its own copies and MMAs,
+// still meets the cluster's barriers, frees its TMEM and leaves.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "skg_internal.h"
+#include "skg_mx.cuh"
+#include "skgemm.h"
+
+namespace skg {
+namespace {
+
+constexpr int kMxThreads = 192;
+constexpr int kMxTile = 128;
+constexpr int kMxRowBytes = 128;              // k bytes of a stage row
+constexpr int kMxOperand = kMxTile * kMxRowBytes;
+constexpr int kMxPitch = 132;                 // floats per row of the partial tile
+constexpr int kMxSplitMax = 8;
+constexpr uint64_t kMxTimeoutNs = 2000000000ull;
+
+struct MxParams {
+  int m, n, k;
+  float alpha, beta;
+  const float* ga;  // fp32 scales of the matrices (NULL = 1)
+  const float* gb;
+  void* c;
+  int64_t ldc;
+  int c_vec;        // four elements of a row are aligned together
+  int ksteps;       // stages of k
+  int split;        // CTAs per tile (cluster size)
+  int groups;       // scale tiles along k
+  int tiles_n;
+  int a_rows;       // rows of A's box
+  skg_report_t* report;
+};
+
+struct MxAux {
+  uint64_t full[8], empty[8], tfull, drain;
+  uint32_t tmem_slot;
+  int32_t abort_flag;
+};
+
+template <int FMT>
+struct MxCfg {
+  static constexpr int STEP = kMxRowBytes * 8 / mx_bits(FMT);  // elements per stage: 128 or 256
+  static constexpr int MMA_K = FMT == SKG_MXFP8 ? 32 : 64;
+  static constexpr int CHUNKS = STEP / mx_block(FMT) / 4;      // scale tiles per stage: 1, 2, 4
+  static constexpr int SF_BYTES = CHUNKS * kMxTileBytes;
+  static constexpr int SFA_OFF = 2 * kMxOperand;
+  static constexpr int SFB_OFF = SFA_OFF + SF_BYTES;
+  static constexpr int STAGE_BYTES = 2 * kMxOperand + 2 * SF_BYTES;
+  static constexpr int STAGES = 3;  // two CTAs share an SM
+  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 256;
+  // TMEM: the accumulator, then two buffers of scale columns (A's, B's).
+  static constexpr int SF_COLS = 2 * CHUNKS * 4;
+  static constexpr int TMEM_COLS = 256;
+  static_assert(kMxTile + 2 * SF_COLS <= TMEM_COLS, "TMEM columns");
+  static_assert(kMxTile * kMxPitch * 4 <= STAGES * STAGE_BYTES, "the partial tile fits the ring");
+};
+
+__device__ __forceinline__ bool mx_aborted(MxAux* aux) {
+  return *(volatile int32_t*)&aux->abort_flag != 0;
+}
+
+__device__ __forceinline__ void mx_fail(const MxParams& p, MxAux* aux) {
+  if (atomicExch(&aux->abort_flag, 1) == 0) {
+    atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
+    atomicAdd(&p.report->timeouts, 1u);
+  }
+}
+
+// Bounded wait; `drain` goes on after an abort (the caller's own operations).
+__device__ __forceinline__ bool mx_wait(uint64_t* bar, uint32_t parity, MxAux* aux,
+                                        bool drain = false) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31) == 0) {
+      if (!drain && mx_aborted(aux)) return false;
+      if (globaltimer() - t0 > kMxTimeoutNs) return false;
+    }
+  }
+}
+
+// Four consecutive elements of a row of C.
+template <typename T>
+__device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, float4 v,
+                                          float alpha) {
+  T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
+  float o[4] = {alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w};
+  const int left = p.n - col;
+  if (p.c_vec && left >= 4) {
+    union {
+      T e[4];
+      uint4 q;
+      uint2 d;
+    } u;
+    if (p.beta != 0.f) {
+      if constexpr (sizeof(T) == 4) u.q = *reinterpret_cast<const uint4*>(c);
+      else u.d = *reinterpret_cast<const uint2*>(c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += p.beta * mx_to_f32(u.e[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u.e[i] = mx_from_f32<T>(o[i]);
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(c) = u.q;
+    else *reinterpret_cast<uint2*>(c) = u.d;
+  } else {
+    for (int i = 0; i < 4 && i < left; ++i) {
+      if (p.beta != 0.f) o[i] += p.beta * mx_to_f32(c[i]);
+      c[i] = mx_from_f32<T>(o[i]);
+    }
+  }
+}
+
+template <int FMT, typename T>
+__global__ void __launch_bounds__(kMxThreads, 2)
+mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+               const MxParams p) {
+  using C = MxCfg<FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  MxAux* aux = reinterpret_cast<MxAux*>(ring + C::STAGES * C::STAGE_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int tile = (int)blockIdx.x / p.split;
+  const int tm = tile / p.tiles_n, tn = tile % p.tiles_n;
+  const int kb0 = (int)((int64_t)p.ksteps * rank / p.split);
+  const int kb1 = (int)((int64_t)p.ksteps * (rank + 1) / p.split);
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmSA);
+    prefetch_tmap(&tmSB);
+    aux->abort_flag = 0;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&aux->full[i], 1);
+      mbar_init(&aux->empty[i], 1);
+    }
+    mbar_init(&aux->tfull, 1);
+    mbar_init(&aux->drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&aux->tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = aux->tmem_slot;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+
+  bool fine = true;  // epilogue threads: the accumulator is there
+  int issued = 0;    // thread 0: stages loaded
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t tx = (uint32_t)p.a_rows * kMxRowBytes + kMxOperand + 2 * C::SF_BYTES;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        const int st = issued % C::STAGES;
+        if (!mx_wait(&aux->empty[st], (uint32_t)((issued / C::STAGES) & 1) ^ 1u, aux)) {
+          mx_fail(p, aux);
+          break;
+        }
+        uint8_t* s = ring + st * C::STAGE_BYTES;
+        mbar_arrive_expect_tx(&aux->full[st], tx);
+        tma_load_2d(s, &tmA, &aux->full[st], kb * kMxRowBytes, tm * kMxTile);
+        tma_load_2d(s + kMxOperand, &tmB, &aux->full[st], kb * kMxRowBytes, tn * kMxTile);
+        tma_load_2d(s + C::SFA_OFF, &tmSA, &aux->full[st], 0, tm * p.groups + kb * C::CHUNKS);
+        tma_load_2d(s + C::SFB_OFF, &tmSB, &aux->full[st], 0, tn * p.groups + kb * C::CHUNKS);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true, any = false;
+      int it = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const int st = it % C::STAGES;
+        if (!mx_wait(&aux->full[st], (uint32_t)((it / C::STAGES) & 1), aux)) {
+          mx_fail(p, aux);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t s = smem_u32(ring + st * C::STAGE_BYTES);
+        // Two buffers of scale columns: the copy for this stage does not
+        // touch the ones that the last stage's MMAs read.
+        const uint32_t sfa = tmem + kMxTile + (it & 1) * C::SF_COLS;
+        const uint32_t sfb = sfa + C::CHUNKS * 4;
+#pragma unroll
+        for (int c = 0; c < C::CHUNKS; ++c) {
+          tmem_cp_scales<false>(sfa + c * 4, sdesc_scales(s + C::SFA_OFF + c * kMxTileBytes));
+          tmem_cp_scales<false>(sfb + c * 4, sdesc_scales(s + C::SFB_OFF + c * kMxTileBytes));
+        }
+        const uint64_t ad = sdesc_sw128(s), bd = sdesc_sw128(s + kMxOperand);
+        // MMAs past k's last block of 32 are left out: their scales do not exist.
+        const int left = p.k - kb * C::STEP;
+        const int mmas = min(4, (left + C::MMA_K - 1) / C::MMA_K);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= mmas) break;
+          // mxfp8: byte j of the stage's one scale word; mxfp4: half j & 1 of word
+          // j / 2; nvfp4: the whole word j.
+          constexpr uint32_t F = FMT == SKG_MXFP8 ? 0u : 1u;
+          constexpr uint32_t E8 = FMT == SKG_NVFP4 ? 0u : 1u;
+          const uint32_t byte = FMT == SKG_MXFP8 ? j : (FMT == SKG_MXFP4 ? (j & 1) * 2 : 0);
+          const int word = FMT == SKG_MXFP8 ? 0 : (FMT == SKG_MXFP4 ? j / 2 : j);
+          umma_scaled<FMT, false>(tmem, ad + j * 2, bd + j * 2,
+                                  idesc_scaled(F, E8, kMxTile, kMxTile, byte), sfa + word * 4,
+                                  sfb + word * 4, (it > 0 || j > 0) ? 1u : 0u);
+        }
+        any = true;
+        umma_commit(&aux->empty[st]);
+      }
+      if (ok) umma_commit(&aux->tfull);
+      if (any) {
+        umma_commit(&aux->drain);
+        mx_wait(&aux->drain, 0, aux, true);
+      }
+    }
+    __syncwarp();
+  } else {
+    fine = mx_wait(&aux->tfull, 0, aux);
+    if (!fine) mx_fail(p, aux);
+    fine = epi_all(fine);
+    tc_fence_after();
+    const int q = warp & 3;
+    const int r = q * 32 + lane;
+    float* part = reinterpret_cast<float*>(ring);
+    if (fine && tm * kMxTile + q * 32 < p.m) {
+      // The ring is idle: every stage was read by MMAs that are complete.
+#pragma unroll
+      for (int c = 0; c < kMxTile; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<uint4*>(part + r * kMxPitch + c + i) =
+              make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+    }
+    __syncwarp();
+  }
+  float alpha = p.alpha;
+  if (p.ga) alpha *= *p.ga;
+  if (p.gb) alpha *= *p.gb;
+  const float* part = reinterpret_cast<const float*>(ring);
+  if (p.split == 1) {
+    // A warp writes the 32 rows that its own lanes stored.
+    if (warp >= 2 && fine)
+      for (int i = 0; i < 32; ++i) {
+        const int r = (warp & 3) * 32 + i, row = tm * kMxTile + r;
+        if (row >= p.m) break;
+        const int col = tn * kMxTile + lane * 4;
+        if (col < p.n)
+          mx_write4<T>(p, row, col, *reinterpret_cast<const float4*>(part + r * kMxPitch + lane * 4),
+                       alpha);
+      }
+  } else {
+    cluster_sync();
+    if (warp >= 2 && fine)
+      for (int i = warp - 2;; i += 4) {
+        const int r = rank + i * p.split, row = tm * kMxTile + r;
+        if (r >= kMxTile || row >= p.m) break;
+        const int col = tn * kMxTile + lane * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < p.split; ++s) {
+          const float4 u = ld_shared_cluster_f32x4(
+              cluster_addr(part + r * kMxPitch + lane * 4, (uint32_t)s));
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        }
+        if (col < p.n) mx_write4<T>(p, row, col, v, alpha);
+      }
+    cluster_sync();  // no CTA leaves while another reads its partial sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (threadIdx.x == 0) {
+    if (mx_aborted(aux))  // copies that no MMA waited for land before the CTA leaves
+      for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+        mx_wait(&aux->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), aux, true);
+    if (blockIdx.x == 0) atomicAdd(&p.report->launches, 1u);
+  }
+}
+
+template <int FMT, typename T>
+cudaError_t launch_mx(const CUtensorMap (&t)[4], const MxParams& p, cudaStream_t stream) {
+  using C = MxCfg<FMT>;
+  // The shared-memory opt-in is per device; set it once per device.
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!bit || !(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t tiles = (int64_t)((p.m + kMxTile - 1) / kMxTile) * p.tiles_n;
+  return launch_pdl_cluster(mx_gemm_kernel<FMT, T>, dim3((unsigned)(tiles * p.split)),
+                            dim3(kMxThreads), C::SMEM, stream, p.split, t[0], t[1], t[2], t[3], p);
+}
+
+template <int FMT>
+cudaError_t launch_mx_out(const CUtensorMap (&t)[4], const MxParams& p, int out,
+                          cudaStream_t stream) {
+  if (out == SKG_OUT_F32) return launch_mx<FMT, float>(t, p, stream);
+  if (out == SKG_OUT_F16) return launch_mx<FMT, __half>(t, p, stream);
+  return launch_mx<FMT, __nv_bfloat16>(t, p, stream);
+}
+
+template <int FMT>
+cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const void* B, int64_t ldb,
+                            const void* SB, MxParams p, int out, int sms, cudaStream_t stream,
+                            bool* unsupported) {
+  using C = MxCfg<FMT>;
+  const int64_t tm = (p.m + kMxTile - 1) / kMxTile, tn = (p.n + kMxTile - 1) / kMxTile;
+  p.groups = (int)mx_groups(p.k, FMT);
+  p.ksteps = (p.k + C::STEP - 1) / C::STEP;
+  p.tiles_n = (int)tn;
+  p.split = 1;
+  while (p.split < kMxSplitMax && tm * tn * p.split * 2 <= 2 * sms && p.split * 2 <= p.ksteps)
+    p.split *= 2;
+  p.a_rows = p.m < kMxTile ? (p.m + 7) / 8 * 8 : kMxTile;
+  const uint64_t bytes = ((uint64_t)p.k * mx_bits(FMT) + 7) / 8;
+  const uint64_t chunks_a = (uint64_t)tm * p.groups, chunks_b = (uint64_t)tn * p.groups;
+  *unsupported = tm * tn * p.split > INT32_MAX || chunks_a > INT32_MAX || chunks_b > INT32_MAX;
+  if (*unsupported) return cudaErrorInvalidValue;
+  CUtensorMap t[4];
+  if (encode_tensor_map(&t[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, bytes, (uint64_t)p.m,
+                        (uint64_t)lda, kMxRowBytes, (uint32_t)p.a_rows,
+                        CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tensor_map(&t[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, bytes, (uint64_t)p.n,
+                        (uint64_t)ldb, kMxRowBytes, kMxTile,
+                        CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tensor_map(&t[2], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, SA, kMxTileBytes / 4, chunks_a,
+                        kMxTileBytes / 4, kMxTileBytes / 4, C::CHUNKS,
+                        CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS ||
+      encode_tensor_map(&t[3], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, SB, kMxTileBytes / 4, chunks_b,
+                        kMxTileBytes / 4, kMxTileBytes / 4, C::CHUNKS,
+                        CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return launch_mx_out<FMT>(t, p, out, stream);
+}
+
+}  // namespace
+}  // namespace skg
+
+using namespace skg;
+
+extern "C" {
+
+size_t skg_workspace_size_mx(int64_t m, int64_t n, int64_t k, int32_t format) {
+  if (m < 0 || n < 0 || k < 0 || format < SKG_MXFP8 || format > SKG_NVFP4) return 0;
+  return fixed_header_bytes();
+}
+
+skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const void* A, int64_t lda,
+                         const void* scales_a, const float* tensor_scale_a, const void* B,
+                         int64_t ldb, const void* scales_b, const float* tensor_scale_b,
+                         float beta, void* C, int64_t ldc, int32_t format, int32_t out_dtype,
+                         void* workspace, size_t ws_bytes, void* stream_v) {
+  if (m < 0 || n < 0 || k < 0) return SKG_ERR_ARG;
+  if (format < SKG_MXFP8 || format > SKG_NVFP4) return SKG_ERR_ARG;
+  if (out_dtype < SKG_OUT_F32 || out_dtype > SKG_OUT_BF16) return SKG_ERR_ARG;
+  if (m == 0 || n == 0) return SKG_OK;
+  if (!C || ldc < n) return SKG_ERR_ARG;
+  const int64_t ld = skg_mx_codes_ld(k, format);
+  if (k > 0 && (!A || !B || !scales_a || !scales_b || lda < ld || ldb < ld)) return SKG_ERR_ARG;
+  if (m > INT32_MAX / 4 || n > INT32_MAX / 4 || k > INT32_MAX / 4) return SKG_ERR_UNSUPPORTED;
+  const int es = out_dtype == SKG_OUT_F32 ? 4 : 2;
+  if ((uintptr_t)C & (es - 1)) return SKG_ERR_UNSUPPORTED;
+  cudaStream_t stream = (cudaStream_t)stream_v;
+  if (k == 0)
+    return launch_scale(out_dtype, C, ldc, (int)m, (int)n, beta, stream) == cudaSuccess
+               ? SKG_OK
+               : SKG_ERR_CUDA;
+  // The TMA engine's rule.
+  if (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || ((uintptr_t)scales_a & 15) ||
+      ((uintptr_t)scales_b & 15) || (lda & 15) || (ldb & 15) || ((uintptr_t)tensor_scale_a & 3) ||
+      ((uintptr_t)tensor_scale_b & 3))
+    return SKG_ERR_UNSUPPORTED;
+  if (!workspace || ((uintptr_t)workspace & 255) ||
+      ws_bytes < skg_workspace_size_mx(m, n, k, format))
+    return SKG_ERR_WORKSPACE;
+  const int sms = skg_device_sm_count();
+  if (sms <= 0) return SKG_ERR_CUDA;
+  MxParams p = {};
+  p.m = (int)m;
+  p.n = (int)n;
+  p.k = (int)k;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.ga = tensor_scale_a;
+  p.gb = tensor_scale_b;
+  p.c = C;
+  p.ldc = ldc;
+  p.c_vec = ((uintptr_t)C & (4 * es - 1)) == 0 && ldc % 4 == 0;
+  p.report = workspace_report(workspace);
+  bool unsupported = false;
+  cudaError_t e;
+  if (format == SKG_MXFP8)
+    e = plan_and_launch<SKG_MXFP8>(A, lda, scales_a, B, ldb, scales_b, p, out_dtype, sms, stream,
+                                   &unsupported);
+  else if (format == SKG_MXFP4)
+    e = plan_and_launch<SKG_MXFP4>(A, lda, scales_a, B, ldb, scales_b, p, out_dtype, sms, stream,
+                                   &unsupported);
+  else
+    e = plan_and_launch<SKG_NVFP4>(A, lda, scales_a, B, ldb, scales_b, p, out_dtype, sms, stream,
+                                   &unsupported);
+  if (unsupported) return SKG_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
+}
+
+}  // extern "C"

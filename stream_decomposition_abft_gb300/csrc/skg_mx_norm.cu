@@ -1,0 +1,481 @@
+// skg_rmsnorm_mx: h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight,
+// quantised to a microscaled format as it is formed; and its gradient,
+// skg_rmsnorm_backward.
+//
+// With xhat = h rstd and u = w dy:
+//   dx = rstd (u - xhat mean(u xhat)) + dresidual,   dw = sum over rows of dy xhat.
+// The quantised output's rounding counts as the identity in the gradient.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "skg_internal.h"
+#include "skg_mx.cuh"
+#include "skgemm.h"
+
+namespace skg {
+namespace {
+
+constexpr int kNormMaxThreads = 512;  // threads of one row
+
+struct NormParams {
+  const void* x;
+  int64_t ldx;
+  const void* res;   // may be NULL
+  int64_t ldr;
+  const void* w;
+  int64_t rows;
+  int cols;
+  float eps;
+  void* sum;         // h, may be NULL; may be x or res
+  int64_t lds;
+  float* rstd;       // may be NULL
+  const float* g;
+  uint8_t* codes;
+  int64_t ldq;
+  uint8_t* scales;
+  int x_vec, r_vec, w_vec, s_vec;
+};
+
+// Sum over the TPR threads (a power of two) that share a row; every thread
+// gets it. `red` holds one float per warp.
+__device__ __forceinline__ float row_sum(float v, int log_tpr, float* red) {
+  const int width = log_tpr < 5 ? (1 << log_tpr) : 32;
+  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (log_tpr <= 5) return v;
+  const int warp = threadIdx.x >> 5, nw = 1 << (log_tpr - 5);
+  const int first = warp & ~(nw - 1);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < nw; ++i) v += red[first + i];
+  return v;
+}
+
+// 2^log_tpr threads share a row, V chunks of 16 elements each, h in registers
+// between the sum and the quantisation; V = 0: any width, h formed twice.
+template <typename T, int FMT, int V>
+__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams p, int log_tpr) {
+  __shared__ float red[kNormMaxThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int tpr = 1 << log_tpr;
+  const int t = threadIdx.x & (tpr - 1);
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> log_tpr) + (threadIdx.x >> log_tpr);
+  const bool here = row < p.rows;
+  const int chunks = (p.cols + 31) / 32 * 2;
+  const int groups = (int)mx_groups(p.cols, FMT);
+  const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
+  const T* x = reinterpret_cast<const T*>(p.x) + row * p.ldx;
+  const T* r = reinterpret_cast<const T*>(p.res) + row * p.ldr;
+  const T* w = reinterpret_cast<const T*>(p.w);
+  T* sum = reinterpret_cast<T*>(p.sum) + row * p.lds;
+
+  auto count = [&](int c) {
+    const int left = p.cols - c * 16;
+    return left >= 16 ? 16 : (left > 0 ? left : 0);
+  };
+  auto load_h = [&](int c, float (&h)[16]) {
+    const int n = here ? count(c) : 0;
+    mx_load16(x + c * 16, p.x_vec && n == 16, n, h);
+    if (p.res) {
+      float q[16];
+      mx_load16(r + c * 16, p.r_vec && n == 16, n, q);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) h[i] += q[i];
+    }
+  };
+  auto finish = [&](int c, float (&h)[16], float rstd) {
+    const int n = count(c);
+    if (here && p.sum) mx_store16(sum + c * 16, p.s_vec && n == 16, n, h);
+    float wv[16];
+    mx_load16(w + c * 16, p.w_vec && n == 16, n, wv);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = __fmul_rn(__fmul_rn(h[i], rstd), wv[i]);
+    uint4 codes;
+    uint32_t word;
+    const bool live = here && c < chunks;
+    mx_quantize_chunk<FMT>(h, live, lane, g, codes, word);
+    if (live) mx_store_codes16<FMT>(p.codes + row * p.ldq, c, codes);
+    constexpr int per = mx_group_chunks(FMT);
+    if ((lane & (per - 1)) == 0 && c / per < groups)
+      *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, c / per, groups)) = word;
+  };
+
+  float ss = 0.f, rstd;
+  if constexpr (V > 0) {
+    float h[V][16];
+#pragma unroll
+    for (int j = 0; j < V; ++j) load_h(t + j * tpr, h[j]);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss += h[j][i] * h[j][i];
+    ss = row_sum(ss, log_tpr, red);
+    rstd = rsqrtf(ss / (float)p.cols + p.eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) finish(t + j * tpr, h[j], rstd);
+  } else {
+    float h[16];
+    for (int c = t; c < chunks; c += tpr) {
+      load_h(c, h);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss += h[i] * h[i];
+    }
+    ss = row_sum(ss, log_tpr, red);
+    rstd = rsqrtf(ss / (float)p.cols + p.eps);
+    // Whole strides: every lane takes part in the quantiser's shuffles.
+    for (int c0 = 0; c0 < chunks; c0 += tpr) {
+      load_h(c0 + t, h);
+      finish(c0 + t, h, rstd);
+    }
+  }
+  if (here && p.rstd && t == 0) p.rstd[row] = rstd;
+}
+
+template <typename T, int FMT>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
+  const int chunks = (p.cols + 31) / 32 * 2;
+  int log_tpr = 3;
+  while ((1 << log_tpr) < chunks && (1 << log_tpr) < kNormMaxThreads) ++log_tpr;
+  const int v = (chunks + (1 << log_tpr) - 1) >> log_tpr;
+  const int threads = log_tpr < 7 ? 128 : (1 << log_tpr);
+  const int per = threads >> log_tpr;
+  const int64_t rows = (p.rows + 127) / 128 * 128;  // the scale tiles' rows
+  const dim3 grid((unsigned)(rows / per));
+  if (v <= 1)
+    return launch_pdl(rmsnorm_mx_kernel<T, FMT, 1>, grid, dim3(threads), 0, stream, p, log_tpr);
+  if (v <= 2)
+    return launch_pdl(rmsnorm_mx_kernel<T, FMT, 2>, grid, dim3(threads), 0, stream, p, log_tpr);
+  if (v <= 4)
+    return launch_pdl(rmsnorm_mx_kernel<T, FMT, 4>, grid, dim3(threads), 0, stream, p, log_tpr);
+  return launch_pdl(rmsnorm_mx_kernel<T, FMT, 0>, grid, dim3(threads), 0, stream, p, log_tpr);
+}
+
+template <typename T>
+cudaError_t launch_norm_fmt(const NormParams& p, int fmt, cudaStream_t stream) {
+  if (fmt == SKG_MXFP8) return launch_norm<T, SKG_MXFP8>(p, stream);
+  if (fmt == SKG_MXFP4) return launch_norm<T, SKG_MXFP4>(p, stream);
+  return launch_norm<T, SKG_NVFP4>(p, stream);
+}
+
+// ------------------------------------------------------------------ gradient
+struct GradParams {
+  const void* dy;
+  int64_t lddy;
+  const void* h;
+  int64_t ldh;
+  const void* w;
+  const float* rstd;
+  const void* dres;  // may be NULL
+  int64_t lddr;
+  int64_t rows;
+  int cols;
+  void* dx;
+  int64_t lddx;
+  float* partial;    // gridDim.x x cols: dw of each block's rows
+  int vec;           // every row is 16-byte aligned
+};
+
+// dx, a row at a time per group of 2^log_tpr threads (V chunks of 16 elements
+// each); V = 0: any width, the row read twice.
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(GradParams p, int log_tpr) {
+  __shared__ float red[kNormMaxThreads / 32];
+  extern __shared__ float wsum[];  // blockDim.x / tpr > 1: the groups' dw, cols floats
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tpr = 1 << log_tpr;
+  const int t = threadIdx.x & (tpr - 1);
+  const int per = blockDim.x >> log_tpr, mine = threadIdx.x >> log_tpr;
+  const int chunks = (p.cols + 15) / 16;
+  const T* w = reinterpret_cast<const T*>(p.w);
+  const float inv_n = 1.f / (float)p.cols;
+  auto count = [&](int c) {
+    const int left = p.cols - c * 16;
+    return left >= 16 ? 16 : (left > 0 ? left : 0);
+  };
+  constexpr int VV = V > 0 ? V : 1;
+  float acc[VV][16];
+#pragma unroll
+  for (int j = 0; j < VV; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per) {
+    const int64_t row = r0 + mine;
+    const bool here = row < p.rows;
+    const T* dy = reinterpret_cast<const T*>(p.dy) + row * p.lddy;
+    const T* h = reinterpret_cast<const T*>(p.h) + row * p.ldh;
+    const T* dr = reinterpret_cast<const T*>(p.dres) + row * p.lddr;
+    T* dx = reinterpret_cast<T*>(p.dx) + row * p.lddx;
+    const float rstd = here ? p.rstd[row] : 0.f;
+    float dot = 0.f;
+    auto load = [&](int c, float (&a)[16], float (&b)[16], float (&u)[16]) {
+      const int n = here ? count(c) : 0;
+      mx_load16(dy + c * 16, p.vec && n == 16, n, a);
+      mx_load16(h + c * 16, p.vec && n == 16, n, b);
+      mx_load16(w + c * 16, p.vec && n == 16, n, u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        b[i] *= rstd;   // xhat
+        u[i] *= a[i];   // w dy
+      }
+    };
+    auto store = [&](int c, const float (&b)[16], const float (&u)[16], float mean) {
+      const int n = here ? count(c) : 0;
+      float o[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = 0.f;
+      if (p.dres) mx_load16(dr + c * 16, p.vec && n == 16, n, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] += rstd * (u[i] - b[i] * mean);
+      mx_store16(dx + c * 16, p.vec && n == 16, n, o);
+    };
+    if constexpr (V > 0) {
+      float b[V][16], u[V][16];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float a[16];
+        load(t + j * tpr, a, b[j], u[j]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          acc[j][i] += a[i] * b[j][i];
+          dot += u[j][i] * b[j][i];
+        }
+      }
+      const float mean = row_sum(dot, log_tpr, red) * inv_n;
+#pragma unroll
+      for (int j = 0; j < V; ++j) store(t + j * tpr, b[j], u[j], mean);
+    } else {
+      float a[16], b[16], u[16];
+      for (int c = t; c < chunks; c += tpr) {
+        load(c, a, b, u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dot += u[i] * b[i];
+      }
+      const float mean = row_sum(dot, log_tpr, red) * inv_n;
+      for (int c = t; c < chunks; c += tpr) {
+        load(c, a, b, u);
+        store(c, b, u, mean);
+      }
+    }
+  }
+  if constexpr (V > 0) {
+    float* out = p.partial + (int64_t)blockIdx.x * p.cols;
+    if (per == 1) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = t + j * tpr, n = count(c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) out[c * 16 + i] = acc[j][i];
+      }
+    } else {
+      // The groups add their sums one after another (a fixed order).
+      for (int gq = 0; gq < per; ++gq) {
+        if (gq == mine) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const int c = t + j * tpr, n = count(c);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i < n) wsum[c * 16 + i] = gq == 0 ? acc[j][i] : wsum[c * 16 + i] + acc[j][i];
+          }
+        }
+        __syncthreads();
+      }
+      for (int c = threadIdx.x; c < p.cols; c += blockDim.x) out[c] = wsum[c];
+    }
+  }
+}
+
+// dw of a block's rows, for widths whose sums do not fit the row kernel's
+// registers: a thread per column.
+template <typename T>
+__global__ void __launch_bounds__(256) rmsnorm_grad_columns_kernel(GradParams p, int parts) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.cols) return;
+  float acc = 0.f;
+  for (int64_t row = blockIdx.y; row < p.rows; row += parts)
+    acc += mx_to_f32(reinterpret_cast<const T*>(p.dy)[row * p.lddy + c]) *
+           (mx_to_f32(reinterpret_cast<const T*>(p.h)[row * p.ldh + c]) * p.rstd[row]);
+  p.partial[(int64_t)blockIdx.y * p.cols + c] = acc;
+}
+
+// dw = the sum of the blocks' partials, in a fixed order: 32 columns per
+// block, eight rows of threads over the partials.
+__global__ void __launch_bounds__(256)
+rmsnorm_grad_reduce_kernel(const float* partial, int parts, int cols, float* dw) {
+  __shared__ float s[8][33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + tx;
+  float v = 0.f;
+  if (c < cols)
+    for (int i = ty; i < parts; i += 8) v += partial[(int64_t)i * cols + c];
+  s[ty][tx] = v;
+  __syncthreads();
+  if (ty == 0 && c < cols) {
+    for (int i = 1; i < 8; ++i) v += s[i][tx];
+    dw[c] = v;
+  }
+}
+
+struct GradPlan {
+  int log_tpr, v, threads, per, blocks;
+  size_t smem;
+};
+
+GradPlan grad_plan(int64_t rows, int64_t cols, int sms) {
+  GradPlan g;
+  const int64_t chunks = (cols + 15) / 16;
+  g.log_tpr = 3;
+  while ((1 << g.log_tpr) < chunks && (1 << g.log_tpr) < kNormMaxThreads) ++g.log_tpr;
+  const int64_t v = (chunks + (1 << g.log_tpr) - 1) >> g.log_tpr;
+  g.v = v > 4 ? 0 : (int)v;
+  g.threads = g.log_tpr < 7 ? 128 : (1 << g.log_tpr);
+  g.per = g.threads >> g.log_tpr;
+  g.smem = g.per > 1 ? (size_t)cols * 4 : 0;
+  const int64_t want = (rows + g.per - 1) / g.per;
+  const int64_t most = 2 * (int64_t)(sms > 0 ? sms : 152);
+  g.blocks = (int)(want < most ? want : most);
+  return g;
+}
+
+template <typename T>
+cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaStream_t stream) {
+  cudaError_t e;
+  const dim3 grid(g.blocks), block(g.threads);
+  if (g.v == 1)
+    e = launch_pdl(rmsnorm_grad_kernel<T, 1>, grid, block, g.smem, stream, p, g.log_tpr);
+  else if (g.v == 2)
+    e = launch_pdl(rmsnorm_grad_kernel<T, 2>, grid, block, g.smem, stream, p, g.log_tpr);
+  else if (g.v != 0)
+    e = launch_pdl(rmsnorm_grad_kernel<T, 4>, grid, block, g.smem, stream, p, g.log_tpr);
+  else {
+    e = launch_pdl(rmsnorm_grad_kernel<T, 0>, grid, block, g.smem, stream, p, g.log_tpr);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(rmsnorm_grad_columns_kernel<T>,
+                   dim3((unsigned)((p.cols + 255) / 256), (unsigned)g.blocks), dim3(256), 0,
+                   stream, p, g.blocks);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(256),
+                    0, stream, (const float*)p.partial, g.blocks, p.cols, dw);
+}
+
+bool vec_rows(const void* p, int64_t ld) {
+  return ((uintptr_t)p & 15) == 0 && (ld * 2) % 16 == 0;
+}
+
+}  // namespace
+}  // namespace skg
+
+using namespace skg;
+
+extern "C" {
+
+skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                            const void* residual, int64_t ldr, const void* weight, int32_t type,
+                            float eps, void* sum, int64_t lds, float* rstd, int32_t format,
+                            const float* tensor_scale, void* codes, int64_t ldq, void* scales,
+                            void* stream) {
+  if (rows < 0 || cols < 0 || !(eps >= 0.f)) return SKG_ERR_ARG;
+  if (type != SKG_IN_F16 && type != SKG_IN_BF16) return SKG_ERR_ARG;
+  if (format < SKG_MXFP8 || format > SKG_NVFP4) return SKG_ERR_ARG;
+  if (rows == 0 || cols == 0) return SKG_OK;
+  if (!X || !weight || !codes || !scales || ldx < cols || (residual && ldr < cols) ||
+      (sum && lds < cols) || ldq < skg_mx_codes_ld(cols, format))
+    return SKG_ERR_ARG;
+  if (cols > INT32_MAX / 4 || rows > INT32_MAX / 4) return SKG_ERR_UNSUPPORTED;
+  if (((uintptr_t)codes & 15) || (ldq & 15) || ((uintptr_t)scales & 15) || ((uintptr_t)X & 1) ||
+      ((uintptr_t)residual & 1) || ((uintptr_t)weight & 1) || ((uintptr_t)sum & 1) ||
+      ((uintptr_t)rstd & 3) || ((uintptr_t)tensor_scale & 3))
+    return SKG_ERR_UNSUPPORTED;
+  NormParams p;
+  p.x = X;
+  p.ldx = ldx;
+  p.res = residual;
+  p.ldr = ldr;
+  p.w = weight;
+  p.rows = rows;
+  p.cols = (int)cols;
+  p.eps = eps;
+  p.sum = sum;
+  p.lds = lds;
+  p.rstd = rstd;
+  p.g = tensor_scale;
+  p.codes = (uint8_t*)codes;
+  p.ldq = ldq;
+  p.scales = (uint8_t*)scales;
+  p.x_vec = vec_rows(X, ldx);
+  p.r_vec = vec_rows(residual, ldr);
+  p.w_vec = ((uintptr_t)weight & 15) == 0;
+  p.s_vec = vec_rows(sum, lds);
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = type == SKG_IN_F16 ? launch_norm_fmt<__half>(p, format, st)
+                                           : launch_norm_fmt<__nv_bfloat16>(p, format, st);
+  return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
+}
+
+size_t skg_workspace_size_rmsnorm_backward(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  const GradPlan g = grad_plan(rows, cols, skg_device_sm_count());
+  return (size_t)g.blocks * (size_t)cols * 4;
+}
+
+skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, int64_t lddy,
+                                  const void* H, int64_t ldh, const void* weight,
+                                  const float* rstd, const void* dresidual, int64_t lddr,
+                                  int32_t type, void* dX, int64_t lddx, float* dweight,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  if (rows < 0 || cols < 0) return SKG_ERR_ARG;
+  if (type != SKG_IN_F16 && type != SKG_IN_BF16) return SKG_ERR_ARG;
+  if (cols == 0) return SKG_OK;
+  if (!dweight) return SKG_ERR_ARG;
+  if (cols > INT32_MAX / 4 || rows > INT32_MAX / 4) return SKG_ERR_UNSUPPORTED;
+  if ((uintptr_t)dweight & 3) return SKG_ERR_UNSUPPORTED;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (rows == 0)  // an empty sum
+    return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256),
+                      0, st, (const float*)nullptr, 0, (int)cols, dweight) == cudaSuccess
+               ? SKG_OK
+               : SKG_ERR_CUDA;
+  if (!dY || !H || !weight || !rstd || !dX || lddy < cols || ldh < cols || lddx < cols ||
+      (dresidual && lddr < cols))
+    return SKG_ERR_ARG;
+  if (((uintptr_t)dY & 1) || ((uintptr_t)H & 1) || ((uintptr_t)weight & 1) ||
+      ((uintptr_t)dX & 1) || ((uintptr_t)dresidual & 1) || ((uintptr_t)rstd & 3))
+    return SKG_ERR_UNSUPPORTED;
+  const int sms = skg_device_sm_count();
+  if (sms <= 0) return SKG_ERR_CUDA;
+  const GradPlan g = grad_plan(rows, cols, sms);
+  if (!workspace || ((uintptr_t)workspace & 255) ||
+      ws_bytes < skg_workspace_size_rmsnorm_backward(rows, cols))
+    return SKG_ERR_WORKSPACE;
+  GradParams p;
+  p.dy = dY;
+  p.lddy = lddy;
+  p.h = H;
+  p.ldh = ldh;
+  p.w = weight;
+  p.rstd = rstd;
+  p.dres = dresidual;
+  p.lddr = lddr;
+  p.rows = rows;
+  p.cols = (int)cols;
+  p.dx = dX;
+  p.lddx = lddx;
+  p.partial = (float*)workspace;
+  p.vec = vec_rows(dY, lddy) && vec_rows(H, ldh) && vec_rows(dX, lddx) &&
+          ((uintptr_t)weight & 15) == 0 && (!dresidual || vec_rows(dresidual, lddr));
+  const cudaError_t e = type == SKG_IN_F16 ? launch_grad<__half>(p, g, dweight, st)
+                                           : launch_grad<__nv_bfloat16>(p, g, dweight, st);
+  return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
+}
+
+}  // extern "C"

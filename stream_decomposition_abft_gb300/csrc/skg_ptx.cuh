@@ -337,6 +337,77 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 
+// ---------------------------------------------------------------- block-scaled MMA
+// Shared-memory descriptor of 32 rows x 16 bytes stored contiguously (no
+// swizzle: 8-row core matrices of 128 bytes, stride byte offset 128), the
+// source of one tcgen05.cp of scale factors.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
+         ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// Copy 512 bytes of scale factors (128 rows x 4 blocks) from shared memory to
+// four TMEM columns, replicated over the four lane quadrants. Ordered with
+// the MMAs that the same thread issues; with PAIR the copy runs in both CTAs,
+// each from its own shared memory at the same offset.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+}
+
+// Instruction descriptor of a block-scaled MMA: scale-factor byte within the
+// TMEM word at bits 4-5 (B) and 29-30 (A), element format at bits 7-9 and
+// 10-12 (kind::mxf8f6f4: 0 = e4m3; kind::mxf4, mxf4nvf4: 1 = e2m1), N >> 3 at
+// bits 17-22, scale type at bit 23 (0 = e4m3, 1 = e8m0), M >> 4 at bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_scaled(uint32_t fmt, uint32_t e8m0, uint32_t M,
+                                                    uint32_t N, uint32_t sf_byte) {
+  return (sf_byte << 4) | (fmt << 7) | (fmt << 10) | ((N >> 3) << 17) | (e8m0 << 23) |
+         ((M >> 4) << 24) | (sf_byte << 29);
+}
+
+// D(tmem) (+)= (scaled A) (scaled B). KIND 0: e4m3 codes, one e8m0 scale per 32
+// (K = 32); 1: e2m1 codes, e8m0 per 32 (K = 64); 2: e2m1 codes, e4m3 per 16
+// (K = 64). sfa / sfb: TMEM columns of the scale words.
+#define SKG_UMMA_SCALED(GROUP, WHAT)                                                        \
+  asm volatile("{\n\t.reg .pred p;\n\t"                                                     \
+               "setp.ne.b32 p, %6, 0;\n\t"                                                  \
+               "tcgen05.mma.cta_group::" GROUP "." WHAT " [%0], %1, %2, %3, [%4], [%5], p;" \
+               "\n\t}" ::"r"(d_tmem),                                                       \
+               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)      \
+               : "memory")
+template <int KIND, bool PAIR>
+__device__ __forceinline__ void umma_scaled(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                            uint32_t accumulate) {
+  if constexpr (KIND == 0) {
+    if constexpr (PAIR) SKG_UMMA_SCALED("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    else SKG_UMMA_SCALED("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+  } else if constexpr (KIND == 1) {
+    if constexpr (PAIR) SKG_UMMA_SCALED("2", "kind::mxf4.block_scale.scale_vec::2X");
+    else SKG_UMMA_SCALED("1", "kind::mxf4.block_scale.scale_vec::2X");
+  } else {
+    if constexpr (PAIR) SKG_UMMA_SCALED("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    else SKG_UMMA_SCALED("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  }
+}
+#undef SKG_UMMA_SCALED
+
+// Four floats from the shared memory of a CTA of the cluster (a
+// shared::cluster address from cluster_addr, 16-byte aligned).
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t addr_cluster) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr_cluster)
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- PDL
 // Programmatic dependent launch: wait until the preceding kernel in the
 // stream has completed and its writes are visible (a no-op when this launch

@@ -23,6 +23,7 @@ A_COL = 1
 B_KMAJOR = 0
 B_NMAJOR = 1
 SCHED_DP, SCHED_SK, SCHED_DP_SK1, SCHED_SK2_DP, SCHED_AUTO = 0, 1, 2, 3, 4
+MXFP8, MXFP4, NVFP4 = 0, 1, 2
 ROLE_FULL, ROLE_OWNER, ROLE_PEER = 0, 1, 2
 OK = 0
 ERR_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE = 1, 2, 3, 4
@@ -91,7 +92,9 @@ SYMBOLS = ("skg_opts_default", "skg_workspace_size", "skg_workspace_init", "skg_
            "skg_device_sm_count", "skg_status_string", "skg_gemm_noalloc", "skg_schedule_cost",
            "skg_launch_plan", "skg_workspace_size_layout", "skg_host_staging_size",
            "skg_gemm_host", "skg_abft_encode_layout", "skg_workspace_size_f64", "skg_gemm_f64",
-           "skg_noalloc_report_read")
+           "skg_noalloc_report_read", "skg_mx_codes_ld", "skg_mx_scales_size", "skg_mx_quantize",
+           "skg_rmsnorm_mx", "skg_workspace_size_rmsnorm_backward", "skg_rmsnorm_backward",
+           "skg_workspace_size_mx", "skg_gemm_mx")
 
 _lib = None
 
@@ -161,6 +164,25 @@ def lib() -> ctypes.CDLL:
     L.skg_gemm_noalloc.restype = i32
     L.skg_noalloc_report_read.argtypes = [ctypes.POINTER(Report), i32, vp]
     L.skg_noalloc_report_read.restype = i32
+    L.skg_mx_codes_ld.argtypes = [i64, i32]
+    L.skg_mx_codes_ld.restype = i64
+    L.skg_mx_scales_size.argtypes = [i64, i64, i32]
+    L.skg_mx_scales_size.restype = sz
+    L.skg_mx_quantize.argtypes = [i64, i64, vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp]
+    L.skg_mx_quantize.restype = i32
+    L.skg_rmsnorm_mx.argtypes = [i64, i64, vp, i64, vp, i64, vp, i32, f32, vp, i64, vp, i32, vp,
+                                 vp, i64, vp, vp]
+    L.skg_rmsnorm_mx.restype = i32
+    L.skg_workspace_size_rmsnorm_backward.argtypes = [i64, i64]
+    L.skg_workspace_size_rmsnorm_backward.restype = sz
+    L.skg_rmsnorm_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32, vp, i64,
+                                       vp, vp, sz, vp]
+    L.skg_rmsnorm_backward.restype = i32
+    L.skg_workspace_size_mx.argtypes = [i64, i64, i64, i32]
+    L.skg_workspace_size_mx.restype = sz
+    L.skg_gemm_mx.argtypes = [i64, i64, i64, f32, vp, i64, vp, vp, vp, i64, vp, vp, f32, vp, i64,
+                              i32, i32, vp, sz, vp]
+    L.skg_gemm_mx.restype = i32
     L.skg_device_sm_count.argtypes = []
     L.skg_device_sm_count.restype = i32
     L.skg_status_string.argtypes = [i32]
@@ -319,6 +341,48 @@ def noalloc_report_read(reset: bool = False, stream: int = 0) -> Report:
     if st != OK:
         raise SkgError(st, "skg_noalloc_report_read")
     return rep
+
+
+def mx_codes_ld(k: int, fmt: int) -> int:
+    return int(lib().skg_mx_codes_ld(k, fmt))
+
+
+def mx_scales_size(rows: int, k: int, fmt: int) -> int:
+    return int(lib().skg_mx_scales_size(rows, k, fmt))
+
+
+def mx_quantize(rows, k, X_ptr, ldx, dtype, transpose, fmt, tensor_scale_ptr, codes_ptr, ldq,
+                scales_ptr, values_ptr, ldv, stream) -> int:
+    return lib().skg_mx_quantize(rows, k, X_ptr, ldx, dtype, transpose, fmt, tensor_scale_ptr,
+                                 codes_ptr, ldq, scales_ptr, values_ptr, ldv, stream)
+
+
+def rmsnorm_mx(rows, cols, X_ptr, ldx, residual_ptr, ldr, weight_ptr, in_dtype, eps, sum_ptr, lds,
+               rstd_ptr, fmt, tensor_scale_ptr, codes_ptr, ldq, scales_ptr, stream) -> int:
+    return lib().skg_rmsnorm_mx(rows, cols, X_ptr, ldx, residual_ptr, ldr, weight_ptr, in_dtype,
+                                eps, sum_ptr, lds, rstd_ptr, fmt, tensor_scale_ptr, codes_ptr,
+                                ldq, scales_ptr, stream)
+
+
+def workspace_size_rmsnorm_backward(rows: int, cols: int) -> int:
+    return int(lib().skg_workspace_size_rmsnorm_backward(rows, cols))
+
+
+def rmsnorm_backward(rows, cols, dY_ptr, lddy, H_ptr, ldh, weight_ptr, rstd_ptr, dres_ptr, lddr,
+                     in_dtype, dX_ptr, lddx, dweight_ptr, ws_ptr, ws_bytes, stream) -> int:
+    return lib().skg_rmsnorm_backward(rows, cols, dY_ptr, lddy, H_ptr, ldh, weight_ptr, rstd_ptr,
+                                      dres_ptr, lddr, in_dtype, dX_ptr, lddx, dweight_ptr, ws_ptr,
+                                      ws_bytes, stream)
+
+
+def workspace_size_mx(m: int, n: int, k: int, fmt: int) -> int:
+    return int(lib().skg_workspace_size_mx(m, n, k, fmt))
+
+
+def gemm_mx(m, n, k, alpha, A_ptr, lda, SA_ptr, ga_ptr, B_ptr, ldb, SB_ptr, gb_ptr, beta, C_ptr,
+            ldc, fmt, out_dtype, ws_ptr, ws_bytes, stream) -> int:
+    return lib().skg_gemm_mx(m, n, k, alpha, A_ptr, lda, SA_ptr, ga_ptr, B_ptr, ldb, SB_ptr,
+                             gb_ptr, beta, C_ptr, ldc, fmt, out_dtype, ws_ptr, ws_bytes, stream)
 
 
 def device_sm_count() -> int:
