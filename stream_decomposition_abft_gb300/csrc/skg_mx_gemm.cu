@@ -24,49 +24,18 @@
 
 #include <atomic>
 
-#include "skg_internal.h"
-#include "skg_mx.cuh"
-#include "skgemm.h"
+#include "skg_mx_gemm.cuh"
 
 namespace skg {
 namespace {
 
-constexpr int kMxThreads = 192;
-constexpr int kMxTile = 128;
-constexpr int kMxRowBytes = 128;              // k bytes of a stage row
-constexpr int kMxOperand = kMxTile * kMxRowBytes;
 constexpr int kMxPitch = 132;                 // floats per row of the partial tile
 constexpr int kMxSplitMax = 8;
-constexpr uint64_t kMxTimeoutNs = 2000000000ull;
-
-struct MxParams {
-  int m, n, k;
-  float alpha, beta;
-  const float* ga;  // fp32 scales of the matrices (NULL = 1)
-  const float* gb;
-  void* c;
-  int64_t ldc;
-  int c_vec;        // four elements of a row are aligned together
-  int ksteps;       // stages of k
-  int split;        // CTAs per tile (cluster size)
-  int groups;       // scale tiles along k
-  int tiles_n;
-  int a_rows;       // rows of A's box
-  skg_report_t* report;
-};
-
-struct MxAux {
-  uint64_t full[8], empty[8], tfull, drain;
-  uint32_t tmem_slot;
-  int32_t abort_flag;
-};
 
 template <int FMT>
-struct MxCfg {
-  static constexpr int STEP = kMxRowBytes * 8 / mx_bits(FMT);  // elements per stage: 128 or 256
-  static constexpr int MMA_K = FMT == SKG_MXFP8 ? 32 : 64;
-  static constexpr int CHUNKS = STEP / mx_block(FMT) / 4;      // scale tiles per stage: 1, 2, 4
-  static constexpr int SF_BYTES = CHUNKS * kMxTileBytes;
+struct MxCfg : MxStage<FMT> {
+  using MxStage<FMT>::CHUNKS;
+  using MxStage<FMT>::SF_BYTES;
   static constexpr int SFA_OFF = 2 * kMxOperand;
   static constexpr int SFB_OFF = SFA_OFF + SF_BYTES;
   static constexpr int STAGE_BYTES = 2 * kMxOperand + 2 * SF_BYTES;
@@ -79,62 +48,6 @@ struct MxCfg {
   static_assert(kMxTile * kMxPitch * 4 <= STAGES * STAGE_BYTES, "the partial tile fits the ring");
 };
 
-__device__ __forceinline__ bool mx_aborted(MxAux* aux) {
-  return *(volatile int32_t*)&aux->abort_flag != 0;
-}
-
-__device__ __forceinline__ void mx_fail(const MxParams& p, MxAux* aux) {
-  if (atomicExch(&aux->abort_flag, 1) == 0) {
-    atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
-    atomicAdd(&p.report->timeouts, 1u);
-  }
-}
-
-// Bounded wait; `drain` goes on after an abort (the caller's own operations).
-__device__ __forceinline__ bool mx_wait(uint64_t* bar, uint32_t parity, MxAux* aux,
-                                        bool drain = false) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31) == 0) {
-      if (!drain && mx_aborted(aux)) return false;
-      if (globaltimer() - t0 > kMxTimeoutNs) return false;
-    }
-  }
-}
-
-// Four consecutive elements of a row of C.
-template <typename T>
-__device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, float4 v,
-                                          float alpha) {
-  T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
-  float o[4] = {alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w};
-  const int left = p.n - col;
-  if (p.c_vec && left >= 4) {
-    union {
-      T e[4];
-      uint4 q;
-      uint2 d;
-    } u;
-    if (p.beta != 0.f) {
-      if constexpr (sizeof(T) == 4) u.q = *reinterpret_cast<const uint4*>(c);
-      else u.d = *reinterpret_cast<const uint2*>(c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += p.beta * mx_to_f32(u.e[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u.e[i] = mx_from_f32<T>(o[i]);
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(c) = u.q;
-    else *reinterpret_cast<uint2*>(c) = u.d;
-  } else {
-    for (int i = 0; i < 4 && i < left; ++i) {
-      if (p.beta != 0.f) o[i] += p.beta * mx_to_f32(c[i]);
-      c[i] = mx_from_f32<T>(o[i]);
-    }
-  }
-}
-
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads, 2)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -144,7 +57,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   MxAux* aux = reinterpret_cast<MxAux*>(ring + C::STAGES * C::STAGE_BYTES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
   const int tile = (int)blockIdx.x / p.split;
   const int tm = tile / p.tiles_n, tn = tile % p.tiles_n;
@@ -161,7 +74,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       mbar_init(&aux->full[i], 1);
       mbar_init(&aux->empty[i], 1);
     }
-    mbar_init(&aux->tfull, 1);
+    mbar_init(&aux->tfull[0], 1);
     mbar_init(&aux->drain, 1);
     fence_barrier_init();
   }
@@ -177,9 +90,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   bool fine = true;  // epilogue threads: the accumulator is there
-  int issued = 0;    // thread 0: stages loaded
+  int issued = 0;    // the loading thread: stages loaded
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t tx = (uint32_t)p.a_rows * kMxRowBytes + kMxOperand + 2 * C::SF_BYTES;
       for (int kb = kb0; kb < kb1; ++kb, ++issued) {
         const int st = issued % C::STAGES;
@@ -197,7 +110,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true, any = false;
       int it = 0;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -208,37 +121,16 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           break;
         }
         tc_fence_after();
-        const uint32_t s = smem_u32(ring + st * C::STAGE_BYTES);
         // Two buffers of scale columns: the copy for this stage does not
         // touch the ones that the last stage's MMAs read.
         const uint32_t sfa = tmem + kMxTile + (it & 1) * C::SF_COLS;
-        const uint32_t sfb = sfa + C::CHUNKS * 4;
-#pragma unroll
-        for (int c = 0; c < C::CHUNKS; ++c) {
-          tmem_cp_scales<false>(sfa + c * 4, sdesc_scales(s + C::SFA_OFF + c * kMxTileBytes));
-          tmem_cp_scales<false>(sfb + c * 4, sdesc_scales(s + C::SFB_OFF + c * kMxTileBytes));
-        }
-        const uint64_t ad = sdesc_sw128(s), bd = sdesc_sw128(s + kMxOperand);
-        // MMAs past k's last block of 32 are left out: their scales do not exist.
-        const int left = p.k - kb * C::STEP;
-        const int mmas = min(4, (left + C::MMA_K - 1) / C::MMA_K);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= mmas) break;
-          // mxfp8: byte j of the stage's one scale word; mxfp4: half j & 1 of word
-          // j / 2; nvfp4: the whole word j.
-          constexpr uint32_t F = FMT == SKG_MXFP8 ? 0u : 1u;
-          constexpr uint32_t E8 = FMT == SKG_NVFP4 ? 0u : 1u;
-          const uint32_t byte = FMT == SKG_MXFP8 ? j : (FMT == SKG_MXFP4 ? (j & 1) * 2 : 0);
-          const int word = FMT == SKG_MXFP8 ? 0 : (FMT == SKG_MXFP4 ? j / 2 : j);
-          umma_scaled<FMT, false>(tmem, ad + j * 2, bd + j * 2,
-                                  idesc_scaled(F, E8, kMxTile, kMxTile, byte), sfa + word * 4,
-                                  sfb + word * 4, (it > 0 || j > 0) ? 1u : 0u);
-        }
+        mx_stage_mmas<FMT, false, 1>(tmem, sfa, sfa + C::CHUNKS * 4,
+                                     smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF, C::SFB_OFF,
+                                     p.k - kb * C::STEP, it == 0);
         any = true;
         umma_commit(&aux->empty[st]);
       }
-      if (ok) umma_commit(&aux->tfull);
+      if (ok) umma_commit(&aux->tfull[0]);
       if (any) {
         umma_commit(&aux->drain);
         mx_wait(&aux->drain, 0, aux, true);
@@ -246,7 +138,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     __syncwarp();
   } else {
-    fine = mx_wait(&aux->tfull, 0, aux);
+    fine = mx_wait(&aux->tfull[0], 0, aux);
     if (!fine) mx_fail(p, aux);
     fine = epi_all(fine);
     tc_fence_after();
@@ -308,40 +200,39 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  if (threadIdx.x == 0) {
-    if (mx_aborted(aux))  // copies that no MMA waited for land before the CTA leaves
-      for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
-        mx_wait(&aux->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), aux, true);
-    if (blockIdx.x == 0) atomicAdd(&p.report->launches, 1u);
-  }
+  // Copies that no MMA waited for land before the CTA leaves.
+  if (warp == 0 && issued > 0 && mx_aborted(aux))
+    for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+      mx_wait(&aux->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), aux, true);
+  if (blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(&p.report->launches, 1u);
 }
 
 template <int FMT, typename T>
-cudaError_t launch_mx(const CUtensorMap (&t)[4], const MxParams& p, cudaStream_t stream) {
+cudaError_t launch_mx(const CUtensorMap (&t)[5], const MxParams& p, cudaStream_t stream) {
   using C = MxCfg<FMT>;
-  // The shared-memory opt-in is per device; set it once per device.
   static std::atomic<uint64_t> done_mask{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = mx_opt_in(mx_gemm_kernel<FMT, T>, done_mask, (int)C::SMEM);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (!bit || !(done_mask.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(mx_gemm_kernel<FMT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)C::SMEM);
-    if (e != cudaSuccess) return e;
-    done_mask.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  const int64_t tiles = (int64_t)((p.m + kMxTile - 1) / kMxTile) * p.tiles_n;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   return launch_pdl_cluster(mx_gemm_kernel<FMT, T>, dim3((unsigned)(tiles * p.split)),
                             dim3(kMxThreads), C::SMEM, stream, p.split, t[0], t[1], t[2], t[3], p);
 }
 
 template <int FMT>
-cudaError_t launch_mx_out(const CUtensorMap (&t)[4], const MxParams& p, int out,
+cudaError_t launch_mx_out(const CUtensorMap (&t)[5], const MxParams& p, int out,
                           cudaStream_t stream) {
   if (out == SKG_OUT_F32) return launch_mx<FMT, float>(t, p, stream);
   if (out == SKG_OUT_F16) return launch_mx<FMT, __half>(t, p, stream);
   return launch_mx<FMT, __nv_bfloat16>(t, p, stream);
+}
+
+// Whether a product runs on CTA pairs: their 256 x 256 tiles halve what each SM
+// reads per product, and need enough of them.
+bool wants_pairs(int64_t m, int64_t n, int64_t k, int clusters) {
+#ifdef SKG_MX_PAIR
+  return SKG_MX_PAIR != 0;
+#endif
+  return m > 128 && ((m + 255) / 256) * ((n + 255) / 256) * 2 >= clusters;
 }
 
 template <int FMT>
@@ -349,19 +240,26 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
                             const void* SB, MxParams p, int out, int sms, cudaStream_t stream,
                             bool* unsupported) {
   using C = MxCfg<FMT>;
-  const int64_t tm = (p.m + kMxTile - 1) / kMxTile, tn = (p.n + kMxTile - 1) / kMxTile;
   p.groups = (int)mx_groups(p.k, FMT);
   p.ksteps = (p.k + C::STEP - 1) / C::STEP;
+  const int64_t rt_a = (p.m + kMxTile - 1) / kMxTile, rt_b = (p.n + kMxTile - 1) / kMxTile;
+  const int resident = mx_pair_clusters_resident();
+  const bool pair = resident > 0 && wants_pairs(p.m, p.n, p.k, resident);
+  const int64_t tm = pair ? (rt_a + 1) / 2 : rt_a, tn = pair ? (rt_b + 1) / 2 : rt_b;
+  p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
   p.split = 1;
-  while (p.split < kMxSplitMax && tm * tn * p.split * 2 <= 2 * sms && p.split * 2 <= p.ksteps)
+  while (!pair && p.split < kMxSplitMax && tm * tn * p.split * 2 <= 2 * sms &&
+         p.split * 2 <= p.ksteps)
     p.split *= 2;
-  p.a_rows = p.m < kMxTile ? (p.m + 7) / 8 * 8 : kMxTile;
+  p.a_rows = !pair && p.m < kMxTile ? (p.m + 7) / 8 * 8 : kMxTile;
   const uint64_t bytes = ((uint64_t)p.k * mx_bits(FMT) + 7) / 8;
-  const uint64_t chunks_a = (uint64_t)tm * p.groups, chunks_b = (uint64_t)tn * p.groups;
-  *unsupported = tm * tn * p.split > INT32_MAX || chunks_a > INT32_MAX || chunks_b > INT32_MAX;
+  const uint64_t chunks_a = (uint64_t)rt_a * p.groups, chunks_b = (uint64_t)rt_b * p.groups;
+  // Tile and scale-tile numbers are 32-bit, one tile past the end included.
+  *unsupported = tm * tn * p.split > INT32_MAX || chunks_a + 2 * (uint64_t)p.groups > INT32_MAX ||
+                 chunks_b + 2 * (uint64_t)p.groups > INT32_MAX;
   if (*unsupported) return cudaErrorInvalidValue;
-  CUtensorMap t[4];
+  CUtensorMap t[5];
   if (encode_tensor_map(&t[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, bytes, (uint64_t)p.m,
                         (uint64_t)lda, kMxRowBytes, (uint32_t)p.a_rows,
                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
@@ -375,6 +273,18 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
                         kMxTileBytes / 4, kMxTileBytes / 4, C::CHUNKS,
                         CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
+  t[4] = t[0];
+  if (pair && p.c_tma) {
+    const int es = out == SKG_OUT_F32 ? 4 : 2;
+    const CUtensorMapDataType dt = out == SKG_OUT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : out == SKG_OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (encode_tensor_map(&t[4], dt, es, p.c, (uint64_t)p.n, (uint64_t)p.m, (uint64_t)p.ldc,
+                          (uint32_t)(128 / es), 32, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  if (pair)
+    return launch_mx_pair<FMT>(t, p, out, (int)(tm * tn < resident ? tm * tn : resident), stream);
   return launch_mx_out<FMT>(t, p, out, stream);
 }
 
@@ -431,6 +341,7 @@ skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const voi
   p.c = C;
   p.ldc = ldc;
   p.c_vec = ((uintptr_t)C & (4 * es - 1)) == 0 && ldc % 4 == 0;
+  p.c_tma = ((uintptr_t)C & 15) == 0 && (ldc * es) % 16 == 0 && beta == 0.f;
   p.report = workspace_report(workspace);
   bool unsupported = false;
   cudaError_t e;

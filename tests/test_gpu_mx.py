@@ -331,6 +331,22 @@ def test_product(fmt, m, n, k):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("m,n,k", [(2600, 2900, 352), (2100, 5000, 1300), (6000, 1023, 32)])
+def test_product_many_tiles(fmt, m, n, k):
+    # More tiles than fit the GPU at once: several per CTA, ragged at both ends.
+    a, av = operand(m, k, fmt, 1)
+    b, bv = operand(n, k, fmt, 2)
+    ws = mx.workspace()
+    for dtype in TYPES.values():
+        check_product(mx.matmul(a, b, out_dtype=dtype, workspace=ws), av, bv, k)
+    c0 = draw(m, n, "bf16", 3).cuda()
+    out = c0.clone()
+    mx.matmul(a, b, out=out, alpha=2.0, beta=-1.5, workspace=ws)
+    check_product(out, av, bv, k, 2.0, -1.5, c0)
+    assert ws.report().timeouts == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (3, 1)])
 def test_product_alpha_beta_strides(fmt, dtype, pad, offset):

@@ -107,4 +107,13 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="codes or scales"):
         mx.matmul(q, q)
     with pytest.raises(ValueError, match="other operand"):
-        mx._operand("b", q._replace(format="mxfp4"), "mxfp8", q.codes.device)
+        mx._operand("b", q._replace(format="mxfp4"), "mxfp8", None)
+
+
+def test_binding_sizes():
+    # The binding's own layout arithmetic is the library's.
+    for fmt, code in mx.FORMATS.items():
+        for rows in (0, 1, 127, 128, 129, 5000):
+            for k in (0, 1, 31, 32, 33, 63, 64, 65, 128, 129, 2200, 28672):
+                assert mx._sizes(rows, k, fmt) == (skgemm.mx_codes_ld(k, code),
+                                                   skgemm.mx_scales_size(rows, k, code))
