@@ -963,6 +963,17 @@ CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, int elem_by
                   swz);
 }
 
+cudaError_t opt_in_smem(const void* kernel, std::atomic<uint64_t>& done, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 skg_report_t* workspace_report(void* workspace) {
   return reinterpret_cast<skg_report_t*>((uint8_t*)workspace + sizeof(WsHeader));
 }

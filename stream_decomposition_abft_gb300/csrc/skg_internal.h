@@ -3,6 +3,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "skg_kernel.cuh"
 
 namespace skg {
@@ -43,6 +45,10 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
                        cudaStream_t stream, Args... args) {
   return launch_pdl_cluster(kernel, grid, block, smem, stream, 1, args...);
 }
+
+// The dynamic shared-memory opt-in of a kernel: per device, set once per device
+// (`done`, the kernel's own mask of devices).
+cudaError_t opt_in_smem(const void* kernel, std::atomic<uint64_t>& done, int bytes);
 
 // TMA descriptors of one launch: A (box 64 x 128), B (64 x BLK_N), C (store
 // box 128 bytes x 32 rows); with fused ABFT checksum tiles also B as an

@@ -254,7 +254,49 @@ __device__ __forceinline__ MxScale mx_quantize_chunk(const float (&v)[16], bool 
   return s;
 }
 
-// Chunks of 16 elements per block group, and a group's first lane.
+// The same for pieces of 8 elements (piece c in a lane with lane % 16 == c % 16).
+template <int FMT>
+__device__ __forceinline__ void mx_quantize_piece(const float (&v)[8], bool live, int lane,
+                                                  float g, uint2& codes, uint32_t& word) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  if constexpr (FMT != SKG_NVFP4) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const MxScale s = mx_scale<FMT>(amax, g);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], s.inv);
+  if constexpr (FMT == SKG_MXFP8)
+    codes = make_uint2(mx_e4m3x4(y[0], y[1], y[2], y[3]), mx_e4m3x4(y[4], y[5], y[6], y[7]));
+  else
+    codes = make_uint2(mx_e2m1x8(y), 0u);
+  if (s.bad) codes = make_uint2(0u, 0u);
+  const int slot = FMT == SKG_NVFP4 ? ((lane >> 1) & 3) : ((lane >> 2) & 3);
+  word = live ? s.byte << (8 * slot) : 0u;
+  if constexpr (FMT == SKG_NVFP4) word |= __shfl_xor_sync(0xffffffffu, word, 2);
+  word |= __shfl_xor_sync(0xffffffffu, word, 4);
+  if constexpr (FMT != SKG_NVFP4) word |= __shfl_xor_sync(0xffffffffu, word, 8);
+}
+
+// Eight elements of a 16-bit type.
+template <typename T>
+__device__ __forceinline__ void mx_unpack8(const uint4& u, float (&v)[8]) {
+  const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(e[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 mx_pack8(const float (&v)[8]) {
+  uint4 u;
+  T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = mx_from_f32<T>(v[i]);
+  return u;
+}
+
+// Chunks of 16 elements per block group.
 __host__ __device__ constexpr int mx_group_chunks(int fmt) { return fmt == SKG_NVFP4 ? 4 : 8; }
 
 }  // namespace skg

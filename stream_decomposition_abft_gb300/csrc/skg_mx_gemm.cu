@@ -48,6 +48,44 @@ struct MxCfg : MxStage<FMT> {
   static_assert(kMxTile * kMxPitch * 4 <= STAGES * STAGE_BYTES, "the partial tile fits the ring");
 };
 
+// Rows rank, rank + S, ... of the tile: the S CTAs' partial sums in rank order.
+// The loads of several rows are in flight together (a remote load takes about a
+// quarter of a microsecond).
+template <typename T, int S>
+__device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* part, int warp,
+                                               int lane, int rank, int tm, int tn, float alpha) {
+  constexpr int R = 16 / S;  // rows at a time
+  constexpr int WARPS = kMxThreads / 32;
+  const int rows = min(kMxTile, p.m - tm * kMxTile);
+  const int col = tn * kMxTile + lane * 4;
+  uint32_t base[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) base[s] = cluster_addr(part + lane * 4, (uint32_t)s);
+  for (int i = warp * R; rank + i * S < rows; i += WARPS * R) {
+    float4 u[R][S];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int r = min(rank + (i + j) * S, kMxTile - 1);
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        u[j][s] = ld_shared_cluster_f32x4(base[s] + (uint32_t)r * (kMxPitch * 4));
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int r = rank + (i + j) * S;
+      float4 v = u[j][0];
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        v.x += u[j][s].x;
+        v.y += u[j][s].y;
+        v.z += u[j][s].z;
+        v.w += u[j][s].w;
+      }
+      if (r < rows && col < p.n) mx_write4<T>(p, tm * kMxTile + r, col, v, alpha);
+    }
+  }
+}
+
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads, 2)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -148,13 +186,19 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (fine && tm * kMxTile + q * 32 < p.m) {
       // The ring is idle: every stage was read by MMAs that are complete.
 #pragma unroll
-      for (int c = 0; c < kMxTile; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+      for (int c = 0; c < kMxTile; c += 64) {
+        uint32_t v[2][32];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<uint4*>(part + r * kMxPitch + c + i) =
-              make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (int h = 0; h < 2; ++h)
+          tmem_ld32_async(tmem + ((uint32_t)(q * 32) << 16) + c + h * 32, v[h]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld_wait32(v[h]);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(part + r * kMxPitch + c + h * 32 + i) =
+                make_uint4(v[h][i], v[h][i + 1], v[h][i + 2], v[h][i + 3]);
+        }
       }
     }
     __syncwarp();
@@ -165,33 +209,22 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const float* part = reinterpret_cast<const float*>(ring);
   if (p.split == 1) {
     // A warp writes the 32 rows that its own lanes stored.
-    if (warp >= 2 && fine)
-      for (int i = 0; i < 32; ++i) {
-        const int r = (warp & 3) * 32 + i, row = tm * kMxTile + r;
-        if (row >= p.m) break;
-        const int col = tn * kMxTile + lane * 4;
-        if (col < p.n)
-          mx_write4<T>(p, row, col, *reinterpret_cast<const float4*>(part + r * kMxPitch + lane * 4),
+    const int row0 = tm * kMxTile + (warp & 3) * 32, col = tn * kMxTile + lane * 4;
+    if (warp >= 2 && fine && col < p.n) {
+      const float* src = part + (warp & 3) * 32 * kMxPitch + lane * 4;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i)
+        if (row0 + i < p.m)
+          mx_write4<T>(p, row0 + i, col, *reinterpret_cast<const float4*>(src + i * kMxPitch),
                        alpha);
-      }
+    }
   } else {
     cluster_sync();
-    if (warp >= 2 && fine)
-      for (int i = warp - 2;; i += 4) {
-        const int r = rank + i * p.split, row = tm * kMxTile + r;
-        if (r >= kMxTile || row >= p.m) break;
-        const int col = tn * kMxTile + lane * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < p.split; ++s) {
-          const float4 u = ld_shared_cluster_f32x4(
-              cluster_addr(part + r * kMxPitch + lane * 4, (uint32_t)s));
-          v.x += u.x;
-          v.y += u.y;
-          v.z += u.z;
-          v.w += u.w;
-        }
-        if (col < p.n) mx_write4<T>(p, row, col, v, alpha);
-      }
+    if (fine) {
+      if (p.split == 2) mx_reduce_rows<T, 2>(p, part, warp, lane, rank, tm, tn, alpha);
+      else if (p.split == 4) mx_reduce_rows<T, 4>(p, part, warp, lane, rank, tm, tn, alpha);
+      else mx_reduce_rows<T, 8>(p, part, warp, lane, rank, tm, tn, alpha);
+    }
     cluster_sync();  // no CTA leaves while another reads its partial sums
   }
   tc_fence_before();
@@ -211,7 +244,7 @@ template <int FMT, typename T>
 cudaError_t launch_mx(const CUtensorMap (&t)[5], const MxParams& p, cudaStream_t stream) {
   using C = MxCfg<FMT>;
   static std::atomic<uint64_t> done_mask{0};
-  const cudaError_t e = mx_opt_in(mx_gemm_kernel<FMT, T>, done_mask, (int)C::SMEM);
+  const cudaError_t e = opt_in_smem((const void*)mx_gemm_kernel<FMT, T>, done_mask, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   return launch_pdl_cluster(mx_gemm_kernel<FMT, T>, dim3((unsigned)(tiles * p.split)),
@@ -226,13 +259,33 @@ cudaError_t launch_mx_out(const CUtensorMap (&t)[5], const MxParams& p, int out,
   return launch_mx<FMT, __nv_bfloat16>(t, p, stream);
 }
 
-// Whether a product runs on CTA pairs: their 256 x 256 tiles halve what each SM
-// reads per product, and need enough of them.
-bool wants_pairs(int64_t m, int64_t n, int64_t k, int clusters) {
+// CTAs that share a 128 x 128 tile: doubled while they all fit the GPU at once
+// (two per SM) and each has a stage of k.
+int split_of(int64_t tiles, int ksteps, int sms) {
+  int s = 1;
+  while (s < kMxSplitMax && tiles * s * 2 <= 2 * sms && s * 2 <= ksteps) s *= 2;
+  return s;
+}
+
+// Whether a product runs on CTA pairs: 256 x 256 tiles halve what each SM reads
+// per product, but cannot share a tile's k. Up to 128 rows the single CTAs win at
+// every n and k (1 x 8192 x 8192 in nvfp4: 9.5 against 17.9 us). Beyond, both are
+// estimated: a fixed cost plus the stages of the busiest CTA, with the times of a
+// stage as measured (us; two single CTAs share an SM, so theirs holds for a full
+// one). 1024 x 1024 x 8192 in mxfp8: 14.4 us single (4 CTAs a tile), 21.7 paired;
+// 2048 x 2048 x 2048: 11.9 single, 9.5 paired.
+bool wants_pairs(int64_t m, int64_t n, int ksteps, int clusters, int sms) {
 #ifdef SKG_MX_PAIR
   return SKG_MX_PAIR != 0;
 #endif
-  return m > 128 && ((m + 255) / 256) * ((n + 255) / 256) * 2 >= clusters;
+  if (m <= kMxTile) return false;
+  const int64_t tiles2 = ((m + 255) / 256) * ((n + 255) / 256);
+  const int64_t tiles1 = ((m + 127) / 128) * ((n + 127) / 128);
+  const int split = split_of(tiles1, ksteps, sms);
+  const double pair = 3.3 + 0.29 * (double)((tiles2 + clusters - 1) / clusters) * ksteps;
+  const double single = 6.0 + 0.54 * (double)((tiles1 * split + 2 * sms - 1) / (2 * sms)) *
+                                  ((ksteps + split - 1) / split);
+  return pair <= single;
 }
 
 template <int FMT>
@@ -244,14 +297,11 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
   p.ksteps = (p.k + C::STEP - 1) / C::STEP;
   const int64_t rt_a = (p.m + kMxTile - 1) / kMxTile, rt_b = (p.n + kMxTile - 1) / kMxTile;
   const int resident = mx_pair_clusters_resident();
-  const bool pair = resident > 0 && wants_pairs(p.m, p.n, p.k, resident);
+  const bool pair = resident > 0 && wants_pairs(p.m, p.n, p.ksteps, resident, sms);
   const int64_t tm = pair ? (rt_a + 1) / 2 : rt_a, tn = pair ? (rt_b + 1) / 2 : rt_b;
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
-  p.split = 1;
-  while (!pair && p.split < kMxSplitMax && tm * tn * p.split * 2 <= 2 * sms &&
-         p.split * 2 <= p.ksteps)
-    p.split *= 2;
+  p.split = pair ? 1 : split_of(tm * tn, p.ksteps, sms);
   p.a_rows = !pair && p.m < kMxTile ? (p.m + 7) / 8 * 8 : kMxTile;
   const uint64_t bytes = ((uint64_t)p.k * mx_bits(FMT) + 7) / 8;
   const uint64_t chunks_a = (uint64_t)rt_a * p.groups, chunks_b = (uint64_t)rt_b * p.groups;

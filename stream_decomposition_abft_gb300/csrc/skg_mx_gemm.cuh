@@ -140,21 +140,6 @@ __device__ __forceinline__ void mx_stage_mmas(uint32_t d, uint32_t sfa, uint32_t
   }
 }
 
-// The shared-memory opt-in is per device; set it once per device.
-template <typename K>
-cudaError_t mx_opt_in(K kernel, std::atomic<uint64_t>& done_mask, int bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (!bit || !(done_mask.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    done_mask.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  return cudaSuccess;
-}
-
 // 256 x 256 tiles on clusters of two CTAs (skg_mx_gemm_pair.cu); t: the maps of
 // A, B, their scales and (p.c_tma) C. `clusters` CTA pairs.
 template <int FMT>

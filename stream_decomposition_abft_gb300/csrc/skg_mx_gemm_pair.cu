@@ -297,7 +297,7 @@ cudaError_t launch_pair(const CUtensorMap (&t)[5], const MxParams& p, int cluste
                         cudaStream_t stream) {
   using C = PairCfg<FMT>;
   static std::atomic<uint64_t> done_mask{0};
-  const cudaError_t e = mx_opt_in(mx_gemm_pair_kernel<FMT, T>, done_mask, (int)C::SMEM);
+  const cudaError_t e = opt_in_smem((const void*)mx_gemm_pair_kernel<FMT, T>, done_mask, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(mx_gemm_pair_kernel<FMT, T>, dim3((unsigned)(2 * clusters)),
                             dim3(kMxThreads), C::SMEM, stream, 2, t[0], t[1], t[2], t[3], t[4], p);

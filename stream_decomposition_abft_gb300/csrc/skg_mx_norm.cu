@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "skg_internal.h"
 #include "skg_mx.cuh"
 #include "skgemm.h"
@@ -134,8 +136,143 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams 
   if (here && p.rstd && t == 0) p.rstd[row] = rstd;
 }
 
+// ------------------------------------------------------------------ wide rows
+// A block per row at a time, whole rows on 16-byte boundaries. A thread owns the
+// pieces of 8 elements t, t + blockDim, ... of every row and fetches the next
+// rows' pieces into a ring of its own in shared memory (cp.async): the loads of
+// kNormStages rows are in flight whatever the rows in hand wait for, and no other
+// thread reads what a thread has fetched, so the ring needs no barriers.
+constexpr int kNormStages = 3;
+constexpr int kGradStages = 4;
+
+// Sum over the block; `par` alternates from call to call.
+__device__ __forceinline__ float block_sum(float v, float (*red)[kNormMaxThreads / 32], int par) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int nw = (int)blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[par][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = (threadIdx.x & 31) < nw ? red[par][threadIdx.x & 31] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+template <typename T, int FMT, int V>
+__global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(NormParams p) {
+  extern __shared__ uint4 ring[];  // stages x (x, residual) x V x threads
+  __shared__ float red[2][kNormMaxThreads / 32];
+  const int t = threadIdx.x, lane = t & 31, nt = blockDim.x;
+  const int groups = (int)mx_groups(p.cols, FMT);
+  const int pieces = (p.cols + 31) / 32 * 4;
+  const int64_t rows_pad = (p.rows + 127) / 128 * 128;
+  const T* x = reinterpret_cast<const T*>(p.x);
+  const T* res = reinterpret_cast<const T*>(p.res);
+  griddep_wait();
+  griddep_launch_dependents();
+  const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
+  auto fetch = [&](int64_t row, int st) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = (t + j * nt) * 8;
+        const uint32_t n = c < p.cols ? 16u : 0u;
+        uint4* dst = ring + ((st * 2) * V + j) * nt + t;
+        cp_async16(dst, x + row * p.ldx + (n ? c : 0), n);
+        if (p.res) cp_async16(dst + V * nt, res + row * p.ldr + (n ? c : 0), n);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < kNormStages; ++i)
+    fetch((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
+  uint4 wv[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (t + j * nt) * 8;
+    wv[j] = c < p.cols ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + c)
+                       : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int st = 0, par = 0;
+  for (int64_t row = blockIdx.x; row < rows_pad; row += gridDim.x) {
+    const bool here = row < p.rows;  // the same for the whole block
+    float h[V][8], rstd = 0.f;
+    cp_async_wait<kNormStages - 1>();
+    if (here) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint4* src = ring + ((st * 2) * V + j) * nt + t;
+        mx_unpack8<T>(src[0], h[j]);
+        if (p.res) {
+          float r[8];
+          mx_unpack8<T>(src[V * nt], r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[j][i] += r[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += h[j][i] * h[j][i];
+      }
+      rstd = rsqrtf(block_sum(ss, red, par) / (float)p.cols + p.eps);
+      par ^= 1;
+      if (p.rstd && t == 0) p.rstd[row] = rstd;
+    }
+    fetch(row + (int64_t)kNormStages * gridDim.x, st);
+    if (++st == kNormStages) st = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = t + j * nt;
+      const bool live = here && c < pieces;
+      if (live && p.sum && c * 8 < p.cols)
+        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.sum) + row * p.lds + c * 8) =
+            mx_pack8<T>(h[j]);
+      float w[8], y[8];
+      mx_unpack8<T>(wv[j], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = here ? __fmul_rn(__fmul_rn(h[j][i], rstd), w[i]) : 0.f;
+      uint2 codes;
+      uint32_t word;
+      mx_quantize_piece<FMT>(y, live, lane, g, codes, word);
+      if (live) {
+        if constexpr (FMT == SKG_MXFP8)
+          *reinterpret_cast<uint2*>(p.codes + row * p.ldq + c * 8) = codes;
+        else
+          *reinterpret_cast<uint32_t*>(p.codes + row * p.ldq + c * 4) = codes.x;
+      }
+      constexpr int per = 2 * mx_group_chunks(FMT);
+      if ((lane & (per - 1)) == 0 && c / per < groups)
+        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, c / per, groups)) = word;
+    }
+  }
+}
+
 template <typename T, int FMT>
-cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, int sms,
+                             cudaStream_t stream) {
+  const size_t smem = (size_t)kNormStages * 2 * v * threads * 16;
+  const int64_t rows = (p.rows + 127) / 128 * 128;
+  const dim3 grid((unsigned)(rows < 2 * sms ? rows : 2 * sms));
+  auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
+    const cudaError_t e = opt_in_smem((const void*)kernel, done, kNormStages * 2 * kNormMaxThreads *
+                                                                     16 * 2);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(threads), smem, stream, p);
+  };
+  static std::atomic<uint64_t> d1{0}, d2{0};
+  return v == 1 ? run(rmsnorm_mx_wide_kernel<T, FMT, 1>, d1)
+                : run(rmsnorm_mx_wide_kernel<T, FMT, 2>, d2);
+}
+
+template <typename T, int FMT>
+cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t stream) {
+  // Rows of 1024 to 8192 elements on 16-byte boundaries: a block per row with
+  // its ring (narrower rows share a block, wider ones need more registers).
+  const int pieces = (p.cols + 31) / 32 * 4;
+  if (p.x_vec && p.w_vec && (!p.res || p.r_vec) && (!p.sum || p.s_vec) && p.cols % 8 == 0 &&
+      pieces > 96 && pieces <= 2 * kNormMaxThreads) {
+    const int threads = pieces <= kNormMaxThreads ? (pieces + 31) / 32 * 32
+                                                  : (pieces + 63) / 64 * 32;
+    return launch_norm_wide<T, FMT>(p, pieces <= kNormMaxThreads ? 1 : 2, threads, sms, stream);
+  }
   const int chunks = (p.cols + 31) / 32 * 2;
   int log_tpr = 3;
   while ((1 << log_tpr) < chunks && (1 << log_tpr) < kNormMaxThreads) ++log_tpr;
@@ -154,10 +291,10 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t launch_norm_fmt(const NormParams& p, int fmt, cudaStream_t stream) {
-  if (fmt == SKG_MXFP8) return launch_norm<T, SKG_MXFP8>(p, stream);
-  if (fmt == SKG_MXFP4) return launch_norm<T, SKG_MXFP4>(p, stream);
-  return launch_norm<T, SKG_NVFP4>(p, stream);
+cudaError_t launch_norm_fmt(const NormParams& p, int fmt, int sms, cudaStream_t stream) {
+  if (fmt == SKG_MXFP8) return launch_norm<T, SKG_MXFP8>(p, sms, stream);
+  if (fmt == SKG_MXFP4) return launch_norm<T, SKG_MXFP4>(p, sms, stream);
+  return launch_norm<T, SKG_NVFP4>(p, sms, stream);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -290,6 +427,99 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(GradParam
   }
 }
 
+// The wide rows' gradient: as rmsnorm_mx_wide_kernel, a ring of dy, h and
+// dresidual; dw of the block's rows stays in registers.
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(GradParams p) {
+  extern __shared__ uint4 ring[];  // stages x (dy, h, dres) x V x threads
+  __shared__ float red[2][kNormMaxThreads / 32];
+  const int t = threadIdx.x, nt = blockDim.x;
+  const T* in[3] = {reinterpret_cast<const T*>(p.dy), reinterpret_cast<const T*>(p.h),
+                    reinterpret_cast<const T*>(p.dres)};
+  const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
+  griddep_wait();
+  griddep_launch_dependents();
+  auto fetch = [&](int64_t row, int st) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (k == 2 && !p.dres) break;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c = (t + j * nt) * 8;
+          const uint32_t n = c < p.cols ? 16u : 0u;
+          cp_async16(ring + ((st * 3 + k) * V + j) * nt + t, in[k] + row * ld[k] + (n ? c : 0), n);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < kGradStages; ++i)
+    fetch((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
+  uint4 wv[V];
+  float acc[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (t + j * nt) * 8;
+    wv[j] = c < p.cols ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + c)
+                       : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
+  }
+  const float inv_n = 1.f / (float)p.cols;
+  int st = 0, par = 0;
+  float rstd_next = blockIdx.x < p.rows ? p.rstd[blockIdx.x] : 0.f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float rstd = rstd_next;
+    if (row + gridDim.x < p.rows) rstd_next = p.rstd[row + gridDim.x];
+    float xhat[V][8], u[V][8], o[V][8], dot = 0.f;
+    cp_async_wait<kGradStages - 1>();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint4* src = ring + (st * 3 * V + j) * nt + t;
+      float dy[8];
+      mx_unpack8<T>(src[0], dy);
+      mx_unpack8<T>(src[V * nt], xhat[j]);
+      mx_unpack8<T>(wv[j], u[j]);
+      if (p.dres) {
+        mx_unpack8<T>(src[2 * V * nt], o[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[j][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xhat[j][i] *= rstd;
+        u[j][i] *= dy[i];
+        acc[j][i] += dy[i] * xhat[j][i];
+        dot += u[j][i] * xhat[j][i];
+      }
+    }
+    fetch(row + (int64_t)kGradStages * gridDim.x, st);
+    if (++st == kGradStages) st = 0;
+    const float mean = block_sum(dot, red, par) * inv_n;
+    par ^= 1;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (t + j * nt) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[j][i] += rstd * (u[j][i] - xhat[j][i] * mean);
+      if (c < p.cols)
+        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.dx) + row * p.lddx + c) =
+            mx_pack8<T>(o[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (t + j * nt) * 8;
+    if (c < p.cols) {
+      float4* out = reinterpret_cast<float4*>(p.partial + (int64_t)blockIdx.x * p.cols + c);
+      out[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      out[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+    }
+  }
+}
+
 // dw of a block's rows, for widths whose sums do not fit the row kernel's
 // registers: a thread per column.
 template <typename T>
@@ -347,10 +577,26 @@ GradPlan grad_plan(int64_t rows, int64_t cols, int sms) {
 }
 
 template <typename T>
-cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaStream_t stream) {
+cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, int sms,
+                        cudaStream_t stream) {
   cudaError_t e;
   const dim3 grid(g.blocks), block(g.threads);
-  if (g.v == 1)
+  const int pieces = (p.cols + 7) / 8;
+  int parts = g.blocks;
+  if (p.vec && p.cols % 8 == 0 && pieces > 96 && pieces <= 2 * kNormMaxThreads) {
+    const int v = pieces <= kNormMaxThreads ? 1 : 2;
+    const int threads = (pieces + 32 * v - 1) / (32 * v) * 32;
+    const size_t smem = (size_t)kGradStages * 3 * v * threads * 16;
+    parts = (int)(p.rows < sms ? p.rows : sms);
+    auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
+      const cudaError_t r = opt_in_smem((const void*)kernel, done,
+                                        kGradStages * 3 * 2 * kNormMaxThreads * 16);
+      return r != cudaSuccess ? r
+                              : launch_pdl(kernel, dim3(parts), dim3(threads), smem, stream, p);
+    };
+    static std::atomic<uint64_t> d1{0}, d2{0};
+    e = v == 1 ? run(rmsnorm_grad_wide_kernel<T, 1>, d1) : run(rmsnorm_grad_wide_kernel<T, 2>, d2);
+  } else if (g.v == 1)
     e = launch_pdl(rmsnorm_grad_kernel<T, 1>, grid, block, g.smem, stream, p, g.log_tpr);
   else if (g.v == 2)
     e = launch_pdl(rmsnorm_grad_kernel<T, 2>, grid, block, g.smem, stream, p, g.log_tpr);
@@ -365,7 +611,7 @@ cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaS
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(256),
-                    0, stream, (const float*)p.partial, g.blocks, p.cols, dw);
+                    0, stream, (const float*)p.partial, parts, p.cols, dw);
 }
 
 bool vec_rows(const void* p, int64_t ld) {
@@ -417,8 +663,10 @@ skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t l
   p.w_vec = ((uintptr_t)weight & 15) == 0;
   p.s_vec = vec_rows(sum, lds);
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = type == SKG_IN_F16 ? launch_norm_fmt<__half>(p, format, st)
-                                           : launch_norm_fmt<__nv_bfloat16>(p, format, st);
+  const int sms = skg_device_sm_count();
+  if (sms <= 0) return SKG_ERR_CUDA;
+  const cudaError_t e = type == SKG_IN_F16 ? launch_norm_fmt<__half>(p, format, sms, st)
+                                           : launch_norm_fmt<__nv_bfloat16>(p, format, sms, st);
   return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
 }
 
@@ -473,8 +721,8 @@ skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, in
   p.partial = (float*)workspace;
   p.vec = vec_rows(dY, lddy) && vec_rows(H, ldh) && vec_rows(dX, lddx) &&
           ((uintptr_t)weight & 15) == 0 && (!dresidual || vec_rows(dresidual, lddr));
-  const cudaError_t e = type == SKG_IN_F16 ? launch_grad<__half>(p, g, dweight, st)
-                                           : launch_grad<__nv_bfloat16>(p, g, dweight, st);
+  const cudaError_t e = type == SKG_IN_F16 ? launch_grad<__half>(p, g, dweight, sms, st)
+                                           : launch_grad<__nv_bfloat16>(p, g, dweight, sms, st);
   return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
 }
 

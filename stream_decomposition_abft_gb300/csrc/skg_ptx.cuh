@@ -453,9 +453,26 @@ __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t addr_cluster)
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr_cluster)
-               : "memory");
+               : "r"(addr_cluster));
   return v;
+}
+
+// ---------------------------------------------------------------- cp.async
+// 16 bytes global -> shared (through L2 alone), `bytes` (0 or 16) of them read
+// and the rest zero; both addresses 16-byte aligned.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"((uint64_t)src), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ---------------------------------------------------------------- PDL
