@@ -1,15 +1,20 @@
-"""Build libskgemm.so in-tree with nvcc for sm_103a.
+"""Build libskgemm.so in-tree with nvcc for sm_103a, and the torch binding
+_skg_torch.so next to it.
 
 Each .cu under csrc/ is one translation unit; they compile in parallel
 (one -gencode, no cmake) and link into a shared library with the CUDA
-runtime linked statically, so loading the library needs no GPU.
+runtime linked statically, so loading the library needs no GPU. The binding
+(csrc/skg_torch.cpp, host code) compiles against the installed torch at the
+same time and links to libskgemm.so beside it.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libskgemm.so")
+BINDING = os.path.join(PKG, "_skg_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -37,8 +43,32 @@ def _newest_header() -> float:
     return max(os.path.getmtime(h) for h in hdrs)
 
 
+def _binding_job(force: bool):
+    """(compile command or None, object) of the torch binding; the object's name
+    carries torch's version, whose headers it is compiled against."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        version = "".join(c if c.isalnum() else "_" for c in
+                          next(line for line in f if line.startswith("__version__")))
+    src = os.path.join(CSRC, "skg_torch.cpp")
+    obj = os.path.join(BUILD, f"skg_torch_{version}.o")
+    fresh = os.path.exists(obj) and os.path.getmtime(obj) >= max(
+        os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "skgemm.h")))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I",
+           os.path.join(torch_dir, "include"), "-I",
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], "-c", src, "-o", obj]
+    lib = os.path.join(torch_dir, "lib")
+    link = ["g++", "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+            "-ltorch_python", "-L", PKG, "-l:libskgemm.so", "-Wl,-rpath,$ORIGIN",
+            f"-Wl,-rpath,{lib}"]
+    return (cmd if force or not fresh else None), link
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile (incrementally) and link libskgemm.so; returns its path."""
+    """Compile (incrementally) and link libskgemm.so and the binding; returns the
+    library's path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -60,6 +90,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(res.stdout + res.stderr)
         return res
 
+    binding, binding_link = _binding_job(force)
+    if binding:
+        jobs.insert(0, binding)  # the longest one
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
@@ -67,6 +100,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if jobs or not os.path.exists(BINDING):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        run([*binding_link, "-o", tmp])
+        os.replace(tmp, BINDING)
     return LIB
 
 

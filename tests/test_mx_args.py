@@ -104,16 +104,10 @@ def test_binding_refusals():
         mx.rmsnorm(x, x[0], 1e-5)
     q = mx.Matrix("mxfp8", 4, 64, torch.zeros(4, 64, dtype=torch.uint8),
                   torch.zeros(512, dtype=torch.uint8))
+    ws = type("W", (), {"buf": x})
     with pytest.raises(ValueError, match="codes or scales"):
-        mx.matmul(q, q)
-    with pytest.raises(ValueError, match="other operand"):
-        mx._operand("b", q._replace(format="mxfp4"), "mxfp8", None)
-
-
-def test_binding_sizes():
-    # The binding's own layout arithmetic is the library's.
-    for fmt, code in mx.FORMATS.items():
-        for rows in (0, 1, 127, 128, 129, 5000):
-            for k in (0, 1, 31, 32, 33, 63, 64, 65, 128, 129, 2200, 28672):
-                assert mx._sizes(rows, k, fmt) == (skgemm.mx_codes_ld(k, code),
-                                                   skgemm.mx_scales_size(rows, k, code))
+        mx.matmul(q, q, workspace=ws)
+    with pytest.raises(ValueError, match="tensor is wanted"):
+        mx.quantize(None, "mxfp8")
+    with pytest.raises(ValueError, match="Matrix is wanted"):
+        mx.matmul((), q, workspace=ws)
