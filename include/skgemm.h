@@ -541,6 +541,15 @@ skg_status_t skg_mx_quantize(int64_t rows, int64_t k, const void* X, int64_t ldx
                              void* codes, int64_t ldq, void* scales, void* values, int64_t ldv,
                              void* stream);
 
+/* A matrix and its transpose quantised in one pass over it (the two operands that
+ * a linear layer's gradients take of dY): codes, scales of X (rows x cols, blocks
+ * along the rows) and codes_t, scales_t of X^T (cols x rows), each the same bytes
+ * as skg_mx_quantize's. Arguments as there. */
+skg_status_t skg_mx_quantize_both(int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                                  int32_t type, int32_t format, const float* tensor_scale,
+                                  void* codes, int64_t ldq, void* scales, void* codes_t,
+                                  int64_t ldq_t, void* scales_t, void* stream);
+
 /* RMS norm of x + residual with a quantised output, asynchronous on `stream`:
  *   h = X + residual;  rstd = 1 / sqrt(mean over the row of h^2 + eps);
  *   codes, scales = quantised(h * rstd * weight), in fp32 up to the codes.

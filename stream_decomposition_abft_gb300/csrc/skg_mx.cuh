@@ -207,6 +207,27 @@ __device__ __forceinline__ uint4 mx_codes16(const float (&v)[16], const MxScale&
   return o;
 }
 
+// Eight codes: 8 bytes (e4m3) or 4 (e2m1: .x).
+template <int FMT>
+__device__ __forceinline__ uint2 mx_codes8(const float (&v)[8], const MxScale& s) {
+  if (s.bad) return make_uint2(0u, 0u);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], s.inv);
+  if constexpr (FMT == SKG_MXFP8)
+    return make_uint2(mx_e4m3x4(y[0], y[1], y[2], y[3]), mx_e4m3x4(y[4], y[5], y[6], y[7]));
+  else
+    return make_uint2(mx_e2m1x8(y), 0u);
+}
+
+template <int FMT>
+__device__ __forceinline__ void mx_store_codes8(uint8_t* row, int64_t piece, const uint2& o) {
+  if constexpr (FMT == SKG_MXFP8)
+    *reinterpret_cast<uint2*>(row + piece * 8) = o;
+  else
+    *reinterpret_cast<uint32_t*>(row + piece * 4) = o.x;
+}
+
 // What sixteen codes and their scale stand for (nvfp4: (code * s) * g).
 template <int FMT>
 __device__ __forceinline__ void mx_values16(const uint4& o, const MxScale& s, float g,
@@ -256,27 +277,47 @@ __device__ __forceinline__ MxScale mx_quantize_chunk(const float (&v)[16], bool 
 
 // The same for pieces of 8 elements (piece c in a lane with lane % 16 == c % 16).
 template <int FMT>
-__device__ __forceinline__ void mx_quantize_piece(const float (&v)[8], bool live, int lane,
-                                                  float g, uint2& codes, uint32_t& word) {
+__device__ __forceinline__ MxScale mx_quantize_piece(const float (&v)[8], bool live, int lane,
+                                                     float g, uint2& codes, uint32_t& word) {
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   if constexpr (FMT != SKG_NVFP4) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   const MxScale s = mx_scale<FMT>(amax, g);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], s.inv);
-  if constexpr (FMT == SKG_MXFP8)
-    codes = make_uint2(mx_e4m3x4(y[0], y[1], y[2], y[3]), mx_e4m3x4(y[4], y[5], y[6], y[7]));
-  else
-    codes = make_uint2(mx_e2m1x8(y), 0u);
-  if (s.bad) codes = make_uint2(0u, 0u);
+  codes = mx_codes8<FMT>(v, s);
   const int slot = FMT == SKG_NVFP4 ? ((lane >> 1) & 3) : ((lane >> 2) & 3);
   word = live ? s.byte << (8 * slot) : 0u;
   if constexpr (FMT == SKG_NVFP4) word |= __shfl_xor_sync(0xffffffffu, word, 2);
   word |= __shfl_xor_sync(0xffffffffu, word, 4);
   if constexpr (FMT != SKG_NVFP4) word |= __shfl_xor_sync(0xffffffffu, word, 8);
+  return s;
+}
+
+// Eight consecutive elements as they are. `vec`: the address is 16-byte aligned
+// and all eight exist; else the first n are read one by one, the rest are 0.
+template <typename T>
+struct MxRaw8 {
+  uint4 q[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ MxRaw8<T> mx_load_raw8(const T* p, bool vec, int n) {
+  MxRaw8<T> r;
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = *(reinterpret_cast<const uint4*>(p) + i);
+  } else {
+    T* e = reinterpret_cast<T*>(r.q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : mx_from_f32<T>(0.f);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void mx_unpack_raw8(const MxRaw8<T>& r, float (&v)[8]) {
+  const T* e = reinterpret_cast<const T*>(r.q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(e[i]);
 }
 
 // Eight elements of a 16-bit type.

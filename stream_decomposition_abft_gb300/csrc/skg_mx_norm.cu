@@ -234,10 +234,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
       uint32_t word;
       mx_quantize_piece<FMT>(y, live, lane, g, codes, word);
       if (live) {
-        if constexpr (FMT == SKG_MXFP8)
-          *reinterpret_cast<uint2*>(p.codes + row * p.ldq + c * 8) = codes;
-        else
-          *reinterpret_cast<uint32_t*>(p.codes + row * p.ldq + c * 4) = codes.x;
+        mx_store_codes8<FMT>(p.codes + row * p.ldq, c, codes);
       }
       constexpr int per = 2 * mx_group_chunks(FMT);
       if ((lane & (per - 1)) == 0 && c / per < groups)

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "skg_internal.h"
 #include "skg_mx.cuh"
 #include "skgemm.h"
@@ -29,7 +31,10 @@ struct QuantParams {
   int x_vec, v_vec;        // 16-byte aligned rows
 };
 
-// Along the rows. A thread takes 16 consecutive elements; a warp 32 / TX rows
+// Along the rows. A thread takes 16 consecutive elements (with 8, and four rows'
+// loads in flight per thread, the blocks' scales are formed twice as often, and
+// the kernel is bound by instructions: 8192 x 8192 in mxfp4 with its values 60 us
+// against 50, in nvfp4 86 against 59); a warp 32 / TX rows
 // of TX chunks (TX a power of two of at least 8, so that the lanes of a block
 // group sit together). A block of 256 threads takes the rows 32 q + l of one
 // scale tile for l in a range of TY / 4: the 16 bytes of scales of each l are
@@ -76,100 +81,152 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
   }
 }
 
-// Along the columns: X is stored k x rows. A block stages 128 lines of 64
-// columns in shared memory; a thread then takes 32 consecutive k of one
-// column. Consecutive lanes hold consecutive k ranges of a column, so codes and
-// values leave in whole lines; the words of a line are XORed with the line's
-// k range, so that those lanes read different banks.
-constexpr int kTK = 128, kTC = 64;
+// Along the columns, or along both. X is stored lines x columns; a block takes a
+// tile of 128 x 128 of it. The row direction (ROWS: the quantised X) works on the
+// pieces of 8 elements as they are loaded, 16 lanes a line. For the column
+// direction (the quantised X^T) the tile goes to shared memory (16-bit types),
+// and a thread takes 32 consecutive lines of two adjacent columns: four lanes
+// hold the tile's four line ranges of a column pair, so that codes leave in
+// 64 to 128 bytes at a time; the words of a line are XORed with its line range
+// for those lanes to read different banks.
+constexpr int kTile = 128;
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_quantize_cols_kernel(QuantParams p) {
-  constexpr int EW = 16 / (int)sizeof(T);         // elements per 16 bytes
-  constexpr int VECS = kTC / EW;                  // 16-byte pieces of a line
-  constexpr int XOR = 8 * (int)sizeof(T) / 16;    // 16-byte pieces of 8 columns
-  __shared__ __align__(16) T tile[kTK * kTC];
+template <typename T, int FMT, bool ROWS>
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3)
+mx_quantize_tile_kernel(QuantParams p, QuantParams rp) {
+  constexpr int W = sizeof(T) / 2;           // 32-bit words of a column pair
+  constexpr int LINE = kTile * sizeof(T) / 4;  // words of a line
+  extern __shared__ uint32_t tile[];         // kTile x LINE
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t k0 = (int64_t)blockIdx.x * kTK, c0 = (int64_t)blockIdx.y * kTC;
+  const int lane = threadIdx.x & 31;
+  const int64_t k0 = (int64_t)blockIdx.x * kTile, c0 = (int64_t)blockIdx.y * kTile;
   const T* x = reinterpret_cast<const T*>(p.x);
-  for (int i = threadIdx.x; i < kTK * VECS; i += kQThreads) {
-    const int line = i / VECS, piece = i % VECS;
-    const int64_t kk = k0 + line, c = c0 + piece * EW;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (kk < p.k) {
-      const T* src = x + kk * p.ldx + c;
-      if (p.x_vec && c + EW <= p.rows) {
-        u = *reinterpret_cast<const uint4*>(src);
-      } else {
-        T* e = reinterpret_cast<T*>(&u);
+  const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
+  {
+    const int piece = threadIdx.x & 15;
+    const int64_t c = c0 + piece * 8;
+    const int64_t left = p.rows - c;
+    const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    MxRaw8<T> raw[8];
 #pragma unroll
-        for (int j = 0; j < EW; ++j)
-          if (c + j < p.rows) e[j] = src[j];
+    for (int i = 0; i < 8; ++i) {
+      const int64_t line = k0 + i * 16 + (threadIdx.x >> 4);
+      const int m = line < p.k ? n : 0;
+      raw[i] = mx_load_raw8(x + line * p.ldx + c, p.x_vec && m == 8, m);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int line = i * 16 + (threadIdx.x >> 4);
+      // Word w of a line at w ^ 8 W (line / 32): pieces of 4 words stay whole.
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        *reinterpret_cast<uint4*>(tile + line * LINE +
+                                  ((piece * 4 * W + j * 4) ^ ((line >> 5) * 8 * W))) = raw[i].q[j];
+      if constexpr (ROWS) {
+        const int64_t r = k0 + line;
+        const bool here = r < rp.rows && c < (rp.k + 31) / 32 * 32;
+        float v[8];
+        mx_unpack_raw8(raw[i], v);
+        uint2 codes;
+        uint32_t word;
+        mx_quantize_piece<FMT>(v, here, lane, g, codes, word);
+        if (here) mx_store_codes8<FMT>(rp.codes + r * rp.ldq, c / 8, codes);
+        constexpr int per = 2 * mx_group_chunks(FMT);
+        const int groups = (int)mx_groups(rp.k, FMT);
+        const int64_t grp = c / 8 / per;
+        if ((lane & (per - 1)) == 0 && grp < groups)
+          *reinterpret_cast<uint32_t*>(rp.scales + mx_scale_word(r, (int)grp, groups)) = word;
       }
     }
-    reinterpret_cast<uint4*>(tile)[line * VECS + (piece ^ ((line >> 5) * XOR))] = u;
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int kb = lane & 3, col = (threadIdx.x >> 5) * 8 + (lane >> 2);
-  const int piece = (col / EW) ^ (kb * XOR);
-  const int64_t row = c0 + col;
-  const bool here = row < p.rows;
+  const int kb = lane & 3, pair = (threadIdx.x >> 5) * 8 + (lane >> 2);
   const int64_t kfirst = k0 + kb * 32;
-  const bool live = here && kfirst < p.k;
-  const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
-  float v[2][16];
+  const int groups = (int)mx_groups(p.k, FMT);
+  uint32_t w[32][W];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int i = 0; i < 32; ++i)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[h][i] = mx_to_f32(tile[(kb * 32 + h * 16 + i) * kTC + piece * EW + col % EW]);
-  uint32_t amax[2] = {mx_absmax16(v[0]), mx_absmax16(v[1])};
-  if constexpr (FMT != SKG_NVFP4) amax[0] = amax[1] = max(amax[0], amax[1]);
-  MxScale s[2];
+    for (int j = 0; j < W; ++j)
+      w[i][j] = tile[(kb * 32 + i) * LINE + ((pair * W + j) ^ (kb * 8 * W))];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    s[h] = mx_scale<FMT>(amax[h], g);
-    if (live) {
-      const uint4 codes = mx_codes16<FMT>(v[h], s[h]);
-      mx_store_codes16<FMT>(p.codes + row * p.ldq, kfirst / 16 + h, codes);
-      if (p.values) {
-        float w[16];
-        mx_values16<FMT>(codes, s[h], g, w);
-        const int64_t left = p.k - (kfirst + h * 16);
-        const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
-        mx_store16(reinterpret_cast<T*>(p.values) + row * p.ldv + kfirst + h * 16,
-                   p.v_vec && n == 16, n, w);
+  for (int h = 0; h < 2; ++h) {  // the pair's columns
+    const int64_t row = c0 + pair * 2 + h;
+    const bool live = row < p.rows && kfirst < p.k;
+    uint32_t bytes[2];
+    MxScale s;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {  // 16 lines at a time
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = W == 2 ? w[b * 16 + i][h * (W - 1)] : w[b * 16 + i][0];
+        if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(u);
+        else v[i] = mx_to_f32(reinterpret_cast<const T*>(&u)[h]);
+      }
+      if (FMT == SKG_NVFP4 || b == 0) {
+        uint32_t amax = mx_absmax16(v);
+        if constexpr (FMT != SKG_NVFP4) {
+          float v2[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t u = W == 2 ? w[16 + i][h * (W - 1)] : w[16 + i][0];
+            if constexpr (sizeof(T) == 4) v2[i] = __uint_as_float(u);
+            else v2[i] = mx_to_f32(reinterpret_cast<const T*>(&u)[h]);
+          }
+          amax = max(amax, mx_absmax16(v2));
+        }
+        s = mx_scale<FMT>(amax, g);
+      }
+      bytes[b] = s.byte;
+      if (live) {
+        const uint4 codes = mx_codes16<FMT>(v, s);
+        mx_store_codes16<FMT>(p.codes + row * p.ldq, kfirst / 16 + b, codes);
+        if (p.values) {
+          mx_values16<FMT>(codes, s, g, v);
+          const int64_t left = p.k - (kfirst + b * 16);
+          const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
+          mx_store16(reinterpret_cast<T*>(p.values) + row * p.ldv + kfirst + b * 16,
+                     p.v_vec && n == 16, n, v);
+        }
       }
     }
-  }
-  const int groups = (int)mx_groups(p.k, FMT);
-  uint32_t word;
-  if constexpr (FMT == SKG_NVFP4) {
-    word = live ? (s[0].byte | (s[1].byte << 8)) << (16 * (kb & 1)) : 0u;
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    const int64_t grp = (k0 / 64) + (kb >> 1);
-    if ((kb & 1) == 0 && grp < groups)
-      *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)grp, groups)) = word;
-  } else {
-    word = live ? s[0].byte << (8 * kb) : 0u;
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    const int64_t grp = k0 / 128;
-    if (kb == 0 && grp < groups)
-      *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)grp, groups)) = word;
+    uint32_t word;
+    if constexpr (FMT == SKG_NVFP4) {
+      word = live ? (bytes[0] | (bytes[1] << 8)) << (16 * (kb & 1)) : 0u;
+      word |= __shfl_xor_sync(0xffffffffu, word, 1);
+      const int64_t grp = (k0 / 64) + (kb >> 1);
+      if ((kb & 1) == 0 && grp < groups)
+        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)grp, groups)) = word;
+    } else {
+      word = live ? bytes[0] << (8 * kb) : 0u;
+      word |= __shfl_xor_sync(0xffffffffu, word, 1);
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+      if (kb == 0 && k0 / 128 < groups)
+        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)(k0 / 128), groups)) = word;
+    }
   }
 }
 
+// rp: the row direction of the same matrix too (NULL: columns alone).
 template <typename T, int FMT>
-cudaError_t launch_quantize(const QuantParams& p, bool transpose, cudaStream_t stream) {
-  if (transpose) {
-    const int64_t gx = (p.k + kTK - 1) / kTK, gy = (p.rows + 127) / 128 * 2;
-    if (gy > 65535) return cudaErrorInvalidValue;
-    return launch_pdl(mx_quantize_cols_kernel<T, FMT>, dim3((unsigned)gx, (unsigned)gy),
-                      dim3(kQThreads), 0, stream, p);
-  }
+cudaError_t launch_tile(const QuantParams& p, const QuantParams* rp, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.k + kTile - 1) / kTile), (unsigned)((p.rows + kTile - 1) / kTile));
+  const size_t smem = kTile * kTile * sizeof(T);
+  static std::atomic<uint64_t> d0{0}, d1{0};
+  const void* kernel = rp ? (const void*)mx_quantize_tile_kernel<T, FMT, true>
+                          : (const void*)mx_quantize_tile_kernel<T, FMT, false>;
+  const cudaError_t e = opt_in_smem(kernel, rp ? d1 : d0, (int)smem);
+  if (e != cudaSuccess) return e;
+  return rp ? launch_pdl(mx_quantize_tile_kernel<T, FMT, true>, grid, dim3(kQThreads), smem, stream,
+                         p, *rp)
+            : launch_pdl(mx_quantize_tile_kernel<T, FMT, false>, grid, dim3(kQThreads), smem,
+                         stream, p, p);
+}
+
+template <typename T, int FMT>
+cudaError_t launch_rows(const QuantParams& p, cudaStream_t stream) {
   const int64_t chunks = (p.k + 31) / 32 * 2;
   int log_tx = 3;
   while (log_tx < 5 && (1 << log_tx) < chunks) ++log_tx;
@@ -181,12 +238,30 @@ cudaError_t launch_quantize(const QuantParams& p, bool transpose, cudaStream_t s
                     dim3(kQThreads), 0, stream, p, log_tx);
 }
 
+template <typename T, int FMT>
+cudaError_t launch_one(const QuantParams* rows, const QuantParams* cols, cudaStream_t stream) {
+  return cols ? launch_tile<T, FMT>(*cols, rows, stream) : launch_rows<T, FMT>(*rows, stream);
+}
+
 template <typename T>
-cudaError_t launch_quantize_fmt(const QuantParams& p, int fmt, bool transpose,
-                                cudaStream_t stream) {
-  if (fmt == SKG_MXFP8) return launch_quantize<T, SKG_MXFP8>(p, transpose, stream);
-  if (fmt == SKG_MXFP4) return launch_quantize<T, SKG_MXFP4>(p, transpose, stream);
-  return launch_quantize<T, SKG_NVFP4>(p, transpose, stream);
+cudaError_t launch_fmt(const QuantParams* rows, const QuantParams* cols, int fmt,
+                       cudaStream_t stream) {
+  if (fmt == SKG_MXFP8) return launch_one<T, SKG_MXFP8>(rows, cols, stream);
+  if (fmt == SKG_MXFP4) return launch_one<T, SKG_MXFP4>(rows, cols, stream);
+  return launch_one<T, SKG_NVFP4>(rows, cols, stream);
+}
+
+// The quantised matrix (rows), its transpose (cols), or both.
+cudaError_t launch_quantize(const QuantParams* rows, const QuantParams* cols, int type, int fmt,
+                            cudaStream_t stream) {
+  if (type == SKG_OUT_F32) return launch_fmt<float>(rows, cols, fmt, stream);
+  if (type == SKG_OUT_F16) return launch_fmt<__half>(rows, cols, fmt, stream);
+  return launch_fmt<__nv_bfloat16>(rows, cols, fmt, stream);
+}
+
+// Whether codes, scales and the other pointers are aligned as the kernels ask.
+bool storage_aligned(const void* codes, int64_t ldq, const void* scales) {
+  return !((uintptr_t)codes & 15) && !(ldq & 15) && !((uintptr_t)scales & 15);
 }
 
 }  // namespace
@@ -220,12 +295,11 @@ skg_status_t skg_mx_quantize(int64_t rows, int64_t k, const void* X, int64_t ldx
       ldq < skg_mx_codes_ld(k, format) || (values && ldv < k))
     return SKG_ERR_ARG;
   // The transposed grid counts column tiles in its second dimension.
-  if (k > INT32_MAX / 4 || rows > (transpose ? 65535 * 64 : INT32_MAX / 4))
+  if (k > INT32_MAX / 4 || rows > (transpose ? 65535 * (int64_t)kTile : INT32_MAX / 4))
     return SKG_ERR_UNSUPPORTED;
   const int es = type == SKG_OUT_F32 ? 4 : 2;
-  if (((uintptr_t)codes & 15) || (ldq & 15) || ((uintptr_t)scales & 15) ||
-      ((uintptr_t)X & (es - 1)) || ((uintptr_t)values & (es - 1)) ||
-      ((uintptr_t)tensor_scale & 3))
+  if (!storage_aligned(codes, ldq, scales) || ((uintptr_t)X & (es - 1)) ||
+      ((uintptr_t)values & (es - 1)) || ((uintptr_t)tensor_scale & 3))
     return SKG_ERR_UNSUPPORTED;
   QuantParams p;
   p.x = X;
@@ -240,12 +314,49 @@ skg_status_t skg_mx_quantize(int64_t rows, int64_t k, const void* X, int64_t ldx
   p.ldv = ldv;
   p.x_vec = ((uintptr_t)X & 15) == 0 && (ldx * es) % 16 == 0;
   p.v_vec = ((uintptr_t)values & 15) == 0 && (ldv * es) % 16 == 0;
-  cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e;
-  if (type == SKG_OUT_F32) e = launch_quantize_fmt<float>(p, format, transpose != 0, st);
-  else if (type == SKG_OUT_F16) e = launch_quantize_fmt<__half>(p, format, transpose != 0, st);
-  else e = launch_quantize_fmt<__nv_bfloat16>(p, format, transpose != 0, st);
-  return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
+  return launch_quantize(transpose ? nullptr : &p, transpose ? &p : nullptr, type, format,
+                         (cudaStream_t)stream) == cudaSuccess
+             ? SKG_OK
+             : SKG_ERR_CUDA;
+}
+
+skg_status_t skg_mx_quantize_both(int64_t rows, int64_t cols, const void* X, int64_t ldx,
+                                  int32_t type, int32_t format, const float* tensor_scale,
+                                  void* codes, int64_t ldq, void* scales, void* codes_t,
+                                  int64_t ldq_t, void* scales_t, void* stream) {
+  if (rows < 0 || cols < 0) return SKG_ERR_ARG;
+  if (type < SKG_OUT_F32 || type > SKG_OUT_BF16) return SKG_ERR_ARG;
+  if (format < SKG_MXFP8 || format > SKG_NVFP4) return SKG_ERR_ARG;
+  if (rows == 0 || cols == 0) return SKG_OK;
+  if (!X || !codes || !scales || !codes_t || !scales_t || ldx < cols ||
+      ldq < skg_mx_codes_ld(cols, format) || ldq_t < skg_mx_codes_ld(rows, format))
+    return SKG_ERR_ARG;
+  if (rows > INT32_MAX / 4 || cols > 65535 * (int64_t)kTile) return SKG_ERR_UNSUPPORTED;
+  const int es = type == SKG_OUT_F32 ? 4 : 2;
+  if (!storage_aligned(codes, ldq, scales) || !storage_aligned(codes_t, ldq_t, scales_t) ||
+      ((uintptr_t)X & (es - 1)) || ((uintptr_t)tensor_scale & 3))
+    return SKG_ERR_UNSUPPORTED;
+  QuantParams r;
+  r.x = X;
+  r.ldx = ldx;
+  r.rows = rows;
+  r.k = cols;
+  r.g = tensor_scale;
+  r.codes = (uint8_t*)codes;
+  r.ldq = ldq;
+  r.scales = (uint8_t*)scales;
+  r.values = nullptr;
+  r.ldv = 0;
+  r.x_vec = ((uintptr_t)X & 15) == 0 && (ldx * es) % 16 == 0;
+  r.v_vec = 0;
+  QuantParams c = r;
+  c.rows = cols;
+  c.k = rows;
+  c.codes = (uint8_t*)codes_t;
+  c.ldq = ldq_t;
+  c.scales = (uint8_t*)scales_t;
+  return launch_quantize(&r, &c, type, format, (cudaStream_t)stream) == cudaSuccess ? SKG_OK
+                                                                                   : SKG_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -155,6 +155,24 @@ PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   return st != SKG_OK ? PyLong_FromLong(st) : tuple_of({q.codes, q.scales, v});
 }
 
+// quantize_both(x, format, tensor_scale) -> (codes, scales, codes_t, scales_t)
+PyObject* quantize_both(PyObject* const* a, Py_ssize_t n) {
+  want(n, 3);
+  const int fmt = format_of(a[1]);
+  const at::Tensor& x = tensor_of("x", a[0]);
+  const int type = type_of("x", x.scalar_type(), true);
+  const int64_t ldx = matrix("x", x);
+  const c10::cuda::CUDAGuard guard(x.device());
+  const float* g = tensor_scale(a[2], fmt, x.device());
+  const int64_t rows = x.size(0), cols = x.size(1);
+  Quantized q(rows, cols, fmt, x.device()), t(cols, rows, fmt, x.device());
+  const int st = skg_mx_quantize_both(rows, cols, x.data_ptr(), ldx, type, fmt, g,
+                                      q.codes.data_ptr(), q.ldq, q.scales.data_ptr(),
+                                      t.codes.data_ptr(), t.ldq, t.scales.data_ptr(),
+                                      stream_of(x.device()));
+  return st != SKG_OK ? PyLong_FromLong(st) : tuple_of({q.codes, q.scales, t.codes, t.scales});
+}
+
 // rmsnorm(x, weight, eps, residual, format, tensor_scale) -> (codes, scales, sum, rstd)
 PyObject* rmsnorm(PyObject* const* a, Py_ssize_t n) {
   want(n, 6);
@@ -304,8 +322,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define SKG_ENTRY(name) \
   {#name, (PyCFunction)(void (*)(void))entry<name>, METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {SKG_ENTRY(quantize), SKG_ENTRY(rmsnorm), SKG_ENTRY(rmsnorm_backward),
-                          SKG_ENTRY(matmul), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef kMethods[] = {SKG_ENTRY(quantize), SKG_ENTRY(quantize_both), SKG_ENTRY(rmsnorm),
+                          SKG_ENTRY(rmsnorm_backward), SKG_ENTRY(matmul),
+                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_skg_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

@@ -84,6 +84,19 @@ def quantize(x, format, transpose=False, tensor_scale=None, values=False, stream
     return (q, v) if values else q
 
 
+def quantize_both(x, format, tensor_scale=None, stream=None):
+    """quantize(x) and quantize(x, transpose=True) in one pass over x."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_both(x, format, tensor_scale)
+    r = _native().quantize_both(x, format, tensor_scale)
+    if r.__class__ is int:
+        raise SkgError(r, "skg_mx_quantize_both")
+    rows, cols = x.shape
+    return Matrix(format, rows, cols, r[0], r[1], tensor_scale), \
+        Matrix(format, cols, rows, r[2], r[3], tensor_scale)
+
+
 def rmsnorm(x, weight, eps, residual=None, format="mxfp8", tensor_scale=None, stream=None):
     """h = x + residual; quantised(h / sqrt(mean(h^2) + eps) * weight).
 
@@ -138,12 +151,17 @@ def linear(x, w, tensor_scale=None, workspace=None, stream=None):
 
 
 def linear_backward(dy, wt, xt, tensor_scale=None, workspace=None, stream=None):
-    """Gradients (dx, dW) of y = x W^T in dy's dtype, in one format:
+    """Gradients (dx, dW) of y = x W^T in dy's dtype, each in its operand's format:
     dx = Q(dy) Q(W^T)^T and dW = Q(dy^T) Q(x^T)^T, with wt the Matrix of W^T
     (k, n) and xt the Matrix of x^T (k, m); the quantisations count as the
     identity. tensor_scale: dy's scale, "nvfp4"."""
-    rows = quantize(dy, wt.format, tensor_scale=tensor_scale, stream=stream)
-    cols = quantize(dy, xt.format, transpose=True, tensor_scale=tensor_scale, stream=stream)
+    if wt.format == xt.format:
+        rows, cols = quantize_both(dy, wt.format, tensor_scale=tensor_scale, stream=stream)
+    else:
+        rows = quantize(dy, wt.format, stream=stream,
+                        tensor_scale=tensor_scale if wt.format == "nvfp4" else None)
+        cols = quantize(dy, xt.format, transpose=True, stream=stream,
+                        tensor_scale=tensor_scale if xt.format == "nvfp4" else None)
     dx = matmul(rows, wt, out_dtype=dy.dtype, workspace=workspace, stream=stream)
     dw = matmul(cols, xt, out_dtype=dy.dtype, workspace=workspace, stream=stream)
     return dx, dw

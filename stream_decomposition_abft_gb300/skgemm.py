@@ -93,6 +93,7 @@ SYMBOLS = ("skg_opts_default", "skg_workspace_size", "skg_workspace_init", "skg_
            "skg_launch_plan", "skg_workspace_size_layout", "skg_host_staging_size",
            "skg_gemm_host", "skg_abft_encode_layout", "skg_workspace_size_f64", "skg_gemm_f64",
            "skg_noalloc_report_read", "skg_mx_codes_ld", "skg_mx_scales_size", "skg_mx_quantize",
+           "skg_mx_quantize_both",
            "skg_rmsnorm_mx", "skg_workspace_size_rmsnorm_backward", "skg_rmsnorm_backward",
            "skg_workspace_size_mx", "skg_gemm_mx")
 
@@ -170,6 +171,9 @@ def lib() -> ctypes.CDLL:
     L.skg_mx_scales_size.restype = sz
     L.skg_mx_quantize.argtypes = [i64, i64, vp, i64, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp]
     L.skg_mx_quantize.restype = i32
+    L.skg_mx_quantize_both.argtypes = [i64, i64, vp, i64, i32, i32, vp, vp, i64, vp, vp, i64, vp,
+                                       vp]
+    L.skg_mx_quantize_both.restype = i32
     L.skg_rmsnorm_mx.argtypes = [i64, i64, vp, i64, vp, i64, vp, i32, f32, vp, i64, vp, i32, vp,
                                  vp, i64, vp, vp]
     L.skg_rmsnorm_mx.restype = i32
@@ -355,6 +359,13 @@ def mx_quantize(rows, k, X_ptr, ldx, dtype, transpose, fmt, tensor_scale_ptr, co
                 scales_ptr, values_ptr, ldv, stream) -> int:
     return lib().skg_mx_quantize(rows, k, X_ptr, ldx, dtype, transpose, fmt, tensor_scale_ptr,
                                  codes_ptr, ldq, scales_ptr, values_ptr, ldv, stream)
+
+
+def mx_quantize_both(rows, cols, X_ptr, ldx, dtype, fmt, tensor_scale_ptr, codes_ptr, ldq,
+                     scales_ptr, codes_t_ptr, ldq_t, scales_t_ptr, stream) -> int:
+    return lib().skg_mx_quantize_both(rows, cols, X_ptr, ldx, dtype, fmt, tensor_scale_ptr,
+                                      codes_ptr, ldq, scales_ptr, codes_t_ptr, ldq_t,
+                                      scales_t_ptr, stream)
 
 
 def rmsnorm_mx(rows, cols, X_ptr, ldx, residual_ptr, ldr, weight_ptr, in_dtype, eps, sum_ptr, lds,

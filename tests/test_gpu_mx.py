@@ -99,6 +99,20 @@ def test_quantize_strides(fmt, transpose, pad, offset):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (3, 200, 0), (130, 33, 5), (257, 515, 0),
+                                           (256, 384, 0), (1000, 96, 8), (5, 2200, 1)])
+def test_quantize_both(fmt, dtype, rows, cols, pad):
+    # One pass, the bytes of two.
+    x = strided(draw(rows, cols, dtype, rows + cols), pad)
+    g = torch.tensor([0.01], device="cuda") if fmt == "nvfp4" else None
+    for got, tr in zip(mx.quantize_both(x, fmt, tensor_scale=g), (False, True)):
+        want = mx.quantize(x, fmt, transpose=tr, tensor_scale=g)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+        assert (got.rows, got.k) == (want.rows, want.k)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_quantize_special_values(fmt):
     # Infinities and NaN spoil their own block alone; extremes of fp32, signed
     # zeros, subnormals; exact ties.

@@ -47,6 +47,20 @@ def test_quantize_arguments():
     assert call(k=1 << 30, ldq=1 << 30, ldx=1 << 30) == skgemm.ERR_UNSUPPORTED
 
 
+def test_quantize_both_arguments():
+    def call(rows=4, cols=64, X=P, ldx=64, dtype=skgemm.OUT_BF16, fmt=0, g=None, codes=P, ldq=64,
+             scales=P, ct=P, ldt=32, st=P):
+        return skgemm.mx_quantize_both(rows, cols, X, ldx, dtype, fmt, g, codes, ldq, scales, ct,
+                                       ldt, st, None)
+    assert call(rows=-1) == call(cols=-1) == call(dtype=3) == call(fmt=3) == skgemm.ERR_ARG
+    assert call(rows=0) == call(cols=0) == skgemm.OK
+    for name in ("X", "codes", "scales", "ct", "st"):
+        assert call(**{name: None}) == skgemm.ERR_ARG
+    assert call(ldx=63) == call(ldq=48) == call(ldt=16) == skgemm.ERR_ARG
+    assert call(ct=P + 8) == call(st=P + 4) == call(ldt=40) == call(X=P + 1) == \
+        skgemm.ERR_UNSUPPORTED
+
+
 def test_norm_arguments():
     def call(rows=4, cols=64, X=P, ldx=64, res=None, ldr=0, w=P, dtype=0, eps=1e-5, s=None, lds=0,
              rstd=None, fmt=0, g=None, codes=P, ldq=64, scales=P):
