@@ -259,33 +259,43 @@ cudaError_t launch_mx_out(const CUtensorMap (&t)[5], const MxParams& p, int out,
   return launch_mx<FMT, __nv_bfloat16>(t, p, stream);
 }
 
-// CTAs that share a 128 x 128 tile: doubled while they all fit the GPU at once
-// (two per SM) and each has a stage of k.
-int split_of(int64_t tiles, int ksteps, int sms) {
-  int s = 1;
-  while (s < kMxSplitMax && tiles * s * 2 <= 2 * sms && s * 2 <= ksteps) s *= 2;
-  return s;
+// Single CTAs: how many share a 128 x 128 tile (S), and the estimated time (us).
+// Up to 16 rows of A the sum over the cluster is a few rows, and S is what fits the
+// GPU at once (two CTAs per SM): 1 x 1024 x 8192 in mxfp8 takes 19.8, 9.3, 6.0,
+// 4.6 us with S = 1, 2, 4, 8. Else a CTA's 64 KB of partial sums cross the
+// SM-to-SM network, S = 8 never pays (512 x 512 x 8192 nvfp4: 12.3, 8.8, 7.0,
+// 8.9), and the estimate decides: a fixed cost plus the CTA's stages of k, both
+// higher where two CTAs share an SM.
+struct SinglePlan {
+  int split;
+  double us;
+};
+SinglePlan single_plan(int64_t m, int64_t n, int ksteps, int sms) {
+  const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
+  SinglePlan best = {1, 1e30};
+  for (int s = 1; s <= (m <= 16 ? kMxSplitMax : 4); s *= 2) {
+    if (s > 1 && (tiles * s > 2 * sms || s > ksteps)) break;
+    const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
+    const int stages = (ksteps + s - 1) / s;
+    const double us = tiles * s <= sms ? (s > 1 ? 5.1 : 4.2) + 0.36 * stages
+                                       : (s > 1 && m > 64 ? 7.0 : 5.5) + 0.48 * waves * stages;
+    if (m <= 16 || us < best.us) best = {s, us};
+  }
+  return best;
 }
 
 // Whether a product runs on CTA pairs: 256 x 256 tiles halve what each SM reads
 // per product, but cannot share a tile's k. Up to 128 rows the single CTAs win at
-// every n and k (1 x 8192 x 8192 in nvfp4: 9.5 against 17.9 us). Beyond, both are
-// estimated: a fixed cost plus the stages of the busiest CTA, with the times of a
-// stage as measured (us; two single CTAs share an SM, so theirs holds for a full
-// one). 1024 x 1024 x 8192 in mxfp8: 14.4 us single (4 CTAs a tile), 21.7 paired;
-// 2048 x 2048 x 2048: 11.9 single, 9.5 paired.
-bool wants_pairs(int64_t m, int64_t n, int ksteps, int clusters, int sms) {
+// every n and k (1 x 8192 x 8192 in nvfp4: 9.6 against 17.9 us); beyond, the lower
+// estimate (512 x 512 x 8192 in nvfp4: 12.4 us paired, 7.0 single; 2048 x 2048 x
+// 2048: 6.9 paired, 8.9 single).
+bool wants_pairs(int64_t m, int64_t n, int ksteps, int clusters, double single_us) {
 #ifdef SKG_MX_PAIR
   return SKG_MX_PAIR != 0;
 #endif
   if (m <= kMxTile) return false;
-  const int64_t tiles2 = ((m + 255) / 256) * ((n + 255) / 256);
-  const int64_t tiles1 = ((m + 127) / 128) * ((n + 127) / 128);
-  const int split = split_of(tiles1, ksteps, sms);
-  const double pair = 3.3 + 0.29 * (double)((tiles2 + clusters - 1) / clusters) * ksteps;
-  const double single = 6.0 + 0.54 * (double)((tiles1 * split + 2 * sms - 1) / (2 * sms)) *
-                                  ((ksteps + split - 1) / split);
-  return pair <= single;
+  const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  return 4.4 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;
 }
 
 template <int FMT>
@@ -297,11 +307,12 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
   p.ksteps = (p.k + C::STEP - 1) / C::STEP;
   const int64_t rt_a = (p.m + kMxTile - 1) / kMxTile, rt_b = (p.n + kMxTile - 1) / kMxTile;
   const int resident = mx_pair_clusters_resident();
-  const bool pair = resident > 0 && wants_pairs(p.m, p.n, p.ksteps, resident, sms);
+  const SinglePlan single = single_plan(p.m, p.n, p.ksteps, sms);
+  const bool pair = resident > 0 && wants_pairs(p.m, p.n, p.ksteps, resident, single.us);
   const int64_t tm = pair ? (rt_a + 1) / 2 : rt_a, tn = pair ? (rt_b + 1) / 2 : rt_b;
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
-  p.split = pair ? 1 : split_of(tm * tn, p.ksteps, sms);
+  p.split = pair ? 1 : single.split;
   p.a_rows = !pair && p.m < kMxTile ? (p.m + 7) / 8 * 8 : kMxTile;
   const uint64_t bytes = ((uint64_t)p.k * mx_bits(FMT) + 7) / 8;
   const uint64_t chunks_a = (uint64_t)rt_a * p.groups, chunks_b = (uint64_t)rt_b * p.groups;

@@ -248,7 +248,10 @@ cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, int sms,
                              cudaStream_t stream) {
   const size_t smem = (size_t)kNormStages * 2 * v * threads * 16;
   const int64_t rows = (p.rows + 127) / 128 * 128;
-  const dim3 grid((unsigned)(rows < 2 * sms ? rows : 2 * sms));
+  // 1024 threads per SM: two blocks of 512, four of 256 (4096 x 2048: 15 us with
+  // two of 256).
+  const int64_t most = (int64_t)sms * (1024 / threads < 8 ? 1024 / threads : 8);
+  const dim3 grid((unsigned)(rows < most ? rows : most));
   auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
     const cudaError_t e = opt_in_smem((const void*)kernel, done, kNormStages * 2 * kNormMaxThreads *
                                                                      16 * 2);
@@ -532,29 +535,39 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_columns_kernel(GradParams p,
   p.partial[(int64_t)blockIdx.y * p.cols + c] = acc;
 }
 
-// dw = the sum of the blocks' partials, in a fixed order: 32 columns per
-// block, eight rows of threads over the partials.
-__global__ void __launch_bounds__(256)
+// dw = the sum of the blocks' partials, in a fixed order: 32 columns per block,
+// 32 rows of threads over the partials, four loads in flight each.
+__global__ void __launch_bounds__(1024)
 rmsnorm_grad_reduce_kernel(const float* partial, int parts, int cols, float* dw) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
   griddep_wait();
   griddep_launch_dependents();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
   float v = 0.f;
-  if (c < cols)
-    for (int i = ty; i < parts; i += 8) v += partial[(int64_t)i * cols + c];
+  if (c < cols) {
+    const float* src = partial + c;
+    for (int i = ty; i < parts; i += 128) {
+      float u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        u[j] = i + 32 * j < parts ? src[(int64_t)(i + 32 * j) * cols] : 0.f;
+      v += (u[0] + u[1]) + (u[2] + u[3]);
+    }
+  }
   s[ty][tx] = v;
   __syncthreads();
-  if (ty == 0 && c < cols) {
-    for (int i = 1; i < 8; ++i) v += s[i][tx];
-    dw[c] = v;
-  }
+  // Warp ty sums column ty of the block.
+  v = s[tx][ty];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (tx == 0 && blockIdx.x * 32 + ty < cols) dw[blockIdx.x * 32 + ty] = v;
 }
 
 struct GradPlan {
   int log_tpr, v, threads, per, blocks;
   size_t smem;
+  int wide_v, wide_threads, wide_blocks;  // the kernel with the ring (wide_v = 0: not for it)
 };
 
 GradPlan grad_plan(int64_t rows, int64_t cols, int sms) {
@@ -567,8 +580,18 @@ GradPlan grad_plan(int64_t rows, int64_t cols, int sms) {
   g.threads = g.log_tpr < 7 ? 128 : (1 << g.log_tpr);
   g.per = g.threads >> g.log_tpr;
   g.smem = g.per > 1 ? (size_t)cols * 4 : 0;
-  const int64_t want = (rows + g.per - 1) / g.per;
-  const int64_t most = 2 * (int64_t)(sms > 0 ? sms : 152);
+  // Whole pieces of 8 on 16-byte boundaries take the kernel with the ring: a block
+  // of up to 512 threads per SM, two of up to 256.
+  const int64_t pieces = (cols + 7) / 8;
+  g.wide_v = cols % 8 != 0 || pieces <= 96 || pieces > 2 * kNormMaxThreads ? 0
+             : pieces <= kNormMaxThreads                                   ? 1
+                                                                           : 2;
+  g.wide_threads = g.wide_v ? (int)((pieces + 32 * g.wide_v - 1) / (32 * g.wide_v) * 32) : 0;
+  const int64_t n = sms > 0 ? sms : 152;
+  const int64_t wide = g.wide_threads <= 256 ? 2 * n : n;
+  g.wide_blocks = (int)(rows < wide ? rows : wide);
+  // Else rows per block (blocks of 128 threads hide little each: four per SM).
+  const int64_t want = (rows + g.per - 1) / g.per, most = g.threads <= 128 ? 4 * n : 2 * n;
   g.blocks = (int)(want < most ? want : most);
   return g;
 }
@@ -578,13 +601,11 @@ cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, int s
                         cudaStream_t stream) {
   cudaError_t e;
   const dim3 grid(g.blocks), block(g.threads);
-  const int pieces = (p.cols + 7) / 8;
   int parts = g.blocks;
-  if (p.vec && p.cols % 8 == 0 && pieces > 96 && pieces <= 2 * kNormMaxThreads) {
-    const int v = pieces <= kNormMaxThreads ? 1 : 2;
-    const int threads = (pieces + 32 * v - 1) / (32 * v) * 32;
+  if (p.vec && g.wide_v) {
+    const int v = g.wide_v, threads = g.wide_threads;
     const size_t smem = (size_t)kGradStages * 3 * v * threads * 16;
-    parts = (int)(p.rows < sms ? p.rows : sms);
+    parts = g.wide_blocks;
     auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
       const cudaError_t r = opt_in_smem((const void*)kernel, done,
                                         kGradStages * 3 * 2 * kNormMaxThreads * 16);
@@ -607,7 +628,7 @@ cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, int s
                    stream, p, g.blocks);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(256),
+  return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(1024),
                     0, stream, (const float*)p.partial, parts, p.cols, dw);
 }
 
@@ -670,7 +691,7 @@ skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t l
 size_t skg_workspace_size_rmsnorm_backward(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
   const GradPlan g = grad_plan(rows, cols, skg_device_sm_count());
-  return (size_t)g.blocks * (size_t)cols * 4;
+  return (size_t)(g.blocks > g.wide_blocks ? g.blocks : g.wide_blocks) * (size_t)cols * 4;
 }
 
 skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, int64_t lddy,
@@ -686,7 +707,7 @@ skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, in
   if ((uintptr_t)dweight & 3) return SKG_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0)  // an empty sum
-    return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256),
+    return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024),
                       0, st, (const float*)nullptr, 0, (int)cols, dweight) == cudaSuccess
                ? SKG_OK
                : SKG_ERR_CUDA;
