@@ -151,6 +151,23 @@ __device__ __forceinline__ uint32_t mx_absmax16(const float (&v)[16]) {
   return m;
 }
 
+// The same of 16-bit elements as stored, two at a time (a word's halves apart):
+// their magnitudes, too, are ordered as unsigned integers.
+__device__ __forceinline__ uint32_t mx_absmax2(uint32_t m, uint32_t w) {
+  return __vmaxu2(m, w & 0x7fff7fffu);
+}
+// A 16-bit magnitude as the bits of a float.
+template <typename T>
+__device__ __forceinline__ uint32_t mx_magnitude(uint32_t m16);
+template <>
+__device__ __forceinline__ uint32_t mx_magnitude<__nv_bfloat16>(uint32_t m16) {
+  return m16 << 16;
+}
+template <>
+__device__ __forceinline__ uint32_t mx_magnitude<__half>(uint32_t m16) {
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m16)));
+}
+
 // One block's scale.
 struct MxScale {
   uint32_t byte;  // as stored
@@ -257,13 +274,14 @@ __device__ __forceinline__ void mx_store_codes16(uint8_t* row, int64_t chunk, co
 }
 
 // A warp's lanes hold consecutive 16-element chunks (chunk c in a lane with
-// lane % 8 == c % 8; zeros past the row's end): quantise them, and hand back
+// lane % 8 == c % 8; zeros past the row's end), amax the largest magnitude of its
+// own: quantise them, and hand back
 // in `word` the four scale bytes of the chunk's block group (the OR over the
 // group's lanes; the group's first lane writes it). All 32 lanes take part.
 template <int FMT>
-__device__ __forceinline__ MxScale mx_quantize_chunk(const float (&v)[16], bool live, int lane,
-                                                     float g, uint4& codes, uint32_t& word) {
-  uint32_t amax = mx_absmax16(v);
+__device__ __forceinline__ MxScale mx_quantize_chunk(const float (&v)[16], uint32_t amax, bool live,
+                                                     int lane, float g, uint4& codes,
+                                                     uint32_t& word) {
   if constexpr (FMT != SKG_NVFP4) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const MxScale s = mx_scale<FMT>(amax, g);
   codes = mx_codes16<FMT>(v, s);
@@ -292,6 +310,46 @@ __device__ __forceinline__ MxScale mx_quantize_piece(const float (&v)[8], bool l
   word |= __shfl_xor_sync(0xffffffffu, word, 4);
   if constexpr (FMT != SKG_NVFP4) word |= __shfl_xor_sync(0xffffffffu, word, 8);
   return s;
+}
+
+// Sixteen consecutive elements as they are (see mx_load16), and their largest
+// magnitude.
+template <typename T>
+struct MxRaw16 {
+  uint4 q[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ MxRaw16<T> mx_load_raw16(const T* p, bool vec, int n) {
+  MxRaw16<T> r;
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) r.q[i] = *(reinterpret_cast<const uint4*>(p) + i);
+  } else {
+    T* e = reinterpret_cast<T*>(r.q);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) e[i] = i < n ? p[i] : mx_from_f32<T>(0.f);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void mx_unpack_raw16(const MxRaw16<T>& r, float (&v)[16]) {
+  const T* e = reinterpret_cast<const T*>(r.q);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = mx_to_f32(e[i]);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mx_absmax_raw16(const MxRaw16<T>& r) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.q);
+  uint32_t m = 0;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = mx_absmax2(m, w[i]);
+    return mx_magnitude<T>(max(m & 0xffffu, m >> 16));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+  }
 }
 
 // Eight consecutive elements as they are. `vec`: the address is 16-byte aligned

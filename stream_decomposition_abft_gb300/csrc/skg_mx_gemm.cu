@@ -32,14 +32,20 @@ namespace {
 constexpr int kMxPitch = 132;                 // floats per row of the partial tile
 constexpr int kMxSplitMax = 8;
 
-template <int FMT>
+// FEW: at most 16 rows of A. Its stages hold 16 rows of A (the MMA reads 128 from
+// there: what follows in the stage, for rows of the accumulator that nothing
+// reads), so that five stages of B fit where three do otherwise.
+template <int FMT, bool FEW>
 struct MxCfg : MxStage<FMT> {
   using MxStage<FMT>::CHUNKS;
   using MxStage<FMT>::SF_BYTES;
-  static constexpr int SFA_OFF = 2 * kMxOperand;
+  static constexpr int B_OFF = FEW ? 16 * kMxRowBytes : kMxOperand;
+  static constexpr int SFA_OFF = B_OFF + kMxOperand;
   static constexpr int SFB_OFF = SFA_OFF + SF_BYTES;
-  static constexpr int STAGE_BYTES = 2 * kMxOperand + 2 * SF_BYTES;
-  static constexpr int STAGES = 3;  // two CTAs share an SM
+  static constexpr int STAGE_BYTES = SFA_OFF + 2 * SF_BYTES;
+  static constexpr int STAGES = FEW ? 5 : 3;  // two CTAs share an SM
+  static_assert(STAGE_BYTES % 1024 == 0 && STAGE_BYTES >= kMxOperand,
+                "swizzle atoms; A's 128 rows end inside the ring");
   static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 256;
   // TMEM: the accumulator, then two buffers of scale columns (A's, B's).
   static constexpr int SF_COLS = 2 * CHUNKS * 4;
@@ -86,12 +92,12 @@ __device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* p
   }
 }
 
-template <int FMT, typename T>
+template <int FMT, bool FEW, typename T>
 __global__ void __launch_bounds__(kMxThreads, 2)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                const MxParams p) {
-  using C = MxCfg<FMT>;
+  using C = MxCfg<FMT, FEW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   MxAux* aux = reinterpret_cast<MxAux*>(ring + C::STAGES * C::STAGE_BYTES);
@@ -141,7 +147,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         uint8_t* s = ring + st * C::STAGE_BYTES;
         mbar_arrive_expect_tx(&aux->full[st], tx);
         tma_load_2d(s, &tmA, &aux->full[st], kb * kMxRowBytes, tm * kMxTile);
-        tma_load_2d(s + kMxOperand, &tmB, &aux->full[st], kb * kMxRowBytes, tn * kMxTile);
+        tma_load_2d(s + C::B_OFF, &tmB, &aux->full[st], kb * kMxRowBytes, tn * kMxTile);
         tma_load_2d(s + C::SFA_OFF, &tmSA, &aux->full[st], 0, tm * p.groups + kb * C::CHUNKS);
         tma_load_2d(s + C::SFB_OFF, &tmSB, &aux->full[st], 0, tn * p.groups + kb * C::CHUNKS);
       }
@@ -162,7 +168,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // Two buffers of scale columns: the copy for this stage does not
         // touch the ones that the last stage's MMAs read.
         const uint32_t sfa = tmem + kMxTile + (it & 1) * C::SF_COLS;
-        mx_stage_mmas<FMT, false, 1>(tmem, sfa, sfa + C::CHUNKS * 4,
+        mx_stage_mmas<FMT, false, 1, C::B_OFF>(tmem, sfa, sfa + C::CHUNKS * 4,
                                      smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF, C::SFB_OFF,
                                      p.k - kb * C::STEP, it == 0);
         any = true;
@@ -240,23 +246,23 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   if (blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(&p.report->launches, 1u);
 }
 
-template <int FMT, typename T>
+template <int FMT, bool FEW, typename T>
 cudaError_t launch_mx(const CUtensorMap (&t)[5], const MxParams& p, cudaStream_t stream) {
-  using C = MxCfg<FMT>;
+  using C = MxCfg<FMT, FEW>;
   static std::atomic<uint64_t> done_mask{0};
-  const cudaError_t e = opt_in_smem((const void*)mx_gemm_kernel<FMT, T>, done_mask, (int)C::SMEM);
+  const cudaError_t e = opt_in_smem((const void*)mx_gemm_kernel<FMT, FEW, T>, done_mask, (int)C::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  return launch_pdl_cluster(mx_gemm_kernel<FMT, T>, dim3((unsigned)(tiles * p.split)),
+  return launch_pdl_cluster(mx_gemm_kernel<FMT, FEW, T>, dim3((unsigned)(tiles * p.split)),
                             dim3(kMxThreads), C::SMEM, stream, p.split, t[0], t[1], t[2], t[3], p);
 }
 
-template <int FMT>
+template <int FMT, bool FEW>
 cudaError_t launch_mx_out(const CUtensorMap (&t)[5], const MxParams& p, int out,
                           cudaStream_t stream) {
-  if (out == SKG_OUT_F32) return launch_mx<FMT, float>(t, p, stream);
-  if (out == SKG_OUT_F16) return launch_mx<FMT, __half>(t, p, stream);
-  return launch_mx<FMT, __nv_bfloat16>(t, p, stream);
+  if (out == SKG_OUT_F32) return launch_mx<FMT, FEW, float>(t, p, stream);
+  if (out == SKG_OUT_F16) return launch_mx<FMT, FEW, __half>(t, p, stream);
+  return launch_mx<FMT, FEW, __nv_bfloat16>(t, p, stream);
 }
 
 // Single CTAs: how many share a 128 x 128 tile (S), and the estimated time (us).
@@ -302,7 +308,7 @@ template <int FMT>
 cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const void* B, int64_t ldb,
                             const void* SB, MxParams p, int out, int sms, cudaStream_t stream,
                             bool* unsupported) {
-  using C = MxCfg<FMT>;
+  using C = MxStage<FMT>;
   p.groups = (int)mx_groups(p.k, FMT);
   p.ksteps = (p.k + C::STEP - 1) / C::STEP;
   const int64_t rt_a = (p.m + kMxTile - 1) / kMxTile, rt_b = (p.n + kMxTile - 1) / kMxTile;
@@ -346,7 +352,8 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
   }
   if (pair)
     return launch_mx_pair<FMT>(t, p, out, (int)(tm * tn < resident ? tm * tn : resident), stream);
-  return launch_mx_out<FMT>(t, p, out, stream);
+  return p.m <= 16 ? launch_mx_out<FMT, true>(t, p, out, stream)
+                   : launch_mx_out<FMT, false>(t, p, out, stream);
 }
 
 }  // namespace

@@ -106,10 +106,10 @@ __device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, f
   }
 }
 
-// The MMAs of one stage: the scales go to TMEM columns sfa, sfb (B_TILES scale
+// The MMAs of one stage (A at its start, B at B_OFF): the scales go to TMEM columns sfa, sfb (B_TILES scale
 // tiles of 128 rows of B), then up to four MMAs of 32 bytes of k each. MMAs past
 // k's last block of 32 are left out: their scales do not exist.
-template <int FMT, bool PAIR, int B_TILES>
+template <int FMT, bool PAIR, int B_TILES, int B_OFF>
 __device__ __forceinline__ void mx_stage_mmas(uint32_t d, uint32_t sfa, uint32_t sfb,
                                               uint32_t stage, uint32_t sfa_off, uint32_t sfb_off,
                                               int left, bool first) {
@@ -122,7 +122,7 @@ __device__ __forceinline__ void mx_stage_mmas(uint32_t d, uint32_t sfa, uint32_t
       tmem_cp_scales<PAIR>(sfb + (c * B_TILES + h) * 4,
                            sdesc_scales(stage + sfb_off + h * S::SF_BYTES + c * kMxTileBytes));
   }
-  const uint64_t ad = sdesc_sw128(stage), bd = sdesc_sw128(stage + kMxOperand);
+  const uint64_t ad = sdesc_sw128(stage), bd = sdesc_sw128(stage + B_OFF);
   const int mmas = min(4, (left + S::MMA_K - 1) / S::MMA_K);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

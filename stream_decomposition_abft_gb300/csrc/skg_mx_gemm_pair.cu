@@ -207,7 +207,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           }
           tc_fence_after();
           const uint32_t sf = tmem + C::SF_BASE + (it & 1) * C::SF_COLS;
-          mx_stage_mmas<FMT, true, 2>(d, sf, sf + C::CHUNKS * 4,
+          mx_stage_mmas<FMT, true, 2, kMxOperand>(d, sf, sf + C::CHUNKS * 4,
                                       smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF, C::SFB_OFF,
                                       p.k - kb * C::STEP, kb == 0);
           umma_commit_pair(&aux->empty[st]);

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams 
     uint4 codes;
     uint32_t word;
     const bool live = here && c < chunks;
-    mx_quantize_chunk<FMT>(h, live, lane, g, codes, word);
+    mx_quantize_chunk<FMT>(h, mx_absmax16(h), live, lane, g, codes, word);
     if (live) mx_store_codes16<FMT>(p.codes + row * p.ldq, c, codes);
     constexpr int per = mx_group_chunks(FMT);
     if ((lane & (per - 1)) == 0 && c / per < groups)
@@ -427,13 +427,18 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(GradParam
   }
 }
 
-// The wide rows' gradient: as rmsnorm_mx_wide_kernel, a ring of dy, h and
-// dresidual; dw of the block's rows stays in registers.
+// The wide rows' gradient, with the same ring for dy, h and dresidual. A block
+// takes two rows at a time: the first pass over the fetched pieces forms both
+// rows' sums, which cross the block together (a row's sum, barriers and all, takes
+// longer than its arithmetic: 4096 x 8192 one row at a time 46 us), the second
+// reads them again from shared memory for dx. dw of the block's rows stays in
+// registers.
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(GradParams p) {
   extern __shared__ uint4 ring[];  // stages x (dy, h, dres) x V x threads
-  __shared__ float red[2][kNormMaxThreads / 32];
-  const int t = threadIdx.x, nt = blockDim.x;
+  __shared__ float2 red[2][kNormMaxThreads / 32];
+  static_assert(kGradStages == 4, "two rows in hand, two on the way");
+  const int t = threadIdx.x, nt = blockDim.x, lane = t & 31;
   const T* in[3] = {reinterpret_cast<const T*>(p.dy), reinterpret_cast<const T*>(p.h),
                     reinterpret_cast<const T*>(p.dres)};
   const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
@@ -468,46 +473,84 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
   }
   const float inv_n = 1.f / (float)p.cols;
   int st = 0, par = 0;
-  float rstd_next = blockIdx.x < p.rows ? p.rstd[blockIdx.x] : 0.f;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float rstd = rstd_next;
-    if (row + gridDim.x < p.rows) rstd_next = p.rstd[row + gridDim.x];
-    float xhat[V][8], u[V][8], o[V][8], dot = 0.f;
-    cp_async_wait<kGradStages - 1>();
+  float next[2];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint4* src = ring + (st * 3 * V + j) * nt + t;
-      float dy[8];
-      mx_unpack8<T>(src[0], dy);
-      mx_unpack8<T>(src[V * nt], xhat[j]);
-      mx_unpack8<T>(wv[j], u[j]);
-      if (p.dres) {
-        mx_unpack8<T>(src[2 * V * nt], o[j]);
-      } else {
+  for (int q = 0; q < 2; ++q) {
+    const int64_t r = blockIdx.x + (int64_t)q * gridDim.x;
+    next[q] = r < p.rows ? p.rstd[r] : 0.f;
+  }
+  for (int64_t row = blockIdx.x; row < p.rows; row += 2 * (int64_t)gridDim.x) {
+    float rstd[2], dot[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[j][i] = 0.f;
-      }
+    for (int q = 0; q < 2; ++q) {
+      rstd[q] = next[q];
+      const int64_t r = row + (int64_t)(2 + q) * gridDim.x;
+      next[q] = r < p.rows ? p.rstd[r] : 0.f;
+    }
+    cp_async_wait<kGradStages - 2>();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xhat[j][i] *= rstd;
-        u[j][i] *= dy[i];
-        acc[j][i] += dy[i] * xhat[j][i];
-        dot += u[j][i] * xhat[j][i];
+    for (int q = 0; q < 2; ++q) {
+      if (row + (int64_t)q * gridDim.x >= p.rows) break;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const uint4* src = ring + ((st + q) * 3 * V + j) * nt + t;
+        float dy[8], h[8], w[8];
+        mx_unpack8<T>(src[0], dy);
+        mx_unpack8<T>(src[V * nt], h);
+        mx_unpack8<T>(wv[j], w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = dy[i] * (h[i] * rstd[q]);
+          acc[j][i] += a;
+          dot[q] += a * w[i];
+        }
       }
     }
-    fetch(row + (int64_t)kGradStages * gridDim.x, st);
-    if (++st == kGradStages) st = 0;
-    const float mean = block_sum(dot, red, par) * inv_n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+      dot[1] += __shfl_xor_sync(0xffffffffu, dot[1], o);
+    }
+    if (lane == 0) red[par][t >> 5] = make_float2(dot[0], dot[1]);
+    __syncthreads();
+    float2 part = lane < (nt >> 5) ? red[par][lane] : make_float2(0.f, 0.f);
     par ^= 1;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (t + j * nt) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[j][i] += rstd * (u[j][i] - xhat[j][i] * mean);
-      if (c < p.cols)
-        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.dx) + row * p.lddx + c) =
-            mx_pack8<T>(o[j]);
+    for (int o = kNormMaxThreads / 64; o > 0; o >>= 1) {
+      part.x += __shfl_xor_sync(0xffffffffu, part.x, o);
+      part.y += __shfl_xor_sync(0xffffffffu, part.y, o);
     }
+    const float mean[2] = {__shfl_sync(0xffffffffu, part.x, 0) * inv_n,
+                           __shfl_sync(0xffffffffu, part.y, 0) * inv_n};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t r = row + (int64_t)q * gridDim.x;
+      if (r < p.rows) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c = (t + j * nt) * 8;
+          const uint4* src = ring + ((st + q) * 3 * V + j) * nt + t;
+          float dy[8], h[8], w[8], o[8];
+          mx_unpack8<T>(src[0], dy);
+          mx_unpack8<T>(src[V * nt], h);
+          mx_unpack8<T>(wv[j], w);
+          if (p.dres) {
+            mx_unpack8<T>(src[2 * V * nt], o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] += rstd[q] * (w[i] * dy[i] - h[i] * rstd[q] * mean[q]);
+          if (c < p.cols)
+            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.dx) + r * p.lddx + c) =
+                mx_pack8<T>(o);
+        }
+      }
+      fetch(r + (int64_t)kGradStages * gridDim.x, st + q);
+    }
+    st ^= 2;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {

@@ -54,30 +54,40 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
   const bool live = chunk < chunks;
   const int64_t left = p.k - chunk * 16;
   const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
-  const int64_t tiles = (p.rows + 127) / 128 * 32;  // (scale tile, l) pairs
-  for (int64_t u = (int64_t)blockIdx.y * ls; u < tiles; u += (int64_t)gridDim.y * ls) {
-    const int64_t ul = u + (ty >> 2);
-    const int64_t row = (ul >> 5) * 128 + (ty & 3) * 32 + (ul & 31);
-    const bool here = row < p.rows;
-    float v[16];
-    const T* src = reinterpret_cast<const T*>(p.x) + row * p.ldx + chunk * 16;
-    mx_load16(src, here && p.x_vec && n == 16, here ? n : 0, v);
-    uint4 codes;
-    uint32_t word;
-    const MxScale s = mx_quantize_chunk<FMT>(v, here && live, lane, g, codes, word);
-    if (here && live) {
-      mx_store_codes16<FMT>(p.codes + row * p.ldq, chunk, codes);
-      if (p.values) {
-        float w[16];
-        mx_values16<FMT>(codes, s, g, w);
-        mx_store16(reinterpret_cast<T*>(p.values) + row * p.ldv + chunk * 16, p.v_vec && n == 16,
-                   n, w);
-      }
+  const int64_t units = (p.rows + 127) / 128 * 32;  // (scale tile, l) pairs, 32 a tile
+  for (int64_t u = (int64_t)blockIdx.y * 2 * ls; u < units; u += (int64_t)gridDim.y * 2 * ls) {
+    MxRaw16<T> raw[2];  // both rows' loads in flight
+    int64_t row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t ul = u + h * ls + (ty >> 2);
+      row[h] = (ul >> 5) * 128 + (ty & 3) * 32 + (ul & 31);
+      const int m = row[h] < p.rows ? n : 0;
+      raw[h] = mx_load_raw16(reinterpret_cast<const T*>(p.x) + row[h] * p.ldx + chunk * 16,
+                             p.x_vec && m == 16, m);
     }
-    constexpr int per = mx_group_chunks(FMT);
-    const int64_t grp = chunk / per;
-    if ((lane & (per - 1)) == 0 && grp < groups)
-      *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)grp, groups)) = word;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool here = live && row[h] < p.rows;
+      float v[16];
+      mx_unpack_raw16(raw[h], v);
+      uint4 codes;
+      uint32_t word;
+      const MxScale s =
+          mx_quantize_chunk<FMT>(v, mx_absmax_raw16(raw[h]), here, lane, g, codes, word);
+      if (here) {
+        mx_store_codes16<FMT>(p.codes + row[h] * p.ldq, chunk, codes);
+        if (p.values) {
+          mx_values16<FMT>(codes, s, g, v);
+          mx_store16(reinterpret_cast<T*>(p.values) + row[h] * p.ldv + chunk * 16,
+                     p.v_vec && n == 16, n, v);
+        }
+      }
+      constexpr int per = mx_group_chunks(FMT);
+      const int64_t grp = chunk / per;
+      if ((lane & (per - 1)) == 0 && grp < groups)
+        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row[h], (int)grp, groups)) = word;
+    }
   }
 }
 
@@ -150,10 +160,29 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp) {
 #pragma unroll
     for (int j = 0; j < W; ++j)
       w[i][j] = tile[(kb * 32 + i) * LINE + ((pair * W + j) ^ (kb * 8 * W))];
+  // Largest magnitudes of the two columns' 16-line halves.
+  uint32_t top[2][2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint32_t m[W] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        m[j] = W == 1 ? mx_absmax2(m[j], w[b * 16 + i][j]) : max(m[j], w[b * 16 + i][j] & 0x7fffffffu);
+    if constexpr (W == 1) {
+      top[0][b] = mx_magnitude<T>(m[0] & 0xffffu);
+      top[1][b] = mx_magnitude<T>(m[0] >> 16);
+    } else {
+      top[0][b] = m[0];
+      top[1][b] = m[W - 1];
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {  // the pair's columns
     const int64_t row = c0 + pair * 2 + h;
     const bool live = row < p.rows && kfirst < p.k;
+    if constexpr (FMT != SKG_NVFP4) top[h][0] = max(top[h][0], top[h][1]);
     uint32_t bytes[2];
     MxScale s;
 #pragma unroll
@@ -161,24 +190,11 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp) {
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint32_t u = W == 2 ? w[b * 16 + i][h * (W - 1)] : w[b * 16 + i][0];
+        const uint32_t u = w[b * 16 + i][h * (W - 1)];
         if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(u);
         else v[i] = mx_to_f32(reinterpret_cast<const T*>(&u)[h]);
       }
-      if (FMT == SKG_NVFP4 || b == 0) {
-        uint32_t amax = mx_absmax16(v);
-        if constexpr (FMT != SKG_NVFP4) {
-          float v2[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t u = W == 2 ? w[16 + i][h * (W - 1)] : w[16 + i][0];
-            if constexpr (sizeof(T) == 4) v2[i] = __uint_as_float(u);
-            else v2[i] = mx_to_f32(reinterpret_cast<const T*>(&u)[h]);
-          }
-          amax = max(amax, mx_absmax16(v2));
-        }
-        s = mx_scale<FMT>(amax, g);
-      }
+      if (FMT == SKG_NVFP4 || b == 0) s = mx_scale<FMT>(top[h][b], g);
       bytes[b] = s.byte;
       if (live) {
         const uint4 codes = mx_codes16<FMT>(v, s);
@@ -232,7 +248,7 @@ cudaError_t launch_rows(const QuantParams& p, cudaStream_t stream) {
   while (log_tx < 5 && (1 << log_tx) < chunks) ++log_tx;
   const int ls = (kQThreads >> log_tx) / 4;
   const int64_t gx = (chunks + (1 << log_tx) - 1) >> log_tx;
-  int64_t gy = ((p.rows + 127) / 128 * 32 + ls - 1) / ls;
+  int64_t gy = (p.rows + 127) / 128 * 32 / (2 * ls);
   if (gy > 65535) gy = 65535;
   return launch_pdl(mx_quantize_rows_kernel<T, FMT>, dim3((unsigned)gx, (unsigned)gy),
                     dim3(kQThreads), 0, stream, p, log_tx);
