@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams 
 #pragma unroll
       for (int i = 0; i < 16; ++i) ss += h[j][i] * h[j][i];
     ss = row_sum(ss, log_tpr, red);
-    rstd = rsqrtf(ss / (float)p.cols + p.eps);
+    rstd = __frsqrt_rn(ss / (float)p.cols + p.eps);
 #pragma unroll
     for (int j = 0; j < V; ++j) finish(t + j * tpr, h[j], rstd);
   } else {
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams 
       for (int i = 0; i < 16; ++i) ss += h[i] * h[i];
     }
     ss = row_sum(ss, log_tpr, red);
-    rstd = rsqrtf(ss / (float)p.cols + p.eps);
+    rstd = __frsqrt_rn(ss / (float)p.cols + p.eps);
     // Whole strides: every lane takes part in the quantiser's shuffles.
     for (int c0 = 0; c0 < chunks; c0 += tpr) {
       load_h(c0 + t, h);
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += h[j][i] * h[j][i];
       }
-      rstd = rsqrtf(block_sum(ss, red, par) / (float)p.cols + p.eps);
+      rstd = __frsqrt_rn(block_sum(ss, red, par) / (float)p.cols + p.eps);
       par ^= 1;
       if (p.rstd && t == 0) p.rstd[row] = rstd;
     }
