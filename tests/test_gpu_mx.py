@@ -505,3 +505,19 @@ def test_graph_capture():
         out.zero_()
         graph.replay()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt,bound", [("mxfp8", 0.1), ("mxfp4", 0.5), ("nvfp4", 0.4)])
+def test_example_block(fmt, bound):
+    # The block's outputs and gradients are off fp32 by the codes' rounding: an
+    # e4m3 code is within 1/16 of its value (an e2m1 code within 1/4, or more in
+    # small values), in a product of two such operands, squared between.
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "mx_block.py")
+    spec = importlib.util.spec_from_file_location("mx_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for name, err in example.run(200, 264, 520, fmt).items():
+        assert err < bound, (name, err)
