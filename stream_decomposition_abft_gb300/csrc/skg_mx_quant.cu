@@ -91,154 +91,186 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
   }
 }
 
-// Along the columns, or along both. X is stored lines x columns; a block takes a
-// tile of 128 x 128 of it. The row direction (ROWS: the quantised X) works on the
-// pieces of 8 elements as they are loaded, 16 lanes a line. For the column
-// direction (the quantised X^T) the tile goes to shared memory (16-bit types),
-// and a thread takes 32 consecutive lines of two adjacent columns: four lanes
-// hold the tile's four line ranges of a column pair, so that codes leave in
-// 64 to 128 bytes at a time; the words of a line are XORed with its line range
-// for those lanes to read different banks.
+// Along the columns, or along both. X is stored lines x columns; a block takes
+// tiles of 128 x 128 of it in turn, the next one on its way to shared memory
+// (cp.async) while it works on one. The row direction (ROWS: the quantised X) takes
+// pieces of 8 elements, 16 lanes a line. In the column direction (the quantised
+// X^T) a thread takes 32 consecutive lines of two adjacent columns: four lanes hold
+// the tile's four line ranges of a column pair, so that codes leave in 64 to 128
+// bytes at a time; the words of a line are XORed with its line range for those
+// lanes to read different banks. The tiles of the same columns follow one another,
+// so that what is written along a row of X^T is written together.
 constexpr int kTile = 128;
 
 template <typename T, int FMT, bool ROWS>
-__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 3)
-mx_quantize_tile_kernel(QuantParams p, QuantParams rp) {
-  constexpr int W = sizeof(T) / 2;           // 32-bit words of a column pair
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 1 : 3)
+mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_k) {
+  constexpr int W = sizeof(T) / 2;             // 32-bit words of a column pair
   constexpr int LINE = kTile * sizeof(T) / 4;  // words of a line
-  extern __shared__ uint32_t tile[];         // kTile x LINE
+  extern __shared__ __align__(16) uint32_t smem[];  // two tiles of kTile x LINE
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t k0 = (int64_t)blockIdx.x * kTile, c0 = (int64_t)blockIdx.y * kTile;
   const T* x = reinterpret_cast<const T*>(p.x);
   const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
-  {
-    const int piece = threadIdx.x & 15;
-    const int64_t c = c0 + piece * 8;
-    const int64_t left = p.rows - c;
-    const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-    MxRaw8<T> raw[8];
+  const int piece = threadIdx.x & 15, line0 = threadIdx.x >> 4;
+  // Where this thread's piece of a line lies: word w of line l at w ^ 8 W (l / 32);
+  // pieces of 4 words stay whole.
+  auto place = [&](uint32_t* tile, int line, int j) {
+    return reinterpret_cast<uint4*>(tile + line * LINE +
+                                    ((piece * 4 * W + j * 4) ^ ((line >> 5) * 8 * W)));
+  };
+  auto fetch = [&](int64_t t, uint32_t* tile) {
+    if (t < tiles) {
+      const int64_t k0 = t % tiles_k * kTile, c = t / tiles_k * kTile + piece * 8;
+      const int64_t left = p.rows - c;
+      const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t line = k0 + i * 16 + (threadIdx.x >> 4);
-      const int m = line < p.k ? n : 0;
-      raw[i] = mx_load_raw8(x + line * p.ldx + c, p.x_vec && m == 8, m);
+      for (int i = 0; i < 8; ++i) {
+        const int line = i * 16 + line0;
+        const int m = k0 + line < p.k ? n : 0;
+        const T* src = x + (k0 + line) * p.ldx + c;
+        if (p.x_vec && (m == 8 || m == 0)) {
+#pragma unroll
+          for (int j = 0; j < W; ++j)
+            cp_async16(place(tile, line, j), m ? src + j * (16 / (int)sizeof(T)) : x, m ? 16u : 0u);
+        } else {
+          const MxRaw8<T> raw = mx_load_raw8(src, false, m);
+#pragma unroll
+          for (int j = 0; j < W; ++j) *place(tile, line, j) = raw.q[j];
+        }
+      }
     }
+    cp_async_commit();
+  };
+  fetch(blockIdx.x, smem);
+  int buf = 0;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
+    uint32_t* tile = smem + buf * (kTile * LINE);
+    const int64_t k0 = t % tiles_k * kTile, c0 = t / tiles_k * kTile;
+    fetch(t + gridDim.x, smem + (buf ^ 1) * (kTile * LINE));
+    cp_async_wait<1>();
+    __syncthreads();
+    if constexpr (ROWS) {
+      // Chunks of 16 elements, 8 lanes a line.
+      const int64_t c = c0 + (threadIdx.x & 7) * 16;
+      const int groups = (int)mx_groups(rp.k, FMT);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int line = i * 16 + (threadIdx.x >> 4);
-      // Word w of a line at w ^ 8 W (line / 32): pieces of 4 words stay whole.
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        *reinterpret_cast<uint4*>(tile + line * LINE +
-                                  ((piece * 4 * W + j * 4) ^ ((line >> 5) * 8 * W))) = raw[i].q[j];
-      if constexpr (ROWS) {
+      for (int i = 0; i < 4; ++i) {
+        const int line = i * 32 + (threadIdx.x >> 3);
         const int64_t r = k0 + line;
         const bool here = r < rp.rows && c < (rp.k + 31) / 32 * 32;
-        float v[8];
-        mx_unpack_raw8(raw[i], v);
-        uint2 codes;
+        MxRaw16<T> raw;
+#pragma unroll
+        for (int j = 0; j < 2 * W; ++j)
+          raw.q[j] = *reinterpret_cast<const uint4*>(
+              tile + line * LINE + (((threadIdx.x & 7) * 8 * W + j * 4) ^ ((line >> 5) * 8 * W)));
+        float v[16];
+        mx_unpack_raw16(raw, v);
+        uint4 codes;
         uint32_t word;
-        mx_quantize_piece<FMT>(v, here, lane, g, codes, word);
-        if (here) mx_store_codes8<FMT>(rp.codes + r * rp.ldq, c / 8, codes);
-        constexpr int per = 2 * mx_group_chunks(FMT);
-        const int groups = (int)mx_groups(rp.k, FMT);
-        const int64_t grp = c / 8 / per;
+        mx_quantize_chunk<FMT>(v, mx_absmax_raw16(raw), here, lane, g, codes, word);
+        if (here) mx_store_codes16<FMT>(rp.codes + r * rp.ldq, c / 16, codes);
+        constexpr int per = mx_group_chunks(FMT);
+        const int64_t grp = c / 16 / per;
         if ((lane & (per - 1)) == 0 && grp < groups)
           *reinterpret_cast<uint32_t*>(rp.scales + mx_scale_word(r, (int)grp, groups)) = word;
       }
     }
-  }
-  __syncthreads();
-  const int kb = lane & 3, pair = (threadIdx.x >> 5) * 8 + (lane >> 2);
-  const int64_t kfirst = k0 + kb * 32;
-  const int groups = (int)mx_groups(p.k, FMT);
-  uint32_t w[32][W];
+    const int kb = lane & 3, pair = (threadIdx.x >> 5) * 8 + (lane >> 2);
+    const int64_t kfirst = k0 + kb * 32;
+    const int groups = (int)mx_groups(p.k, FMT);
+    uint32_t w[32][W];
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      w[i][j] = tile[(kb * 32 + i) * LINE + ((pair * W + j) ^ (kb * 8 * W))];
-  // Largest magnitudes of the two columns' 16-line halves.
-  uint32_t top[2][2];
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint32_t m[W] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 32; ++i)
 #pragma unroll
       for (int j = 0; j < W; ++j)
-        m[j] = W == 1 ? mx_absmax2(m[j], w[b * 16 + i][j]) : max(m[j], w[b * 16 + i][j] & 0x7fffffffu);
-    if constexpr (W == 1) {
-      top[0][b] = mx_magnitude<T>(m[0] & 0xffffu);
-      top[1][b] = mx_magnitude<T>(m[0] >> 16);
-    } else {
-      top[0][b] = m[0];
-      top[1][b] = m[W - 1];
-    }
-  }
+        w[i][j] = tile[(kb * 32 + i) * LINE + ((pair * W + j) ^ (kb * 8 * W))];
+    // Largest magnitudes of the two columns' 16-line halves.
+    uint32_t top[2][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // the pair's columns
-    const int64_t row = c0 + pair * 2 + h;
-    const bool live = row < p.rows && kfirst < p.k;
-    if constexpr (FMT != SKG_NVFP4) top[h][0] = max(top[h][0], top[h][1]);
-    uint32_t bytes[2];
-    MxScale s;
+    for (int b = 0; b < 2; ++b) {
+      uint32_t m[W] = {};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {  // 16 lines at a time
-      float v[16];
+      for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t u = w[b * 16 + i][h * (W - 1)];
-        if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(u);
-        else v[i] = mx_to_f32(reinterpret_cast<const T*>(&u)[h]);
+        for (int j = 0; j < W; ++j)
+          m[j] = W == 1 ? mx_absmax2(m[j], w[b * 16 + i][j]) : max(m[j], w[b * 16 + i][j] & 0x7fffffffu);
+      if constexpr (W == 1) {
+        top[0][b] = mx_magnitude<T>(m[0] & 0xffffu);
+        top[1][b] = mx_magnitude<T>(m[0] >> 16);
+      } else {
+        top[0][b] = m[0];
+        top[1][b] = m[W - 1];
       }
-      if (FMT == SKG_NVFP4 || b == 0) s = mx_scale<FMT>(top[h][b], g);
-      bytes[b] = s.byte;
-      if (live) {
-        const uint4 codes = mx_codes16<FMT>(v, s);
-        mx_store_codes16<FMT>(p.codes + row * p.ldq, kfirst / 16 + b, codes);
-        if (p.values) {
-          mx_values16<FMT>(codes, s, g, v);
-          const int64_t left = p.k - (kfirst + b * 16);
-          const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
-          mx_store16(reinterpret_cast<T*>(p.values) + row * p.ldv + kfirst + b * 16,
-                     p.v_vec && n == 16, n, v);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // the pair's columns
+      const int64_t row = c0 + pair * 2 + h;
+      const bool live = row < p.rows && kfirst < p.k;
+      if constexpr (FMT != SKG_NVFP4) top[h][0] = max(top[h][0], top[h][1]);
+      uint32_t bytes[2];
+      MxScale s;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {  // 16 lines at a time
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t u = w[b * 16 + i][h * (W - 1)];
+          if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(u);
+          else v[i] = mx_to_f32(reinterpret_cast<const T*>(&u)[h]);
+        }
+        if (FMT == SKG_NVFP4 || b == 0) s = mx_scale<FMT>(top[h][b], g);
+        bytes[b] = s.byte;
+        if (live) {
+          const uint4 codes = mx_codes16<FMT>(v, s);
+          mx_store_codes16<FMT>(p.codes + row * p.ldq, kfirst / 16 + b, codes);
+          if (p.values) {
+            mx_values16<FMT>(codes, s, g, v);
+            const int64_t left = p.k - (kfirst + b * 16);
+            const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
+            mx_store16(reinterpret_cast<T*>(p.values) + row * p.ldv + kfirst + b * 16,
+                       p.v_vec && n == 16, n, v);
+          }
         }
       }
+      uint32_t word;
+      if constexpr (FMT == SKG_NVFP4) {
+        word = live ? (bytes[0] | (bytes[1] << 8)) << (16 * (kb & 1)) : 0u;
+        word |= __shfl_xor_sync(0xffffffffu, word, 1);
+        const int64_t grp = (k0 / 64) + (kb >> 1);
+        if ((kb & 1) == 0 && grp < groups)
+          *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)grp, groups)) = word;
+      } else {
+        word = live ? bytes[0] << (8 * kb) : 0u;
+        word |= __shfl_xor_sync(0xffffffffu, word, 1);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2);
+        if (kb == 0 && k0 / 128 < groups)
+          *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)(k0 / 128), groups)) = word;
+      }
     }
-    uint32_t word;
-    if constexpr (FMT == SKG_NVFP4) {
-      word = live ? (bytes[0] | (bytes[1] << 8)) << (16 * (kb & 1)) : 0u;
-      word |= __shfl_xor_sync(0xffffffffu, word, 1);
-      const int64_t grp = (k0 / 64) + (kb >> 1);
-      if ((kb & 1) == 0 && grp < groups)
-        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)grp, groups)) = word;
-    } else {
-      word = live ? bytes[0] << (8 * kb) : 0u;
-      word |= __shfl_xor_sync(0xffffffffu, word, 1);
-      word |= __shfl_xor_sync(0xffffffffu, word, 2);
-      if (kb == 0 && k0 / 128 < groups)
-        *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)(k0 / 128), groups)) = word;
-    }
+    __syncthreads();  // the tile is free for the one after the next
   }
 }
 
 // rp: the row direction of the same matrix too (NULL: columns alone).
 template <typename T, int FMT>
 cudaError_t launch_tile(const QuantParams& p, const QuantParams* rp, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.k + kTile - 1) / kTile), (unsigned)((p.rows + kTile - 1) / kTile));
-  const size_t smem = kTile * kTile * sizeof(T);
+  const int64_t tiles_k = (p.k + kTile - 1) / kTile;
+  const int64_t tiles = (p.rows + kTile - 1) / kTile * tiles_k;
+  const size_t smem = 2 * kTile * kTile * sizeof(T);
+  const int64_t most = (int64_t)skg_device_sm_count() * (sizeof(T) == 4 ? 1 : 3);
+  if (most <= 0) return cudaErrorNoDevice;
+  const dim3 grid((unsigned)(tiles < most ? tiles : most));
   static std::atomic<uint64_t> d0{0}, d1{0};
   const void* kernel = rp ? (const void*)mx_quantize_tile_kernel<T, FMT, true>
                           : (const void*)mx_quantize_tile_kernel<T, FMT, false>;
   const cudaError_t e = opt_in_smem(kernel, rp ? d1 : d0, (int)smem);
   if (e != cudaSuccess) return e;
   return rp ? launch_pdl(mx_quantize_tile_kernel<T, FMT, true>, grid, dim3(kQThreads), smem, stream,
-                         p, *rp)
+                         p, *rp, tiles, (int)tiles_k)
             : launch_pdl(mx_quantize_tile_kernel<T, FMT, false>, grid, dim3(kQThreads), smem,
-                         stream, p, p);
+                         stream, p, p, tiles, (int)tiles_k);
 }
 
 template <typename T, int FMT>
@@ -310,8 +342,7 @@ skg_status_t skg_mx_quantize(int64_t rows, int64_t k, const void* X, int64_t ldx
   if (!X || !codes || !scales || ldx < (transpose ? rows : k) ||
       ldq < skg_mx_codes_ld(k, format) || (values && ldv < k))
     return SKG_ERR_ARG;
-  // The transposed grid counts column tiles in its second dimension.
-  if (k > INT32_MAX / 4 || rows > (transpose ? 65535 * (int64_t)kTile : INT32_MAX / 4))
+  if (k > INT32_MAX / 4 || rows > INT32_MAX / 4)
     return SKG_ERR_UNSUPPORTED;
   const int es = type == SKG_OUT_F32 ? 4 : 2;
   if (!storage_aligned(codes, ldq, scales) || ((uintptr_t)X & (es - 1)) ||
@@ -347,7 +378,7 @@ skg_status_t skg_mx_quantize_both(int64_t rows, int64_t cols, const void* X, int
   if (!X || !codes || !scales || !codes_t || !scales_t || ldx < cols ||
       ldq < skg_mx_codes_ld(cols, format) || ldq_t < skg_mx_codes_ld(rows, format))
     return SKG_ERR_ARG;
-  if (rows > INT32_MAX / 4 || cols > 65535 * (int64_t)kTile) return SKG_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX / 4 || cols > INT32_MAX / 4) return SKG_ERR_UNSUPPORTED;
   const int es = type == SKG_OUT_F32 ? 4 : 2;
   if (!storage_aligned(codes, ldq, scales) || !storage_aligned(codes_t, ldq_t, scales_t) ||
       ((uintptr_t)X & (es - 1)) || ((uintptr_t)tensor_scale & 3))
