@@ -378,6 +378,82 @@ __device__ __forceinline__ void mx_unpack_raw8(const MxRaw8<T>& r, float (&v)[8]
   for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(e[i]);
 }
 
+// Eight elements of a 16-bit type from an address that is a multiple of 2 alone:
+// the two aligned 16-byte pieces that hold them, shifted together (one load of
+// eight would take eight instructions). lo, hi: the matrix; a piece that reaches
+// outside of it is read element by element. Elements n .. 7 are 0.
+template <typename T>
+__device__ __forceinline__ uint4 mx_aligned_piece(uintptr_t at, const T* lo, const T* hi) {
+  if (at >= (uintptr_t)lo && at + 16 <= (uintptr_t)hi) return *reinterpret_cast<const uint4*>(at);
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  T* e = reinterpret_cast<T*>(&q);
+  const T* src = reinterpret_cast<const T*>(at);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (src + i >= lo && src + i < hi) e[i] = src[i];
+  return q;
+}
+template <typename T>
+__device__ __forceinline__ uint4 mx_load8_any(const T* p, int n, const T* lo, const T* hi) {
+  static_assert(sizeof(T) == 2, "16-bit elements");
+  if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  const uintptr_t at = (uintptr_t)p & ~(uintptr_t)15;
+  const int o = (int)(((uintptr_t)p & 15) >> 1);
+  const uint4 a = mx_aligned_piece(at, lo, hi);
+  const uint4 b = o + n > 8 ? mx_aligned_piece(at + 16, lo, hi) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (o & 4) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (o & 2) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (o & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n < 2 * i + 2) w[i] &= 0xffffu;
+    if (n < 2 * i + 1) w[i] = 0u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A warp's consecutive pieces of 8 elements to a row of any alignment, 32
+// neighbouring elements an instruction (a lane's own eight would touch a sector
+// each): `total` elements from the first lane's on. buf: 32 pieces of shared memory
+// of the warp's own.
+template <typename T>
+__device__ __forceinline__ void mx_warp_store8(T* first, int total, const uint4& q, uint4* buf,
+                                               int lane) {
+  __syncwarp();
+  buf[lane] = q;
+  __syncwarp();
+  const T* e = reinterpret_cast<const T*>(buf);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i * 32 + lane < total) first[i * 32 + lane] = e[i * 32 + lane];
+}
+
+template <typename T>
+__device__ __forceinline__ void mx_store8(T* p, bool vec, int n, const float (&v)[8]) {
+  MxRaw8<T> r;
+  T* e = reinterpret_cast<T*>(r.q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = mx_from_f32<T>(v[i]);
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) *(reinterpret_cast<uint4*>(p) + i) = r.q[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = e[i];
+  }
+}
+
 // Eight elements of a 16-bit type.
 template <typename T>
 __device__ __forceinline__ void mx_unpack8(const uint4& u, float (&v)[8]) {

@@ -171,9 +171,10 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[kNormMaxThreads
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-template <typename T, int FMT, int V>
+template <typename T, int FMT, int V, bool VEC>
 __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(NormParams p) {
   extern __shared__ uint4 ring[];  // stages x (x, residual) x V x threads
+  __shared__ uint4 wbuf[VEC ? 1 : kNormMaxThreads / 32][32];
   __shared__ float red[2][kNormMaxThreads / 32];
   const int t = threadIdx.x, lane = t & 31, nt = blockDim.x;
   const int groups = (int)mx_groups(p.cols, FMT);
@@ -184,15 +185,22 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
   griddep_wait();
   griddep_launch_dependents();
   const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
+  auto count = [&](int c) { return c + 8 <= p.cols ? 8 : (c < p.cols ? p.cols - c : 0); };
   auto fetch = [&](int64_t row, int st) {
     if (row < p.rows) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int c = (t + j * nt) * 8;
-        const uint32_t n = c < p.cols ? 16u : 0u;
+        const int c = (t + j * nt) * 8, n = count(c);
         uint4* dst = ring + ((st * 2) * V + j) * nt + t;
-        cp_async16(dst, x + row * p.ldx + (n ? c : 0), n);
-        if (p.res) cp_async16(dst + V * nt, res + row * p.ldr + (n ? c : 0), n);
+        if constexpr (VEC) {
+          cp_async16(dst, x + row * p.ldx + (n ? c : 0), n ? 16u : 0u);
+          if (p.res) cp_async16(dst + V * nt, res + row * p.ldr + (n ? c : 0), n ? 16u : 0u);
+        } else {
+          *dst = mx_load8_any(x + row * p.ldx + c, n, x, x + (p.rows - 1) * p.ldx + p.cols);
+          if (p.res)
+            dst[V * nt] =
+                mx_load8_any(res + row * p.ldr + c, n, res, res + (p.rows - 1) * p.ldr + p.cols);
+        }
       }
     }
     cp_async_commit();
@@ -203,8 +211,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (t + j * nt) * 8;
-    wv[j] = c < p.cols ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + c)
-                       : make_uint4(0u, 0u, 0u, 0u);
+    wv[j] = mx_load_raw8(reinterpret_cast<const T*>(p.w) + c, VEC && count(c) == 8, count(c)).q[0];
   }
   const float inv_n = 1.f / (float)p.cols;
   int st = 0, par = 0;
@@ -237,9 +244,15 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
     for (int j = 0; j < V; ++j) {
       const int c = t + j * nt;
       const bool live = here && c < pieces;
-      if (live && p.sum && c * 8 < p.cols)
-        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.sum) + row * p.lds + c * 8) =
-            mx_pack8<T>(h[j]);
+      if (here && p.sum) {
+        T* out = reinterpret_cast<T*>(p.sum) + row * p.lds;
+        if constexpr (VEC) {
+          if (c * 8 < p.cols) *reinterpret_cast<uint4*>(out + c * 8) = mx_pack8<T>(h[j]);
+        } else {
+          const int c0 = (c - lane) * 8;
+          mx_warp_store8(out + c0, p.cols - c0, mx_pack8<T>(h[j]), wbuf[t >> 5], lane);
+        }
+      }
       float w[8], y[8];
       mx_unpack8<T>(wv[j], w);
 #pragma unroll
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
 }
 
 template <typename T, int FMT>
-cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, int sms,
+cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, bool vec, int sms,
                              cudaStream_t stream) {
   const size_t smem = (size_t)kNormStages * 2 * v * threads * 16;
   const int64_t rows = (p.rows + 127) / 128 * 128;
@@ -271,21 +284,26 @@ cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, int sms,
                                                                      16 * 2);
     return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(threads), smem, stream, p);
   };
-  static std::atomic<uint64_t> d1{0}, d2{0};
-  return v == 1 ? run(rmsnorm_mx_wide_kernel<T, FMT, 1>, d1)
-                : run(rmsnorm_mx_wide_kernel<T, FMT, 2>, d2);
+  static std::atomic<uint64_t> d[4] = {};
+  if (v == 1)
+    return vec ? run(rmsnorm_mx_wide_kernel<T, FMT, 1, true>, d[0])
+               : run(rmsnorm_mx_wide_kernel<T, FMT, 1, false>, d[1]);
+  return vec ? run(rmsnorm_mx_wide_kernel<T, FMT, 2, true>, d[2])
+             : run(rmsnorm_mx_wide_kernel<T, FMT, 2, false>, d[3]);
 }
 
 template <typename T, int FMT>
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t stream) {
-  // Rows of 1024 to 8192 elements on 16-byte boundaries: a block per row with
-  // its ring (narrower rows share a block, wider ones need more registers).
+  // Rows of up to 8192 elements: a block per row with its ring. (Narrow ones on
+  // 16-byte boundaries share a block; wider ones need more registers.)
   const int pieces = (p.cols + 31) / 32 * 4;
-  if (p.x_vec && p.w_vec && (!p.res || p.r_vec) && (!p.sum || p.s_vec) && p.cols % 8 == 0 &&
-      pieces > 96 && pieces <= 2 * kNormMaxThreads) {
+  const bool vec = p.x_vec && p.w_vec && (!p.res || p.r_vec) && (!p.sum || p.s_vec) &&
+                   p.cols % 8 == 0;
+  if (pieces <= 2 * kNormMaxThreads && (pieces > 96 || !vec)) {
     const int threads = pieces <= kNormMaxThreads ? (pieces + 31) / 32 * 32
                                                   : (pieces + 63) / 64 * 32;
-    return launch_norm_wide<T, FMT>(p, pieces <= kNormMaxThreads ? 1 : 2, threads, sms, stream);
+    return launch_norm_wide<T, FMT>(p, pieces <= kNormMaxThreads ? 1 : 2, threads, vec, sms,
+                                    stream);
   }
   const int chunks = (p.cols + 31) / 32 * 2;
   int log_tpr = 3;
@@ -329,17 +347,15 @@ struct GradParams {
   int vec;           // every row is 16-byte aligned
 };
 
-// dx, a row at a time per group of 2^log_tpr threads (V chunks of 16 elements
-// each); V = 0: any width, the row read twice.
+// Rows of more than 8192 elements: a row at a time per block of 512 threads, V
+// chunks of 16 elements each, in registers between the sum and dx; V = 0: any width,
+// the row read twice (and dw formed by rmsnorm_grad_columns_kernel).
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(GradParams p, int log_tpr) {
-  __shared__ float red[kNormMaxThreads / 32];
-  extern __shared__ float wsum[];  // blockDim.x / tpr > 1: the groups' dw, cols floats
+__global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_long_kernel(GradParams p) {
+  __shared__ float red[2][kNormMaxThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int tpr = 1 << log_tpr;
-  const int t = threadIdx.x & (tpr - 1);
-  const int per = blockDim.x >> log_tpr, mine = threadIdx.x >> log_tpr;
+  const int t = threadIdx.x;
   const int chunks = (p.cols + 15) / 16;
   const T* w = reinterpret_cast<const T*>(p.w);
   const float inv_n = 1.f / (float)p.cols;
@@ -353,28 +369,30 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(GradParam
   for (int j = 0; j < VV; ++j)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
-  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per) {
-    const int64_t row = r0 + mine;
-    const bool here = row < p.rows;
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
     const T* dy = reinterpret_cast<const T*>(p.dy) + row * p.lddy;
     const T* h = reinterpret_cast<const T*>(p.h) + row * p.ldh;
     const T* dr = reinterpret_cast<const T*>(p.dres) + row * p.lddr;
     T* dx = reinterpret_cast<T*>(p.dx) + row * p.lddx;
-    const float rstd = here ? p.rstd[row] : 0.f;
+    const float rstd = p.rstd[row];
     float dot = 0.f;
-    auto load = [&](int c, float (&a)[16], float (&b)[16], float (&u)[16]) {
-      const int n = here ? count(c) : 0;
+    auto load = [&](int c, float (&a)[16], float (&b)[16]) {  // dy; xhat
+      const int n = count(c);
       mx_load16(dy + c * 16, p.vec && n == 16, n, a);
       mx_load16(h + c * 16, p.vec && n == 16, n, b);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) b[i] *= rstd;
+    };
+    auto weigh = [&](int c, float (&a)[16]) {  // dy -> w dy
+      const int n = count(c);
+      float u[16];
       mx_load16(w + c * 16, p.vec && n == 16, n, u);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        b[i] *= rstd;   // xhat
-        u[i] *= a[i];   // w dy
-      }
+      for (int i = 0; i < 16; ++i) a[i] *= u[i];
     };
     auto store = [&](int c, const float (&b)[16], const float (&u)[16], float mean) {
-      const int n = here ? count(c) : 0;
+      const int n = count(c);
       float o[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = 0.f;
@@ -384,78 +402,65 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(GradParam
       mx_store16(dx + c * 16, p.vec && n == 16, n, o);
     };
     if constexpr (V > 0) {
-      float b[V][16], u[V][16];
+      float a[V][16], b[V][16];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float a[16];
-        load(t + j * tpr, a, b[j], u[j]);
+        load(t + j * kNormMaxThreads, a[j], b[j]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          acc[j][i] += a[i] * b[j][i];
-          dot += u[j][i] * b[j][i];
-        }
+        for (int i = 0; i < 16; ++i) acc[j][i] += a[j][i] * b[j][i];
+        weigh(t + j * kNormMaxThreads, a[j]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dot += a[j][i] * b[j][i];
       }
-      const float mean = row_sum(dot, log_tpr, red) * inv_n;
+      const float mean = block_sum(dot, red, par) * inv_n;
 #pragma unroll
-      for (int j = 0; j < V; ++j) store(t + j * tpr, b[j], u[j], mean);
+      for (int j = 0; j < V; ++j) store(t + j * kNormMaxThreads, b[j], a[j], mean);
     } else {
-      float a[16], b[16], u[16];
-      for (int c = t; c < chunks; c += tpr) {
-        load(c, a, b, u);
+      float a[16], b[16];
+      for (int c = t; c < chunks; c += kNormMaxThreads) {
+        load(c, a, b);
+        weigh(c, a);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dot += u[i] * b[i];
+        for (int i = 0; i < 16; ++i) dot += a[i] * b[i];
       }
-      const float mean = row_sum(dot, log_tpr, red) * inv_n;
-      for (int c = t; c < chunks; c += tpr) {
-        load(c, a, b, u);
-        store(c, b, u, mean);
+      const float mean = block_sum(dot, red, par) * inv_n;
+      for (int c = t; c < chunks; c += kNormMaxThreads) {
+        load(c, a, b);
+        weigh(c, a);
+        store(c, b, a, mean);
       }
     }
   }
   if constexpr (V > 0) {
     float* out = p.partial + (int64_t)blockIdx.x * p.cols;
-    if (per == 1) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c = t + j * tpr, n = count(c);
+    for (int j = 0; j < V; ++j) {
+      const int c = t + j * kNormMaxThreads, n = count(c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < n) out[c * 16 + i] = acc[j][i];
-      }
-    } else {
-      // The groups add their sums one after another (a fixed order).
-      for (int gq = 0; gq < per; ++gq) {
-        if (gq == mine) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int c = t + j * tpr, n = count(c);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i < n) wsum[c * 16 + i] = gq == 0 ? acc[j][i] : wsum[c * 16 + i] + acc[j][i];
-          }
-        }
-        __syncthreads();
-      }
-      for (int c = threadIdx.x; c < p.cols; c += blockDim.x) out[c] = wsum[c];
+      for (int i = 0; i < 16; ++i)
+        if (i < n) out[c * 16 + i] = acc[j][i];
     }
   }
 }
 
-// The wide rows' gradient, with the same ring for dy, h and dresidual. A block
+// The gradient of rows of up to 8192 elements, with the same ring for dy, h and
+// dresidual (rows off 16-byte boundaries go there through registers). A block
 // takes two rows at a time: the first pass over the fetched pieces forms both
 // rows' sums, which cross the block together (a row's sum, barriers and all, takes
 // longer than its arithmetic: 4096 x 8192 one row at a time 46 us), the second
 // reads them again from shared memory for dx. dw of the block's rows stays in
 // registers.
-template <typename T, int V>
+template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(GradParams p) {
   extern __shared__ uint4 ring[];  // stages x (dy, h, dres) x V x threads
   __shared__ float2 red[2][kNormMaxThreads / 32];
+  __shared__ uint4 wbuf[VEC ? 1 : kNormMaxThreads / 32][32];
   static_assert(kGradStages == 4, "two rows in hand, two on the way");
   const int t = threadIdx.x, nt = blockDim.x, lane = t & 31;
   const T* in[3] = {reinterpret_cast<const T*>(p.dy), reinterpret_cast<const T*>(p.h),
                     reinterpret_cast<const T*>(p.dres)};
   const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
+  auto count = [&](int c) { return c + 8 <= p.cols ? 8 : (c < p.cols ? p.cols - c : 0); };
   griddep_wait();
   griddep_launch_dependents();
   auto fetch = [&](int64_t row, int st) {
@@ -466,8 +471,11 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int c = (t + j * nt) * 8;
-          const uint32_t n = c < p.cols ? 16u : 0u;
-          cp_async16(ring + ((st * 3 + k) * V + j) * nt + t, in[k] + row * ld[k] + (n ? c : 0), n);
+          uint4* dst = ring + ((st * 3 + k) * V + j) * nt + t;
+          const int n = count(c);
+          if constexpr (VEC) cp_async16(dst, in[k] + row * ld[k] + (n ? c : 0), n ? 16u : 0u);
+          else *dst = mx_load8_any(in[k] + row * ld[k] + c, n, in[k],
+                                   in[k] + (p.rows - 1) * ld[k] + p.cols);
         }
       }
     }
@@ -480,8 +488,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (t + j * nt) * 8;
-    wv[j] = c < p.cols ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.w) + c)
-                       : make_uint4(0u, 0u, 0u, 0u);
+    wv[j] = mx_load_raw8(reinterpret_cast<const T*>(p.w) + c, VEC && count(c) == 8, count(c)).q[0];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
   }
@@ -557,9 +564,13 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             o[i] += rstd[q] * (w[i] * dy[i] - h[i] * rstd[q] * mean[q]);
-          if (c < p.cols)
-            *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.dx) + r * p.lddx + c) =
-                mx_pack8<T>(o);
+          T* out = reinterpret_cast<T*>(p.dx) + r * p.lddx;
+          if constexpr (VEC) {
+            if (c < p.cols) *reinterpret_cast<uint4*>(out + c) = mx_pack8<T>(o);
+          } else {
+            const int c0 = c - lane * 8;
+            mx_warp_store8(out + c0, p.cols - c0, mx_pack8<T>(o), wbuf[t >> 5], lane);
+          }
         }
       }
       fetch(r + (int64_t)kGradStages * gridDim.x, st + q);
@@ -569,11 +580,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (t + j * nt) * 8;
-    if (c < p.cols) {
-      float4* out = reinterpret_cast<float4*>(p.partial + (int64_t)blockIdx.x * p.cols + c);
-      out[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      out[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
-    }
+    mx_store8(p.partial + (int64_t)blockIdx.x * p.cols + c, VEC && count(c) == 8, count(c), acc[j]);
   }
 }
 
@@ -622,71 +629,60 @@ rmsnorm_grad_reduce_kernel(const float* partial, int parts, int cols, float* dw)
 }
 
 struct GradPlan {
-  int log_tpr, v, threads, per, blocks;
-  size_t smem;
-  int wide_v, wide_threads, wide_blocks;  // the kernel with the ring (wide_v = 0: not for it)
+  int v;        // pieces or chunks of a thread
+  int threads;  // of rmsnorm_grad_wide_kernel; 0: rmsnorm_grad_long_kernel (512)
+  int blocks;
 };
 
 GradPlan grad_plan(int64_t rows, int64_t cols, int sms) {
   GradPlan g;
-  const int64_t chunks = (cols + 15) / 16;
-  g.log_tpr = 3;
-  while ((1 << g.log_tpr) < chunks && (1 << g.log_tpr) < kNormMaxThreads) ++g.log_tpr;
-  const int64_t v = (chunks + (1 << g.log_tpr) - 1) >> g.log_tpr;
-  g.v = v > 4 ? 0 : (int)v;
-  g.threads = g.log_tpr < 7 ? 128 : (1 << g.log_tpr);
-  g.per = g.threads >> g.log_tpr;
-  g.smem = g.per > 1 ? (size_t)cols * 4 : 0;
-  // Whole pieces of 8 on 16-byte boundaries take the kernel with the ring: a block
-  // of up to 512 threads per SM, two of up to 256.
-  const int64_t pieces = (cols + 7) / 8;
-  g.wide_v = cols % 8 != 0 || pieces <= 96 || pieces > 2 * kNormMaxThreads ? 0
-             : pieces <= kNormMaxThreads                                   ? 1
-                                                                           : 2;
-  g.wide_threads = g.wide_v ? (int)((pieces + 32 * g.wide_v - 1) / (32 * g.wide_v) * 32) : 0;
-  const int64_t n = sms > 0 ? sms : 152;
-  const int64_t wide = g.wide_threads <= 256 ? 2 * n : n;
-  g.wide_blocks = (int)(rows < wide ? rows : wide);
-  // Else rows per block (blocks of 128 threads hide little each: four per SM).
-  const int64_t want = (rows + g.per - 1) / g.per, most = g.threads <= 128 ? 4 * n : 2 * n;
-  g.blocks = (int)(want < most ? want : most);
+  const int64_t pieces = (cols + 7) / 8, n = sms > 0 ? sms : 152;
+  int64_t most = n;
+  if (pieces <= 2 * kNormMaxThreads) {
+    g.v = pieces <= kNormMaxThreads ? 1 : 2;
+    g.threads = (int)((pieces + 32 * g.v - 1) / (32 * g.v) * 32);
+    // Blocks of few threads share an SM; each adds a row of partial sums to reduce.
+    most = g.threads <= 64 ? 4 * n : (g.threads <= 256 ? 2 * n : n);
+  } else {
+    const int64_t chunks = (cols + 15) / 16, v = (chunks + kNormMaxThreads - 1) / kNormMaxThreads;
+    g.v = v <= 2 ? 2 : 0;
+    g.threads = 0;
+  }
+  g.blocks = (int)(rows < most ? rows : most);
   return g;
 }
 
 template <typename T>
-cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, int sms,
-                        cudaStream_t stream) {
+cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaStream_t stream) {
   cudaError_t e;
-  const dim3 grid(g.blocks), block(g.threads);
-  int parts = g.blocks;
-  if (p.vec && g.wide_v) {
-    const int v = g.wide_v, threads = g.wide_threads;
-    const size_t smem = (size_t)kGradStages * 3 * v * threads * 16;
-    parts = g.wide_blocks;
+  const dim3 grid(g.blocks), wide(g.threads), block(kNormMaxThreads);
+  const bool vec = p.vec && p.cols % 8 == 0;
+  if (g.threads) {
+    const size_t smem = (size_t)kGradStages * 3 * g.v * g.threads * 16;
     auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
       const cudaError_t r = opt_in_smem((const void*)kernel, done,
                                         kGradStages * 3 * 2 * kNormMaxThreads * 16);
-      return r != cudaSuccess ? r
-                              : launch_pdl(kernel, dim3(parts), dim3(threads), smem, stream, p);
+      return r != cudaSuccess ? r : launch_pdl(kernel, grid, wide, smem, stream, p);
     };
-    static std::atomic<uint64_t> d1{0}, d2{0};
-    e = v == 1 ? run(rmsnorm_grad_wide_kernel<T, 1>, d1) : run(rmsnorm_grad_wide_kernel<T, 2>, d2);
-  } else if (g.v == 1)
-    e = launch_pdl(rmsnorm_grad_kernel<T, 1>, grid, block, g.smem, stream, p, g.log_tpr);
-  else if (g.v == 2)
-    e = launch_pdl(rmsnorm_grad_kernel<T, 2>, grid, block, g.smem, stream, p, g.log_tpr);
-  else if (g.v != 0)
-    e = launch_pdl(rmsnorm_grad_kernel<T, 4>, grid, block, g.smem, stream, p, g.log_tpr);
-  else {
-    e = launch_pdl(rmsnorm_grad_kernel<T, 0>, grid, block, g.smem, stream, p, g.log_tpr);
+    static std::atomic<uint64_t> d[4] = {};
+    if (g.v == 1)
+      e = vec ? run(rmsnorm_grad_wide_kernel<T, 1, true>, d[0])
+              : run(rmsnorm_grad_wide_kernel<T, 1, false>, d[1]);
+    else
+      e = vec ? run(rmsnorm_grad_wide_kernel<T, 2, true>, d[2])
+              : run(rmsnorm_grad_wide_kernel<T, 2, false>, d[3]);
+  } else if (g.v == 2) {
+    e = launch_pdl(rmsnorm_grad_long_kernel<T, 2>, grid, block, 0, stream, p);
+  } else {
+    e = launch_pdl(rmsnorm_grad_long_kernel<T, 0>, grid, block, 0, stream, p);
     if (e != cudaSuccess) return e;
     e = launch_pdl(rmsnorm_grad_columns_kernel<T>,
                    dim3((unsigned)((p.cols + 255) / 256), (unsigned)g.blocks), dim3(256), 0,
                    stream, p, g.blocks);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(1024),
-                    0, stream, (const float*)p.partial, parts, p.cols, dw);
+  return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(1024), 0,
+                    stream, (const float*)p.partial, g.blocks, p.cols, dw);
 }
 
 bool vec_rows(const void* p, int64_t ld) {
@@ -748,7 +744,7 @@ skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t l
 size_t skg_workspace_size_rmsnorm_backward(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols <= 0) return 0;
   const GradPlan g = grad_plan(rows, cols, skg_device_sm_count());
-  return (size_t)(g.blocks > g.wide_blocks ? g.blocks : g.wide_blocks) * (size_t)cols * 4;
+  return (size_t)g.blocks * (size_t)cols * 4;
 }
 
 skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, int64_t lddy,
@@ -796,8 +792,8 @@ skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, in
   p.partial = (float*)workspace;
   p.vec = vec_rows(dY, lddy) && vec_rows(H, ldh) && vec_rows(dX, lddx) &&
           ((uintptr_t)weight & 15) == 0 && (!dresidual || vec_rows(dresidual, lddr));
-  const cudaError_t e = type == SKG_IN_F16 ? launch_grad<__half>(p, g, dweight, sms, st)
-                                           : launch_grad<__nv_bfloat16>(p, g, dweight, sms, st);
+  const cudaError_t e = type == SKG_IN_F16 ? launch_grad<__half>(p, g, dweight, st)
+                                           : launch_grad<__nv_bfloat16>(p, g, dweight, st);
   return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
 }
 

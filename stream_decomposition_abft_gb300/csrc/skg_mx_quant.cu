@@ -63,8 +63,19 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
       const int64_t ul = u + h * ls + (ty >> 2);
       row[h] = (ul >> 5) * 128 + (ty & 3) * 32 + (ul & 31);
       const int m = row[h] < p.rows ? n : 0;
-      raw[h] = mx_load_raw16(reinterpret_cast<const T*>(p.x) + row[h] * p.ldx + chunk * 16,
-                             p.x_vec && m == 16, m);
+      const T* x = reinterpret_cast<const T*>(p.x);
+      const T* src = x + row[h] * p.ldx + chunk * 16;
+      if constexpr (sizeof(T) == 2) {
+        if (p.x_vec && m == 16) {
+          raw[h] = mx_load_raw16(src, true, m);
+        } else {
+          const T* end = x + (p.rows - 1) * p.ldx + p.k;
+          raw[h].q[0] = mx_load8_any(src, m < 8 ? m : 8, x, end);
+          raw[h].q[1] = mx_load8_any(src + 8, m - 8, x, end);
+        }
+      } else {
+        raw[h] = mx_load_raw16(src, p.x_vec && m == 16, m);
+      }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -113,6 +124,7 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
   const int lane = threadIdx.x & 31;
   const T* x = reinterpret_cast<const T*>(p.x);
   const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
+  const T* end = x + (p.k - 1) * p.ldx + p.rows;
   const int piece = threadIdx.x & 15, line0 = threadIdx.x >> 4;
   // Where this thread's piece of a line lies: word w of line l at w ^ 8 W (l / 32);
   // pieces of 4 words stay whole.
@@ -135,7 +147,9 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
           for (int j = 0; j < W; ++j)
             cp_async16(place(tile, line, j), m ? src + j * (16 / (int)sizeof(T)) : x, m ? 16u : 0u);
         } else {
-          const MxRaw8<T> raw = mx_load_raw8(src, false, m);
+          MxRaw8<T> raw;
+          if constexpr (sizeof(T) == 2) raw.q[0] = mx_load8_any(src, m, x, end);
+          else raw = mx_load_raw8(src, false, m);
 #pragma unroll
           for (int j = 0; j < W; ++j) *place(tile, line, j) = raw.q[j];
         }
