@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "skg_ptx.cuh"
 #include "skgemm.h"
 
 namespace skg {
@@ -378,6 +379,29 @@ __device__ __forceinline__ void mx_unpack_raw8(const MxRaw8<T>& r, float (&v)[8]
   for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(e[i]);
 }
 
+// Elements o .. o + 7 (o < 8) of the sixteen 16-bit ones in a, b; those from n on 0.
+__device__ __forceinline__ uint4 mx_shift8(const uint4& a, const uint4& b, int o, int n) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (o & 4) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (o & 2) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (o & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n < 2 * i + 2) w[i] &= 0xffffu;
+    if (n < 2 * i + 1) w[i] = 0u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Eight elements of a 16-bit type from an address that is a multiple of 2 alone:
 // the two aligned 16-byte pieces that hold them, shifted together (one load of
 // eight would take eight instructions). lo, hi: the matrix; a piece that reaches
@@ -401,25 +425,31 @@ __device__ __forceinline__ uint4 mx_load8_any(const T* p, int n, const T* lo, co
   const int o = (int)(((uintptr_t)p & 15) >> 1);
   const uint4 a = mx_aligned_piece(at, lo, hi);
   const uint4 b = o + n > 8 ? mx_aligned_piece(at + 16, lo, hi) : make_uint4(0u, 0u, 0u, 0u);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (o & 4) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  return mx_shift8(a, b, o, n);
+}
+
+// One of the aligned 16-byte pieces that cover n elements from `first` on, piece q
+// of them, to shared memory (cp.async; only bytes of those elements and of the ones
+// before them in the matrix are read, nothing before lo).
+template <typename T>
+__device__ __forceinline__ void mx_fetch_window(uint4* dst, const T* first, int n, int q,
+                                                const T* lo) {
+  const uintptr_t at = ((uintptr_t)first & ~(uintptr_t)15) + (uintptr_t)q * 16;
+  const int64_t left = (int64_t)((uintptr_t)(first + n) - at);
+  if (n <= 0 || left <= 0) return;
+  if (at >= (uintptr_t)lo) {
+    cp_async16(dst, reinterpret_cast<const void*>(at), left < 16 ? (uint32_t)left : 16u);
+  } else {
+    *dst = mx_aligned_piece(at, lo, first + n);
   }
-  if (o & 2) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  if (o & 1) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n < 2 * i + 2) w[i] &= 0xffffu;
-    if (n < 2 * i + 1) w[i] = 0u;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Elements 8 c .. of a row fetched so (piece 0 at `window`), n of them.
+template <typename T>
+__device__ __forceinline__ uint4 mx_from_window(const uint4* window, const T* first, int c, int n) {
+  if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  const int o = (int)(((uintptr_t)first & 15) >> 1);
+  return mx_shift8(window[c], window[c + (o + n > 8 ? 1 : 0)], o, n);
 }
 
 // A warp's consecutive pieces of 8 elements to a row of any alignment, 32

@@ -39,8 +39,11 @@ struct QuantParams {
 // group sit together). A block of 256 threads takes the rows 32 q + l of one
 // scale tile for l in a range of TY / 4: the 16 bytes of scales of each l are
 // then written together. Rows past the end only write their zero scales.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams p, int log_tx) {
+// VEC: x and the values have their rows on 16-byte boundaries.
+template <typename T, int FMT, bool VEC>
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 3 : 4)
+mx_quantize_rows_kernel(QuantParams p, int log_tx) {
+  __shared__ T vbuf[VEC ? 1 : kQThreads / 32][32 * 17];  // a warp's values
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -65,16 +68,12 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
       const int m = row[h] < p.rows ? n : 0;
       const T* x = reinterpret_cast<const T*>(p.x);
       const T* src = x + row[h] * p.ldx + chunk * 16;
-      if constexpr (sizeof(T) == 2) {
-        if (p.x_vec && m == 16) {
-          raw[h] = mx_load_raw16(src, true, m);
-        } else {
-          const T* end = x + (p.rows - 1) * p.ldx + p.k;
-          raw[h].q[0] = mx_load8_any(src, m < 8 ? m : 8, x, end);
-          raw[h].q[1] = mx_load8_any(src + 8, m - 8, x, end);
-        }
+      if constexpr (!VEC && sizeof(T) == 2) {
+        const T* end = x + (p.rows - 1) * p.ldx + p.k;
+        raw[h].q[0] = mx_load8_any(src, m < 8 ? m : 8, x, end);
+        raw[h].q[1] = mx_load8_any(src + 8, m - 8, x, end);
       } else {
-        raw[h] = mx_load_raw16(src, p.x_vec && m == 16, m);
+        raw[h] = mx_load_raw16(src, VEC && m == 16, m);
       }
     }
 #pragma unroll
@@ -90,8 +89,25 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
         mx_store_codes16<FMT>(p.codes + row[h] * p.ldq, chunk, codes);
         if (p.values) {
           mx_values16<FMT>(codes, s, g, v);
-          mx_store16(reinterpret_cast<T*>(p.values) + row[h] * p.ldv + chunk * 16,
-                     p.v_vec && n == 16, n, v);
+          if (VEC || log_tx < 5)
+            mx_store16(reinterpret_cast<T*>(p.values) + row[h] * p.ldv + chunk * 16,
+                       VEC && n == 16, n, v);
+        }
+      }
+      // Values of rows off 16-byte boundaries: a warp's 512 of a row leave 32
+      // neighbours at a time.
+      if (!VEC && p.values && log_tx == 5 && row[h] < p.rows) {
+        const int warp = VEC ? 0 : threadIdx.x >> 5;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) vbuf[warp][lane * 17 + i] = mx_from_f32<T>(v[i]);
+        __syncwarp();
+        const int64_t first = (int64_t)blockIdx.x * 512;
+        T* out = reinterpret_cast<T*>(p.values) + row[h] * p.ldv + first;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = i * 32 + lane;
+          if (first + e < p.k) out[e] = vbuf[warp][(e >> 4) * 17 + (e & 15)];
         }
       }
       constexpr int per = mx_group_chunks(FMT);
@@ -113,18 +129,20 @@ __global__ void __launch_bounds__(kQThreads) mx_quantize_rows_kernel(QuantParams
 // so that what is written along a row of X^T is written together.
 constexpr int kTile = 128;
 
-template <typename T, int FMT, bool ROWS>
+template <typename T, int FMT, bool ROWS, bool WIN>
 __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 1 : 3)
 mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_k) {
   constexpr int W = sizeof(T) / 2;             // 32-bit words of a column pair
   constexpr int LINE = kTile * sizeof(T) / 4;  // words of a line
-  extern __shared__ __align__(16) uint32_t smem[];  // two tiles of kTile x LINE
+  // Two tiles of kTile x LINE words; WIN (16-bit lines off 16-byte boundaries): one,
+  // and the aligned pieces that cover the next tile's lines.
+  static_assert(!WIN || sizeof(T) == 2, "windows of 16-bit elements");
+  extern __shared__ __align__(16) uint32_t smem[];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const T* x = reinterpret_cast<const T*>(p.x);
   const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
-  const T* end = x + (p.k - 1) * p.ldx + p.rows;
   const int piece = threadIdx.x & 15, line0 = threadIdx.x >> 4;
   // Where this thread's piece of a line lies: word w of line l at w ^ 8 W (l / 32);
   // pieces of 4 words stay whole.
@@ -147,9 +165,7 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
           for (int j = 0; j < W; ++j)
             cp_async16(place(tile, line, j), m ? src + j * (16 / (int)sizeof(T)) : x, m ? 16u : 0u);
         } else {
-          MxRaw8<T> raw;
-          if constexpr (sizeof(T) == 2) raw.q[0] = mx_load8_any(src, m, x, end);
-          else raw = mx_load_raw8(src, false, m);
+          const MxRaw8<T> raw = mx_load_raw8(src, false, m);
 #pragma unroll
           for (int j = 0; j < W; ++j) *place(tile, line, j) = raw.q[j];
         }
@@ -157,14 +173,45 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
     }
     cp_async_commit();
   };
-  fetch(blockIdx.x, smem);
+  constexpr int PIECES = kTile / 8 + 1;  // of a line's window
+  uint4* window = reinterpret_cast<uint4*>(smem + kTile * LINE);
+  auto fetch_windows = [&](int64_t t) {
+    if (t < tiles) {
+      const int64_t k0 = t % tiles_k * kTile, c0 = t / tiles_k * kTile;
+      const int n = (int)(p.rows - c0 < kTile ? p.rows - c0 : kTile);
+      for (int i = threadIdx.x; i < kTile * PIECES; i += kQThreads) {
+        const int64_t line = k0 + i / PIECES;
+        if constexpr (WIN)
+          if (line < p.k) mx_fetch_window(window + i, x + line * p.ldx + c0, n, i % PIECES, x);
+      }
+    }
+    cp_async_commit();
+  };
+  if constexpr (WIN) fetch_windows(blockIdx.x);
+  else fetch(blockIdx.x, smem);
   int buf = 0;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
-    uint32_t* tile = smem + buf * (kTile * LINE);
+    uint32_t* tile = smem + (WIN ? 0 : buf) * (kTile * LINE);
     const int64_t k0 = t % tiles_k * kTile, c0 = t / tiles_k * kTile;
-    fetch(t + gridDim.x, smem + (buf ^ 1) * (kTile * LINE));
-    cp_async_wait<1>();
-    __syncthreads();
+    if constexpr (WIN) {
+      cp_async_wait<0>();
+      __syncthreads();
+      const int64_t left = p.rows - (c0 + piece * 8);
+      const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int line = i * 16 + line0;
+        *place(tile, line, 0) =
+            mx_from_window(window + line * PIECES, x + (k0 + line) * p.ldx + c0, piece,
+                           k0 + line < p.k ? n : 0);
+      }
+      __syncthreads();
+      fetch_windows(t + gridDim.x);
+    } else {
+      fetch(t + gridDim.x, smem + (buf ^ 1) * (kTile * LINE));
+      cp_async_wait<1>();
+      __syncthreads();
+    }
     if constexpr (ROWS) {
       // Chunks of 16 elements, 8 lanes a line.
       const int64_t c = c0 + (threadIdx.x & 7) * 16;
@@ -200,6 +247,12 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
 #pragma unroll
       for (int j = 0; j < W; ++j)
         w[i][j] = tile[(kb * 32 + i) * LINE + ((pair * W + j) ^ (kb * 8 * W))];
+    // The values leave by rows of X^T, through the tile (its pieces of 16 bytes
+    // XORed for the lanes of a column pair to write different banks).
+    auto value_piece = [&](int col, int q) {
+      return reinterpret_cast<uint4*>(tile + col * LINE) + (q ^ ((q >> 3) & 1) ^ (((col >> 1) & 1) << 1));
+    };
+    if (p.values) __syncthreads();  // every thread has its words
     // Largest magnitudes of the two columns' 16-line halves.
     uint32_t top[2][2];
 #pragma unroll
@@ -241,10 +294,13 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
           mx_store_codes16<FMT>(p.codes + row * p.ldq, kfirst / 16 + b, codes);
           if (p.values) {
             mx_values16<FMT>(codes, s, g, v);
-            const int64_t left = p.k - (kfirst + b * 16);
-            const int n = left >= 16 ? 16 : (left > 0 ? (int)left : 0);
-            mx_store16(reinterpret_cast<T*>(p.values) + row * p.ldv + kfirst + b * 16,
-                       p.v_vec && n == 16, n, v);
+            MxRaw16<T> o;
+            T* e = reinterpret_cast<T*>(o.q);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) e[i] = mx_from_f32<T>(v[i]);
+#pragma unroll
+            for (int j = 0; j < 2 * W; ++j)
+              *value_piece(pair * 2 + h, (kb * 2 + b) * 2 * W + j) = o.q[j];
           }
         }
       }
@@ -263,6 +319,37 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
           *reinterpret_cast<uint32_t*>(p.scales + mx_scale_word(row, (int)(k0 / 128), groups)) = word;
       }
     }
+    if (p.values) {
+      __syncthreads();
+      T* values = reinterpret_cast<T*>(p.values);
+      if (p.v_vec) {
+        constexpr int Q = 16 * W;  // 16-byte pieces of a row
+        for (int i = threadIdx.x; i < kTile * Q; i += kQThreads) {
+          const int col = i / Q, q = i % Q;
+          const int64_t row = c0 + col, k = k0 + q * (16 / (int)sizeof(T));
+          if (row >= p.rows || k >= p.k) continue;
+          const uint4 u = *value_piece(col, q);
+          T* out = values + row * p.ldv + k;
+          if (k + 16 / (int)sizeof(T) <= p.k) {
+            *reinterpret_cast<uint4*>(out) = u;
+          } else {
+            const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+            for (int j = 0; j < 16 / (int)sizeof(T); ++j)
+              if (k + j < p.k) out[j] = e[j];
+          }
+        }
+      } else {
+        constexpr int PER = 16 / (int)sizeof(T);
+        for (int i = threadIdx.x; i < kTile * kTile; i += kQThreads) {
+          const int col = i / kTile, l = i % kTile;
+          const int64_t row = c0 + col;
+          if (row < p.rows && k0 + l < p.k)
+            values[row * p.ldv + k0 + l] =
+                reinterpret_cast<const T*>(value_piece(col, l / PER))[l % PER];
+        }
+      }
+    }
     __syncthreads();  // the tile is free for the one after the next
   }
 }
@@ -272,19 +359,25 @@ template <typename T, int FMT>
 cudaError_t launch_tile(const QuantParams& p, const QuantParams* rp, cudaStream_t stream) {
   const int64_t tiles_k = (p.k + kTile - 1) / kTile;
   const int64_t tiles = (p.rows + kTile - 1) / kTile * tiles_k;
-  const size_t smem = 2 * kTile * kTile * sizeof(T);
   const int64_t most = (int64_t)skg_device_sm_count() * (sizeof(T) == 4 ? 1 : 3);
   if (most <= 0) return cudaErrorNoDevice;
   const dim3 grid((unsigned)(tiles < most ? tiles : most));
-  static std::atomic<uint64_t> d0{0}, d1{0};
-  const void* kernel = rp ? (const void*)mx_quantize_tile_kernel<T, FMT, true>
-                          : (const void*)mx_quantize_tile_kernel<T, FMT, false>;
-  const cudaError_t e = opt_in_smem(kernel, rp ? d1 : d0, (int)smem);
-  if (e != cudaSuccess) return e;
-  return rp ? launch_pdl(mx_quantize_tile_kernel<T, FMT, true>, grid, dim3(kQThreads), smem, stream,
-                         p, *rp, tiles, (int)tiles_k)
-            : launch_pdl(mx_quantize_tile_kernel<T, FMT, false>, grid, dim3(kQThreads), smem,
-                         stream, p, p, tiles, (int)tiles_k);
+  auto run = [&](auto kernel, std::atomic<uint64_t>& done, size_t smem) {
+    const cudaError_t e = opt_in_smem((const void*)kernel, done, (int)smem);
+    return e != cudaSuccess ? e
+                            : launch_pdl(kernel, grid, dim3(kQThreads), smem, stream, p,
+                                         rp ? *rp : p, tiles, (int)tiles_k);
+  };
+  static std::atomic<uint64_t> d[4] = {};
+  if constexpr (sizeof(T) == 2) {
+    const size_t smem = kTile * kTile * sizeof(T) + kTile * (kTile / 8 + 1) * 16;
+    if (!p.x_vec)
+      return rp ? run(mx_quantize_tile_kernel<T, FMT, true, true>, d[0], smem)
+                : run(mx_quantize_tile_kernel<T, FMT, false, true>, d[1], smem);
+  }
+  const size_t smem = 2 * kTile * kTile * sizeof(T);
+  return rp ? run(mx_quantize_tile_kernel<T, FMT, true, false>, d[2], smem)
+            : run(mx_quantize_tile_kernel<T, FMT, false, false>, d[3], smem);
 }
 
 template <typename T, int FMT>
@@ -296,8 +389,12 @@ cudaError_t launch_rows(const QuantParams& p, cudaStream_t stream) {
   const int64_t gx = (chunks + (1 << log_tx) - 1) >> log_tx;
   int64_t gy = (p.rows + 127) / 128 * 32 / (2 * ls);
   if (gy > 65535) gy = 65535;
-  return launch_pdl(mx_quantize_rows_kernel<T, FMT>, dim3((unsigned)gx, (unsigned)gy),
-                    dim3(kQThreads), 0, stream, p, log_tx);
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  return p.x_vec && (!p.values || p.v_vec)
+             ? launch_pdl(mx_quantize_rows_kernel<T, FMT, true>, grid, dim3(kQThreads), 0, stream, p,
+                          log_tx)
+             : launch_pdl(mx_quantize_rows_kernel<T, FMT, false>, grid, dim3(kQThreads), 0, stream,
+                          p, log_tx);
 }
 
 template <typename T, int FMT>
