@@ -8,6 +8,17 @@
 // accumulators overlap: number 1 starts inside number 0's last columns. The
 // epilogue takes half of a tile, the shared columns in it, to registers first, and
 // with them out the next tile's MMAs run while it writes the tile.
+//
+// What it measured on GB300 (each step at 8192 x 28672 x 8192 in mxfp4): the first
+// form 903 us; one elected thread issuing (the compiler had wrapped every tcgen05
+// instruction behind `lane == 0` in a loop over the lanes, 1540 cycles per stage of
+// nvfp4 against 650) 560 us; TMA stores and a hand-over of the accumulator without a
+// release at cluster scope (1200 cycles a tile) 517 us; 490 us now in short runs, 550
+// in long ones: 7.0 to 7.9 PFLOP/s, 3.6 to 4.1 times the card's bf16 burst rate. In
+// mxfp8 4096 x 8192 x 8192 takes 152 us (3.6 PFLOP/s). The tensor pipe is busy 76 %
+// (4 bits) and 85 % (8 bits) of the time, and the clock falls to 1.65 GHz under the
+// 8-bit load: power bounds the large products (with the loads left out of a copy of
+// the kernel, at the same cycles per stage, the clock stays at 1.9 GHz).
 #include "skg_mx_gemm.cuh"
 
 namespace skg {

@@ -5,6 +5,12 @@
 // With xhat = h rstd and u = w dy:
 //   dx = rstd (u - xhat mean(u xhat)) + dresidual,   dw = sum over rows of dy xhat.
 // The quantised output's rounding counts as the identity in the gradient.
+//
+// Both are bound by memory: 7 bytes per element forward (x and the residual read,
+// their sum and the code written), 8 backward. Measured on GB300, bf16, against
+// 6.69 TB/s of a copy: 8192 x 8192 forward 75 us (6.3 TB/s); 4096 x 8192 backward
+// 48 us (5.6 TB/s: 43 us for dx and the blocks' dw, the rest for the sum of the 152
+// partial dw); one row of 8192 3 us forward. Sums and statistics are fp32.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -67,7 +73,8 @@ __device__ __forceinline__ float row_sum(float v, int log_tpr, float* red) {
   return v;
 }
 
-// 2^log_tpr threads share a row, V chunks of 16 elements each, h in registers
+// Rows that the kernel below does not take (narrow ones on 16-byte boundaries,
+// several to a block; more than 8192 elements): 2^log_tpr threads share a row, V chunks of 16 elements each, h in registers
 // between the sum and the quantisation; V = 0: any width, h formed twice.
 template <typename T, int FMT, int V>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams p, int log_tpr) {

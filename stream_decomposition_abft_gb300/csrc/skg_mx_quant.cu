@@ -2,8 +2,13 @@
 // its columns (the transposed operand of a gradient), with the values that
 // the codes stand for on request.
 //
-// Every element is read once and every code, scale and value is written once;
-// the kernels are bound by memory.
+// Every element is read once and every code, scale and value is written once, so
+// memory bounds the kernels, with the instructions of the conversion close behind
+// (an issue slot is taken in 2 of 3 cycles). Measured on GB300, bf16, against
+// 6.69 TB/s of a copy: 8192 x 8192 to mxfp4 with its values 46 us (6.5 TB/s), to
+// mxfp8 along the rows 35 us (5.8), along the columns 33 us (6.1), to nvfp4 with its
+// values 50 us (6.2); 4096 x 8192 to mxfp8 both ways in one pass 27 us (5.0; the two
+// passes take 34).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
