@@ -681,11 +681,12 @@ cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaS
   } else if (g.v == 2) {
     e = launch_pdl(rmsnorm_grad_long_kernel<T, 2>, grid, block, 0, stream, p);
   } else {
-    e = launch_pdl(rmsnorm_grad_long_kernel<T, 0>, grid, block, 0, stream, p);
-    if (e != cudaSuccess) return e;
+    // dw first: dx may take dy's place.
     e = launch_pdl(rmsnorm_grad_columns_kernel<T>,
                    dim3((unsigned)((p.cols + 255) / 256), (unsigned)g.blocks), dim3(256), 0,
                    stream, p, g.blocks);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(rmsnorm_grad_long_kernel<T, 0>, grid, block, 0, stream, p);
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(rmsnorm_grad_reduce_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(1024), 0,

@@ -274,6 +274,27 @@ def test_rmsnorm_backward(dtype, rows, cols):
         assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("cols", [48, 333, 1111, 8192, 12000, 40000])
+@pytest.mark.parametrize("place", ["dy", "dresidual"])
+def test_rmsnorm_backward_in_place(cols, place):
+    # dX may take the place of dY or of the residual path's gradient.
+    rows = 700 if cols < 2000 else 5
+    h, dy, dr = (draw(rows, cols, "bf16", cols + i, 0.5).cuda() for i in range(3))
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    rstd = torch.rsqrt(h.float().square().mean(1) + 1e-5)
+    want = mx.rmsnorm_backward(dy, h, w, rstd, dresidual=dr)
+    out = {"dy": dy, "dresidual": dr}[place]
+    dw = torch.empty(cols, device="cuda")
+    n = skgemm.workspace_size_rmsnorm_backward(rows, cols)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    st = skgemm.rmsnorm_backward(rows, cols, dy.data_ptr(), cols, h.data_ptr(), cols, w.data_ptr(),
+                                 rstd.data_ptr(), dr.data_ptr(), cols, skgemm.IN_BF16,
+                                 out.data_ptr(), cols, dw.data_ptr(), ws.data_ptr(), n,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert st == skgemm.OK
+    assert torch.equal(out, want[0]) and torch.equal(dw, want[1])
+
+
 def test_rmsnorm_backward_against_differences():
     # Central differences of the 64-bit forward formula, through the kernel's
     # stored rstd; inputs are exact in fp16, so the formula's gradient is what
@@ -377,6 +398,18 @@ def test_product_alpha_beta_strides(fmt, dtype, pad, offset):
     assert bool((buf[:, keep] == 9.0).all())
     # beta = 0 does not read C.
     out.fill_(float("nan"))
+    mx.matmul(a, b, out=out)
+    check_product(out, av, bv, k)
+
+
+@pytest.mark.parametrize("m", [9, 200, 520])
+def test_product_large_offset(m):
+    # Rows of C whose element offsets pass 2^31, in each of the kernels.
+    n, k, ldc = 300, 160, (1 << 31) // (m - 1) // 8 * 8 + 64
+    a, av = operand(m, k, "mxfp8", 1)
+    b, bv = operand(n, k, "mxfp8", 2)
+    buf = torch.empty(m * ldc, dtype=torch.bfloat16, device="cuda")
+    out = buf.view(m, ldc)[:, :n]
     mx.matmul(a, b, out=out)
     check_product(out, av, bv, k)
 
