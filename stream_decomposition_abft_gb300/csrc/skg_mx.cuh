@@ -381,25 +381,31 @@ __device__ __forceinline__ void mx_unpack_raw8(const MxRaw8<T>& r, float (&v)[8]
 
 // Elements o .. o + 7 (o < 8) of the sixteen 16-bit ones in a, b; those from n on 0.
 __device__ __forceinline__ uint4 mx_shift8(const uint4& a, const uint4& b, int o, int n) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
   if (o & 4) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    w[0] = w[2];
+    w[1] = w[3];
+    w[2] = w[4];
+    w[3] = w[5];
+    w[4] = w[6];
+    w[5] = b.w;
   }
   if (o & 2) {
 #pragma unroll
     for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
   }
-  if (o & 1) {
+  const uint32_t odd = (o & 1) * 16;
+  uint4 q = make_uint4(__funnelshift_r(w[0], w[1], odd), __funnelshift_r(w[1], w[2], odd),
+                       __funnelshift_r(w[2], w[3], odd), __funnelshift_r(w[3], w[4], odd));
+  if (n < 8) {
+    uint32_t* e = reinterpret_cast<uint32_t*>(&q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    for (int i = 0; i < 4; ++i) {
+      if (n < 2 * i + 2) e[i] &= 0xffffu;
+      if (n < 2 * i + 1) e[i] = 0u;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n < 2 * i + 2) w[i] &= 0xffffu;
-    if (n < 2 * i + 1) w[i] = 0u;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return q;
 }
 
 // Eight elements of a 16-bit type from an address that is a multiple of 2 alone:
@@ -428,29 +434,35 @@ __device__ __forceinline__ uint4 mx_load8_any(const T* p, int n, const T* lo, co
   return mx_shift8(a, b, o, n);
 }
 
-// One of the aligned 16-byte pieces that cover n elements from `first` on, piece q
-// of them, to shared memory (cp.async; only bytes of those elements and of the ones
-// before them in the matrix are read, nothing before lo).
+// A row of 16-bit elements at any address, by the aligned 16-byte pieces that cover
+// it: piece c holds elements 8 c - o .. of the row. Only bytes of the row and of the
+// elements before it in the matrix are read, nothing before lo, the matrix's start.
 template <typename T>
-__device__ __forceinline__ void mx_fetch_window(uint4* dst, const T* first, int n, int q,
-                                                const T* lo) {
-  const uintptr_t at = ((uintptr_t)first & ~(uintptr_t)15) + (uintptr_t)q * 16;
-  const int64_t left = (int64_t)((uintptr_t)(first + n) - at);
-  if (n <= 0 || left <= 0) return;
-  if (at >= (uintptr_t)lo) {
-    cp_async16(dst, reinterpret_cast<const void*>(at), left < 16 ? (uint32_t)left : 16u);
-  } else {
-    *dst = mx_aligned_piece(at, lo, first + n);
+struct MxRow {
+  const uint8_t* base;
+  const T* lo;
+  int o, bytes;  // from base to the row's end
+  __device__ __forceinline__ MxRow(const T* row, int n, const T* matrix)
+      : base(reinterpret_cast<const uint8_t*>((uintptr_t)row & ~(uintptr_t)15)),
+        lo(matrix),
+        o((int)(((uintptr_t)row & 15) >> 1)),
+        bytes(2 * ((int)(((uintptr_t)row & 15) >> 1) + n)) {}
+  // Piece c to shared memory (cp.async).
+  __device__ __forceinline__ void fetch(uint4* dst, int c) const {
+    const int left = bytes - 16 * c;
+    if (left <= 0) return;
+    const uint8_t* at = base + 16 * (int64_t)c;
+    if (c > 0 || at >= reinterpret_cast<const uint8_t*>(lo))
+      cp_async16(dst, at, left < 16 ? (uint32_t)left : 16u);
+    else
+      *dst = mx_aligned_piece((uintptr_t)at, lo, reinterpret_cast<const T*>(base + bytes));
   }
-}
-
-// Elements 8 c .. of a row fetched so (piece 0 at `window`), n of them.
-template <typename T>
-__device__ __forceinline__ uint4 mx_from_window(const uint4* window, const T* first, int c, int n) {
-  if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
-  const int o = (int)(((uintptr_t)first & 15) >> 1);
-  return mx_shift8(window[c], window[c + (o + n > 8 ? 1 : 0)], o, n);
-}
+  // Eight elements from 8 c on, n of them in the row, of pieces c and c + 1.
+  __device__ __forceinline__ uint4 elements(const uint4* first, const uint4* second, int n) const {
+    if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
+    return mx_shift8(*first, *second, o, n);
+  }
+};
 
 // A warp's consecutive pieces of 8 elements to a row of any alignment, 32
 // neighbouring elements an instruction (a lane's own eight would touch a sector

@@ -193,20 +193,26 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
   griddep_launch_dependents();
   const float g = FMT == SKG_NVFP4 && p.g ? *p.g : 1.f;
   auto count = [&](int c) { return c + 8 <= p.cols ? 8 : (c < p.cols ? p.cols - c : 0); };
+  // Off 16-byte boundaries a thread holds the two aligned pieces around its own.
+  constexpr int HELD = VEC ? 1 : 2;
   auto fetch = [&](int64_t row, int st) {
     if (row < p.rows) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int c = (t + j * nt) * 8, n = count(c);
-        uint4* dst = ring + ((st * 2) * V + j) * nt + t;
+        uint4* dst = ring + ((st * 2) * V * HELD + j) * nt + t;
         if constexpr (VEC) {
           cp_async16(dst, x + row * p.ldx + (n ? c : 0), n ? 16u : 0u);
           if (p.res) cp_async16(dst + V * nt, res + row * p.ldr + (n ? c : 0), n ? 16u : 0u);
         } else {
-          *dst = mx_load8_any(x + row * p.ldx + c, n, x, x + (p.rows - 1) * p.ldx + p.cols);
-          if (p.res)
-            dst[V * nt] =
-                mx_load8_any(res + row * p.ldr + c, n, res, res + (p.rows - 1) * p.ldr + p.cols);
+          const MxRow<T> rx(x + row * p.ldx, p.cols, x);
+          rx.fetch(dst, t + j * nt);
+          rx.fetch(dst + V * nt, t + j * nt + 1);
+          if (p.res) {
+            const MxRow<T> rr(res + row * p.ldr, p.cols, res);
+            rr.fetch(dst + V * HELD * nt, t + j * nt);
+            rr.fetch(dst + V * (HELD + 1) * nt, t + j * nt + 1);
+          }
         }
       }
     }
@@ -230,11 +236,17 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const uint4* src = ring + ((st * 2) * V + j) * nt + t;
-        mx_unpack8<T>(src[0], h[j]);
+        const int c = (t + j * nt) * 8, n = count(c);
+        const uint4* src = ring + ((st * 2) * V * HELD + j) * nt + t;
+        mx_unpack8<T>(VEC ? src[0]
+                          : MxRow<T>(x + row * p.ldx, p.cols, x).elements(src, src + V * nt, n),
+                      h[j]);
         if (p.res) {
           float r[8];
-          mx_unpack8<T>(src[V * nt], r);
+          mx_unpack8<T>(VEC ? src[V * nt]
+                            : MxRow<T>(res + row * p.ldr, p.cols, res)
+                                  .elements(src + V * HELD * nt, src + V * (HELD + 1) * nt, n),
+                        r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) h[j][i] += r[i];
         }
@@ -280,15 +292,15 @@ __global__ void __launch_bounds__(kNormMaxThreads, 2) rmsnorm_mx_wide_kernel(Nor
 template <typename T, int FMT>
 cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, bool vec, int sms,
                              cudaStream_t stream) {
-  const size_t smem = (size_t)kNormStages * 2 * v * threads * 16;
+  const size_t smem = (size_t)kNormStages * 2 * v * threads * 16 * (vec ? 1 : 2);
   const int64_t rows = (p.rows + 127) / 128 * 128;
   // 1024 threads per SM: two blocks of 512, four of 256 (4096 x 2048: 15 us with
   // two of 256).
   const int64_t most = (int64_t)sms * (1024 / threads < 8 ? 1024 / threads : 8);
   const dim3 grid((unsigned)(rows < most ? rows : most));
   auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
-    const cudaError_t e = opt_in_smem((const void*)kernel, done, kNormStages * 2 * kNormMaxThreads *
-                                                                     16 * 2);
+    const cudaError_t e = opt_in_smem((const void*)kernel, done,
+                                      kNormStages * 2 * 2 * kNormMaxThreads * 16 * (vec ? 1 : 2));
     return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(threads), smem, stream, p);
   };
   static std::atomic<uint64_t> d[4] = {};
@@ -468,6 +480,14 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
                     reinterpret_cast<const T*>(p.dres)};
   const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
   auto count = [&](int c) { return c + 8 <= p.cols ? 8 : (c < p.cols ? p.cols - c : 0); };
+  // Pieces of a thread's eight elements in the ring: off 16-byte boundaries the two
+  // aligned ones that hold them (V = 2: no room, shifted on the way).
+  constexpr int HELD = VEC || V == 2 ? 1 : 2;
+  auto piece = [&](int k, int64_t row, int st, int j) -> uint4 {
+    const uint4* src = ring + ((st * 3 + k) * V * HELD + j) * nt + t;
+    if constexpr (HELD == 1) return src[0];
+    else return MxRow<T>(in[k] + row * ld[k], p.cols, in[k]).elements(src, src + nt, count(t * 8));
+  };
   griddep_wait();
   griddep_launch_dependents();
   auto fetch = [&](int64_t row, int st) {
@@ -478,10 +498,14 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int c = (t + j * nt) * 8;
-          uint4* dst = ring + ((st * 3 + k) * V + j) * nt + t;
+          uint4* dst = ring + ((st * 3 + k) * V * HELD + j) * nt + t;
           const int n = count(c);
           if constexpr (VEC) cp_async16(dst, in[k] + row * ld[k] + (n ? c : 0), n ? 16u : 0u);
-          else *dst = mx_load8_any(in[k] + row * ld[k] + c, n, in[k],
+          else if constexpr (HELD == 2) {
+            const MxRow<T> r(in[k] + row * ld[k], p.cols, in[k]);
+            r.fetch(dst, t);
+            r.fetch(dst + nt, t + 1);
+          } else *dst = mx_load8_any(in[k] + row * ld[k] + c, n, in[k],
                                    in[k] + (p.rows - 1) * ld[k] + p.cols);
         }
       }
@@ -521,10 +545,10 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
       if (row + (int64_t)q * gridDim.x >= p.rows) break;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const uint4* src = ring + ((st + q) * 3 * V + j) * nt + t;
+        const int64_t r = row + (int64_t)q * gridDim.x;
         float dy[8], h[8], w[8];
-        mx_unpack8<T>(src[0], dy);
-        mx_unpack8<T>(src[V * nt], h);
+        mx_unpack8<T>(piece(0, r, st + q, j), dy);
+        mx_unpack8<T>(piece(1, r, st + q, j), h);
         mx_unpack8<T>(wv[j], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -557,13 +581,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int c = (t + j * nt) * 8;
-          const uint4* src = ring + ((st + q) * 3 * V + j) * nt + t;
           float dy[8], h[8], w[8], o[8];
-          mx_unpack8<T>(src[0], dy);
-          mx_unpack8<T>(src[V * nt], h);
+          mx_unpack8<T>(piece(0, r, st + q, j), dy);
+          mx_unpack8<T>(piece(1, r, st + q, j), h);
           mx_unpack8<T>(wv[j], w);
           if (p.dres) {
-            mx_unpack8<T>(src[2 * V * nt], o);
+            mx_unpack8<T>(piece(2, r, st + q, j), o);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = 0.f;
@@ -665,7 +688,7 @@ cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaS
   const dim3 grid(g.blocks), wide(g.threads), block(kNormMaxThreads);
   const bool vec = p.vec && p.cols % 8 == 0;
   if (g.threads) {
-    const size_t smem = (size_t)kGradStages * 3 * g.v * g.threads * 16;
+    const size_t smem = (size_t)kGradStages * 3 * (vec ? g.v : 2) * g.threads * 16;
     auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
       const cudaError_t r = opt_in_smem((const void*)kernel, done,
                                         kGradStages * 3 * 2 * kNormMaxThreads * 16);

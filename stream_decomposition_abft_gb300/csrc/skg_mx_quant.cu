@@ -187,7 +187,7 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
       for (int i = threadIdx.x; i < kTile * PIECES; i += kQThreads) {
         const int64_t line = k0 + i / PIECES;
         if constexpr (WIN)
-          if (line < p.k) mx_fetch_window(window + i, x + line * p.ldx + c0, n, i % PIECES, x);
+          if (line < p.k) MxRow<T>(x + line * p.ldx + c0, n, x).fetch(window + i, i % PIECES);
       }
     }
     cp_async_commit();
@@ -206,9 +206,9 @@ mx_quantize_tile_kernel(QuantParams p, QuantParams rp, int64_t tiles, int tiles_
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int line = i * 16 + line0;
-        *place(tile, line, 0) =
-            mx_from_window(window + line * PIECES, x + (k0 + line) * p.ldx + c0, piece,
-                           k0 + line < p.k ? n : 0);
+        const uint4* src = window + line * PIECES + piece;
+        *place(tile, line, 0) = MxRow<T>(x + (k0 + line) * p.ldx + c0, n, x)
+                                    .elements(src, src + 1, k0 + line < p.k ? n : 0);
       }
       __syncthreads();
       fetch_windows(t + gridDim.x);
