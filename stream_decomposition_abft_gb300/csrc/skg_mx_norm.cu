@@ -481,12 +481,16 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
   const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
   auto count = [&](int c) { return c + 8 <= p.cols ? 8 : (c < p.cols ? p.cols - c : 0); };
   // Pieces of a thread's eight elements in the ring: off 16-byte boundaries the two
-  // aligned ones that hold them (V = 2: no room, shifted on the way).
-  constexpr int HELD = VEC || V == 2 ? 1 : 2;
+  // aligned ones that hold them, or (V = 2: no room) one of its own and the next
+  // thread's.
+  constexpr bool SHARE = !VEC && V == 2;
+  constexpr int HELD = VEC || SHARE ? 1 : 2;
+  const int slot = V * HELD * nt + (SHARE ? 1 : 0);
   auto piece = [&](int k, int64_t row, int st, int j) -> uint4 {
-    const uint4* src = ring + ((st * 3 + k) * V * HELD + j) * nt + t;
-    if constexpr (HELD == 1) return src[0];
-    else return MxRow<T>(in[k] + row * ld[k], p.cols, in[k]).elements(src, src + nt, count(t * 8));
+    const uint4* src = ring + (st * 3 + k) * slot + j * nt + t;
+    if constexpr (VEC) return src[0];
+    else return MxRow<T>(in[k] + row * ld[k], p.cols, in[k])
+        .elements(src, src + (SHARE ? 1 : nt), count((t + j * nt) * 8));
   };
   griddep_wait();
   griddep_launch_dependents();
@@ -498,15 +502,16 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int c = (t + j * nt) * 8;
-          uint4* dst = ring + ((st * 3 + k) * V * HELD + j) * nt + t;
+          uint4* dst = ring + (st * 3 + k) * slot + j * nt + t;
           const int n = count(c);
-          if constexpr (VEC) cp_async16(dst, in[k] + row * ld[k] + (n ? c : 0), n ? 16u : 0u);
-          else if constexpr (HELD == 2) {
+          if constexpr (VEC) {
+            cp_async16(dst, in[k] + row * ld[k] + (n ? c : 0), n ? 16u : 0u);
+          } else {
             const MxRow<T> r(in[k] + row * ld[k], p.cols, in[k]);
-            r.fetch(dst, t);
-            r.fetch(dst + nt, t + 1);
-          } else *dst = mx_load8_any(in[k] + row * ld[k] + c, n, in[k],
-                                   in[k] + (p.rows - 1) * ld[k] + p.cols);
+            r.fetch(dst, t + j * nt);
+            if (!SHARE) r.fetch(dst + nt, t + 1);
+            else if (j == 0 && t == 0) r.fetch(dst + V * nt, V * nt);
+          }
         }
       }
     }
@@ -540,6 +545,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
       next[q] = r < p.rows ? p.rstd[r] : 0.f;
     }
     cp_async_wait<kGradStages - 2>();
+    if constexpr (SHARE) __syncthreads();
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (row + (int64_t)q * gridDim.x >= p.rows) break;
@@ -603,7 +609,12 @@ __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(G
           }
         }
       }
-      fetch(r + (int64_t)kGradStages * gridDim.x, st + q);
+      if constexpr (!SHARE) fetch(r + (int64_t)kGradStages * gridDim.x, st + q);
+    }
+    if constexpr (SHARE) {
+      __syncthreads();  // the threads before have read their second pieces
+      fetch(row + (int64_t)kGradStages * gridDim.x, st);
+      fetch(row + (int64_t)(kGradStages + 1) * gridDim.x, st + 1);
     }
     st ^= 2;
   }
@@ -688,10 +699,12 @@ cudaError_t launch_grad(const GradParams& p, const GradPlan& g, float* dw, cudaS
   const dim3 grid(g.blocks), wide(g.threads), block(kNormMaxThreads);
   const bool vec = p.vec && p.cols % 8 == 0;
   if (g.threads) {
-    const size_t smem = (size_t)kGradStages * 3 * (vec ? g.v : 2) * g.threads * 16;
+    // Off 16-byte boundaries two pieces a thread, or one and one more per row.
+    const int pieces = vec ? g.v * g.threads : 2 * g.threads + (g.v == 2 ? 1 : 0);
+    const size_t smem = (size_t)kGradStages * 3 * pieces * 16;
     auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
       const cudaError_t r = opt_in_smem((const void*)kernel, done,
-                                        kGradStages * 3 * 2 * kNormMaxThreads * 16);
+                                        kGradStages * 3 * (2 * kNormMaxThreads + 1) * 16);
       return r != cudaSuccess ? r : launch_pdl(kernel, grid, wide, smem, stream, p);
     };
     static std::atomic<uint64_t> d[4] = {};

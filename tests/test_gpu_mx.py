@@ -274,6 +274,29 @@ def test_rmsnorm_backward(dtype, rows, cols):
         assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("cols", [97, 1030, 4095, 5001, 8191, 8192])
+@pytest.mark.parametrize("pad,offset", [(1, 0), (3, 1), (8, 7), (13, 4)])
+def test_rmsnorm_rows_off_boundaries(cols, pad, offset):
+    # Rows that start at every distance from a 16-byte boundary, forward and backward:
+    # the same bits as from contiguous, aligned copies padded to the same width.
+    rows = 330
+    x, r, dy = (strided(draw(rows, cols, "f16", cols + i, 0.5), pad, offset) for i in range(3))
+    w = strided(draw(1, cols, "f16", 9, 0.2), 1, 1)[0]
+    q, h, rstd = mx.rmsnorm(x, w, 1e-5, residual=r)
+    q2, h2, rstd2 = mx.rmsnorm(x.contiguous(), w.clone(), 1e-5, residual=r.contiguous())
+    assert torch.equal(h, h2) and torch.equal(rstd, rstd2)
+    assert torch.equal(q.codes, q2.codes) and torch.equal(q.scales, q2.scales)
+    check_norm(x[:40], w, r[:40], "mxfp8", 1e-5)
+    dx, dw = mx.rmsnorm_backward(dy, x, w, rstd, dresidual=r)
+    a, b, ww = np64(dy), np64(x), np64(w)
+    want, want_w = mr.rmsnorm_backward(a, b, ww, np64(rstd), np64(r))
+    xhat, u = np.abs(b * np64(rstd)[:, None]), np.abs(a * ww)
+    mag = np64(rstd)[:, None] * (u + xhat * (u * xhat).mean(1, keepdims=True)) + np.abs(np64(r))
+    assert np.all(np.abs(np64(dx) - want) <=
+                  200 * U * mag + 2.0 ** -11 * np.abs(want) + 2.0 ** -25)
+    assert np.all(np.abs(np64(dw) - want_w) <= (rows + 8) * U * (np.abs(a) * xhat).sum(0) * 2)
+
+
 @pytest.mark.parametrize("cols", [48, 333, 1111, 8192, 12000, 40000])
 @pytest.mark.parametrize("place", ["dy", "dresidual"])
 def test_rmsnorm_backward_in_place(cols, place):
