@@ -60,8 +60,8 @@ def _binding_job(force: bool):
            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", cuda,
            "-I", sysconfig.get_paths()["include"], "-c", src, "-o", obj]
     lib = os.path.join(torch_dir, "lib")
-    link = ["g++", "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
-            "-ltorch_python", "-L", PKG, "-l:libskgemm.so", "-Wl,-rpath,$ORIGIN",
+    link = ["g++", "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch", "-ltorch_python", "-L", PKG, "-l:libskgemm.so", "-Wl,-rpath,$ORIGIN",
             f"-Wl,-rpath,{lib}"]
     return (cmd if force or not fresh else None), link
 

@@ -302,9 +302,6 @@ SinglePlan single_plan(int64_t m, int64_t n, int ksteps, int sms) {
 // estimate (512 x 512 x 8192 in nvfp4: 12.4 us paired, 7.0 single; 2048 x 2048 x
 // 2048: 6.9 paired, 8.9 single).
 bool wants_pairs(int64_t m, int64_t n, int ksteps, int clusters, double single_us) {
-#ifdef SKG_MX_PAIR
-  return SKG_MX_PAIR != 0;
-#endif
   if (m <= kMxTile) return false;
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
   return 4.4 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;

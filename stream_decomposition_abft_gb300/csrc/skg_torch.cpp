@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -108,14 +109,18 @@ void* stream_of(c10::Device d) {
   return (void*)c10::cuda::getCurrentCUDAStream(d.index()).stream();
 }
 
+// An uninitialised contiguous CUDA tensor, past the dispatcher.
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device d) {
+  return at::detail::empty_cuda(sizes, type, d, std::nullopt);
+}
+
 struct Quantized {
   at::Tensor codes, scales;
   int64_t ldq;
   Quantized(int64_t rows, int64_t k, int fmt, c10::Device d)
       : ldq(skg_mx_codes_ld(k, fmt)) {
-    const auto u8 = at::TensorOptions().dtype(at::kByte).device(d);
-    codes = at::empty({rows, ldq}, u8);
-    scales = at::empty({(int64_t)skg_mx_scales_size(rows, k, fmt)}, u8);
+    codes = empty({rows, ldq}, at::kByte, d);
+    scales = empty({(int64_t)skg_mx_scales_size(rows, k, fmt)}, at::kByte, d);
   }
 };
 
@@ -148,7 +153,7 @@ PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   const int64_t rows = x.size(tr ? 1 : 0), k = x.size(tr ? 0 : 1);
   Quantized q(rows, k, fmt, x.device());
   at::Tensor v;
-  if (values) v = at::empty({rows, k}, x.options());
+  if (values) v = empty({rows, k}, x.scalar_type(), x.device());
   const int st = skg_mx_quantize(rows, k, x.data_ptr(), ldx, type, tr ? 1 : 0, fmt, g,
                                  q.codes.data_ptr(), q.ldq, q.scales.data_ptr(),
                                  values ? v.data_ptr() : nullptr, k, stream_of(x.device()));
@@ -194,10 +199,10 @@ PyObject* rmsnorm(PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& res = tensor_of("residual", a[3]);
     ldr = matrix_like("residual", res, x);
     r = res.data_ptr();
-    sum = at::empty({rows, cols}, x.options());
+    sum = empty({rows, cols}, x.scalar_type(), d);
   }
   Quantized q(rows, cols, fmt, d);
-  at::Tensor rstd = at::empty({rows}, x.options().dtype(at::kFloat));
+  at::Tensor rstd = empty({rows}, at::kFloat, d);
   const int st = skg_rmsnorm_mx(rows, cols, x.data_ptr(), ldx, r, ldr, w, type, (float)eps,
                                 sum.defined() ? sum.data_ptr() : nullptr, cols,
                                 (float*)rstd.data_ptr(), fmt, g, q.codes.data_ptr(), q.ldq,
@@ -226,9 +231,9 @@ PyObject* rmsnorm_backward(PyObject* const* a, Py_ssize_t n) {
     dr = t.data_ptr();
   }
   const size_t bytes = skg_workspace_size_rmsnorm_backward(rows, cols);
-  at::Tensor dx = at::empty({rows, cols}, dy.options());
-  at::Tensor dw = at::empty({cols}, dy.options().dtype(at::kFloat));
-  at::Tensor ws = at::empty({(int64_t)bytes}, dy.options().dtype(at::kByte));
+  at::Tensor dx = empty({rows, cols}, dy.scalar_type(), d);
+  at::Tensor dw = empty({cols}, at::kFloat, d);
+  at::Tensor ws = empty({(int64_t)bytes}, at::kByte, d);
   const int st = skg_rmsnorm_backward(rows, cols, dy.data_ptr(), ldy, h.data_ptr(), ldh, w,
                                       (const float*)rstd, dr, ldr, type, dx.data_ptr(), cols,
                                       (float*)dw.data_ptr(), ws.data_ptr(), bytes, stream_of(d));
@@ -288,7 +293,7 @@ PyObject* matmul(PyObject* const* v, Py_ssize_t n) {
     if (!THPDtype_Check(v[3])) refuse("out_dtype: a dtype is wanted");
     const at::ScalarType t = reinterpret_cast<THPDtype*>(v[3])->scalar_type;
     type_of("out_dtype", t, true);
-    out = at::empty({a.rows, b.rows}, a.codes->options().dtype(t));
+    out = empty({a.rows, b.rows}, t, d);
   } else {
     out = tensor_of("out", v[2]);
     ldc = matrix("out", out);
