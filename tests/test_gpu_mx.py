@@ -149,6 +149,17 @@ def test_quantize_large_offset(fmt):
     check_quantized(mx.quantize(view, fmt), codes, scales)
 
 
+def test_quantize_many_rows():
+    # More rows than one grid covers: the same bytes as for their last tiles alone.
+    rows, k = 1_100_000, 512
+    x = torch.randn(rows, k, device="cuda", dtype=torch.bfloat16)
+    q = mx.quantize(x, "mxfp8")
+    first = (rows - 1000) // 128 * 128
+    tail = mx.quantize(x[first:], "mxfp8")
+    assert torch.equal(q.codes[first:], tail.codes)
+    assert torch.equal(q.scales[first // 128 * (k // 128) * 512:], tail.scales)
+
+
 # ------------------------------------------------------------------ norm
 def check_norm(x, w, res, fmt, eps, g=None):
     gt = None if g is None else torch.tensor([g], device="cuda")
