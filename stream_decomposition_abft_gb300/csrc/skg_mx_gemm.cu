@@ -73,6 +73,7 @@ __device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* p
   uint32_t base[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) base[s] = cluster_addr(part + lane * 4, (uint32_t)s);
+#pragma unroll 1
   for (int i = warp * R; rank + i * S < rows; i += WARPS * R) {
     float4 u[R][S];
 #pragma unroll
@@ -139,6 +140,13 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
+  auto factor = [&]() {
+    float a = p.alpha;
+    if (p.ga) a *= *p.ga;
+    if (p.gb) a *= *p.gb;
+    return a;
+  };
+  float alpha = 0.f;
   bool fine = true;  // epilogue threads: the accumulator is there
   int issued = 0;    // the loading thread: stages loaded
   if (warp == 0) {
@@ -188,6 +196,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     __syncwarp();
   } else {
+    // What the way out needs is read while the accumulator is on its way.
+    alpha = factor();
+    asm volatile("" ::"l"(p.c), "l"(p.ldc), "f"(alpha), "f"(p.beta), "r"(p.m), "r"(p.n), "r"(p.c_vec));
     fine = mx_wait(&aux->tfull[0], 0, aux);
     if (!fine) mx_fail(p, aux);
     fine = epi_all(fine);
@@ -215,20 +226,22 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     __syncwarp();
   }
-  float alpha = p.alpha;
-  if (p.ga) alpha *= *p.ga;
-  if (p.gb) alpha *= *p.gb;
+  if (warp < 2) alpha = factor();
   const float* part = reinterpret_cast<const float*>(ring);
   if (p.split == 1) {
     // A warp writes the 32 rows that its own lanes stored.
     const int row0 = tm * kMxTile + (warp & 3) * 32, col = tn * kMxTile + lane * 4;
     if (warp >= 2 && fine && col < p.n) {
       const float* src = part + (warp & 3) * 32 * kMxPitch + lane * 4;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i)
-        if (row0 + i < p.m)
-          mx_write4<T>(p, row0 + i, col, *reinterpret_cast<const float4*>(src + i * kMxPitch),
-                       alpha);
+#pragma unroll 1
+      for (int i = 0; i < 32 && row0 + i < p.m; i += 4) {
+        float4 u[4];  // read before the stores, which the compiler would keep them behind
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const float4*>(src + (i + j) * kMxPitch);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (row0 + i + j < p.m) mx_write4<T>(p, row0 + i + j, col, u[j], alpha);
+      }
     }
   } else {
     cluster_sync();
@@ -237,7 +250,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       else if (p.split == 4) mx_reduce_rows<T, 4>(p, part, warp, lane, rank, tm, tn, alpha);
       else mx_reduce_rows<T, 8>(p, part, warp, lane, rank, tm, tn, alpha);
     }
-    cluster_sync();  // no CTA leaves while another reads its partial sums
+    cluster_meet();  // no CTA leaves while another reads its partial sums
   }
   tc_fence_before();
   __syncthreads();

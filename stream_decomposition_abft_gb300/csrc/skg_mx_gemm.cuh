@@ -75,35 +75,58 @@ __device__ __forceinline__ bool mx_wait(uint64_t* bar, uint32_t parity, MxAux* a
   }
 }
 
-// Four consecutive elements of a row of C.
+// Four consecutive elements of a row of C: aligned together and beta = 0, or
+// (mx_write4_any, out of the way of the instruction cache: a launch runs each line of
+// this once) whatever they are.
 template <typename T>
-__device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, float4 v,
-                                          float alpha) {
-  T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
+__device__ __forceinline__ void mx_write4_plain(T* c, const float4& v, float alpha) {
+  union {
+    T e[4];
+    uint4 q;
+    uint2 d;
+  } u;
+  u.e[0] = mx_from_f32<T>(alpha * v.x);
+  u.e[1] = mx_from_f32<T>(alpha * v.y);
+  u.e[2] = mx_from_f32<T>(alpha * v.z);
+  u.e[3] = mx_from_f32<T>(alpha * v.w);
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(c) = u.q;
+  else *reinterpret_cast<uint2*>(c) = u.d;
+}
+
+template <typename T>
+__device__ __noinline__ void mx_write4_any(T* c, float4 v, float alpha, float beta, int left,
+                                           bool vec) {
   float o[4] = {alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w};
-  const int left = p.n - col;
-  if (p.c_vec && left >= 4) {
+  if (vec && left >= 4) {
     union {
       T e[4];
       uint4 q;
       uint2 d;
     } u;
-    if (p.beta != 0.f) {
+    if (beta != 0.f) {
       if constexpr (sizeof(T) == 4) u.q = *reinterpret_cast<const uint4*>(c);
       else u.d = *reinterpret_cast<const uint2*>(c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += p.beta * mx_to_f32(u.e[i]);
+      for (int i = 0; i < 4; ++i) o[i] += beta * mx_to_f32(u.e[i]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u.e[i] = mx_from_f32<T>(o[i]);
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(c) = u.q;
-    else *reinterpret_cast<uint2*>(c) = u.d;
+    mx_write4_plain<T>(c, make_float4(o[0], o[1], o[2], o[3]), 1.f);
   } else {
-    for (int i = 0; i < 4 && i < left; ++i) {
-      if (p.beta != 0.f) o[i] += p.beta * mx_to_f32(c[i]);
-      c[i] = mx_from_f32<T>(o[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < left) {
+        if (beta != 0.f) o[i] += beta * mx_to_f32(c[i]);
+        c[i] = mx_from_f32<T>(o[i]);
+      }
     }
   }
+}
+
+template <typename T>
+__device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, const float4& v,
+                                          float alpha) {
+  T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
+  if (p.c_vec && p.beta == 0.f && col + 4 <= p.n) mx_write4_plain<T>(c, v, alpha);
+  else mx_write4_any<T>(c, v, alpha, p.beta, p.n - col, p.c_vec != 0);
 }
 
 // The MMAs of one stage (A at its start, B at B_OFF): the scales go to TMEM columns sfa, sfb (B_TILES scale

@@ -295,7 +295,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
       mx_wait(&aux->full[i % C::STAGES], (i / C::STAGES) & 1u, aux, true);
   __syncwarp();
-  cluster_sync();
+  cluster_meet();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

@@ -98,6 +98,13 @@ __device__ __forceinline__ void cluster_sync() {
                    "memory");
 }
 
+// The same without ordering memory: nobody leaves before everybody has come. (The
+// release above waits for the thread's global stores, one to two microseconds.)
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" :::
+                   "memory");
+}
+
 // Shared::cluster address of `p`'s counterpart in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   uint32_t r;
