@@ -19,7 +19,7 @@
 // What bounds it: a few rows of A (decode) stream B once, so memory does (1 x 28672
 // x 8192 in nvfp4, 132 MB: 23.4 us, 5.6 TB/s; in mxfp8 37.7 us, 6.4 TB/s); small
 // products the fixed cost of a launch, a first load and the sum over the cluster
-// (333 x 1000 x 2200 in mxfp8: 6.8 us). Larger ones run on CTA pairs
+// (333 x 1000 x 2200 in mxfp8: 6.0 us). Larger ones run on CTA pairs
 // (skg_mx_gemm_pair.cu).
 //
 // Every wait is bounded; when one runs out the CTA records
@@ -147,6 +147,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     return a;
   };
   float alpha = 0.f;
+  const bool direct = !FEW && p.direct != 0;
   bool fine = true;  // epilogue threads: the accumulator is there
   int issued = 0;    // the loading thread: stages loaded
   if (warp == 0) {
@@ -206,7 +207,33 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int q = warp & 3;
     const int r = q * 32 + lane;
     float* part = reinterpret_cast<float*>(ring);
-    if (fine && tm * kMxTile + q * 32 < p.m) {
+    if (fine && direct && tm * kMxTile + q * 32 < p.m) {
+      // A lane's row, 16 bytes at a time (see plan_and_launch).
+      T* out = reinterpret_cast<T*>(p.c) + (int64_t)(tm * kMxTile + r) * p.ldc + tn * kMxTile;
+      const int left = tm * kMxTile + r < p.m ? p.n - tn * kMxTile : 0;
+#pragma unroll 1
+      for (int c = 0; c < kMxTile; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+        constexpr int PER = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 32; i += PER) {
+          union {
+            T e[PER];
+            uint4 u;
+          } o;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) o.e[j] = mx_from_f32<T>(alpha * __uint_as_float(v[i + j]));
+          if (c + i + PER <= left) {
+            *reinterpret_cast<uint4*>(out + c + i) = o.u;
+          } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+              if (c + i + j < left) out[c + i + j] = o.e[j];
+          }
+        }
+      }
+    } else if (fine && tm * kMxTile + q * 32 < p.m) {
       // The ring is idle: every stage was read by MMAs that are complete.
 #pragma unroll
       for (int c = 0; c < kMxTile; c += 64) {
@@ -231,7 +258,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   if (p.split == 1) {
     // A warp writes the 32 rows that its own lanes stored.
     const int row0 = tm * kMxTile + (warp & 3) * 32, col = tn * kMxTile + lane * 4;
-    if (warp >= 2 && fine && col < p.n) {
+    if (warp >= 2 && fine && !direct && col < p.n) {
       const float* src = part + (warp & 3) * 32 * kMxPitch + lane * 4;
 #pragma unroll 1
       for (int i = 0; i < 32 && row0 + i < p.m; i += 4) {
@@ -302,8 +329,8 @@ SinglePlan single_plan(int64_t m, int64_t n, int ksteps, int sms) {
     if (s > 1 && (tiles * s > 2 * sms || s > ksteps)) break;
     const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
     const int stages = (ksteps + s - 1) / s;
-    const double us = tiles * s <= sms ? (s > 1 ? 5.1 : 4.2) + 0.36 * stages
-                                       : (s > 1 && m > 64 ? 7.0 : 5.5) + 0.48 * waves * stages;
+    const double us = tiles * s <= sms ? (s > 1 ? 4.2 : 3.2) + 0.36 * stages
+                                       : (s > 1 && m > 64 ? 6.5 : 5.2) + 0.48 * waves * stages;
     if (m <= 16 || us < best.us) best = {s, us};
   }
   return best;
@@ -312,12 +339,12 @@ SinglePlan single_plan(int64_t m, int64_t n, int ksteps, int sms) {
 // Whether a product runs on CTA pairs: 256 x 256 tiles halve what each SM reads
 // per product, but cannot share a tile's k. Up to 128 rows the single CTAs win at
 // every n and k (1 x 8192 x 8192 in nvfp4: 9.6 against 17.9 us); beyond, the lower
-// estimate (512 x 512 x 8192 in nvfp4: 12.4 us paired, 7.0 single; 2048 x 2048 x
-// 2048: 6.9 paired, 8.9 single).
+// estimate (512 x 512 x 8192 in nvfp4: 12.4 us paired, 6.7 single; 2048 x 2048 x
+// 2048: 6.5 paired, 8.9 single).
 bool wants_pairs(int64_t m, int64_t n, int ksteps, int clusters, double single_us) {
   if (m <= kMxTile) return false;
   const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  return 4.4 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;
+  return 4.2 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;
 }
 
 template <int FMT>
@@ -335,6 +362,11 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
   p.split = pair ? 1 : single.split;
+  // A CTA that has a tile and an SM to itself writes it from its registers: half
+  // sectors, but without the way through shared memory (128 x 8192 x 512 in mxfp8 4.1
+  // against 5.0 us). With more tiles, or one row of 32 lanes in use, whole sectors are
+  // faster (128 x 28672 x 2048 14.5 against 15.1, 1 x 28672 x 1024 7.8 against 8.5).
+  p.direct = !pair && p.split == 1 && p.c_tma && p.m > 16 && tm * tn <= sms;
   p.a_rows = !pair && p.m < kMxTile ? (p.m + 7) / 8 * 8 : kMxTile;
   const uint64_t bytes = ((uint64_t)p.k * mx_bits(FMT) + 7) / 8;
   const uint64_t chunks_a = (uint64_t)rt_a * p.groups, chunks_b = (uint64_t)rt_b * p.groups;

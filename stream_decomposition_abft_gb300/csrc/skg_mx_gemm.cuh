@@ -26,11 +26,12 @@ struct MxParams {
   void* c;
   int64_t ldc;
   int c_vec;        // four elements of a row are aligned together
-  int c_tma;        // pairs: C is stored by TMA (rows on 16-byte boundaries, beta = 0)
+  int c_tma;        // rows of C on 16-byte boundaries, beta = 0: pairs store it by TMA
   int ksteps;       // stages of k
   int groups;       // scale tiles along k
   int tiles_m, tiles_n;
   int split;        // single CTAs: CTAs per tile (cluster size)
+  int direct;       // single CTAs: C is written from registers
   int a_rows;       // single CTAs: rows of A's box
   skg_report_t* report;
 };

@@ -382,7 +382,8 @@ def check_product(got, a, b, k, alpha=1.0, beta=0.0, c0=None):
 
 PRODUCTS = [(1, 1, 1), (1, 128, 32), (3, 5, 7), (17, 200, 96), (128, 128, 128), (128, 256, 256),
             (129, 257, 300), (64, 1000, 2200), (16, 2048, 8192), (1, 28672, 1024), (300, 130, 1056),
-            (257, 513, 544), (512, 768, 4096), (1000, 1500, 800)]
+            (257, 513, 544), (512, 768, 4096), (1000, 1500, 800),
+            (200, 1000, 96), (100, 328, 64), (17, 88, 32), (130, 4, 32)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
