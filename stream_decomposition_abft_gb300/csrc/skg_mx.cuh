@@ -372,12 +372,6 @@ __device__ __forceinline__ MxRaw8<T> mx_load_raw8(const T* p, bool vec, int n) {
   }
   return r;
 }
-template <typename T>
-__device__ __forceinline__ void mx_unpack_raw8(const MxRaw8<T>& r, float (&v)[8]) {
-  const T* e = reinterpret_cast<const T*>(r.q);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(e[i]);
-}
 
 // Elements o .. o + 7 (o < 8) of the sixteen 16-bit ones in a, b; those from n on 0.
 __device__ __forceinline__ uint4 mx_shift8(const uint4& a, const uint4& b, int o, int n) {

@@ -61,8 +61,9 @@ struct MxCfg : MxStage<FMT> {
 };
 
 // Rows rank, rank + S, ... of the tile: the S CTAs' partial sums in rank order.
-// The loads of several rows are in flight together (a remote load takes about a
-// quarter of a microsecond).
+// The loads of several rows are in flight together. Every value that is loaded is
+// stored, so no load is still on its way to another CTA's shared memory when a thread
+// comes to the barrier that lets that CTA leave.
 template <typename T, int S>
 __device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* part, int warp,
                                                int lane, int rank, int tm, int tn, float alpha) {
@@ -70,6 +71,7 @@ __device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* p
   constexpr int WARPS = kMxThreads / 32;
   const int rows = min(kMxTile, p.m - tm * kMxTile);
   const int col = tn * kMxTile + lane * 4;
+  if (col >= p.n) return;
   uint32_t base[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) base[s] = cluster_addr(part + lane * 4, (uint32_t)s);
@@ -78,14 +80,17 @@ __device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* p
     float4 u[R][S];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      const int r = min(rank + (i + j) * S, kMxTile - 1);
+      const int r = rank + (i + j) * S;
+      if (r < rows) {
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-        u[j][s] = ld_shared_cluster_f32x4(base[s] + (uint32_t)r * (kMxPitch * 4));
+        for (int s = 0; s < S; ++s)
+          u[j][s] = ld_shared_cluster_f32x4(base[s] + (uint32_t)r * (kMxPitch * 4));
+      }
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int r = rank + (i + j) * S;
+      if (r >= rows) break;
       float4 v = u[j][0];
 #pragma unroll
       for (int s = 1; s < S; ++s) {
@@ -94,7 +99,7 @@ __device__ __forceinline__ void mx_reduce_rows(const MxParams& p, const float* p
         v.z += u[j][s].z;
         v.w += u[j][s].w;
       }
-      if (r < rows && col < p.n) mx_write4<T>(p, tm * kMxTile + r, col, v, alpha);
+      mx_write4<T>(p, tm * kMxTile + r, col, v, alpha);
     }
   }
 }
@@ -183,9 +188,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // Two buffers of scale columns: the copy for this stage does not
         // touch the ones that the last stage's MMAs read.
         const uint32_t sfa = tmem + kMxTile + (it & 1) * C::SF_COLS;
-        mx_stage_mmas<FMT, false, 1, C::B_OFF>(tmem, sfa, sfa + C::CHUNKS * 4,
-                                     smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF, C::SFB_OFF,
-                                     p.k - kb * C::STEP, it == 0);
+        mx_stage_mmas<FMT, false, 1, C::B_OFF>(
+            tmem, sfa, sfa + C::CHUNKS * 4, smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF,
+            C::SFB_OFF, p.k - kb * C::STEP, it == 0);
         any = true;
         umma_commit(&aux->empty[st]);
       }
@@ -199,7 +204,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   } else {
     // What the way out needs is read while the accumulator is on its way.
     alpha = factor();
-    asm volatile("" ::"l"(p.c), "l"(p.ldc), "f"(alpha), "f"(p.beta), "r"(p.m), "r"(p.n), "r"(p.c_vec));
+    asm volatile("" ::"l"(p.c), "l"(p.ldc), "f"(alpha), "f"(p.beta), "r"(p.m), "r"(p.n),
+                 "r"(p.c_vec));
     fine = mx_wait(&aux->tfull[0], 0, aux);
     if (!fine) mx_fail(p, aux);
     fine = epi_all(fine);
@@ -277,6 +283,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       else if (p.split == 4) mx_reduce_rows<T, 4>(p, part, warp, lane, rank, tm, tn, alpha);
       else mx_reduce_rows<T, 8>(p, part, warp, lane, rank, tm, tn, alpha);
     }
+    __syncwarp();
     cluster_meet();  // no CTA leaves while another reads its partial sums
   }
   tc_fence_before();

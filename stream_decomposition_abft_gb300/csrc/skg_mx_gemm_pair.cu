@@ -218,9 +218,9 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
           }
           tc_fence_after();
           const uint32_t sf = tmem + C::SF_BASE + (it & 1) * C::SF_COLS;
-          mx_stage_mmas<FMT, true, 2, kMxOperand>(d, sf, sf + C::CHUNKS * 4,
-                                      smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF, C::SFB_OFF,
-                                      p.k - kb * C::STEP, kb == 0);
+          mx_stage_mmas<FMT, true, 2, kMxOperand>(
+              d, sf, sf + C::CHUNKS * 4, smem_u32(ring + st * C::STAGE_BYTES), C::SFA_OFF,
+              C::SFB_OFF, p.k - kb * C::STEP, kb == 0);
           umma_commit_pair(&aux->empty[st]);
           if (++st == C::STAGES) {
             st = 0;
@@ -289,13 +289,16 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
   tc_fence_before();
   __syncthreads();
   // Copies that no MMA waited for land before the pair parts (the leader's
-  // barriers count both CTAs' bytes); then no CTA leaves while the other may still
-  // signal its barriers.
+  // barriers count both CTAs' bytes), and the leader's last commit has reached the
+  // other CTA's barrier; then no CTA leaves while the other may still signal its
+  // barriers (the last hand-over of an accumulator is a remote arrival, which the
+  // cluster barrier's release waits for).
+  if (warp == 1 && rank == 1 && first < tiles && elect_one()) mx_wait(&aux->drain, 0, aux, true);
   if (warp == 0 && rank == 0 && issued > 0 && mx_aborted(aux))
     for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
       mx_wait(&aux->full[i % C::STAGES], (i / C::STAGES) & 1u, aux, true);
   __syncwarp();
-  cluster_meet();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

@@ -99,7 +99,9 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The same without ordering memory: nobody leaves before everybody has come. (The
-// release above waits for the thread's global stores, one to two microseconds.)
+// release above waits for the thread's global stores, one to two microseconds.) What a
+// thread does to another CTA's shared memory has to be over by itself: loads whose
+// values were used; not stores or arrivals.
 __device__ __forceinline__ void cluster_meet() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" :::
                    "memory");
