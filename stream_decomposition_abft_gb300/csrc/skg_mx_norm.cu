@@ -44,10 +44,11 @@ struct NormParams {
   int x_vec, r_vec, w_vec, s_vec;
 };
 
-// 1 / sqrt(ss / n + eps), each step corrected by its remainder: about half the
-// instructions of the rounded division and root, which every warp runs for every
-// row (8192 x 8192: 77 us with those, 75 so), and as near (a code is decided by which
-// side of a tie its value falls on). Zero and infinity as the plain root has them.
+// 1 / sqrt(ss / n + eps): the product with 1 / n and the approximate root, each with
+// one Newton step whose remainder a fused multiply-add gives exactly. About half the
+// instructions of a rounded division and root, which every warp runs for every row
+// (8192 x 8192: 77 us with those, 75 so), and as near (a code is decided by which side
+// of a tie its value falls on). Zero and infinity as the plain root has them.
 __device__ __forceinline__ float row_rstd(float ss, float n, float inv_n, float eps) {
   const float q = ss * inv_n;
   const float m = fmaf(fmaf(-q, n, ss), inv_n, q) + eps;
@@ -74,8 +75,9 @@ __device__ __forceinline__ float row_sum(float v, int log_tpr, float* red) {
 }
 
 // Rows that the kernel below does not take (narrow ones on 16-byte boundaries,
-// several to a block; more than 8192 elements): 2^log_tpr threads share a row, V chunks of 16 elements each, h in registers
-// between the sum and the quantisation; V = 0: any width, h formed twice.
+// several to a block; more than 8192 elements): 2^log_tpr threads share a row, V
+// chunks of 16 elements each, h in registers between the sum and the quantisation;
+// V = 0: any width, h formed twice.
 template <typename T, int FMT, int V>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams p, int log_tpr) {
   __shared__ float red[kNormMaxThreads / 32];

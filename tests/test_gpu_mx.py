@@ -207,7 +207,8 @@ def check_norm(x, w, res, fmt, eps, g=None):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 8192), (2, 40), (7, 128), (130, 333),
-                                       (64, 2200), (3, 16384), (2, 28672), (2, 40000)])
+                                       (64, 2200), (3, 16384), (2, 28672), (2, 40000), (3, 12001),
+                                       (2, 30001), (2, 33333)])
 def test_rmsnorm(fmt, dtype, rows, cols):
     g = torch.Generator().manual_seed(cols)
     w = (1 + 0.3 * torch.randn(cols, generator=g)).to(TYPES[dtype]).cuda()
@@ -261,7 +262,8 @@ def test_rmsnorm_nan_row_stays_alone():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 8192), (5, 40), (130, 333), (333, 1111),
-                                       (700, 64), (64, 2200), (9, 16384), (3, 28672), (2, 40000)])
+                                       (700, 64), (64, 2200), (9, 16384), (3, 28672), (2, 40000),
+                                       (3, 12001), (2, 30001), (2, 33333)])
 def test_rmsnorm_backward(dtype, rows, cols):
     g = torch.Generator().manual_seed(cols)
     w = (1 + 0.3 * torch.randn(cols, generator=g)).to(TYPES[dtype]).cuda()
