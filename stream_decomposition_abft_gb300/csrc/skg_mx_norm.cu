@@ -48,12 +48,13 @@ struct NormParams {
 // one Newton step whose remainder a fused multiply-add gives exactly. About half the
 // instructions of a rounded division and root, which every warp runs for every row
 // (8192 x 8192: 77 us with those, 75 so), and as near (a code is decided by which side
-// of a tie its value falls on). Zero and infinity as the plain root has them.
+// of a tie its value falls on). Zero and infinity, also of the sum q + eps alone, as the
+// plain root has them.
 __device__ __forceinline__ float row_rstd(float ss, float n, float inv_n, float eps) {
   const float q = ss * inv_n;
   const float m = fmaf(fmaf(-q, n, ss), inv_n, q) + eps;
   const float r = rsqrtf(m);
-  if (!(m > 0.f) || !(q < 3.402823466e38f)) return rsqrtf(q + eps);
+  if (!(m > 0.f && m <= 3.402823466e38f)) return rsqrtf(q + eps);
   const float t = m * r, low = fmaf(m, r, -t);
   return fmaf(0.5f * r, fmaf(-t, r, 1.f) - low * r, r);
 }

@@ -1,0 +1,21 @@
+"""Ends of the microscaled operators' ranges and of their Python interface, on the GPU."""
+import pytest
+import torch
+
+from stream_decomposition_abft_gb300 import mx
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("cols", [264, 1111, 4096, 16384, 40000])
+@pytest.mark.parametrize("eps,size", [(float("inf"), 1.0), (3.4028e38, 2.0 ** 56)])
+def test_norm_statistics_that_overflow(cols, eps, size):
+    # mean(h^2) + eps is infinite, though the sum of h^2 is not: 1 / sqrt of it is 0, and so
+    # is the output.
+    x = torch.full((3, cols), size, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    q, _, rstd = mx.rmsnorm(x, w, eps)
+    if eps < float("inf"):
+        assert float(x[0].float().square().sum()) < 3.4e38
+    assert rstd.tolist() == [0.0] * 3
+    assert not bool(q.codes.any()) and not bool(q.scales.any())
