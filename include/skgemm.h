@@ -555,7 +555,7 @@ skg_status_t skg_mx_quantize_both(int64_t rows, int64_t cols, const void* X, int
  *   codes, scales = quantised(h * rstd * weight), in fp32 up to the codes.
  *   X, residual (NULL = none), weight (cols), sum: device, `type` (skg_in_t).
  *   sum: NULL, or h rounded to `type`; may be X or residual themselves.
- *   rstd: NULL, or device, rows floats (for the gradient).
+ *   rstd: NULL, or device, rows floats (for the gradient; NaN with cols = 0).
  * tensor_scale, codes, ldq and scales as in skg_mx_quantize. */
 skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t ldx,
                             const void* residual, int64_t ldr, const void* weight, int32_t type,

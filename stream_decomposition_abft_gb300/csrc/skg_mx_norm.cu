@@ -752,7 +752,13 @@ skg_status_t skg_rmsnorm_mx(int64_t rows, int64_t cols, const void* X, int64_t l
   if (rows < 0 || cols < 0 || !(eps >= 0.f)) return SKG_ERR_ARG;
   if (type != SKG_IN_F16 && type != SKG_IN_BF16) return SKG_ERR_ARG;
   if (format < SKG_MXFP8 || format > SKG_NVFP4) return SKG_ERR_ARG;
-  if (rows == 0 || cols == 0) return SKG_OK;
+  if (rows == 0 || (cols == 0 && !rstd)) return SKG_OK;
+  if (cols == 0) {  // the mean over no elements is NaN: all bits set
+    if (rows > INT32_MAX / 4 || ((uintptr_t)rstd & 3)) return SKG_ERR_UNSUPPORTED;
+    return cudaMemsetAsync(rstd, 0xff, (size_t)rows * 4, (cudaStream_t)stream) == cudaSuccess
+               ? SKG_OK
+               : SKG_ERR_CUDA;
+  }
   if (!X || !weight || !codes || !scales || ldx < cols || (residual && ldr < cols) ||
       (sum && lds < cols) || ldq < skg_mx_codes_ld(cols, format))
     return SKG_ERR_ARG;

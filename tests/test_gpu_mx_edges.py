@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from stream_decomposition_abft_gb300 import mx
+from stream_decomposition_abft_gb300 import mx, skgemm
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +19,17 @@ def test_norm_statistics_that_overflow(cols, eps, size):
         assert float(x[0].float().square().sum()) < 3.4e38
     assert rstd.tolist() == [0.0] * 3
     assert not bool(q.codes.any()) and not bool(q.scales.any())
+
+
+def test_norm_of_empty_rows():
+    # The mean over no elements is NaN; rstd is written for every row.
+    rstd = torch.full((5,), 7.0, device="cuda")
+    x = torch.empty(5, 8, dtype=torch.bfloat16, device="cuda")
+    p = x.data_ptr()
+    st = skgemm.rmsnorm_mx(5, 0, p, 8, None, 0, p, skgemm.IN_BF16, 1e-5, None, 0, rstd.data_ptr(),
+                           skgemm.MXFP8, None, p, 0, p, torch.cuda.current_stream().cuda_stream)
+    assert st == skgemm.OK
+    assert bool(torch.isnan(rstd).all())
+    q, h, rstd = mx.rmsnorm(x[:, :0], x[0, :0], 1e-5, residual=x[:, :0])
+    assert q.codes.shape == (5, 0) and h.shape == (5, 0)
+    assert rstd.shape == (5,) and bool(torch.isnan(rstd).all())
