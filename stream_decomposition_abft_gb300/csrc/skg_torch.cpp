@@ -114,6 +114,15 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, c10::Device d) {
   return at::detail::empty_cuda(sizes, type, d, std::nullopt);
 }
 
+bool flag(const char* name, PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + ": a truth value is wanted");
+  }
+  return v == 1;
+}
+
 struct Quantized {
   at::Tensor codes, scales;
   int64_t ldq;
@@ -147,7 +156,7 @@ PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = tensor_of("x", a[0]);
   const int type = type_of("x", x.scalar_type(), true);
   const int64_t ldx = matrix("x", x);
-  const bool tr = PyObject_IsTrue(a[2]) == 1, values = PyObject_IsTrue(a[4]) == 1;
+  const bool tr = flag("transpose", a[2]), values = flag("values", a[4]);
   const c10::cuda::CUDAGuard guard(x.device());
   const float* g = tensor_scale(a[3], fmt, x.device());
   const int64_t rows = x.size(tr ? 1 : 0), k = x.size(tr ? 0 : 1);

@@ -7,6 +7,11 @@ from stream_decomposition_abft_gb300 import mx, skgemm
 pytestmark = pytest.mark.gpu
 
 
+def randn(*shape, seed, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
 @pytest.mark.parametrize("cols", [264, 1111, 4096, 16384, 40000])
 @pytest.mark.parametrize("eps,size", [(float("inf"), 1.0), (3.4028e38, 2.0 ** 56)])
 def test_norm_statistics_that_overflow(cols, eps, size):
@@ -33,3 +38,12 @@ def test_norm_of_empty_rows():
     q, h, rstd = mx.rmsnorm(x[:, :0], x[0, :0], 1e-5, residual=x[:, :0])
     assert q.codes.shape == (5, 0) and h.shape == (5, 0)
     assert rstd.shape == (5,) and bool(torch.isnan(rstd).all())
+
+
+def test_flags_without_a_truth_value():
+    x = randn(4, 64, seed=1)
+    two = torch.ones(2, dtype=torch.bool)
+    with pytest.raises(ValueError, match="transpose"):
+        mx.quantize(x, "mxfp8", transpose=two)
+    with pytest.raises(ValueError, match="values"):
+        mx.quantize(x, "mxfp8", values=two)
