@@ -63,6 +63,21 @@ def workspace(device="cuda") -> Workspace:
 
 
 _new_workspace = workspace
+_defaults = {}  # device: default_workspace's
+
+
+def default_workspace(device="cuda") -> Workspace:
+    """The workspace of the matmul calls on a device that are given none, made on first use
+    and kept: its report() shows a wait of theirs that ran out."""
+    d = torch.device(device)
+    if d.index is None:
+        d = torch.device(d.type, torch.cuda.current_device())
+    ws = _defaults.get(d)
+    if ws is None:
+        ws = _new_workspace(d)
+        torch.cuda.current_stream(d).synchronize()  # zeroed before another stream's call
+        ws = _defaults.setdefault(d, ws)
+    return ws
 
 
 def quantize(x, format, transpose=False, tensor_scale=None, values=False, stream=None):
@@ -131,12 +146,18 @@ def matmul(a, b, out=None, out_dtype=torch.bfloat16, alpha=1.0, beta=0.0, worksp
            stream=None):
     """alpha * a b^T + beta * out of two Matrix operands (m, k) and (n, k) of one
     format; ``out`` (m, n) is written in place, or allocated in ``out_dtype``.
-    workspace: mx.workspace(), kept between calls; None allocates one."""
+    workspace: mx.workspace(), kept between calls; None: default_workspace() (in a CUDA
+    graph's capture before its first use: one of the graph's own, whose report is lost)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return matmul(a, b, out, out_dtype, alpha, beta, workspace)
     if workspace is None:
-        workspace = _new_workspace(a.codes.device)
+        d = a.codes.device
+        workspace = _defaults.get(d)
+        if workspace is None:
+            with torch.cuda.device(d):
+                capturing = torch.cuda.is_current_stream_capturing()
+            workspace = _new_workspace(d) if capturing else default_workspace(d)
     r = _native().matmul(a, b, out, out_dtype, alpha, beta, workspace.buf)
     if r.__class__ is int:
         raise SkgError(r, "skg_gemm_mx")

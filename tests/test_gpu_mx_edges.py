@@ -47,3 +47,26 @@ def test_flags_without_a_truth_value():
         mx.quantize(x, "mxfp8", transpose=two)
     with pytest.raises(ValueError, match="values"):
         mx.quantize(x, "mxfp8", values=two)
+
+
+def test_report_of_calls_without_a_workspace():
+    a, b = mx.quantize(randn(40, 512, seed=1), "mxfp8"), mx.quantize(randn(300, 512, seed=2), "mxfp8")
+    ws = mx.default_workspace()
+    assert mx.default_workspace(a.codes.device) is ws
+    ws.report(reset=True)
+    want = mx.matmul(a, b, workspace=mx.workspace())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [mx.matmul(a, b), mx.matmul(a, b, stream=s), mx.linear(randn(3, 512, seed=3), b)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
+    rep = ws.report(reset=True)
+    assert rep.launches == 3 and rep.timeouts == 0 and rep.status_bits == 0
+    # Captured: the graph's launches are counted there as well.
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mx.matmul(a, b)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and ws.report().launches == 2
