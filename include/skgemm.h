@@ -519,7 +519,11 @@ skg_status_t skg_gemm_f64(int64_t m, int64_t n, int64_t k, double alpha, const d
  * Scales: tiles of 128 rows x 4 blocks of 512 bytes, the tiles of the same rows
  * after one another; within a tile row 32 q + l (0 <= l < 32) and block b are
  * byte 16 l + 4 q + b. skg_mx_scales_size bytes; the quantisers write zeros where
- * the matrix ends inside a tile. Codes and scales are 16-byte aligned. */
+ * the matrix ends inside a tile. Codes and scales are 16-byte aligned.
+ * skg_gemm_mx needs the zero codes from k on, and in the 4-bit formats, whose
+ * instructions span 64 elements, zero scales of the matrix's rows from k up to the
+ * next multiple of 64 (a NaN there times a zero code is NaN). What else lies in the
+ * scale tiles past the matrix's rows and blocks does not reach C. */
 typedef enum { SKG_MXFP8 = 0, SKG_MXFP4 = 1, SKG_NVFP4 = 2 } skg_mx_t;
 
 /* Least ldq of a matrix with rows of k elements (a multiple of 16 bytes), and

@@ -48,7 +48,9 @@ def _native():
 class Matrix(NamedTuple):
     """A quantised rows x k matrix: ``codes`` (rows, pitch) bytes, ``scales`` in
     tiles of 128 rows x 4 blocks (bytes, one dimension), and ``tensor_scale``
-    (one float on the device, or None = 1)."""
+    (one float on the device, or None = 1). One that another program made has zero
+    codes from k up to a multiple of 32 and, in 4 bits, zero scales from k up to a
+    multiple of 64 (include/skgemm.h)."""
     format: str
     rows: int
     k: int

@@ -1,7 +1,9 @@
 """Ends of the microscaled operators' ranges and of their Python interface, on the GPU."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import mx_ref as mr
 from stream_decomposition_abft_gb300 import mx, skgemm
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +72,31 @@ def test_report_of_calls_without_a_workspace():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and ws.report().launches == 2
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m,n,k", [(5, 9, 32), (5, 9, 72), (40, 200, 40), (140, 150, 352),
+                                   (600, 600, 288)])
+def test_product_reads_no_scales_past_the_end(fmt, m, n, k):
+    # NaN in every scale byte that the storage rules leave open: rows past m and n, blocks
+    # past k (mxfp8), or past the multiple of 64 elements that a 4-bit instruction spans.
+    span = 32 if fmt == "mxfp8" else 64
+    live = -(-k // span) * span // mr.BLOCK[fmt]
+    nb = -(-k // 32) * 32 // mr.BLOCK[fmt]
+    groups = -(-nb // 4)
+    ops = []
+    for rows, seed in ((m, 1), (n, 2)):
+        x = randn(rows, k, seed=seed, dtype=torch.float32)
+        codes, scales = mr.quantize(x.cpu().numpy(), fmt)
+        stored = np.full(-(-rows // 128) * groups * 512, 0x7F if fmt == "nvfp4" else 0xFF, np.uint8)
+        r, b = np.meshgrid(np.arange(rows), np.arange(min(live, groups * 4)), indexing="ij")
+        stored[mr.scale_offset(r, b, groups)] = 0
+        r, b = np.meshgrid(np.arange(rows), np.arange(nb), indexing="ij")
+        stored[mr.scale_offset(r, b, groups)] = scales
+        q = mx.Matrix(fmt, rows, k, torch.from_numpy(mr.pack(codes, fmt)).cuda(),
+                      torch.from_numpy(stored).cuda())
+        zeros = torch.from_numpy(mr.tile_scales(scales)).cuda()
+        ops.append((q, q._replace(scales=zeros)))
+    got = mx.matmul(ops[0][0], ops[1][0], out_dtype=torch.float32)
+    want = mx.matmul(ops[0][1], ops[1][1], out_dtype=torch.float32)
+    assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
