@@ -1,4 +1,7 @@
 """Ends of the microscaled operators' ranges and of their Python interface, on the GPU."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +10,8 @@ from oracle import mx_ref as mr
 from stream_decomposition_abft_gb300 import mx, skgemm
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def randn(*shape, seed, dtype=torch.bfloat16):
@@ -100,3 +105,25 @@ def test_product_reads_no_scales_past_the_end(fmt, m, n, k):
     got = mx.matmul(ops[0][0], ops[1][0], out_dtype=torch.float32)
     want = mx.matmul(ops[0][1], ops[1][1], out_dtype=torch.float32)
     assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
+
+
+def test_readme_example():
+    # The README's norm and linear layer run as they stand there, with the layers' results.
+    with open(os.path.join(ROOT, "README.md")) as f:
+        code = re.search(r"```python\n(.*?mx\.rmsnorm.*?)```", f.read(), re.S).group(1)
+    m, k, n = 96, 256, 160
+    env = dict(x=randn(m, k, seed=1), r=randn(m, k, seed=2), dy=randn(m, n, seed=3),
+               w=randn(n, k, seed=4), norm_weight=1 + 0.1 * randn(k, seed=5))
+    exec(code, env)
+    h = env["x"].double() + env["r"].double()
+    u = h / (h.square().mean(1, keepdim=True) + 1e-5).sqrt() * env["norm_weight"].double()
+    dy, w = env["dy"].double(), env["w"].double()
+    for got, want in ((env["y"], u @ w.t()), (env["dn"], dy @ w), (env["dw"], dy.t() @ u)):
+        # Codes of e4m3 are within 1/16 of the values, independently: two of them in a product.
+        assert float((got.double() - want).norm() / want.norm()) < 2 / 16
+    dx, dnorm = mr.rmsnorm_backward(*(env[t].double().cpu().numpy() for t in
+                                      ("dn", "h", "norm_weight", "rstd")))
+    for got, want in ((env["dx"], dx), (env["dnorm"], dnorm)):
+        # Of the given dn: one rounding to bf16.
+        got = got.double().cpu().numpy()
+        assert np.linalg.norm(got - want) / np.linalg.norm(want) < 2.0 ** -8
