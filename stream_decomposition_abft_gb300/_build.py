@@ -5,7 +5,8 @@ Each .cu under csrc/ is one translation unit; they compile in parallel
 (one -gencode, no cmake) and link into a shared library with the CUDA
 runtime linked statically, so loading the library needs no GPU. The binding
 (csrc/skg_torch.cpp, host code) compiles against the installed torch at the
-same time and links to libskgemm.so beside it.
+same time and links to libskgemm.so beside it; without torch the library alone is
+built.
 """
 from __future__ import annotations
 
@@ -43,10 +44,19 @@ def _newest_header() -> float:
     return max(os.path.getmtime(h) for h in hdrs)
 
 
-def _binding_job(force: bool):
-    """(compile command or None, object) of the torch binding; the object's name
+def torch_dir():
+    """The folder of the installed torch; None without one (the library needs none, and the
+    binding is then not built)."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        return None
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
+def _binding_job(force: bool, torch_dir: str):
+    """(compile command or None, link command) of the torch binding; the object's name
     carries torch's version, whose headers it is compiled against."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     with open(os.path.join(torch_dir, "version.py")) as f:
         version = "".join(c if c.isalnum() else "_" for c in
                           next(line for line in f if line.startswith("__version__")))
@@ -67,8 +77,8 @@ def _binding_job(force: bool):
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile (incrementally) and link libskgemm.so and the binding; returns the
-    library's path."""
+    """Compile (incrementally) and link libskgemm.so and, where torch is installed, the
+    binding; returns the library's path."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -90,17 +100,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(res.stdout + res.stderr)
         return res
 
-    binding, binding_link = _binding_job(force)
+    link_lib = bool(jobs) or not os.path.exists(LIB)
+    torch = torch_dir()
+    binding, binding_link = _binding_job(force, torch) if torch else (None, None)
     if binding:
         jobs.insert(0, binding)  # the longest one
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
-    if jobs or not os.path.exists(LIB):
+    if link_lib:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if jobs or not os.path.exists(BINDING):
+    if torch and (binding or not os.path.exists(BINDING)):
         tmp = BINDING + f".tmp{os.getpid()}"
         run([*binding_link, "-o", tmp])
         os.replace(tmp, BINDING)
