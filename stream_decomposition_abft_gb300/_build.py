@@ -44,6 +44,19 @@ def _newest_header() -> float:
     return max(os.path.getmtime(h) for h in hdrs)
 
 
+def _stale(target: str, objs) -> bool:
+    """Whether target is missing or older than one of the objects it is linked of."""
+    return not os.path.exists(target) or \
+        os.path.getmtime(target) < max(os.path.getmtime(o) for o in objs)
+
+
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
 def torch_dir():
     """The folder of the installed torch; None without one (the library needs none, and the
     binding is then not built)."""
@@ -55,8 +68,8 @@ def torch_dir():
 
 
 def _binding_job(force: bool, torch_dir: str):
-    """(compile command or None, link command) of the torch binding; the object's name
-    carries torch's version, whose headers it is compiled against."""
+    """(compile command or None, object, link command) of the torch binding; the object's
+    name carries torch's version, whose headers it is compiled against."""
     with open(os.path.join(torch_dir, "version.py")) as f:
         version = "".join(c if c.isalnum() else "_" for c in
                           next(line for line in f if line.startswith("__version__")))
@@ -73,7 +86,7 @@ def _binding_job(force: bool, torch_dir: str):
     link = ["g++", "-shared", obj, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
             "-ltorch", "-ltorch_python", "-L", PKG, "-l:libskgemm.so", "-Wl,-rpath,$ORIGIN",
             f"-Wl,-rpath,{lib}"]
-    return (cmd if force or not fresh else None), link
+    return (cmd if force or not fresh else None), obj, link
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -100,22 +113,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(res.stdout + res.stderr)
         return res
 
-    link_lib = bool(jobs) or not os.path.exists(LIB)
     torch = torch_dir()
-    binding, binding_link = _binding_job(force, torch) if torch else (None, None)
-    if binding:
-        jobs.insert(0, binding)  # the longest one
+    if torch:
+        binding, binding_obj, binding_link = _binding_job(force, torch)
+        if binding:
+            jobs.insert(0, binding)  # the longest one
     if jobs:
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
-    if link_lib:
+    if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if torch and (binding or not os.path.exists(BINDING)):
-        tmp = BINDING + f".tmp{os.getpid()}"
-        run([*binding_link, "-o", tmp])
-        os.replace(tmp, BINDING)
+    if torch:
+        # The link line names the object and torch's libraries: kept beside the objects, it
+        # shows a binding that was linked for another torch.
+        line, linked = " ".join(binding_link), os.path.join(BUILD, "skg_torch.linked")
+        if _stale(BINDING, [binding_obj]) or _read(linked) != line:
+            tmp = BINDING + f".tmp{os.getpid()}"
+            run([*binding_link, "-o", tmp])
+            os.replace(tmp, BINDING)
+            with open(linked, "w") as f:
+                f.write(line)
     return LIB
 
 

@@ -85,3 +85,33 @@ def test_entry_without_torch(hide):
     res = subprocess.run([sys.executable, "-c", hide + "; import __graft_entry__ as g; g.build()"],
                          cwd=root, capture_output=True, text=True, timeout=600)
     assert res.returncode == 0, res.stderr[-2000:]
+
+
+def test_torch_changed_and_back(tree):
+    # The binding is linked from the object that fits the torch at hand, also when that
+    # object was there from before.
+    tree.install("2.9.1")
+    assert tree.build()[1] == [LIB, BINDING]
+    for version, compiled in (("2.11.0", 1), ("2.9.1", 0), ("2.11.0", 0)):
+        tree.install(version)
+        got = tree.build()
+        assert (len(got[0]), got[1]) == (compiled, [BINDING]), version
+        link = tree.ran[-1]
+        name = "skg_torch_" + "".join(c if c.isalnum() else "_" for c in
+                                      f"__version__ = '{version}'\n") + ".o"
+        assert any(os.path.basename(a) == name for a in link)
+        assert any(tree.torch in a for a in link)  # the libraries of that torch
+        assert tree.build() == ([], [])
+
+
+@pytest.mark.parametrize("step", [LIB, BINDING])
+def test_link_cut_off(tree, step):
+    # A build that ended between compiling and linking is taken up there.
+    tree.install("2.9.1")
+    tree.build()
+    tree.fail = step
+    with pytest.raises(RuntimeError):
+        tree.build(force=True)
+    tree.fail = None
+    assert tree.build() == ([], [LIB, BINDING] if step == LIB else [BINDING])
+    assert tree.build() == ([], [])
