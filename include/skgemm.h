@@ -594,8 +594,9 @@ skg_status_t skg_rmsnorm_backward(int64_t rows, int64_t cols, const void* dY, in
  *      read only if beta != 0.
  *   workspace: device, 256-byte aligned, skg_workspace_size_mx bytes, zeroed once
  *      with skg_workspace_init; holds the report (skg_report_read) that a wait
- *      which runs out is recorded in (SKG_ERR_PIPELINE_TIMEOUT). Nothing else is
- *      kept there: calls may share it, also at the same time.
+ *      which runs out is recorded in (SKG_ERR_PIPELINE_TIMEOUT; C is then
+ *      undefined). Nothing else is kept there: calls may share it, also at the
+ *      same time.
  * m, n or k of zero is valid (k = 0 gives C = beta * C). */
 size_t skg_workspace_size_mx(int64_t m, int64_t n, int64_t k, int32_t format);
 skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const void* A, int64_t lda,
@@ -603,6 +604,12 @@ skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const voi
                          int64_t ldb, const void* scales_b, const float* tensor_scale_b,
                          float beta, void* C, int64_t ldc, int32_t format, int32_t out_dtype,
                          void* workspace, size_t ws_bytes, void* stream);
+
+/* Testing only: in the skg_gemm_mx calls of this process from now on a CTA loads no
+ * more than `stages` stages of k (128 bytes of each row; 0 = all of them, as ever) and
+ * a wait is bounded by timeout_ns (0 = 2 s), so that a longer product's waits run out
+ * and the launch ends with SKG_ERR_PIPELINE_TIMEOUT in its report. */
+skg_status_t skg_mx_test_stall(int32_t stages, uint64_t timeout_ns);
 
 /* Number of SMs of the current device (0 if there is no device). */
 int32_t skg_device_sm_count(void);

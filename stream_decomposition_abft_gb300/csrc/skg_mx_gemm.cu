@@ -126,6 +126,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     prefetch_tmap(&tmSA);
     prefetch_tmap(&tmSB);
     aux->abort_flag = 0;
+    aux->limit = p.limit;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&aux->full[i], 1);
       mbar_init(&aux->empty[i], 1);
@@ -158,7 +159,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   if (warp == 0) {
     if (elect_one()) {
       const uint32_t tx = (uint32_t)p.a_rows * kMxRowBytes + kMxOperand + 2 * C::SF_BYTES;
-      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+      for (int kb = kb0; kb < kb1 && (uint32_t)issued < p.stages; ++kb, ++issued) {
         const int st = issued % C::STAGES;
         if (!mx_wait(&aux->empty[st], (uint32_t)((issued / C::STAGES) & 1) ^ 1u, aux)) {
           mx_fail(p, aux);
@@ -416,7 +417,22 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
 
 using namespace skg;
 
+namespace {
+
+// skg_mx_test_stall's settings.
+std::atomic<uint32_t> g_test_stages{0};
+std::atomic<uint64_t> g_test_limit{0};
+
+}  // namespace
+
 extern "C" {
+
+skg_status_t skg_mx_test_stall(int32_t stages, uint64_t timeout_ns) {
+  if (stages < 0) return SKG_ERR_ARG;
+  g_test_stages.store((uint32_t)stages, std::memory_order_relaxed);
+  g_test_limit.store(timeout_ns, std::memory_order_relaxed);
+  return SKG_OK;
+}
 
 size_t skg_workspace_size_mx(int64_t m, int64_t n, int64_t k, int32_t format) {
   if (m < 0 || n < 0 || k < 0 || format < SKG_MXFP8 || format > SKG_NVFP4) return 0;
@@ -466,6 +482,10 @@ skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const voi
   p.c_vec = ((uintptr_t)C & (4 * es - 1)) == 0 && ldc % 4 == 0;
   p.c_tma = ((uintptr_t)C & 15) == 0 && (ldc * es) % 16 == 0 && beta == 0.f;
   p.report = workspace_report(workspace);
+  const uint32_t stages = g_test_stages.load(std::memory_order_relaxed);
+  const uint64_t limit = g_test_limit.load(std::memory_order_relaxed);
+  p.stages = stages ? stages : UINT32_MAX;
+  p.limit = limit ? limit : kMxTimeoutNs;
   bool unsupported = false;
   cudaError_t e;
   if (format == SKG_MXFP8)

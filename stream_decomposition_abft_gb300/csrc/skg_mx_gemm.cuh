@@ -16,7 +16,7 @@ constexpr int kMxThreads = 192;
 constexpr int kMxTile = 128;
 constexpr int kMxRowBytes = 128;              // k bytes of a stage row
 constexpr int kMxOperand = kMxTile * kMxRowBytes;
-constexpr uint64_t kMxTimeoutNs = 2000000000ull;
+constexpr uint64_t kMxTimeoutNs = 2000000000ull;  // bound of a wait
 
 struct MxParams {
   int m, n, k;
@@ -33,6 +33,8 @@ struct MxParams {
   int split;        // single CTAs: CTAs per tile (cluster size)
   int direct;       // single CTAs: C is written from registers
   int a_rows;       // single CTAs: rows of A's box
+  uint32_t stages;  // a CTA loads no more stages than this (see skg_mx_test_stall)
+  uint64_t limit;   // bound of a wait, ns
   skg_report_t* report;
 };
 
@@ -47,6 +49,7 @@ struct MxStage {
 
 struct MxAux {
   uint64_t full[8], empty[8], tfull[2], tempty, drain;
+  uint64_t limit;
   uint32_t tmem_slot;
   int32_t abort_flag;
 };
@@ -62,7 +65,8 @@ __device__ __forceinline__ void mx_fail(const MxParams& p, MxAux* aux) {
   }
 }
 
-// Bounded wait; `drain` goes on after an abort (the caller's own operations).
+// Wait bounded by aux->limit; `drain` goes on after an abort, for as long as ever (the
+// caller's own operations).
 __device__ __forceinline__ bool mx_wait(uint64_t* bar, uint32_t parity, MxAux* aux,
                                         bool drain = false) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -71,7 +75,7 @@ __device__ __forceinline__ bool mx_wait(uint64_t* bar, uint32_t parity, MxAux* a
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 31) == 0) {
       if (!drain && mx_aborted(aux)) return false;
-      if (globaltimer() - t0 > kMxTimeoutNs) return false;
+      if (globaltimer() - t0 > (drain ? kMxTimeoutNs : aux->limit)) return false;
     }
   }
 }

@@ -141,6 +141,7 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     prefetch_tmap(&tmSB);
     prefetch_tmap(&tmC);
     aux->abort_flag = 0;
+    aux->limit = p.limit;
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&aux->full[i], 1);
       mbar_init(&aux->empty[i], 1);
@@ -173,6 +174,10 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
         pair_tile(p, t, tm, tn);
         const int rt = 2 * tm + rank;
         for (int kb = 0; kb < p.ksteps; ++kb) {
+          if (issued >= p.stages) {
+            ok = false;
+            break;
+          }
           if (!mx_wait(&aux->empty[st], phase ^ 1u, aux)) {
             mx_fail(p, aux);
             ok = false;
@@ -292,11 +297,15 @@ mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
   // barriers count both CTAs' bytes), and the leader's last commit has reached the
   // other CTA's barrier; then no CTA leaves while the other may still signal its
   // barriers (the last hand-over of an accumulator is a remote arrival, which the
-  // cluster barrier's release waits for).
+  // cluster barrier's release waits for). After a wait that ran out the other CTA may
+  // have loaded stages that the leader did not come to, whose barriers no longer
+  // complete: it gives those copies a millisecond, some thousand times what one takes.
   if (warp == 1 && rank == 1 && first < tiles && elect_one()) mx_wait(&aux->drain, 0, aux, true);
   if (warp == 0 && rank == 0 && issued > 0 && mx_aborted(aux))
     for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
       mx_wait(&aux->full[i % C::STAGES], (i / C::STAGES) & 1u, aux, true);
+  if (warp == 0 && rank == 1 && issued > 0 && mx_aborted(aux))
+    for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) __nanosleep(1000);
   __syncwarp();
   cluster_sync();
   if (warp == 1) {

@@ -95,7 +95,7 @@ SYMBOLS = ("skg_opts_default", "skg_workspace_size", "skg_workspace_init", "skg_
            "skg_noalloc_report_read", "skg_mx_codes_ld", "skg_mx_scales_size", "skg_mx_quantize",
            "skg_mx_quantize_both",
            "skg_rmsnorm_mx", "skg_workspace_size_rmsnorm_backward", "skg_rmsnorm_backward",
-           "skg_workspace_size_mx", "skg_gemm_mx")
+           "skg_workspace_size_mx", "skg_gemm_mx", "skg_mx_test_stall")
 
 _lib = None
 
@@ -187,6 +187,8 @@ def lib() -> ctypes.CDLL:
     L.skg_gemm_mx.argtypes = [i64, i64, i64, f32, vp, i64, vp, vp, vp, i64, vp, vp, f32, vp, i64,
                               i32, i32, vp, sz, vp]
     L.skg_gemm_mx.restype = i32
+    L.skg_mx_test_stall.argtypes = [i32, ctypes.c_uint64]
+    L.skg_mx_test_stall.restype = i32
     L.skg_device_sm_count.argtypes = []
     L.skg_device_sm_count.restype = i32
     L.skg_status_string.argtypes = [i32]
@@ -394,6 +396,10 @@ def gemm_mx(m, n, k, alpha, A_ptr, lda, SA_ptr, ga_ptr, B_ptr, ldb, SB_ptr, gb_p
             ldc, fmt, out_dtype, ws_ptr, ws_bytes, stream) -> int:
     return lib().skg_gemm_mx(m, n, k, alpha, A_ptr, lda, SA_ptr, ga_ptr, B_ptr, ldb, SB_ptr,
                              gb_ptr, beta, C_ptr, ldc, fmt, out_dtype, ws_ptr, ws_bytes, stream)
+
+
+def mx_test_stall(stages: int, timeout_ns: int = 0) -> int:
+    return lib().skg_mx_test_stall(stages, timeout_ns)
 
 
 def device_sm_count() -> int:

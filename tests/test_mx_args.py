@@ -125,3 +125,8 @@ def test_binding_refusals():
         mx.quantize(None, "mxfp8")
     with pytest.raises(ValueError, match="Matrix is wanted"):
         mx.matmul((), q, workspace=ws)
+
+
+def test_stall_arguments():
+    assert skgemm.mx_test_stall(-1) == skgemm.ERR_ARG
+    assert skgemm.mx_test_stall(0, 0) == skgemm.OK
