@@ -19,7 +19,7 @@
 // What bounds it: a few rows of A (decode) stream B once, so memory does (1 x 28672
 // x 8192 in nvfp4, 132 MB: 22.7 us, 5.8 TB/s; in mxfp8 37.9 us, 6.4 TB/s); small
 // products the fixed cost of a launch, a first load and the sum over the cluster
-// (333 x 1000 x 2200 in mxfp8: 6.0 us). Larger ones run on CTA pairs
+// (333 x 1000 x 2200 in mxfp8: 6.3 us). Larger ones run on CTA pairs
 // (skg_mx_gemm_pair.cu).
 //
 // Every wait is bounded; when one runs out the CTA records

@@ -134,11 +134,11 @@ __device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, c
   else mx_write4_any<T>(c, v, alpha, p.beta, p.n - col, p.c_vec != 0);
 }
 
-// The MMAs of one stage (A at its start, B at B_OFF): the scales go to TMEM columns sfa, sfb (B_TILES scale
-// tiles of 128 rows of B), then up to four MMAs of 32 bytes of k each (32 elements of 8
-// bits, 64 of 4). MMAs wholly past k are left out: their scales need not exist. The last
-// one of 4 bits may reach past k's last block of 32: it takes zero codes there, with
-// scales that the storage rules have be zero.
+// The MMAs of one stage (A at its start, B at B_OFF): the scales go to TMEM columns sfa,
+// sfb (B_TILES scale tiles of 128 rows of B), then up to four MMAs of 32 bytes of k each
+// (32 elements of 8 bits, 64 of 4). MMAs wholly past k are left out: their scales need
+// not exist. The last one of 4 bits may reach past k's last block of 32: it takes zero
+// codes there, with scales that the storage rules have be zero.
 template <int FMT, bool PAIR, int B_TILES, int B_OFF>
 __device__ __forceinline__ void mx_stage_mmas(uint32_t d, uint32_t sfa, uint32_t sfb,
                                               uint32_t stage, uint32_t sfa_off, uint32_t sfb_off,

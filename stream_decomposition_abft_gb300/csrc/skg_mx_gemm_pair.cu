@@ -13,12 +13,16 @@
 // form 903 us; one elected thread issuing (the compiler had wrapped every tcgen05
 // instruction behind `lane == 0` in a loop over the lanes, 1540 cycles per stage of
 // nvfp4 against 650) 560 us; TMA stores and a hand-over of the accumulator without a
-// release at cluster scope (1200 cycles a tile) 517 us; 490 us now in short runs, 550
-// in long ones: 7.0 to 7.9 PFLOP/s, 3.6 to 4.1 times the card's bf16 burst rate. In
-// mxfp8 4096 x 8192 x 8192 takes 152 us (3.6 PFLOP/s). The tensor pipe is busy 76 %
-// (4 bits) and 85 % (8 bits) of the time, and the clock falls to 1.65 GHz under the
-// 8-bit load: power bounds the large products (with the loads left out of a copy of
-// the kernel, at the same cycles per stage, the clock stays at 1.9 GHz).
+// release at cluster scope (1200 cycles a tile) 517 us; 490 us now in short runs, 560
+// in long ones: 6.9 to 7.9 PFLOP/s, 3.6 to 4.1 times the card's bf16 burst rate. In
+// mxfp8 4096 x 8192 x 8192 takes 151 us (3.6 PFLOP/s). The tensor pipe is busy 85 % of
+// the time in 8 bits, and the clock falls to 1.65 GHz under that load (with the loads
+// left out of a copy of the kernel, at the same cycles per stage, it stays at 1.9 GHz):
+// power bounds these. In 4 bits the pipe is busy 76 % of the time and what the rest
+// waits for has not been shown; the MMAs are those of K = 64 (the K = 96 ones of 4 bits
+// have not been tried). With beta, or rows of C off 16-byte boundaries, C does not go
+// through TMA and the epilogue takes longer than the MMAs: 4096 x 8192 x 8192 with
+// beta = 1 279 us in mxfp8 and 273 in nvfp4 (79 without beta), 358 and 345 into fp32.
 #include "skg_mx_gemm.cuh"
 
 namespace skg {

@@ -10,7 +10,12 @@
 // their sum and the code written), 8 backward. Measured on GB300, bf16, against
 // 6.69 TB/s of a copy: 8192 x 8192 forward 75 us (6.3 TB/s); 4096 x 8192 backward
 // 48 us (5.6 TB/s: 43 us for dx and the blocks' dw, the rest for the sum of the 152
-// partial dw); one row of 8192 3 us forward. Sums and statistics are fp32.
+// partial dw); one row of 8192 3 us forward. Sums and statistics are fp32. Further from
+// that rate: 2048 columns (4096 rows: 14 us forward, 17 backward, 4.3 and 3.9 TB/s),
+// where a block's barriers, and backward the rows of partial dw, weigh against few
+// elements; more than 8192, where no row is fetched ahead (2048 x 28672: 130 and 246 us,
+// 3.2 and 1.9 TB/s); rows off 16-byte boundaries (4096 x 8001: 88 and 87 us, 2.6 and 3.0
+// TB/s), whose pieces are fetched twice and leave two bytes a lane.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -78,7 +83,7 @@ __device__ __forceinline__ float row_sum(float v, int log_tpr, float* red) {
 // Rows that the kernel below does not take (narrow ones on 16-byte boundaries,
 // several to a block; more than 8192 elements): 2^log_tpr threads share a row, V
 // chunks of 16 elements each, h in registers between the sum and the quantisation;
-// V = 0: any width, h formed twice.
+// V = 0 (over 32768): any width, h formed twice.
 template <typename T, int FMT, int V>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams p, int log_tpr) {
   __shared__ float red[kNormMaxThreads / 32];
@@ -160,11 +165,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_mx_kernel(NormParams 
 }
 
 // ------------------------------------------------------------------ wide rows
-// A block per row at a time, whole rows on 16-byte boundaries. A thread owns the
-// pieces of 8 elements t, t + blockDim, ... of every row and fetches the next
-// rows' pieces into a ring of its own in shared memory (cp.async): the loads of
-// kNormStages rows are in flight whatever the rows in hand wait for, and no other
-// thread reads what a thread has fetched, so the ring needs no barriers.
+// A block per row at a time. A thread owns the pieces of 8 elements t, t + blockDim,
+// ... of every row and fetches the next rows' pieces (off 16-byte boundaries the
+// aligned ones that cover them) into a ring of its own in shared memory (cp.async): the
+// loads of kNormStages rows are in flight whatever the rows in hand wait for, and no
+// other thread reads what a thread has fetched, so the ring needs no barriers.
 constexpr int kNormStages = 3;
 constexpr int kGradStages = 4;
 
@@ -298,7 +303,8 @@ cudaError_t launch_norm_wide(const NormParams& p, int v, int threads, bool vec, 
   const size_t smem = (size_t)kNormStages * 2 * v * threads * 16 * (vec ? 1 : 2);
   const int64_t rows = (p.rows + 127) / 128 * 128;
   // 1024 threads per SM: two blocks of 512, four of 256 (4096 x 2048: 15 us with
-  // two of 256).
+  // two of 256). The double ring of rows off 16-byte boundaries lets three of 256 fit:
+  // the last quarter of the blocks starts when the others end (4096 x 2001: 23 us).
   const int64_t most = (int64_t)sms * (1024 / threads < 8 ? 1024 / threads : 8);
   const dim3 grid((unsigned)(rows < most ? rows : most));
   auto run = [&](auto kernel, std::atomic<uint64_t>& done) {
@@ -370,8 +376,8 @@ struct GradParams {
 };
 
 // Rows of more than 8192 elements: a row at a time per block of 512 threads, V
-// chunks of 16 elements each, in registers between the sum and dx; V = 0: any width,
-// the row read twice (and dw formed by rmsnorm_grad_columns_kernel).
+// chunks of 16 elements each, in registers between the sum and dx; V = 0 (over 16384):
+// any width, the row read twice (and once more for dw by rmsnorm_grad_columns_kernel).
 template <typename T, int V>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_long_kernel(GradParams p) {
   __shared__ float red[2][kNormMaxThreads / 32];
@@ -466,12 +472,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_long_kernel(Grad
 }
 
 // The gradient of rows of up to 8192 elements, with the same ring for dy, h and
-// dresidual (rows off 16-byte boundaries go there through registers). A block
-// takes two rows at a time: the first pass over the fetched pieces forms both
-// rows' sums, which cross the block together (a row's sum, barriers and all, takes
-// longer than its arithmetic: 4096 x 8192 one row at a time 46 us), the second
-// reads them again from shared memory for dx. dw of the block's rows stays in
-// registers.
+// dresidual (off 16-byte boundaries and over 4096 elements a thread also reads the next
+// one's piece, behind a barrier). A block takes two rows at a time: the first pass over
+// the fetched pieces forms both rows' sums, which cross the block together (a row's sum,
+// barriers and all, takes longer than its arithmetic: 4096 x 8192 one row at a time
+// 46 us), the second reads them again from shared memory for dx. dw of the block's rows
+// stays in registers.
 template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(kNormMaxThreads, 1) rmsnorm_grad_wide_kernel(GradParams p) {
   extern __shared__ uint4 ring[];  // stages x (dy, h, dres) x V x threads
@@ -686,7 +692,8 @@ GradPlan grad_plan(int64_t rows, int64_t cols, int sms) {
     g.v = pieces <= kNormMaxThreads ? 1 : 2;
     g.threads = (int)((pieces + 32 * g.v - 1) / (32 * g.v) * 32);
     // Blocks of few threads share an SM; each adds a row of partial sums to reduce (4096 x
-    // 2048: two 20.4, three 17.1, four 19.5 us).
+    // 2048: two 20.4, three 17.1, four 19.5 us). Off 16-byte boundaries two of 192 to 256
+    // threads fit with their double rings, and the rest start later (4096 x 2001: 34 us).
     most = g.threads <= 64 ? 4 * n : (g.threads <= 256 ? 3 * n : n);
   } else {
     const int64_t chunks = (cols + 15) / 16, v = (chunks + kNormMaxThreads - 1) / kNormMaxThreads;

@@ -467,7 +467,7 @@ __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t addr_cluster)
 }
 
 // ---------------------------------------------------------------- cp.async
-// 16 bytes global -> shared (through L2 alone), `bytes` (0 or 16) of them read
+// 16 bytes global -> shared (through L2 alone), the first `bytes` (0 to 16) of them read
 // and the rest zero; both addresses 16-byte aligned.
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),

@@ -13,6 +13,9 @@ A training step of a linear layer y = x W^T in 8 bits::
     xt = mx.quantize(x, "mxfp8", transpose=True)       # (k, m), blocks along m
     dx, dw = mx.linear_backward(dy, qwt, xt, workspace=ws)   # qwt: W^T, (k, n)
 
+The functions return plain tensors, without autograd history: gradients are the
+calls above. The norm's weight has x's type.
+
 Every function runs on the current stream of the tensors' device, or on
 ``stream``; the tensors it allocates then belong to that stream. Wrong
 arguments raise ValueError, a refusal by the library SkgError.
