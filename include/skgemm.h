@@ -611,6 +611,96 @@ skg_status_t skg_gemm_mx(int64_t m, int64_t n, int64_t k, float alpha, const voi
  * and the launch ends with SKG_ERR_PIPELINE_TIMEOUT in its report. */
 skg_status_t skg_mx_test_stall(int32_t stages, uint64_t timeout_ns);
 
+/* ------------------------------------------------------------------------
+ * A layer's projections in 16 bits: a shared projection with the low-rank
+ * adapters of many requests, and the gated feed-forward with its gradients.
+ *
+ * Matrices are row-major on the device, of one type (dtype: skg_in_t), with ld
+ * elements from row to row: a multiple of 8 (where there is more than one row),
+ * base addresses 16-byte aligned (the TMA engine's rules), else
+ * SKG_ERR_UNSUPPORTED. `hidden` is a multiple of 8. Products and sums are in
+ * fp32 on the tensor cores; results are rounded once to dtype. The same inputs
+ * give the same result every time. Outputs overlap no input and no other output.
+ * Sizes of zero are valid (sums over nothing are zero).
+ *
+ * workspace: device, 256-byte aligned, skg_workspace_size_layers bytes, zeroed
+ * once with skg_workspace_init; holds the report (skg_report_read) that a wait
+ * which runs out is recorded in (SKG_ERR_PIPELINE_TIMEOUT; the outputs are then
+ * undefined). Nothing else is kept there: calls may share it, also at the same
+ * time. scratch: device, 256-byte aligned, of the call's own (calls at the same
+ * time need one each), not initialised; skg_scratch_size_* bytes. */
+size_t skg_workspace_size_layers(void);
+
+/* Low-rank adapters: a stack of `count` pairs (A_s rank x k, B_s n x rank), the
+ * matrices stride_* elements apart (a multiple of 8), and the adapter of each row
+ * of x. Ranks are multiples of 8, at most 512; adapters of different ranks share a
+ * stack whose unused rows of A_s and columns of B_s are zero. */
+typedef struct {
+  const void* down;     /* A: count x rank x k */
+  int64_t ld_down, stride_down;
+  const void* up;       /* B: count x n x rank */
+  int64_t ld_up, stride_up;
+  const int32_t* index; /* m: the adapter of each row, in any order; a value that is
+                           negative or not below count: none */
+  const float* scale;   /* count, or NULL = 1 */
+  int32_t count, rank;
+} skg_adapters_t;
+
+/* Y = X W^T (X m x k, W n x k, Y m x n) and, with adapters (NULL: none), for every
+ * row i with adapter s = index[i]
+ *     y_i += scale_s (x_i A_s^T) B_s^T.
+ * x_i A_s^T is held in twice dtype's mantissa between the products (in fp16 up to
+ * 65504, infinite beyond). An adapter's infinities and NaN reach its own rows alone.
+ */
+size_t skg_scratch_size_linear(int64_t m, int32_t rank);
+skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                        int64_t ldw, const skg_adapters_t* adapters, void* Y, int64_t ldy,
+                        int32_t dtype, void* workspace, size_t ws_bytes, void* scratch,
+                        size_t scratch_bytes, void* stream);
+
+/* act: SKG_ACT_SILU g / (1 + e^-g); SKG_ACT_GELU g Phi(g); SKG_ACT_GELU_TANH
+ * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2; SKG_ACT_RELU max(g, 0). */
+typedef enum {
+  SKG_ACT_SILU = 0,
+  SKG_ACT_GELU = 1,
+  SKG_ACT_GELU_TANH = 2,
+  SKG_ACT_RELU = 3
+} skg_act_t;
+
+/* H = act(X W_gate^T) * (X W_up^T): X m x k, W 2 hidden x k (W_gate's rows, then
+ * W_up's), H m x hidden; PRE: NULL, or m x 2 hidden, both projections (the gate's
+ * columns, then the other's) as the gradients want them. */
+skg_status_t skg_gated(int64_t m, int64_t hidden, int64_t k, const void* X, int64_t ldx,
+                       const void* W, int64_t ldw, int32_t act, void* H, int64_t ldh, void* PRE,
+                       int64_t ldp, int32_t dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* Its gradients from dH: with (g | u) = PRE,
+ *     dPRE = (dH * u * act'(g) | dH * act(g)), rounded to dtype (up to 128 rows held
+ *     in twice its mantissa), dX = dPRE W (m x k), dW = dPRE^T X (2 hidden x k). */
+size_t skg_scratch_size_gated_backward(int64_t m, int64_t hidden);
+skg_status_t skg_gated_backward(int64_t m, int64_t hidden, int64_t k, const void* dH, int64_t lddh,
+                                const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                const void* PRE, int64_t ldp, int32_t act, void* dX, int64_t lddx,
+                                void* dW, int64_t lddw, int32_t dtype, void* workspace,
+                                size_t ws_bytes, void* scratch, size_t scratch_bytes, void* stream);
+
+/* The gradients of Y = H W_out^T (W_out k x hidden) with H = gated(X, W_in), from dY
+ * (m x k): dH = dY W_out in fp32, dX and dW_in as above, and
+ *     dW_out = dY^T H (k x hidden), H formed again from PRE and rounded as dPRE is. */
+size_t skg_scratch_size_feed_forward_backward(int64_t m, int64_t hidden);
+skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, const void* dY,
+                                       int64_t lddy, const void* X, int64_t ldx, const void* W_in,
+                                       int64_t ldw_in, const void* W_out, int64_t ldw_out,
+                                       const void* PRE, int64_t ldp, int32_t act, void* dX,
+                                       int64_t lddx, void* dW_in, int64_t lddw_in, void* dW_out,
+                                       int64_t lddw_out, int32_t dtype, void* workspace,
+                                       size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                       void* stream);
+
+/* Testing only: as skg_mx_test_stall, for the entry points above (stages of 64
+ * elements of k). */
+skg_status_t skg_layers_test_stall(int32_t stages, uint64_t timeout_ns);
+
 /* Number of SMs of the current device (0 if there is no device). */
 int32_t skg_device_sm_count(void);
 

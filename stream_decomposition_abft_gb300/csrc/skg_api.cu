@@ -963,6 +963,22 @@ CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, int elem_by
                   swz);
 }
 
+CUresult encode_tensor_map3(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes,
+                            const void* base, uint64_t inner, uint64_t rows, uint64_t matrices,
+                            uint64_t row_stride_elems, uint64_t matrix_stride_elems,
+                            uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz) {
+  if (!tensor_map_encoder()) return CUDA_ERROR_NOT_SUPPORTED;
+  cuuint64_t dims[3] = {inner, rows, matrices};
+  cuuint64_t strides[2] = {row_stride_elems * (uint64_t)elem_bytes,
+                           matrix_stride_elems * (uint64_t)elem_bytes};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return tensor_map_encoder()(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 cudaError_t opt_in_smem(const void* kernel, std::atomic<uint64_t>& done, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -144,6 +144,12 @@ CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dt, int elem_by
                            uint64_t row_stride_elems, uint32_t box_inner, uint32_t box_outer,
                            CUtensorMapSwizzle swz);
 
+// The same of a stack of row-major matrices, boxes of box_inner x box_rows of one matrix.
+CUresult encode_tensor_map3(CUtensorMap* map, CUtensorMapDataType dt, int elem_bytes,
+                            const void* base, uint64_t inner, uint64_t rows, uint64_t matrices,
+                            uint64_t row_stride_elems, uint64_t matrix_stride_elems,
+                            uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
+
 // The report in a workspace's header.
 skg_report_t* workspace_report(void* workspace);
 

@@ -1,0 +1,650 @@
+// The entry points of a layer's projections (skgemm.h): checks, the choice of kernel, tensor
+// maps and launches; and the elementwise kernel of the gated product's gradient.
+//
+//   skg_linear                   t = scale (x A^T) (skg_lora.cu), then y = x W^T + t B^T
+//   skg_gated                    one kernel: both projections, the activation, the product
+//   skg_gated_backward           dPRE elementwise; dX = dPRE W; dW = dPRE^T X
+//   skg_feed_forward_backward    dH = dY W_out (fp32); dPRE and H elementwise; dX; dW_in;
+//                                dW_out = dY^T H
+//
+// The products run on skg_lin_single.cu's or skg_lin_pair.cu's kernels, which read operands
+// stored along either dimension in place.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "skg_lin.cuh"
+
+namespace skg {
+namespace {
+
+std::atomic<uint32_t> g_test_stages{0};
+std::atomic<uint64_t> g_test_limit{0};
+
+// Up to so many rows, dPRE and H are kept as sums of two numbers of dtype. Rounding them
+// once adds as much error to a gradient as its own rounding: in the root of the mean square
+// sqrt(2) times the latter alone over many elements, and anything over few. Up to 128 rows
+// the products wait for the weights' bytes and twice the MMAs cost nothing.
+constexpr int64_t kTwoTermRows = 128;
+
+constexpr int64_t kMaxDim = INT32_MAX / 4;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// ------------------------------------------------------------------ dPRE and H
+struct DgateParams {
+  int64_t m;
+  int f, f32, act;
+  const void* dh;
+  int64_t lddh;
+  const void* pre;
+  int64_t ldp;
+  void* dpre;     // m x 2 f
+  void* dpre_lo;  // its low parts, or NULL
+  void* h;        // m x f, or NULL
+  void* h_lo;
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  union {
+    uint4 q;
+    T e[8];
+  } u;
+  u.q = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(u.e[i]);
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = a.z;
+  v[3] = a.w;
+  v[4] = b.x;
+  v[5] = b.y;
+  v[6] = b.z;
+  v[7] = b.w;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* hi, T* lo, const float (&v)[8]) {
+  union {
+    uint4 q;
+    T e[8];
+  } h, l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h.e[i] = mx_from_f32<T>(v[i]);
+    const float r = v[i] - mx_to_f32(h.e[i]);
+    l.e[i] = mx_from_f32<T>(isfinite(r) ? r : 0.f);
+  }
+  *reinterpret_cast<uint4*>(hi) = h.q;
+  if (lo) *reinterpret_cast<uint4*>(lo) = l.q;
+}
+
+// Eight elements of a row per thread; reads and writes each element once, so memory bounds it.
+template <typename T, typename D>
+__global__ void __launch_bounds__(128) dgate_kernel(const DgateParams p) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int col = ((int)blockIdx.x * 128 + (int)threadIdx.x) * 8;
+  if (col >= p.f) return;
+  for (int64_t row = blockIdx.y; row < p.m; row += gridDim.y) {
+    float d[8], g[8], u[8], dg[8], du[8], h[8];
+    load8<D>(reinterpret_cast<const D*>(p.dh) + row * p.lddh + col, d);
+    const T* pre = reinterpret_cast<const T*>(p.pre) + row * p.ldp + col;
+    load8<T>(pre, g);
+    load8<T>(pre + p.f, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float da;
+      const float a = lin_act<true>(p.act, g[i], da);
+      dg[i] = d[i] * u[i] * da;
+      du[i] = d[i] * a;
+      h[i] = a * u[i];
+    }
+    const int64_t at = row * 2 * p.f + col;
+    T *hi = reinterpret_cast<T*>(p.dpre) + at, *lo = reinterpret_cast<T*>(p.dpre_lo);
+    lo = lo ? lo + at : lo;
+    store8<T>(hi, lo, dg);
+    store8<T>(hi + p.f, lo ? lo + p.f : lo, du);
+    if (p.h) {
+      T* hlo = reinterpret_cast<T*>(p.h_lo);
+      store8<T>(reinterpret_cast<T*>(p.h) + row * p.f + col, hlo ? hlo + row * p.f + col : hlo, h);
+    }
+  }
+}
+
+cudaError_t launch_dgate(int dtype, const DgateParams& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.f / 8 + 127) / 128), (unsigned)(p.m < 32768 ? p.m : 32768));
+  if (dtype == SKG_IN_F16)
+    return p.f32 ? launch_pdl(dgate_kernel<__half, float>, grid, dim3(128), 0, stream, p)
+                 : launch_pdl(dgate_kernel<__half, __half>, grid, dim3(128), 0, stream, p);
+  return p.f32 ? launch_pdl(dgate_kernel<__nv_bfloat16, float>, grid, dim3(128), 0, stream, p)
+               : launch_pdl(dgate_kernel<__nv_bfloat16, __nv_bfloat16>, grid, dim3(128), 0, stream,
+                            p);
+}
+
+// ------------------------------------------------------------------ products
+struct Operand {
+  const void* p;
+  int64_t ld;
+  bool mn;          // stored k x rows
+  const void* lo;   // low parts, or NULL
+};
+
+struct Product {
+  int mode;
+  int64_t m, n, k;
+  Operand a, b;
+  void* c;
+  int64_t ldc;
+  int out;          // skg_out_t
+  int act;
+  void* pre;
+  int64_t ldp;
+  const skg_adapters_t* adapters;
+  void* t;
+  LoraPlan* plan;
+  int rank_pad;
+};
+
+struct Common {
+  int dtype, sms;
+  skg_report_t* report;
+  uint32_t stages;
+  uint64_t limit;
+  cudaStream_t stream;
+};
+
+int out_of(int dtype) { return dtype == SKG_IN_F16 ? SKG_OUT_F16 : SKG_OUT_BF16; }
+
+CUtensorMapDataType tma_type(int dtype) {
+  return dtype == SKG_IN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// Rows of a matrix of one row lie nowhere: any stride that the engine takes.
+int64_t ld_of(int64_t ld, int64_t rows, int64_t inner) {
+  return rows > 1 ? ld : (inner + 7) / 8 * 8;
+}
+
+bool map2(CUtensorMap* t, int dtype, const void* p, int64_t inner, int64_t rows, int64_t ld,
+          int box_inner, int box_rows) {
+  return encode_tensor_map(t, tma_type(dtype), 2, p, (uint64_t)inner, (uint64_t)rows,
+                           (uint64_t)ld_of(ld, rows, inner), (uint32_t)box_inner,
+                           (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+// An operand of `rows` rows: K-major boxes of 64 x box_rows, MN-major ones of 64 x 64.
+bool map_operand(CUtensorMap* t, int dtype, const Operand& o, const void* p, int64_t rows,
+                 int64_t k, int box_rows) {
+  return o.mn ? map2(t, dtype, p, rows, k, o.ld, 64, kLinK)
+              : map2(t, dtype, p, k, rows, o.ld, kLinK, box_rows);
+}
+
+// Single CTAs: how many share a 128 x 128 tile (S), and the estimated time (us).
+struct SinglePlan {
+  int split;
+  double us;
+};
+SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms) {
+  SinglePlan best = {1, 1e30};
+  for (int s = 1; s <= (m <= 16 ? 8 : 4); s *= 2) {
+    if (s > 1 && (tiles * s > 2 * sms || s > ksteps)) break;
+    const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
+    const int stages = (ksteps + s - 1) / s;
+    const double us = tiles * s <= sms ? (s > 1 ? 4.2 : 3.2) + 0.36 * stages
+                                       : (s > 1 && m > 64 ? 6.5 : 5.2) + 0.48 * waves * stages;
+    if (m <= 16 || us < best.us) best = {s, us};
+  }
+  return best;
+}
+
+// Whether a product runs on CTA pairs.
+bool wants_pairs(int64_t m, int64_t tiles, int ksteps, int clusters, double single_us) {
+  if (m <= kLinTile) return false;
+  return 4.2 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;
+}
+
+skg_status_t run_product(const Product& q, const Common& c) {
+  LinParams p = {};
+  p.m = (int)q.m;
+  p.n = (int)q.n;
+  p.k = (int)q.k;
+  p.ksteps = (int)((q.k + kLinK - 1) / kLinK);
+  p.terms = q.a.lo || q.b.lo ? 2 : 1;
+  p.lo_b = q.b.lo != nullptr;
+  p.act = q.act;
+  p.c = q.c;
+  p.ldc = ld_of(q.ldc, q.m, q.n);
+  p.pre = q.pre;
+  p.ldp = ld_of(q.ldp, q.m, 2 * q.n);
+  p.plan = q.plan;
+  p.rank_pad = q.rank_pad;
+  p.report = c.report;
+  p.stages = c.stages ? c.stages : UINT32_MAX;
+  p.limit = c.limit ? c.limit : kMxTimeoutNs;
+  const bool gated = q.mode == kLinGated;
+  const int64_t cols = gated ? 2 * q.n : q.n;  // of the accumulators
+  const int64_t tm1 = (q.m + 127) / 128, tn1 = (cols + 127) / 128;
+  const int64_t tm2 = (q.m + 255) / 256, tn2 = (cols + 255) / 256;
+  const int resident = lin_pair_clusters_resident();
+  const SinglePlan single = single_plan(q.m, tm1 * tn1, p.ksteps * p.terms, c.sms);
+  const bool pair = q.out != SKG_OUT_F32 && resident > 0 &&
+                    wants_pairs(q.m, tm2 * tn2, p.ksteps * p.terms, resident, single.us);
+  p.tiles_m = (int)(pair ? tm2 : tm1);
+  p.tiles_n = (int)(pair ? tn2 : tn1);
+  p.split = pair ? 1 : single.split;
+  if ((int64_t)p.tiles_m * p.tiles_n * p.split > INT32_MAX) return SKG_ERR_UNSUPPORTED;
+  p.a_rows = !pair && q.m < kLinTile ? (p.m + 7) / 8 * 8 : kLinTile;
+  const uint32_t bf16 = c.dtype == SKG_IN_BF16;
+  p.idesc = idesc_f16(bf16, pair ? 256 : 128, pair ? 256 : 128) | ((uint32_t)q.a.mn << 15) |
+            ((uint32_t)q.b.mn << 16);
+
+  // Rows of B's box: a tile's (K-major) columns, or one projection's share of them.
+  const int b_box = pair ? 128 : (gated ? 64 : 128);
+  LinMaps t;
+  if (!map_operand(&t.a, c.dtype, q.a, q.a.p, q.m, q.k, p.a_rows) ||
+      !map_operand(&t.b, c.dtype, q.b, q.b.p, cols, q.k, b_box))
+    return SKG_ERR_CUDA;
+  t.lo = t.t = t.up = t.c = t.gate = t.pre_up = t.a;
+  if (p.terms == 2 &&
+      !(p.lo_b ? map_operand(&t.lo, c.dtype, q.b, q.b.lo, cols, q.k, b_box)
+               : map_operand(&t.lo, c.dtype, q.a, q.a.lo, q.m, q.k, p.a_rows)))
+    return SKG_ERR_CUDA;
+  if (q.plan) {
+    const skg_adapters_t& ad = *q.adapters;
+    if (!map2(&t.t, c.dtype, q.t, 2 * q.rank_pad, q.m, 2 * q.rank_pad, 64, p.a_rows) ||
+        encode_tensor_map3(&t.up, tma_type(c.dtype), 2, ad.up, (uint64_t)ad.rank, (uint64_t)q.n,
+                           (uint64_t)ad.count, (uint64_t)ld_of(ad.ld_up, q.n, ad.rank),
+                           (uint64_t)ld_of(ad.stride_up, ad.count, ad.rank), 64, 128,
+                           CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return SKG_ERR_CUDA;
+  }
+  if (pair) {
+    if (!map2(&t.c, c.dtype, q.c, q.n, q.m, p.ldc, 64, 32)) return SKG_ERR_CUDA;
+    if (q.pre && (!map2(&t.gate, c.dtype, q.pre, q.n, q.m, p.ldp, 64, 32) ||
+                  !map2(&t.pre_up, c.dtype, (const uint16_t*)q.pre + q.n, q.n, q.m, p.ldp, 64, 32)))
+      return SKG_ERR_CUDA;
+  }
+  const LinVariant v = {q.mode, q.a.mn, q.b.mn, q.out};
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  const cudaError_t e =
+      pair ? launch_lin_pair(v, t, p, (int)(tiles < resident ? tiles : resident), c.stream)
+           : launch_lin_single(v, t, p, c.stream);
+  return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
+}
+
+skg_status_t zero(void* c, int64_t ldc, int64_t m, int64_t n, const Common& k) {
+  if (m <= 0 || n <= 0) return SKG_OK;
+  return launch_scale(out_of(k.dtype), c, ldc, (int)m, (int)n, 0.f, k.stream) == cudaSuccess
+             ? SKG_OK
+             : SKG_ERR_CUDA;
+}
+
+// A product whose sums may be over nothing.
+skg_status_t product_or_zero(const Product& q, const Common& c) {
+  if (q.m == 0 || q.n == 0) return SKG_OK;
+  if (q.k == 0) return zero(q.c, ld_of(q.ldc, q.m, q.n), q.m, q.n, c);
+  return run_product(q, c);
+}
+
+// ------------------------------------------------------------------ checks
+// A row-major matrix of rows x cols with elements in it: there, and rows that hold cols.
+bool there(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return rows == 0 || cols == 0 || (p && (rows <= 1 || ld >= cols));
+}
+
+// The TMA engine's rules, of a matrix with elements in it.
+bool aligned(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return rows == 0 || cols == 0 || (((uintptr_t)p & 15) == 0 && (rows == 1 || ld % 8 == 0));
+}
+
+skg_status_t check_sizes(int64_t m, int64_t n, int64_t k, int32_t dtype) {
+  if (m < 0 || n < 0 || k < 0 || (dtype != SKG_IN_F16 && dtype != SKG_IN_BF16)) return SKG_ERR_ARG;
+  if (m > kMaxDim || n > kMaxDim / 2 || k > kMaxDim) return SKG_ERR_UNSUPPORTED;
+  return SKG_OK;
+}
+
+skg_status_t check_memory(void* workspace, size_t ws_bytes, const void* scratch,
+                          size_t scratch_bytes, size_t need) {
+  if (!workspace || ((uintptr_t)workspace & 255) || ws_bytes < skg_workspace_size_layers())
+    return SKG_ERR_WORKSPACE;
+  if (need && (!scratch || ((uintptr_t)scratch & 255) || scratch_bytes < need))
+    return SKG_ERR_WORKSPACE;
+  return SKG_OK;
+}
+
+skg_status_t common(int32_t dtype, void* workspace, void* stream, Common* c) {
+  c->dtype = dtype;
+  c->sms = skg_device_sm_count();
+  if (c->sms <= 0) return SKG_ERR_CUDA;
+  c->report = workspace_report(workspace);
+  c->stages = g_test_stages.load(std::memory_order_relaxed);
+  c->limit = g_test_limit.load(std::memory_order_relaxed);
+  c->stream = (cudaStream_t)stream;
+  return SKG_OK;
+}
+
+// Scratch of the gradients, from its start.
+struct BackwardScratch {
+  size_t dpre, dpre_lo, h, h_lo, dh, total;
+};
+BackwardScratch backward_scratch(int64_t m, int64_t f, bool block) {
+  BackwardScratch s = {};
+  const size_t n = (size_t)m * (size_t)f, two = m <= kTwoTermRows ? 1 : 0;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t a = at;
+    at += up256(bytes);
+    return a;
+  };
+  s.dpre = take(n * 4);
+  s.dpre_lo = take(two * n * 4);
+  s.h = take(block ? n * 2 : 0);
+  s.h_lo = take(block ? two * n * 2 : 0);
+  s.dh = take(block ? n * 4 : 0);
+  s.total = at;
+  return s;
+}
+
+// dX = dPRE W (m x k) and dW = dPRE^T X (2 f x k).
+skg_status_t in_gradients(int64_t m, int64_t f, int64_t k, const void* dpre, const void* dpre_lo,
+                          const void* X, int64_t ldx, const void* W, int64_t ldw, void* dX,
+                          int64_t lddx, void* dW, int64_t lddw, const Common& c) {
+  Product q = {};
+  q.m = m;
+  q.n = k;
+  q.k = 2 * f;
+  q.a = {dpre, 2 * f, false, dpre_lo};
+  q.b = {W, ldw, true, nullptr};
+  q.c = dX;
+  q.ldc = lddx;
+  q.out = out_of(c.dtype);
+  skg_status_t st = product_or_zero(q, c);
+  if (st != SKG_OK) return st;
+  q.m = 2 * f;
+  q.k = m;
+  q.a.mn = true;
+  q.b = {X, ldx, true, nullptr};
+  q.c = dW;
+  q.ldc = lddw;
+  return product_or_zero(q, c);
+}
+
+}  // namespace
+}  // namespace skg
+
+using namespace skg;
+
+extern "C" {
+
+skg_status_t skg_layers_test_stall(int32_t stages, uint64_t timeout_ns) {
+  if (stages < 0) return SKG_ERR_ARG;
+  g_test_stages.store((uint32_t)stages, std::memory_order_relaxed);
+  g_test_limit.store(timeout_ns, std::memory_order_relaxed);
+  return SKG_OK;
+}
+
+size_t skg_workspace_size_layers(void) { return fixed_header_bytes(); }
+
+size_t skg_scratch_size_linear(int64_t m, int32_t rank) {
+  if (m <= 0 || m > kMaxDim || rank <= 0 || rank > 512) return 0;
+  const size_t rp = (size_t)(rank + 15) / 16 * 16;
+  return up256((size_t)((m + kLoraRows - 1) / kLoraRows) * sizeof(LoraPlan)) +
+         up256((size_t)m * 4 * rp);
+}
+
+skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                        int64_t ldw, const skg_adapters_t* ad, void* Y, int64_t ldy, int32_t dtype,
+                        void* workspace, size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                        void* stream) {
+  skg_status_t st = check_sizes(m, n, k, dtype);
+  if (st != SKG_OK) return st;
+  if (!there(X, m, k, ldx) || !there(W, n, k, ldw) || !there(Y, m, n, ldy)) return SKG_ERR_ARG;
+  if (ad) {
+    if (ad->count < 0 || ad->rank < 0 || (m > 0 && !ad->index)) return SKG_ERR_ARG;
+    const bool some = ad->count > 0 && ad->rank > 0;
+    if (some && (!there(ad->down, ad->rank, k, ad->ld_down) ||
+                 !there(ad->up, n, ad->rank, ad->ld_up)))
+      return SKG_ERR_ARG;
+    if (some && ad->count > 1 && (ad->stride_down < 0 || ad->stride_up < 0)) return SKG_ERR_ARG;
+    if (ad->rank > 512 || ad->rank % 8) return SKG_ERR_UNSUPPORTED;
+    if (some && (!aligned(ad->down, ad->rank, k, ad->ld_down) || !aligned(ad->up, n, ad->rank, ad->ld_up) ||
+                 (ad->count > 1 && (ad->stride_down % 8 || ad->stride_up % 8)) ||
+                 ((uintptr_t)ad->index & 3) || ((uintptr_t)ad->scale & 3)))
+      return SKG_ERR_UNSUPPORTED;
+    if (!some) ad = nullptr;
+  }
+  if (m == 0 || n == 0) return SKG_OK;
+  if (!aligned(X, m, k, ldx) || !aligned(W, n, k, ldw) || !aligned(Y, m, n, ldy)) return SKG_ERR_UNSUPPORTED;
+  if (k == 0) ad = nullptr;
+  const size_t need = ad ? skg_scratch_size_linear(m, ad->rank) : 0;
+  st = check_memory(workspace, ws_bytes, scratch, scratch_bytes, need);
+  if (st != SKG_OK) return st;
+  Common c;
+  st = common(dtype, workspace, stream, &c);
+  if (st != SKG_OK) return st;
+  Product q = {};
+  q.m = m;
+  q.n = n;
+  q.k = k;
+  q.a = {X, ldx, false, nullptr};
+  q.b = {W, ldw, false, nullptr};
+  q.c = Y;
+  q.ldc = ldy;
+  q.out = out_of(dtype);
+  if (ad) {
+    q.adapters = ad;
+    q.rank_pad = (ad->rank + 15) / 16 * 16;
+    q.plan = reinterpret_cast<LoraPlan*>(scratch);
+    q.t = (uint8_t*)scratch +
+          up256((size_t)((m + kLoraRows - 1) / kLoraRows) * sizeof(LoraPlan));
+    LoraParams p = {};
+    p.m = (int)m;
+    p.k = (int)k;
+    p.rank = ad->rank;
+    p.rank_pad = q.rank_pad;
+    p.count = ad->count;
+    p.ksteps = (int)((k + kLinK - 1) / kLinK);
+    p.a_rows = m < kLinTile ? (p.m + 7) / 8 * 8 : kLinTile;
+    const int cols = q.rank_pad < 128 ? q.rank_pad : 128, per = 128 / cols;
+    p.idesc = idesc_f16(dtype == SKG_IN_BF16, 128, (uint32_t)(per * cols));
+    p.index = ad->index;
+    p.scale = ad->scale;
+    p.t = q.t;
+    p.plan = q.plan;
+    p.stages = c.stages ? c.stages : UINT32_MAX;
+    p.limit = c.limit ? c.limit : kMxTimeoutNs;
+    p.report = c.report;
+    // As many CTAs to the rows' k as fit the GPU at once, then clusters for more passes.
+    const int64_t tiles = (m + kLinTile - 1) / kLinTile;
+    p.split = 1;
+    while (p.split < 8 && tiles * p.split * 2 <= 2 * c.sms && p.split * 2 <= p.ksteps) p.split *= 2;
+    const int most = ad->count < kLinTile ? ad->count : kLinTile;
+    const int passes = q.rank_pad > 128 ? most * ((q.rank_pad + 127) / 128) : (most + per - 1) / per;
+    const int64_t room = 2 * c.sms / (tiles * p.split);
+    p.groups = (int)(room < 1 ? 1 : (room < passes ? room : passes));
+    CUtensorMap tx, td;
+    if (!map2(&tx, dtype, X, k, m, ldx, kLinK, p.a_rows) ||
+        encode_tensor_map3(&td, tma_type(dtype), 2, ad->down, (uint64_t)k, (uint64_t)ad->rank,
+                           (uint64_t)ad->count, (uint64_t)ld_of(ad->ld_down, ad->rank, k),
+                           (uint64_t)ld_of(ad->stride_down, ad->count, k), kLinK, (uint32_t)cols,
+                           CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return SKG_ERR_CUDA;
+    if (launch_lora_down(dtype, tx, td, p, c.stream) != cudaSuccess) return SKG_ERR_CUDA;
+  }
+  return product_or_zero(q, c);
+}
+
+skg_status_t skg_gated(int64_t m, int64_t hidden, int64_t k, const void* X, int64_t ldx,
+                       const void* W, int64_t ldw, int32_t act, void* H, int64_t ldh, void* PRE,
+                       int64_t ldp, int32_t dtype, void* workspace, size_t ws_bytes, void* stream) {
+  skg_status_t st = check_sizes(m, hidden, k, dtype);
+  if (st != SKG_OK) return st;
+  if (act < SKG_ACT_SILU || act > SKG_ACT_RELU) return SKG_ERR_ARG;
+  if (!there(X, m, k, ldx) || !there(W, 2 * hidden, k, ldw) || !there(H, m, hidden, ldh) ||
+      (PRE && !there(PRE, m, 2 * hidden, ldp)))
+    return SKG_ERR_ARG;
+  if (hidden % 8) return SKG_ERR_UNSUPPORTED;
+  if (m == 0 || hidden == 0) return SKG_OK;
+  if (!aligned(X, m, k, ldx) || !aligned(W, 2, k, ldw) || !aligned(H, m, hidden, ldh) ||
+      (PRE && !aligned(PRE, m, 2 * hidden, ldp)))
+    return SKG_ERR_UNSUPPORTED;
+  st = check_memory(workspace, ws_bytes, nullptr, 0, 0);
+  if (st != SKG_OK) return st;
+  Common c;
+  st = common(dtype, workspace, stream, &c);
+  if (st != SKG_OK) return st;
+  if (k == 0) {  // act(0) * 0
+    st = zero(H, ld_of(ldh, m, hidden), m, hidden, c);
+    return st == SKG_OK && PRE ? zero(PRE, ld_of(ldp, m, 2 * hidden), m, 2 * hidden, c) : st;
+  }
+  Product q = {};
+  q.mode = kLinGated;
+  q.m = m;
+  q.n = hidden;
+  q.k = k;
+  q.a = {X, ldx, false, nullptr};
+  q.b = {W, ldw, false, nullptr};
+  q.c = H;
+  q.ldc = ldh;
+  q.out = out_of(dtype);
+  q.act = act;
+  q.pre = PRE;
+  q.ldp = ldp;
+  return run_product(q, c);
+}
+
+size_t skg_scratch_size_gated_backward(int64_t m, int64_t hidden) {
+  if (m <= 0 || hidden <= 0 || m > kMaxDim || hidden > kMaxDim / 2) return 0;
+  return backward_scratch(m, hidden, false).total;
+}
+
+skg_status_t skg_gated_backward(int64_t m, int64_t hidden, int64_t k, const void* dH, int64_t lddh,
+                                const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                const void* PRE, int64_t ldp, int32_t act, void* dX, int64_t lddx,
+                                void* dW, int64_t lddw, int32_t dtype, void* workspace,
+                                size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                void* stream) {
+  skg_status_t st = check_sizes(m, hidden, k, dtype);
+  if (st != SKG_OK) return st;
+  if (act < SKG_ACT_SILU || act > SKG_ACT_RELU) return SKG_ERR_ARG;
+  if (!there(dH, m, hidden, lddh) || !there(X, m, k, ldx) || !there(W, 2 * hidden, k, ldw) ||
+      !there(PRE, m, 2 * hidden, ldp) || !there(dX, m, k, lddx) || !there(dW, 2 * hidden, k, lddw))
+    return SKG_ERR_ARG;
+  if (hidden % 8) return SKG_ERR_UNSUPPORTED;
+  if (!aligned(dH, m, hidden, lddh) || !aligned(X, m, k, ldx) || !aligned(W, 2 * hidden, k, ldw) ||
+      !aligned(PRE, m, 2 * hidden, ldp) || !aligned(dX, m, k, lddx) ||
+      !aligned(dW, 2 * hidden, k, lddw))
+    return SKG_ERR_UNSUPPORTED;
+  if (k == 0 || (m == 0 && hidden == 0)) return SKG_OK;
+  st = check_memory(workspace, ws_bytes, scratch, scratch_bytes,
+                    skg_scratch_size_gated_backward(m, hidden));
+  if (st != SKG_OK) return st;
+  Common c;
+  st = common(dtype, workspace, stream, &c);
+  if (st != SKG_OK) return st;
+  const BackwardScratch s = backward_scratch(m, hidden, false);
+  uint8_t* base = (uint8_t*)scratch;
+  const bool two = m <= kTwoTermRows;
+  if (m > 0 && hidden > 0) {
+    DgateParams d = {};
+    d.m = m;
+    d.f = (int)hidden;
+    d.act = act;
+    d.dh = dH;
+    d.lddh = lddh;
+    d.pre = PRE;
+    d.ldp = ldp;
+    d.dpre = base + s.dpre;
+    d.dpre_lo = two ? base + s.dpre_lo : nullptr;
+    if (launch_dgate(dtype, d, c.stream) != cudaSuccess) return SKG_ERR_CUDA;
+  }
+  return in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W, ldw,
+                      dX, lddx, dW, lddw, c);
+}
+
+size_t skg_scratch_size_feed_forward_backward(int64_t m, int64_t hidden) {
+  if (m <= 0 || hidden <= 0 || m > kMaxDim || hidden > kMaxDim / 2) return 0;
+  return backward_scratch(m, hidden, true).total;
+}
+
+skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, const void* dY,
+                                       int64_t lddy, const void* X, int64_t ldx, const void* W_in,
+                                       int64_t ldw_in, const void* W_out, int64_t ldw_out,
+                                       const void* PRE, int64_t ldp, int32_t act, void* dX,
+                                       int64_t lddx, void* dW_in, int64_t lddw_in, void* dW_out,
+                                       int64_t lddw_out, int32_t dtype, void* workspace,
+                                       size_t ws_bytes, void* scratch, size_t scratch_bytes,
+                                       void* stream) {
+  skg_status_t st = check_sizes(m, hidden, k, dtype);
+  if (st != SKG_OK) return st;
+  if (act < SKG_ACT_SILU || act > SKG_ACT_RELU) return SKG_ERR_ARG;
+  if (!there(dY, m, k, lddy) || !there(X, m, k, ldx) || !there(W_in, 2 * hidden, k, ldw_in) ||
+      !there(W_out, k, hidden, ldw_out) || !there(PRE, m, 2 * hidden, ldp) ||
+      !there(dX, m, k, lddx) || !there(dW_in, 2 * hidden, k, lddw_in) ||
+      !there(dW_out, k, hidden, lddw_out))
+    return SKG_ERR_ARG;
+  if (hidden % 8) return SKG_ERR_UNSUPPORTED;
+  if (!aligned(dY, m, k, lddy) || !aligned(X, m, k, ldx) ||
+      !aligned(W_in, 2 * hidden, k, ldw_in) || !aligned(W_out, k, hidden, ldw_out) ||
+      !aligned(PRE, m, 2 * hidden, ldp) || !aligned(dX, m, k, lddx) ||
+      !aligned(dW_in, 2 * hidden, k, lddw_in) || !aligned(dW_out, k, hidden, lddw_out))
+    return SKG_ERR_UNSUPPORTED;
+  if (k == 0 || (m == 0 && hidden == 0)) return SKG_OK;
+  st = check_memory(workspace, ws_bytes, scratch, scratch_bytes,
+                    skg_scratch_size_feed_forward_backward(m, hidden));
+  if (st != SKG_OK) return st;
+  Common c;
+  st = common(dtype, workspace, stream, &c);
+  if (st != SKG_OK) return st;
+  const BackwardScratch s = backward_scratch(m, hidden, true);
+  uint8_t* base = (uint8_t*)scratch;
+  const bool two = m <= kTwoTermRows;
+  if (m > 0 && hidden > 0) {
+    Product q = {};
+    q.m = m;
+    q.n = hidden;
+    q.k = k;
+    q.a = {dY, lddy, false, nullptr};
+    q.b = {W_out, ldw_out, true, nullptr};
+    q.c = base + s.dh;
+    q.ldc = hidden;
+    q.out = SKG_OUT_F32;
+    st = run_product(q, c);
+    if (st != SKG_OK) return st;
+    DgateParams d = {};
+    d.m = m;
+    d.f = (int)hidden;
+    d.f32 = 1;
+    d.act = act;
+    d.dh = base + s.dh;
+    d.lddh = hidden;
+    d.pre = PRE;
+    d.ldp = ldp;
+    d.dpre = base + s.dpre;
+    d.dpre_lo = two ? base + s.dpre_lo : nullptr;
+    d.h = base + s.h;
+    d.h_lo = two ? base + s.h_lo : nullptr;
+    if (launch_dgate(dtype, d, c.stream) != cudaSuccess) return SKG_ERR_CUDA;
+  }
+  st = in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W_in,
+                    ldw_in, dX, lddx, dW_in, lddw_in, c);
+  if (st != SKG_OK) return st;
+  Product q = {};
+  q.m = k;
+  q.n = hidden;
+  q.k = m;
+  q.a = {dY, lddy, true, nullptr};
+  q.b = {base + s.h, hidden, true, two ? base + s.h_lo : nullptr};
+  q.c = dW_out;
+  q.ldc = lddw_out;
+  q.out = out_of(dtype);
+  return product_or_zero(q, c);
+}
+
+}  // extern "C"

@@ -1,0 +1,254 @@
+// What the kernels of a layer's projections share: parameters, bounded waits, the
+// activations, one stage's MMAs and the plan of the low-rank adapters.
+//
+// All of them form sums over k of A[i][l] B[j][l] in 16 bits with fp32 accumulation on
+// tcgen05 (kind::f16), 64 elements of k (128 bytes of a K-major row) to a stage:
+//
+//   skg_lin_single.cu  128 x 128 tiles on single CTAs, k split over a cluster where the
+//                      tiles are few
+//   skg_lin_pair.cu    256 x 256 tiles on CTA pairs
+//
+// with these ways out (LinMode):
+//   kLinPlain   C = A B^T, and with adapters + scale_s (x A_s^T) B_s^T per row
+//   kLinGated   B holds two projections of n rows each; a tile takes half of its columns
+//               from either, so one thread holds gate and up of an output:
+//               H = act(gate) * up, and PRE = (gate | up) where it is asked for
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "skg_internal.h"
+#include "skg_mx.cuh"
+#include "skg_mx_gemm.cuh"
+#include "skgemm.h"
+
+namespace skg {
+
+constexpr int kLinThreads = 192;
+constexpr int kLinTile = 128;
+constexpr int kLinK = 64;                      // elements of k in a stage
+constexpr int kLinOperand = kLinTile * 128;    // bytes of an operand's 128 rows in a stage
+constexpr int kLinBox = 64 * 128;              // bytes of an MN-major box: 64 k x 64 elements
+constexpr int kLoraRows = 256;                 // rows that one adapter plan covers
+
+enum LinMode { kLinPlain = 0, kLinGated = 1 };
+
+// The adapters that 256 rows use, in the order of their first rows, and the rows of each
+// (word w, bit b: row 32 w + b).
+struct LoraPlan {
+  int32_t count;
+  int32_t pad[3];
+  int32_t id[kLoraRows];
+  uint32_t rows[kLoraRows][8];
+};
+
+struct LinParams {
+  int m, n, k;        // rows and columns of the result (of one projection), length of the sums
+  int ksteps;         // stages of k
+  int terms;          // 2: one operand is a sum of two (high and low parts): each stage of k runs
+                      // once with either
+  int lo_b;           // that operand is B, not A
+  int tiles_m, tiles_n;
+  int split;          // single CTAs: CTAs per tile (cluster size)
+  int direct;         // single CTAs: C is written from registers
+  int a_rows;         // single CTAs, K-major A: rows of A's box
+  uint32_t idesc;
+  int act;            // kLinGated
+  void* c;
+  int64_t ldc;
+  void* pre;          // kLinGated: (gate | up), or NULL
+  int64_t ldp;
+  const LoraPlan* plan;  // adapters: one per 256 rows, or NULL
+  int rank_pad;          // their rank, rounded up to 16
+  uint32_t stages;    // a CTA loads no more stages than this (skg_layers_test_stall)
+  uint64_t limit;     // bound of a wait, ns
+  skg_report_t* report;
+};
+
+// The tensor maps of one launch. Unused ones repeat a.
+struct LinMaps {
+  CUtensorMap a, b;
+  CUtensorMap lo;         // the two-term operand's low parts
+  CUtensorMap t, up;      // adapters: scale (x A^T) in high and low parts; their B (3 dimensions)
+  CUtensorMap c, gate, pre_up;  // pairs: stores
+};
+
+struct LinAux : MxAux {
+  uint64_t tempty1;
+};
+
+__device__ __forceinline__ void lin_fail(const LinParams& p, LinAux* aux) {
+  if (atomicExch(&aux->abort_flag, 1) == 0) {
+    atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
+    atomicAdd(&p.report->timeouts, 1u);
+  }
+}
+
+// ------------------------------------------------------------------ activations
+// act(g), and its derivative in d. Relative errors of a few 2^-24 (times |g| / 8 where e^-g
+// is far from 1): below a 16-bit result's rounding by a thousand times.
+__device__ __forceinline__ float lin_sigmoid(float x) {
+  return __fdividef(1.f, 1.f + __expf(-x));  // e^-x = inf gives 0
+}
+
+template <bool GRAD>
+__device__ __forceinline__ float lin_act(int act, float g, float& d) {
+  if (act == SKG_ACT_SILU) {
+    const float p = lin_sigmoid(g);
+    if (GRAD) d = p * (1.f + g * (1.f - p));
+    return g * p;
+  }
+  if (act == SKG_ACT_GELU) {
+    const float p = 0.5f * erfcf(-0.70710678f * g);  // not 1 + erf, whose sum cancels for g < 0
+    if (GRAD) d = p + g * (0.39894228f * __expf(-0.5f * g * g));
+    return g * p;
+  }
+  if (act == SKG_ACT_GELU_TANH) {
+    // (1 + tanh u) / 2 = sigmoid(2 u)
+    const float p = lin_sigmoid(1.59576912f * (g + 0.044715f * g * g * g));
+    const float q = p * (1.f - p);
+    if (GRAD) d = q == 0.f ? p : p + g * q * (1.59576912f * (1.f + 0.134145f * g * g));
+    return g * p;
+  }
+  if (GRAD) d = g > 0.f ? 1.f : (g == g ? 0.f : g);
+  return g > 0.f ? g : (g == g ? 0.f : g);
+}
+
+__device__ __forceinline__ float lin_gated(int act, float gate, float up) {
+  float d;
+  return lin_act<false>(act, gate, d) * up;
+}
+
+// ------------------------------------------------------------------ MMAs
+// Masked forms: rows of the accumulator (TMEM lanes) whose bit in `off` is set keep their
+// values, whatever the products for them are.
+__device__ __forceinline__ void umma_f16_rows(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_f16_rows_pair(uint32_t d, uint64_t a, uint64_t b,
+                                                   uint32_t idesc, const uint32_t (&off)[8]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, "
+      "{%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
+      "r"(off[5]), "r"(off[6]), "r"(off[7])
+      : "memory");
+}
+
+// 3D tiled loads (adapter s's rows of a stack): as tma_load_2d and tma_load_2d_pair.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int32_t c0, int32_t c1,
+                                                 int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Descriptors of an operand in a stage at shared address `at`, and their advance for 16
+// elements of k: 32 bytes within a K-major row; two groups of eight k rows (2048 bytes) of an
+// MN-major box, whose 64-element boxes lie kLinBox apart (the leading byte offset).
+template <bool MN>
+__device__ __forceinline__ uint64_t lin_desc(uint32_t at) {
+  const uint64_t d = sdesc_sw128(at);
+  return MN ? d + ((uint64_t)((kLinBox >> 4) - 1) << 16) : d;
+}
+template <bool MN>
+__host__ __device__ constexpr int lin_step() { return MN ? 2048 >> 4 : 2; }
+
+// The MMAs of one stage; those wholly past k are left out.
+template <bool PAIR, bool AMN, bool BMN>
+__device__ __forceinline__ void lin_stage_mmas(uint32_t d, uint32_t a_at, uint32_t b_at,
+                                               uint32_t idesc, int left, bool first) {
+  const uint64_t a = lin_desc<AMN>(a_at), b = lin_desc<BMN>(b_at);
+  const int mmas = min(4, (left + 15) >> 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= mmas) break;
+    const uint32_t acc = (!first || j > 0) ? 1u : 0u;
+    if constexpr (PAIR) umma_f16_pair(d, a + j * lin_step<AMN>(), b + j * lin_step<BMN>(), idesc, acc);
+    else umma_f16(d, a + j * lin_step<AMN>(), b + j * lin_step<BMN>(), idesc, acc);
+  }
+}
+
+// ------------------------------------------------------------------ adapters
+// The stages that one adapter adds to a tile. T holds a row's rp high parts, then its rp low
+// parts (t = high + low to 16 bits of mantissa in bf16, 22 in fp16: rounding t once would add
+// as much error as the rounding of y). Up to rank 32 both lie in one stage of A; beyond,
+// stage s has the parts s & 1 of columns 64 (s / 2)...
+__host__ __device__ constexpr int lora_stages(int rp) {
+  return rp <= 32 ? 1 : 2 * ((rp + 63) / 64);
+}
+__device__ __forceinline__ int lora_col_t(int rp, int s) {
+  return rp <= 32 ? 0 : (s & 1) * rp + (s >> 1) * 64;
+}
+__device__ __forceinline__ int lora_col_b(int rp, int s) { return rp <= 32 ? 0 : (s >> 1) * 64; }
+
+template <bool PAIR, int W>
+__device__ __forceinline__ void lora_stage_mmas(uint32_t d, uint32_t a_at, uint32_t b_at,
+                                                uint32_t idesc, int rp, int s,
+                                                const uint32_t (&off)[W]) {
+  const uint64_t a = sdesc_sw128(a_at), b = sdesc_sw128(b_at);
+  const int per = (rp <= 32 ? rp : min(64, rp - (s >> 1) * 64)) >> 4;  // 16-column pieces
+  const int halves = rp <= 32 ? 2 : 1;
+  for (int h = 0; h < halves; ++h)
+    for (int j = 0; j < per; ++j) {
+      if constexpr (PAIR) umma_f16_rows_pair(d, a + h * (rp >> 3) + j * 2, b + j * 2, idesc, off);
+      else umma_f16_rows(d, a + h * (rp >> 3) + j * 2, b + j * 2, idesc, off);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+// The kernels' variants. out: skg_out_t of C (kLinPlain with N-major B: also fp32).
+struct LinVariant {
+  int mode;
+  bool a_mn, b_mn;  // M-major A, N-major B
+  int out;
+};
+
+cudaError_t launch_lin_single(const LinVariant& v, const LinMaps& t, const LinParams& p,
+                              cudaStream_t stream);
+cudaError_t launch_lin_pair(const LinVariant& v, const LinMaps& t, const LinParams& p,
+                            int clusters, cudaStream_t stream);
+
+// CTA pairs of the pair kernel that can be resident on the current device at once.
+int lin_pair_clusters_resident();
+
+// t = scale (x A^T) of every row's adapter, and the plans (skg_lora.cu).
+struct LoraParams {
+  int m, k, rank, rank_pad, count;  // count: adapters in the stack
+  int ksteps, split, groups, a_rows;
+  uint32_t idesc;
+  const int32_t* index;
+  const float* scale;  // NULL = 1
+  void* t;             // m x 2 rank_pad: high parts, then low parts
+  LoraPlan* plan;
+  uint32_t stages;
+  uint64_t limit;
+  skg_report_t* report;
+};
+cudaError_t launch_lora_down(int dtype, const CUtensorMap& x, const CUtensorMap& down,
+                             const LoraParams& p, cudaStream_t stream);
+
+}  // namespace skg

@@ -1,0 +1,413 @@
+// A layer's projections on CTA pairs: persistent clusters of two CTAs, 256 x 256 tiles of
+// the accumulator with one M = 256 MMA (tcgen05 cta_group::2). Each CTA loads its 128 rows
+// of A and half of B's 256 rows per stage; the leader issues the MMAs. TMEM holds two
+// accumulators, so the way out of one tile runs under the MMAs of the next.
+//
+// In the gated mode the leader's half of B is 128 columns of the gate's projection and the
+// other CTA's the same 128 of the other, so every thread finds both of its row in its own
+// TMEM lane, 128 columns apart. Adapters as in skg_lin_single.cu: more stages of k for each
+// adapter that the tile's 256 rows use, with the other rows left out of the MMA.
+//
+// What the waits' bounds and the way out share with the block-scaled product's pairs is
+// explained there (skg_mx_gemm_pair.cu).
+#include "skg_lin.cuh"
+
+namespace skg {
+namespace {
+
+struct PairCfg {
+  static constexpr int STAGE_BYTES = 2 * kLinOperand;
+  static constexpr int STAGING = 4 * 8192;  // per epilogue warp: two boxes of 32 rows x 128 bytes
+  static constexpr int STAGES = 6;
+  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + STAGING + 512;
+  static_assert(SMEM <= kSmemLimit, "shared memory");
+  static_assert(sizeof(LinAux) <= 512, "aux size");
+};
+
+// A box of 32 rows x 128 bytes (this lane's row: the values f(0), f(1), ...) in the 128-byte
+// swizzle, and its store by TMA; two boxes per warp in turn. The engine clips what is past
+// the matrix.
+template <typename T, typename F>
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* staging, uint32_t& box,
+                                          int lane, int col, int row, bool in, F f) {
+  constexpr int PER = 16 / (int)sizeof(T);
+  uint8_t* st = staging + (box & 1) * 4096;
+  ++box;
+  if (lane == 0) bulk_wait_read<1>();  // the box's last store has read it
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    union {
+      T e[PER];
+      uint4 q;
+    } u;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) u.e[i] = mx_from_f32<T>(f(j * PER + i));
+    *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = u.q;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (in) tma_store_2d(map, st, col, row);
+    bulk_commit();
+  }
+}
+
+// Tile t in an order that keeps the tiles in flight close together: bands of eight rows of
+// tiles, column by column within a band (2048 rows of A stay in L2 while B passes).
+__device__ __forceinline__ void pair_tile(const LinParams& p, int t, int& tm, int& tn) {
+  constexpr int kBand = 8;
+  const int band = t / (kBand * p.tiles_n);
+  const int rows = min(kBand, p.tiles_m - band * kBand);
+  const int i = t - band * kBand * p.tiles_n;
+  tn = i / rows;
+  tm = band * kBand + i % rows;
+}
+
+template <int MODE, bool AMN, bool BMN, typename T>
+__global__ void __launch_bounds__(kLinThreads, 1)
+lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
+  using C = PairCfg;
+  constexpr bool G = MODE == kLinGated;
+  constexpr bool LORA = MODE == kLinPlain && !AMN && !BMN;
+  constexpr int TILE_N = G ? 128 : 256;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* staging = ring + C::STAGES * C::STAGE_BYTES;
+  LinAux* aux = reinterpret_cast<LinAux*>(staging + C::STAGING);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int first = (int)blockIdx.x >> 1, stride = (int)gridDim.x >> 1;
+  const bool lora = LORA && p.plan != nullptr;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    prefetch_tmap(&maps.c);
+    aux->abort_flag = 0;
+    aux->limit = p.limit;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&aux->full[i], 1);
+      mbar_init(&aux->empty[i], 1);
+    }
+    mbar_init(&aux->tfull[0], 1);
+    mbar_init(&aux->tfull[1], 1);
+    mbar_init(&aux->tempty, 8);  // the epilogue warps of both CTAs
+    mbar_init(&aux->tempty1, 8);
+    mbar_init(&aux->drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&aux->tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = aux->tmem_slot;
+  if (!lora) {  // see skg_lin_single.cu
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+  }
+
+  uint32_t issued = 0;  // the loading thread: stages loaded
+  if (warp == 0) {
+    if (elect_one()) {
+      int st = 0;
+      uint32_t phase = 0;
+      bool ok = true, waited = false;
+      // The next stage, once it is free, with its barrier (the leader's); NULL when its wait
+      // or the stages ran out.
+      uint32_t bar = 0;
+      auto next = [&]() -> uint8_t* {
+        if (issued >= p.stages) {
+          ok = false;
+          return nullptr;
+        }
+        if (!mx_wait(&aux->empty[st], phase ^ 1u, aux)) {
+          lin_fail(p, aux);
+          ok = false;
+          return nullptr;
+        }
+        uint8_t* s = ring + st * C::STAGE_BYTES;
+        bar = cluster_addr(&aux->full[st], 0);
+        if (rank == 0) mbar_arrive_expect_tx(&aux->full[st], 2 * C::STAGE_BYTES);
+        ++issued;
+        if (++st == C::STAGES) {
+          st = 0;
+          phase ^= 1u;
+        }
+        return s;
+      };
+      const int ks = p.ksteps * p.terms;
+      for (int t = first; ok && t < tiles; t += stride) {
+        int tm, tn;
+        pair_tile(p, t, tm, tn);
+        const int row = (2 * tm + rank) * kLinTile;
+        // Rows of B: this CTA's projection (gated), else its half of the tile's columns.
+        const int col = G ? rank * p.n + tn * 128 : tn * 256 + rank * 128;
+        for (int i = 0; i < ks; ++i) {
+          const bool lo = p.terms == 2 && (i & 1);
+          const int k0 = (p.terms == 2 ? i >> 1 : i) * kLinK;
+          uint8_t* s = next();
+          if (!s) break;
+          const CUtensorMap* ma = lo && !p.lo_b ? &maps.lo : &maps.a;
+          const CUtensorMap* mb = lo && p.lo_b ? &maps.lo : &maps.b;
+          if constexpr (AMN) {
+            tma_load_2d_pair(s, ma, bar, row, k0);
+            tma_load_2d_pair(s + kLinBox, ma, bar, row + 64, k0);
+          } else {
+            tma_load_2d_pair(s, ma, bar, k0, row);
+          }
+          if constexpr (BMN) {
+            tma_load_2d_pair(s + kLinOperand, mb, bar, col, k0);
+            tma_load_2d_pair(s + kLinOperand + kLinBox, mb, bar, col + 64, k0);
+          } else {
+            tma_load_2d_pair(s + kLinOperand, mb, bar, k0, col);
+          }
+        }
+        if (ok && lora) {
+          if (!waited) {
+            griddep_wait();
+            griddep_launch_dependents();
+            waited = true;
+          }
+          const LoraPlan* plan = p.plan + tm;
+          const int count = plan->count, per = lora_stages(p.rank_pad);
+          for (int u = 0; ok && u < count; ++u) {
+            const int id = plan->id[u];
+            for (int j = 0; j < per; ++j) {
+              uint8_t* s = next();
+              if (!s) break;
+              tma_load_2d_pair(s, &maps.t, bar, lora_col_t(p.rank_pad, j), row);
+              tma_load_3d_pair(s + kLinOperand, &maps.up, bar, lora_col_b(p.rank_pad, j), col, id);
+            }
+          }
+        }
+      }
+      // A grid ends behind the one that it waits for.
+      if (lora && !waited) griddep_wait();
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one() && rank == 0) {
+      int st = 0, n = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true, waited = false;
+      auto stage = [&]() -> uint32_t {  // 0: the wait ran out
+        if (!mx_wait(&aux->full[st], phase, aux)) {
+          lin_fail(p, aux);
+          ok = false;
+          return 0;
+        }
+        tc_fence_after();
+        return smem_u32(ring + st * C::STAGE_BYTES);
+      };
+      auto done = [&]() {
+        umma_commit_pair(&aux->empty[st]);
+        ++it;
+        if (++st == C::STAGES) {
+          st = 0;
+          phase ^= 1u;
+        }
+      };
+      const int ks = p.ksteps * p.terms;
+      for (int t = first; ok && t < tiles; t += stride, ++n) {
+        // The accumulator's last tile is out of it.
+        if (n > 1 && !mx_wait((n & 1) ? &aux->tempty1 : &aux->tempty, (uint32_t)((n >> 1) - 1) & 1u,
+                              aux)) {
+          lin_fail(p, aux);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (n & 1) * 256;
+        for (int i = 0; i < ks; ++i) {
+          const uint32_t s = stage();
+          if (!s) break;
+          lin_stage_mmas<true, AMN, BMN>(d, s, s + kLinOperand, p.idesc,
+                                         p.k - (p.terms == 2 ? i >> 1 : i) * kLinK, i == 0);
+          done();
+        }
+        if (ok && lora) {
+          if (!waited) griddep_wait();
+          waited = true;
+          int tm, tn;
+          pair_tile(p, t, tm, tn);
+          const LoraPlan* plan = p.plan + tm;
+          const int count = plan->count, per = lora_stages(p.rank_pad);
+          for (int u = 0; ok && u < count; ++u) {
+            uint32_t off[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) off[w] = ~plan->rows[u][w];
+            for (int j = 0; j < per; ++j) {
+              const uint32_t s = stage();
+              if (!s) break;
+              lora_stage_mmas<true>(d, s, s + kLinOperand, p.idesc, p.rank_pad, j, off);
+              done();
+            }
+          }
+        }
+        if (ok) umma_commit_pair(&aux->tfull[n & 1]);
+      }
+      if (it > 0) {
+        umma_commit_pair(&aux->drain);
+        mx_wait(&aux->drain, 0, aux, true);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    uint8_t* mine = staging + q * 8192;
+    uint32_t box = 0;
+    int n = 0;
+    for (int t = first; t < tiles; t += stride, ++n) {
+      int tm, tn;
+      pair_tile(p, t, tm, tn);
+      const int row0 = (2 * tm + rank) * kLinTile + q * 32, col0 = tn * TILE_N;
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * 256;
+      const bool got = mx_wait(&aux->tfull[n & 1], (uint32_t)(n >> 1) & 1u, aux);
+      if (!got) lin_fail(p, aux);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
+      const bool live = row0 < p.m;
+      // Four pieces of 64 accumulator columns: 64 columns of C each; gated: the gate's 64,
+      // then the other projection's 64 of the same outputs.
+      uint32_t v[2][2][32];
+      auto fetch = [&](int s) {
+        const int c = G ? (s & 1) * 128 + (s >> 1) * 64 : s * 64;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) tmem_ld32_async(acc + c + i * 32, v[s & 1][i]);
+      };
+      fetch(0);
+      fetch(1);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (!G || (s & 1) == 0) {
+          // (A wait is for all loads under way.)
+          tmem_ld_wait32(v[s & 1][0]);
+          tmem_ld_wait32(v[s & 1][1]);
+        }
+        if (G) {
+          if (s & 1) continue;
+          tmem_ld_wait32(v[1][0]);
+          tmem_ld_wait32(v[1][1]);
+          const int col = col0 + (s >> 1) * 64;
+          const bool in = live && col < p.n;
+          if (s == 2) {  // all of the tile is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_remote(cluster_addr((n & 1) ? &aux->tempty1 : &aux->tempty, 0u));
+          }
+          if (in) {
+            store_box<T>(&maps.c, mine, box, lane, col, row0, true, [&](int i) {
+              return lin_gated(p.act, __uint_as_float(v[0][i >> 5][i & 31]),
+                               __uint_as_float(v[1][i >> 5][i & 31]));
+            });
+            if (p.pre) {
+              store_box<T>(&maps.gate, mine, box, lane, col, row0, true,
+                           [&](int i) { return __uint_as_float(v[0][i >> 5][i & 31]); });
+              store_box<T>(&maps.pre_up, mine, box, lane, col, row0, true,
+                           [&](int i) { return __uint_as_float(v[1][i >> 5][i & 31]); });
+            }
+          }
+          if (s == 0) {
+            fetch(2);
+            fetch(3);
+          }
+        } else {
+          const int col = col0 + s * 64;
+          if (s == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_remote(cluster_addr((n & 1) ? &aux->tempty1 : &aux->tempty, 0u));
+          }
+          if (live && col < p.n)
+            store_box<T>(&maps.c, mine, box, lane, col, row0, true,
+                         [&](int i) { return __uint_as_float(v[s & 1][i >> 5][i & 31]); });
+          if (s < 2) fetch(s + 2);
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // As in skg_mx_gemm_pair.cu: copies that no MMA waited for land before the pair parts, the
+  // leader's last commit has reached the other CTA's barrier, and no CTA leaves while the
+  // other may still signal its barriers.
+  if (warp == 1 && rank == 1 && first < tiles && elect_one()) mx_wait(&aux->drain, 0, aux, true);
+  if (warp == 0 && rank == 0 && issued > 0 && mx_aborted(aux))
+    for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+      mx_wait(&aux->full[i % C::STAGES], (i / C::STAGES) & 1u, aux, true);
+  if (warp == 0 && rank == 1 && issued > 0 && mx_aborted(aux))
+    for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) __nanosleep(1000);
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(&p.report->launches, 1u);
+}
+
+template <int MODE, bool AMN, bool BMN, typename T>
+cudaError_t launch(const LinMaps& t, const LinParams& p, int clusters, cudaStream_t stream) {
+  auto kernel = lin_pair_kernel<MODE, AMN, BMN, T>;
+  static std::atomic<uint64_t> done_mask{0};
+  const cudaError_t e = opt_in_smem((const void*)kernel, done_mask, (int)PairCfg::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(kernel, dim3((unsigned)(2 * clusters)), dim3(kLinThreads),
+                            PairCfg::SMEM, stream, 2, t, p);
+}
+
+template <typename T>
+cudaError_t launch_type(const LinVariant& v, const LinMaps& t, const LinParams& p, int clusters,
+                        cudaStream_t stream) {
+  if (v.mode == kLinGated) return launch<kLinGated, false, false, T>(t, p, clusters, stream);
+  if (v.a_mn) return launch<kLinPlain, true, true, T>(t, p, clusters, stream);
+  if (v.b_mn) return launch<kLinPlain, false, true, T>(t, p, clusters, stream);
+  return launch<kLinPlain, false, false, T>(t, p, clusters, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_pair(const LinVariant& v, const LinMaps& t, const LinParams& p,
+                            int clusters, cudaStream_t stream) {
+  if (v.out == SKG_OUT_F16) return launch_type<__half>(v, t, p, clusters, stream);
+  return launch_type<__nv_bfloat16>(v, t, p, clusters, stream);
+}
+
+int lin_pair_clusters_resident() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int have = cached[dev].load(std::memory_order_acquire);
+  if (have != 0) return have > 0 ? have : 0;
+  auto kernel = lin_pair_kernel<kLinGated, false, false, __nv_bfloat16>;  // all alike in resources
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)PairCfg::SMEM) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 256);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = PairCfg::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  cached[dev].store(n > 0 ? n : -1, std::memory_order_release);
+  return n;
+}
+
+}  // namespace skg

@@ -1,0 +1,401 @@
+// A layer's projections on single CTAs: 128 x 128 tiles of the accumulator over a range of
+// k. Warp 0 fills a ring of stages by TMA, warp 1 issues the MMAs, warps 2-5 take the
+// accumulator out. In the gated mode a tile's columns are 64 of the gate's projection and
+// the same 64 of the other.
+//
+// When the tiles are fewer than the CTAs that fit the GPU, the S CTAs of a cluster share a
+// tile, a range of k each: every one leaves its partial sums in its own shared memory, and
+// after a cluster barrier each adds the rows r, r + S, ... of all of them in rank order
+// through distributed shared memory. No workspace, no atomics, the same result every time.
+//
+// Adapters. t = scale_s (x A_s^T) of all rows comes from the kernel before (skg_lora.cu),
+// and y's low-rank part is a few more stages of k on the same accumulator: for each adapter
+// s that a tile's rows use, the stage's A is t and its B is B_s, and the MMA leaves out the
+// rows (TMEM lanes) of other adapters. So rows of any mixture share a tile, an adapter with
+// infinities or NaN reaches its own rows alone, and y is written once. The stages over W
+// need nothing of the kernel before: only the first one that does waits for it
+// (griddepcontrol.wait), so t is formed while W streams.
+//
+// Every wait is bounded; when one runs out the CTA records SKG_ERR_PIPELINE_TIMEOUT in the
+// report, waits for its own copies and MMAs, still meets the cluster's barriers, frees its
+// TMEM and leaves.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "skg_lin.cuh"
+
+namespace skg {
+namespace {
+
+constexpr int kPitch = 132;  // floats per row of the partial tile
+
+// FEW: at most 16 rows of A. Its stages hold 16 rows of A (the MMA reads 128 from there:
+// what follows in the stage, for rows of the accumulator that nothing reads), so that six
+// stages of B fit where three do otherwise.
+template <bool FEW>
+struct SingleCfg {
+  static constexpr int B_OFF = FEW ? 16 * 128 : kLinOperand;
+  static constexpr int STAGE_BYTES = B_OFF + kLinOperand;
+  static constexpr int STAGES = FEW ? 6 : 3;  // two CTAs share an SM
+  static_assert(STAGE_BYTES % 1024 == 0 && STAGE_BYTES >= kLinOperand,
+                "swizzle atoms; A's 128 rows end inside the ring");
+  static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + 256;
+  static_assert(kLinTile * kPitch * 4 <= STAGES * STAGE_BYTES, "the partial tile fits the ring");
+  static_assert(sizeof(LinAux) <= 256, "aux size");
+};
+
+template <typename T>
+__device__ __forceinline__ void write4(T* c, const float (&v)[4], int left) {
+  if (left >= 4) {
+    mx_write4_plain<T>(c, make_float4(v[0], v[1], v[2], v[3]), 1.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) c[i] = mx_from_f32<T>(v[i]);
+  }
+}
+
+// Four output columns of row r: v as the accumulator has them; gated: gate and up.
+template <int MODE, typename T>
+__device__ __forceinline__ void finish4(const LinParams& p, int row, int col, const float4& v,
+                                        const float4& u) {
+  T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
+  if constexpr (MODE == kLinGated) {
+    const float h[4] = {lin_gated(p.act, v.x, u.x), lin_gated(p.act, v.y, u.y),
+                        lin_gated(p.act, v.z, u.z), lin_gated(p.act, v.w, u.w)};
+    write4<T>(c, h, p.n - col);
+    if (p.pre) {
+      T* g = reinterpret_cast<T*>(p.pre) + (int64_t)row * p.ldp + col;
+      const float a[4] = {v.x, v.y, v.z, v.w}, b[4] = {u.x, u.y, u.z, u.w};
+      write4<T>(g, a, p.n - col);
+      write4<T>(g + p.n, b, p.n - col);
+    }
+  } else {
+    const float a[4] = {v.x, v.y, v.z, v.w};
+    write4<T>(c, a, p.n - col);
+  }
+}
+
+// Rows `first`, `first` + step, ... of the tile, S CTAs' partial sums in rank order (S = 1:
+// this CTA's own). A warp takes a row of 128 columns at once, or two rows of 64 gated
+// outputs; the loads of several rows are in flight together. Every value that is loaded is
+// used, so no load is still on its way to another CTA's shared memory when a thread comes to
+// the barrier that lets that CTA leave.
+template <int MODE, typename T, int S>
+__device__ __forceinline__ void reduce_rows(const LinParams& p, const float* part, int w0,
+                                            int warps, int lane, int first, int limit, int tm,
+                                            int tn) {
+  constexpr bool G = MODE == kLinGated;
+  constexpr int PER = G ? 2 : 1;                 // rows that a warp takes at once
+  constexpr int R = (G ? 8 : 16) / S > 4 ? 4 : (G ? 8 : 16) / S;  // of those, in flight
+  constexpr int TILE_N = G ? 64 : 128;
+  const int piece = (G ? lane & 15 : lane) * 4, sub = G ? lane >> 4 : 0;
+  const int rows = min(limit, p.m - tm * kLinTile);
+  const int col = tn * TILE_N + piece;
+  const bool in = col < p.n;
+  uint32_t base[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) base[s] = S > 1 ? cluster_addr(part + piece, (uint32_t)s) : 0;
+#pragma unroll 1
+  for (int i = w0 * R * PER; first + i * S < rows; i += warps * R * PER) {
+    float4 v[R][S], u[R][S];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int r = first + (i + j * PER + sub) * S;
+      if (r < rows && in) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if constexpr (S == 1) {
+            v[j][s] = *reinterpret_cast<const float4*>(part + r * kPitch + piece);
+            if (G) u[j][s] = *reinterpret_cast<const float4*>(part + r * kPitch + 64 + piece);
+          } else {
+            v[j][s] = ld_shared_cluster_f32x4(base[s] + (uint32_t)r * (kPitch * 4));
+            if (G) u[j][s] = ld_shared_cluster_f32x4(base[s] + (uint32_t)r * (kPitch * 4) + 256);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int r = first + (i + j * PER + sub) * S;
+      if (r >= rows || !in) break;
+      float4 a = v[j][0], b = G ? u[j][0] : a;
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        a.x += v[j][s].x;
+        a.y += v[j][s].y;
+        a.z += v[j][s].z;
+        a.w += v[j][s].w;
+        if (G) {
+          b.x += u[j][s].x;
+          b.y += u[j][s].y;
+          b.z += u[j][s].z;
+          b.w += u[j][s].w;
+        }
+      }
+      finish4<MODE, T>(p, tm * kLinTile + r, col, a, b);
+    }
+  }
+}
+
+// The rows of the plan's adapter u in this tile, as the lanes to leave out; false: none.
+__device__ __forceinline__ bool lora_rows(const LoraPlan* plan, int u, int half,
+                                          uint32_t (&off)[4]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(&plan->rows[u][half * 4]);
+  off[0] = ~r.x;
+  off[1] = ~r.y;
+  off[2] = ~r.z;
+  off[3] = ~r.w;
+  return (r.x | r.y | r.z | r.w) != 0;
+}
+
+template <int MODE, bool FEW, bool AMN, bool BMN, typename T>
+__global__ void __launch_bounds__(kLinThreads, 2)
+lin_single_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
+  using C = SingleCfg<FEW>;
+  constexpr bool G = MODE == kLinGated;
+  constexpr bool LORA = MODE == kLinPlain && !AMN && !BMN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  LinAux* aux = reinterpret_cast<LinAux*>(ring + C::STAGES * C::STAGE_BYTES);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int tile = (int)blockIdx.x / p.split;
+  // Few rows: one row of tiles. Else a column of tiles after another, so that the CTAs in
+  // flight share B.
+  const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
+  const int ks = p.ksteps * p.terms;
+  const int kb0 = (int)((int64_t)ks * rank / p.split);
+  const int kb1 = (int)((int64_t)ks * (rank + 1) / p.split);
+  const LoraPlan* plan = LORA && p.plan ? p.plan + (tm >> 1) : nullptr;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    aux->abort_flag = 0;
+    aux->limit = p.limit;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&aux->full[i], 1);
+      mbar_init(&aux->empty[i], 1);
+    }
+    mbar_init(&aux->tfull[0], 1);
+    mbar_init(&aux->drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&aux->tmem_slot, kLinTile);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = aux->tmem_slot;
+  // With adapters the kernel before is the one that forms t, which itself has waited for
+  // all that ran before it: x and w are there, and y is free.
+  if (!(LORA && plan)) {
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+  }
+
+  bool fine = true;  // epilogue threads: the accumulator is there
+  int issued = 0;    // the loading thread: stages loaded
+  if (warp == 0) {
+    if (elect_one()) {
+      const uint32_t tx = (AMN ? (uint32_t)kLinOperand : (uint32_t)p.a_rows * 128) + kLinOperand;
+      bool ok = true;
+      // The next stage, once it is free: NULL when its wait or the stages ran out.
+      auto next = [&]() -> uint8_t* {
+        if ((uint32_t)issued >= p.stages) {
+          ok = false;
+          return nullptr;
+        }
+        const int st = issued % C::STAGES;
+        if (!mx_wait(&aux->empty[st], (uint32_t)((issued / C::STAGES) & 1) ^ 1u, aux)) {
+          lin_fail(p, aux);
+          ok = false;
+          return nullptr;
+        }
+        mbar_arrive_expect_tx(&aux->full[st], tx);
+        ++issued;
+        return ring + st * C::STAGE_BYTES;
+      };
+      for (int i = kb0; i < kb1; ++i) {
+        const bool lo = p.terms == 2 && (i & 1);
+        const int kb = p.terms == 2 ? i >> 1 : i;
+        uint8_t* s = next();
+        if (!s) break;
+        uint64_t* bar = &aux->full[(issued - 1) % C::STAGES];
+        const CUtensorMap* ma = lo && !p.lo_b ? &maps.lo : &maps.a;
+        const CUtensorMap* mb = lo && p.lo_b ? &maps.lo : &maps.b;
+        if constexpr (AMN) {
+          tma_load_2d(s, ma, bar, tm * kLinTile, kb * kLinK);
+          tma_load_2d(s + kLinBox, ma, bar, tm * kLinTile + 64, kb * kLinK);
+        } else {
+          tma_load_2d(s, ma, bar, kb * kLinK, tm * kLinTile);
+        }
+        if constexpr (G) {
+          tma_load_2d(s + C::B_OFF, mb, bar, kb * kLinK, tn * 64);
+          tma_load_2d(s + C::B_OFF + kLinOperand / 2, mb, bar, kb * kLinK, p.n + tn * 64);
+        } else if constexpr (BMN) {
+          tma_load_2d(s + C::B_OFF, mb, bar, tn * kLinTile, kb * kLinK);
+          tma_load_2d(s + C::B_OFF + kLinBox, mb, bar, tn * kLinTile + 64, kb * kLinK);
+        } else {
+          tma_load_2d(s + C::B_OFF, mb, bar, kb * kLinK, tn * kLinTile);
+        }
+      }
+      if (LORA && plan) {
+        griddep_wait();
+        griddep_launch_dependents();
+        const int count = plan->count, per = lora_stages(p.rank_pad);
+        for (int u = rank; ok && u < count; u += p.split) {
+          uint32_t off[4];
+          if (!lora_rows(plan, u, tm & 1, off)) continue;
+          const int id = plan->id[u];
+          for (int j = 0; j < per; ++j) {
+            uint8_t* s = next();
+            if (!s) break;
+            uint64_t* bar = &aux->full[(issued - 1) % C::STAGES];
+            tma_load_2d(s, &maps.t, bar, lora_col_t(p.rank_pad, j), tm * kLinTile);
+            tma_load_3d(s + C::B_OFF, &maps.up, bar, lora_col_b(p.rank_pad, j), tn * kLinTile, id);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one()) {
+      bool ok = true;
+      int it = 0;
+      auto stage = [&]() -> uint32_t {  // 0: the wait ran out
+        const int st = it % C::STAGES;
+        if (!mx_wait(&aux->full[st], (uint32_t)((it / C::STAGES) & 1), aux)) {
+          lin_fail(p, aux);
+          ok = false;
+          return 0;
+        }
+        tc_fence_after();
+        return smem_u32(ring + st * C::STAGE_BYTES);
+      };
+      for (int i = kb0; i < kb1; ++i) {
+        const int kb = p.terms == 2 ? i >> 1 : i;
+        const uint32_t s = stage();
+        if (!s) break;
+        lin_stage_mmas<false, AMN, BMN>(tmem, s, s + C::B_OFF, p.idesc, p.k - kb * kLinK, it == 0);
+        umma_commit(&aux->empty[it % C::STAGES]);
+        ++it;
+      }
+      if (LORA && plan) {
+        griddep_wait();
+        const int count = plan->count, per = lora_stages(p.rank_pad);
+        for (int u = rank; ok && u < count; u += p.split) {
+          uint32_t off[4];
+          if (!lora_rows(plan, u, tm & 1, off)) continue;
+          for (int j = 0; j < per; ++j) {
+            const uint32_t s = stage();
+            if (!s) break;
+            lora_stage_mmas<false>(tmem, s, s + C::B_OFF, p.idesc, p.rank_pad, j, off);
+            umma_commit(&aux->empty[it % C::STAGES]);
+            ++it;
+          }
+        }
+      }
+      if (ok) umma_commit(&aux->tfull[0]);
+      if (it > 0) {
+        umma_commit(&aux->drain);
+        mx_wait(&aux->drain, 0, aux, true);
+      }
+    }
+    __syncwarp();
+  } else {
+    fine = mx_wait(&aux->tfull[0], 0, aux);
+    if (!fine) lin_fail(p, aux);
+    fine = epi_all(fine);
+    tc_fence_after();
+    const int q = warp & 3;
+    const int r = q * 32 + lane;
+    float* part = reinterpret_cast<float*>(ring);
+    if (fine && tm * kLinTile + q * 32 < p.m) {
+      // The ring is idle: every stage was read by MMAs that are complete.
+#pragma unroll
+      for (int c = 0; c < kLinTile; c += 64) {
+        uint32_t v[2][32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          tmem_ld32_async(tmem + ((uint32_t)(q * 32) << 16) + c + h * 32, v[h]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld_wait32(v[h]);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(part + r * kPitch + c + h * 32 + i) =
+                make_uint4(v[h][i], v[h][i + 1], v[h][i + 2], v[h][i + 3]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+  const float* part = reinterpret_cast<const float*>(ring);
+  if (p.split == 1) {
+    // A warp writes the 32 rows that its own lanes stored.
+    const int q = warp & 3;
+    if (warp >= 2 && fine)
+      reduce_rows<MODE, T, 1>(p, part, 0, 1, lane, q * 32, q * 32 + 32, tm, tn);
+  } else {
+    cluster_sync();
+    if (fine) {
+      if (p.split == 2) reduce_rows<MODE, T, 2>(p, part, warp, 6, lane, rank, kLinTile, tm, tn);
+      else if (p.split == 4) reduce_rows<MODE, T, 4>(p, part, warp, 6, lane, rank, kLinTile, tm, tn);
+      else reduce_rows<MODE, T, 8>(p, part, warp, 6, lane, rank, kLinTile, tm, tn);
+    }
+    __syncwarp();
+    cluster_meet();  // no CTA leaves while another reads its partial sums
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kLinTile);
+  }
+  // Copies that no MMA waited for land before the CTA leaves.
+  if (warp == 0 && issued > 0 && mx_aborted(aux))
+    for (int i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+      mx_wait(&aux->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), aux, true);
+  if (blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(&p.report->launches, 1u);
+}
+
+template <int MODE, bool FEW, bool AMN, bool BMN, typename T>
+cudaError_t launch(const LinMaps& t, const LinParams& p, cudaStream_t stream) {
+  using C = SingleCfg<FEW>;
+  auto kernel = lin_single_kernel<MODE, FEW, AMN, BMN, T>;
+  static std::atomic<uint64_t> done_mask{0};
+  const cudaError_t e = opt_in_smem((const void*)kernel, done_mask, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = (int64_t)p.tiles_m * p.tiles_n * p.split;
+  return launch_pdl_cluster(kernel, dim3((unsigned)ctas), dim3(kLinThreads), C::SMEM, stream,
+                            p.split, t, p);
+}
+
+template <typename T>
+cudaError_t launch_type(const LinVariant& v, const LinMaps& t, const LinParams& p,
+                        cudaStream_t stream) {
+  if (v.mode == kLinGated)
+    return p.m <= 16 ? launch<kLinGated, true, false, false, T>(t, p, stream)
+                     : launch<kLinGated, false, false, false, T>(t, p, stream);
+  if (v.a_mn) return launch<kLinPlain, false, true, true, T>(t, p, stream);
+  if (v.b_mn) return launch<kLinPlain, false, false, true, T>(t, p, stream);
+  return p.m <= 16 ? launch<kLinPlain, true, false, false, T>(t, p, stream)
+                   : launch<kLinPlain, false, false, false, T>(t, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_single(const LinVariant& v, const LinMaps& t, const LinParams& p,
+                              cudaStream_t stream) {
+  if (v.out == SKG_OUT_F32) return launch<kLinPlain, false, false, true, float>(t, p, stream);
+  if (v.out == SKG_OUT_F16) return launch_type<__half>(v, t, p, stream);
+  return launch_type<__nv_bfloat16>(v, t, p, stream);
+}
+
+}  // namespace skg

@@ -1,5 +1,5 @@
-// Python module _skg_torch: the microscaled entry points of libskgemm.so on torch
-// tensors. It checks the arguments, allocates the outputs, and hands pointers,
+// Python module _skg_torch: the microscaled entry points of libskgemm.so, and those of a
+// layer's projections in 16 bits, on torch tensors. It checks the arguments, allocates the outputs, and hands pointers,
 // strides and the current stream to the C ABI; all arithmetic runs there. (A
 // call of one token takes the GPU 3 to 4 us; the same marshalling in Python took
 // 14 to 20 us.) Functions take their arguments by position, return the library's
@@ -321,6 +321,197 @@ PyObject* matmul(PyObject* const* v, Py_ssize_t n) {
   return st != SKG_OK ? PyLong_FromLong(st) : THPVariable_Wrap(out);
 }
 
+// ------------------------------------------------------------------ a layer's projections
+const char* kActivations[] = {"silu", "gelu", "gelu_tanh", "relu"};
+
+int activation_of(PyObject* o) {
+  if (PyUnicode_Check(o))
+    for (int i = 0; i < 4; ++i)
+      if (PyUnicode_CompareWithASCIIString(o, kActivations[i]) == 0) return i;
+  refuse("unknown activation: one of silu, gelu, gelu_tanh, relu");
+}
+
+// A 16-bit matrix (rows, cols) of x's type and device (cols < 0: any); returns its row stride.
+int64_t operand_like(const char* name, const at::Tensor& t, int64_t rows, int64_t cols,
+                     const at::Tensor& x) {
+  const int64_t ld = matrix(name, t);
+  if (t.size(0) != rows || (cols >= 0 && t.size(1) != cols))
+    refuse(std::string(name) + ": a matrix of " + std::to_string(rows) + " x " +
+           (cols < 0 ? "?" : std::to_string(cols)) + " is wanted");
+  if (t.scalar_type() != x.scalar_type())
+    refuse(std::string(name) + ": " + c10::toString(t.scalar_type()) + ", the other operands are " +
+           c10::toString(x.scalar_type()));
+  on_device(name, t, x.device());
+  return ld;
+}
+
+// An uninitialised matrix whose rows start on 16-byte boundaries.
+at::Tensor padded(int64_t rows, int64_t cols, const at::Tensor& x) {
+  const int64_t ld = (cols + 7) / 8 * 8;
+  at::Tensor t = empty({rows, ld}, x.scalar_type(), x.device());
+  return ld == cols ? t : t.narrow(1, 0, cols);
+}
+
+int64_t ld_of(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
+at::Tensor scratch_of(size_t bytes, c10::Device d) {
+  return empty({(int64_t)(bytes ? bytes : 1)}, at::kByte, d);
+}
+
+// One matrix of a stack (count, rows, cols): its row and matrix strides.
+void stack_like(const char* name, const at::Tensor& t, int64_t count, int64_t rows, int64_t cols,
+                const at::Tensor& x, int64_t* ld, int64_t* stride) {
+  if (t.dim() != 3 || t.size(0) != count || t.size(1) != rows || t.size(2) != cols)
+    refuse(std::string(name) + ": a stack of " + std::to_string(count) + " x " +
+           std::to_string(rows) + " x " + std::to_string(cols) + " is wanted");
+  if (t.scalar_type() != x.scalar_type())
+    refuse(std::string(name) + ": " + c10::toString(t.scalar_type()) + ", x is " +
+           c10::toString(x.scalar_type()));
+  on_device(name, t, x.device());
+  if (cols > 1 && t.stride(2) != 1)
+    refuse(std::string(name) + ": the last dimension must be contiguous");
+  *ld = rows > 1 ? t.stride(1) : cols;
+  *stride = count > 1 ? t.stride(0) : rows * cols;
+}
+
+// linear(x, w, (a, b, scale) or None, index, out or None, workspace) -> y
+PyObject* linear(PyObject* const* v, Py_ssize_t n) {
+  want(n, 6);
+  const at::Tensor& x = tensor_of("x", v[0]);
+  const int type = type_of("x", x.scalar_type(), false);
+  const int64_t ldx = matrix("x", x);
+  const int64_t m = x.size(0), k = x.size(1);
+  const c10::Device d = x.device();
+  const c10::cuda::CUDAGuard guard(d);
+  const at::Tensor& w = tensor_of("w", v[1]);
+  if (w.dim() != 2) refuse("w: a matrix is wanted");
+  const int64_t ldw = operand_like("w", w, w.size(0), k, x), rows = w.size(0);
+  skg_adapters_t ad = {};
+  const bool adapted = v[2] != Py_None;
+  if (!adapted && v[3] != Py_None) refuse("index belongs to adapters");
+  if (adapted) {
+    if (!PyTuple_Check(v[2]) || PyTuple_GET_SIZE(v[2]) != 3) refuse("adapters: Adapters are wanted");
+    const at::Tensor& a = tensor_of("adapters.down", PyTuple_GET_ITEM(v[2], 0));
+    const at::Tensor& b = tensor_of("adapters.up", PyTuple_GET_ITEM(v[2], 1));
+    if (a.dim() != 3) refuse("adapters.down: a stack of matrices is wanted");
+    if (a.size(0) > INT32_MAX || a.size(1) > INT32_MAX) refuse("adapters.down: too many");
+    ad.count = (int32_t)a.size(0);
+    ad.rank = (int32_t)a.size(1);
+    stack_like("adapters.down", a, ad.count, ad.rank, k, x, &ad.ld_down, &ad.stride_down);
+    stack_like("adapters.up", b, ad.count, rows, ad.rank, x, &ad.ld_up, &ad.stride_up);
+    ad.down = a.data_ptr();
+    ad.up = b.data_ptr();
+    ad.index = (const int32_t*)vector("index", tensor_of("index", v[3]), m, at::kInt, d);
+    PyObject* scale = PyTuple_GET_ITEM(v[2], 2);
+    if (scale != Py_None)
+      ad.scale = (const float*)vector("adapters.scale", tensor_of("adapters.scale", scale),
+                                      ad.count, at::kFloat, d);
+  }
+  const at::Tensor& ws = tensor_of("workspace", v[5]);
+  on_device("workspace", ws, d);
+  at::Tensor out;
+  int64_t ldo;
+  if (v[4] == Py_None) {
+    out = padded(m, rows, x);
+    ldo = ld_of(out);
+  } else {
+    out = tensor_of("out", v[4]);
+    ldo = operand_like("out", out, m, rows, x);
+  }
+  const size_t bytes = adapted ? skg_scratch_size_linear(m, ad.rank) : 0;
+  at::Tensor scratch;
+  if (bytes) scratch = scratch_of(bytes, d);
+  const int st = skg_linear(m, rows, k, x.data_ptr(), ldx, w.data_ptr(), ldw,
+                            adapted ? &ad : nullptr, out.data_ptr(), ldo, type, ws.data_ptr(),
+                            (size_t)ws.nbytes(), bytes ? scratch.data_ptr() : nullptr, bytes,
+                            stream_of(d));
+  return st != SKG_OK ? PyLong_FromLong(st) : THPVariable_Wrap(out);
+}
+
+// Rows of one projection of w_in (2 hidden, k).
+int64_t hidden_of(const at::Tensor& w, int64_t k) {
+  if (w.dim() != 2 || w.size(0) % 2 || w.size(1) != k)
+    refuse("w_in: a matrix of 2 hidden x " + std::to_string(k) + " is wanted");
+  return w.size(0) / 2;
+}
+
+// gated(x, w_in, activation, save, workspace) -> (h, pre or None)
+PyObject* gated(PyObject* const* v, Py_ssize_t n) {
+  want(n, 5);
+  const at::Tensor& x = tensor_of("x", v[0]);
+  const int type = type_of("x", x.scalar_type(), false);
+  const int64_t ldx = matrix("x", x);
+  const int64_t m = x.size(0), k = x.size(1);
+  const c10::Device d = x.device();
+  const c10::cuda::CUDAGuard guard(d);
+  const at::Tensor& w = tensor_of("w_in", v[1]);
+  const int64_t f = hidden_of(w, k), ldw = operand_like("w_in", w, 2 * f, k, x);
+  const int act = activation_of(v[2]);
+  const bool save = flag("save", v[3]);
+  const at::Tensor& ws = tensor_of("workspace", v[4]);
+  on_device("workspace", ws, d);
+  at::Tensor h = padded(m, f, x), pre;
+  if (save) pre = padded(m, 2 * f, x);
+  const int st = skg_gated(m, f, k, x.data_ptr(), ldx, w.data_ptr(), ldw, act, h.data_ptr(),
+                           ld_of(h), save ? pre.data_ptr() : nullptr, save ? ld_of(pre) : 0, type,
+                           ws.data_ptr(), (size_t)ws.nbytes(), stream_of(d));
+  return st != SKG_OK ? PyLong_FromLong(st) : tuple_of({h, pre});
+}
+
+// gated_backward(dh, x, w_in, pre, activation, workspace) -> (dx, dw_in)
+PyObject* gated_backward(PyObject* const* v, Py_ssize_t n) {
+  want(n, 6);
+  const at::Tensor& x = tensor_of("x", v[1]);
+  const int type = type_of("x", x.scalar_type(), false);
+  const int64_t ldx = matrix("x", x);
+  const int64_t m = x.size(0), k = x.size(1);
+  const c10::Device d = x.device();
+  const c10::cuda::CUDAGuard guard(d);
+  const at::Tensor &dh = tensor_of("dh", v[0]), &w = tensor_of("w_in", v[2]),
+                   &pre = tensor_of("pre", v[3]);
+  const int64_t f = hidden_of(w, k), ldw = operand_like("w_in", w, 2 * f, k, x),
+                lddh = operand_like("dh", dh, m, f, x), ldp = operand_like("pre", pre, m, 2 * f, x);
+  const int act = activation_of(v[4]);
+  const at::Tensor& ws = tensor_of("workspace", v[5]);
+  on_device("workspace", ws, d);
+  at::Tensor dx = padded(m, k, x), dw = padded(2 * f, k, x);
+  const size_t bytes = skg_scratch_size_gated_backward(m, f);
+  at::Tensor scratch = scratch_of(bytes, d);
+  const int st = skg_gated_backward(m, f, k, dh.data_ptr(), lddh, x.data_ptr(), ldx, w.data_ptr(),
+                                    ldw, pre.data_ptr(), ldp, act, dx.data_ptr(), ld_of(dx),
+                                    dw.data_ptr(), ld_of(dw), type, ws.data_ptr(),
+                                    (size_t)ws.nbytes(), scratch.data_ptr(), bytes, stream_of(d));
+  return st != SKG_OK ? PyLong_FromLong(st) : tuple_of({dx, dw});
+}
+
+// feed_forward_backward(dy, x, w_in, w_out, pre, activation, workspace) -> (dx, dw_in, dw_out)
+PyObject* feed_forward_backward(PyObject* const* v, Py_ssize_t n) {
+  want(n, 7);
+  const at::Tensor& x = tensor_of("x", v[1]);
+  const int type = type_of("x", x.scalar_type(), false);
+  const int64_t ldx = matrix("x", x);
+  const int64_t m = x.size(0), k = x.size(1);
+  const c10::Device d = x.device();
+  const c10::cuda::CUDAGuard guard(d);
+  const at::Tensor &dy = tensor_of("dy", v[0]), &wi = tensor_of("w_in", v[2]),
+                   &wo = tensor_of("w_out", v[3]), &pre = tensor_of("pre", v[4]);
+  const int64_t f = hidden_of(wi, k), ldwi = operand_like("w_in", wi, 2 * f, k, x),
+                ldwo = operand_like("w_out", wo, k, f, x), lddy = operand_like("dy", dy, m, k, x),
+                ldp = operand_like("pre", pre, m, 2 * f, x);
+  const int act = activation_of(v[5]);
+  const at::Tensor& ws = tensor_of("workspace", v[6]);
+  on_device("workspace", ws, d);
+  at::Tensor dx = padded(m, k, x), dwi = padded(2 * f, k, x), dwo = padded(k, f, x);
+  const size_t bytes = skg_scratch_size_feed_forward_backward(m, f);
+  at::Tensor scratch = scratch_of(bytes, d);
+  const int st = skg_feed_forward_backward(
+      m, f, k, dy.data_ptr(), lddy, x.data_ptr(), ldx, wi.data_ptr(), ldwi, wo.data_ptr(), ldwo,
+      pre.data_ptr(), ldp, act, dx.data_ptr(), ld_of(dx), dwi.data_ptr(), ld_of(dwi),
+      dwo.data_ptr(), ld_of(dwo), type, ws.data_ptr(), (size_t)ws.nbytes(), scratch.data_ptr(),
+      bytes, stream_of(d));
+  return st != SKG_OK ? PyLong_FromLong(st) : tuple_of({dx, dwi, dwo});
+}
+
 // No C++ exception crosses into the interpreter.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -338,7 +529,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   {#name, (PyCFunction)(void (*)(void))entry<name>, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {SKG_ENTRY(quantize), SKG_ENTRY(quantize_both), SKG_ENTRY(rmsnorm),
                           SKG_ENTRY(rmsnorm_backward), SKG_ENTRY(matmul),
-                          {nullptr, nullptr, 0, nullptr}};
+                          SKG_ENTRY(linear), SKG_ENTRY(gated), SKG_ENTRY(gated_backward),
+                          SKG_ENTRY(feed_forward_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_skg_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 

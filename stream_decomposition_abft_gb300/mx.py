@@ -85,6 +85,18 @@ def default_workspace(device="cuda") -> Workspace:
     return ws
 
 
+def workspace_for(device) -> Workspace:
+    """The workspace of a call on a CUDA device (with an index) that was given none: the
+    default one, or in a CUDA graph's capture before that one's first use one of the
+    graph's own."""
+    ws = _defaults.get(device)
+    if ws is None:
+        with torch.cuda.device(device):
+            capturing = torch.cuda.is_current_stream_capturing()
+        ws = _new_workspace(device) if capturing else default_workspace(device)
+    return ws
+
+
 def quantize(x, format, transpose=False, tensor_scale=None, values=False, stream=None):
     """Quantise x (rows, k), or with ``transpose`` its transpose (x: (k, rows)).
 
@@ -157,12 +169,7 @@ def matmul(a, b, out=None, out_dtype=torch.bfloat16, alpha=1.0, beta=0.0, worksp
         with torch.cuda.stream(stream):
             return matmul(a, b, out, out_dtype, alpha, beta, workspace)
     if workspace is None:
-        d = a.codes.device
-        workspace = _defaults.get(d)
-        if workspace is None:
-            with torch.cuda.device(d):
-                capturing = torch.cuda.is_current_stream_capturing()
-            workspace = _new_workspace(d) if capturing else default_workspace(d)
+        workspace = workspace_for(a.codes.device)
     r = _native().matmul(a, b, out, out_dtype, alpha, beta, workspace.buf)
     if r.__class__ is int:
         raise SkgError(r, "skg_gemm_mx")

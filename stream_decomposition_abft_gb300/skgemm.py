@@ -24,6 +24,7 @@ B_KMAJOR = 0
 B_NMAJOR = 1
 SCHED_DP, SCHED_SK, SCHED_DP_SK1, SCHED_SK2_DP, SCHED_AUTO = 0, 1, 2, 3, 4
 MXFP8, MXFP4, NVFP4 = 0, 1, 2
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
 ROLE_FULL, ROLE_OWNER, ROLE_PEER = 0, 1, 2
 OK = 0
 ERR_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE = 1, 2, 3, 4
@@ -75,6 +76,15 @@ class Plan(ctypes.Structure):
                 ("inloop_checksums", ctypes.c_int32), ("side_checksum_ctas", ctypes.c_int32)]
 
 
+class AdaptersArg(ctypes.Structure):
+    """skg_adapters_t"""
+    _fields_ = [("down", ctypes.c_void_p), ("ld_down", ctypes.c_int64),
+                ("stride_down", ctypes.c_int64), ("up", ctypes.c_void_p),
+                ("ld_up", ctypes.c_int64), ("stride_up", ctypes.c_int64),
+                ("index", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
 class Report(ctypes.Structure):
     _fields_ = [("status_bits", ctypes.c_uint32), ("launches", ctypes.c_uint32),
                 ("tiles_checked", ctypes.c_uint32), ("detected", ctypes.c_uint32),
@@ -95,7 +105,11 @@ SYMBOLS = ("skg_opts_default", "skg_workspace_size", "skg_workspace_init", "skg_
            "skg_noalloc_report_read", "skg_mx_codes_ld", "skg_mx_scales_size", "skg_mx_quantize",
            "skg_mx_quantize_both",
            "skg_rmsnorm_mx", "skg_workspace_size_rmsnorm_backward", "skg_rmsnorm_backward",
-           "skg_workspace_size_mx", "skg_gemm_mx", "skg_mx_test_stall")
+           "skg_workspace_size_mx", "skg_gemm_mx", "skg_mx_test_stall",
+           "skg_workspace_size_layers", "skg_scratch_size_linear", "skg_linear", "skg_gated",
+           "skg_scratch_size_gated_backward", "skg_gated_backward",
+           "skg_scratch_size_feed_forward_backward", "skg_feed_forward_backward",
+           "skg_layers_test_stall")
 
 _lib = None
 
@@ -189,6 +203,27 @@ def lib() -> ctypes.CDLL:
     L.skg_gemm_mx.restype = i32
     L.skg_mx_test_stall.argtypes = [i32, ctypes.c_uint64]
     L.skg_mx_test_stall.restype = i32
+    L.skg_workspace_size_layers.argtypes = []
+    L.skg_workspace_size_layers.restype = sz
+    L.skg_scratch_size_linear.argtypes = [i64, i32]
+    L.skg_scratch_size_linear.restype = sz
+    L.skg_linear.argtypes = [i64, i64, i64, vp, i64, vp, i64, ctypes.POINTER(AdaptersArg), vp, i64,
+                             i32, vp, sz, vp, sz, vp]
+    L.skg_linear.restype = i32
+    L.skg_gated.argtypes = [i64, i64, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp, sz, vp]
+    L.skg_gated.restype = i32
+    L.skg_scratch_size_gated_backward.argtypes = [i64, i64]
+    L.skg_scratch_size_gated_backward.restype = sz
+    L.skg_gated_backward.argtypes = [i64, i64, i64] + [vp, i64] * 4 + [i32] + [vp, i64] * 2 + \
+        [i32, vp, sz, vp, sz, vp]
+    L.skg_gated_backward.restype = i32
+    L.skg_scratch_size_feed_forward_backward.argtypes = [i64, i64]
+    L.skg_scratch_size_feed_forward_backward.restype = sz
+    L.skg_feed_forward_backward.argtypes = [i64, i64, i64] + [vp, i64] * 5 + [i32] + \
+        [vp, i64] * 3 + [i32, vp, sz, vp, sz, vp]
+    L.skg_feed_forward_backward.restype = i32
+    L.skg_layers_test_stall.argtypes = [i32, ctypes.c_uint64]
+    L.skg_layers_test_stall.restype = i32
     L.skg_device_sm_count.argtypes = []
     L.skg_device_sm_count.restype = i32
     L.skg_status_string.argtypes = [i32]
@@ -400,6 +435,56 @@ def gemm_mx(m, n, k, alpha, A_ptr, lda, SA_ptr, ga_ptr, B_ptr, ldb, SB_ptr, gb_p
 
 def mx_test_stall(stages: int, timeout_ns: int = 0) -> int:
     return lib().skg_mx_test_stall(stages, timeout_ns)
+
+
+def workspace_size_layers() -> int:
+    return int(lib().skg_workspace_size_layers())
+
+
+def scratch_size_linear(m: int, rank: int) -> int:
+    return int(lib().skg_scratch_size_linear(m, rank))
+
+
+def linear(m, n, k, X_ptr, ldx, W_ptr, ldw, adapters, Y_ptr, ldy, dtype, ws_ptr, ws_bytes,
+           scratch_ptr, scratch_bytes, stream) -> int:
+    return lib().skg_linear(m, n, k, X_ptr, ldx, W_ptr, ldw,
+                            ctypes.byref(adapters) if adapters else None, Y_ptr, ldy, dtype,
+                            ws_ptr, ws_bytes, scratch_ptr, scratch_bytes, stream)
+
+
+def gated(m, hidden, k, X_ptr, ldx, W_ptr, ldw, act, H_ptr, ldh, PRE_ptr, ldp, dtype, ws_ptr,
+          ws_bytes, stream) -> int:
+    return lib().skg_gated(m, hidden, k, X_ptr, ldx, W_ptr, ldw, act, H_ptr, ldh, PRE_ptr, ldp,
+                           dtype, ws_ptr, ws_bytes, stream)
+
+
+def scratch_size_gated_backward(m: int, hidden: int) -> int:
+    return int(lib().skg_scratch_size_gated_backward(m, hidden))
+
+
+def gated_backward(m, hidden, k, dH_ptr, lddh, X_ptr, ldx, W_ptr, ldw, PRE_ptr, ldp, act, dX_ptr,
+                   lddx, dW_ptr, lddw, dtype, ws_ptr, ws_bytes, scratch_ptr, scratch_bytes,
+                   stream) -> int:
+    return lib().skg_gated_backward(m, hidden, k, dH_ptr, lddh, X_ptr, ldx, W_ptr, ldw, PRE_ptr,
+                                    ldp, act, dX_ptr, lddx, dW_ptr, lddw, dtype, ws_ptr, ws_bytes,
+                                    scratch_ptr, scratch_bytes, stream)
+
+
+def scratch_size_feed_forward_backward(m: int, hidden: int) -> int:
+    return int(lib().skg_scratch_size_feed_forward_backward(m, hidden))
+
+
+def feed_forward_backward(m, hidden, k, dY_ptr, lddy, X_ptr, ldx, Wi_ptr, ldwi, Wo_ptr, ldwo,
+                          PRE_ptr, ldp, act, dX_ptr, lddx, dWi_ptr, lddwi, dWo_ptr, lddwo, dtype,
+                          ws_ptr, ws_bytes, scratch_ptr, scratch_bytes, stream) -> int:
+    return lib().skg_feed_forward_backward(m, hidden, k, dY_ptr, lddy, X_ptr, ldx, Wi_ptr, ldwi,
+                                           Wo_ptr, ldwo, PRE_ptr, ldp, act, dX_ptr, lddx, dWi_ptr,
+                                           lddwi, dWo_ptr, lddwo, dtype, ws_ptr, ws_bytes,
+                                           scratch_ptr, scratch_bytes, stream)
+
+
+def layers_test_stall(stages: int, timeout_ns: int = 0) -> int:
+    return lib().skg_layers_test_stall(stages, timeout_ns)
 
 
 def device_sm_count() -> int:
