@@ -238,6 +238,7 @@ skg_status_t run_product(const Product& q, const Common& c) {
   p.tiles_m = (int)(pair ? tm2 : tm1);
   p.tiles_n = (int)(pair ? tn2 : tn1);
   p.split = pair ? 1 : single.split;
+  p.deep = !pair && tm1 * tn1 * p.split <= c.sms;
   if ((int64_t)p.tiles_m * p.tiles_n * p.split > INT32_MAX) return SKG_ERR_UNSUPPORTED;
   p.a_rows = !pair && q.m < kLinTile ? (p.m + 7) / 8 * 8 : kLinTile;
   const uint32_t bf16 = c.dtype == SKG_IN_BF16;
@@ -260,8 +261,11 @@ skg_status_t run_product(const Product& q, const Common& c) {
     if (!map2(&t.t, c.dtype, q.t, 2 * q.rank_pad, q.m, 2 * q.rank_pad, 64, p.a_rows) ||
         encode_tensor_map3(&t.up, tma_type(c.dtype), 2, ad.up, (uint64_t)ad.rank, (uint64_t)q.n,
                            (uint64_t)ad.count, (uint64_t)ld_of(ad.ld_up, q.n, ad.rank),
-                           (uint64_t)ld_of(ad.stride_up, ad.count, ad.rank), 64, 128,
-                           CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+                           (uint64_t)ld_of(ad.stride_up, ad.count, ad.rank),
+                           (uint32_t)(q.rank_pad <= 32 ? q.rank_pad : 64), 128,
+                           q.rank_pad == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                           : q.rank_pad == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
       return SKG_ERR_CUDA;
   }
   if (pair) {
@@ -451,8 +455,7 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     p.count = ad->count;
     p.ksteps = (int)((k + kLinK - 1) / kLinK);
     p.a_rows = m < kLinTile ? (p.m + 7) / 8 * 8 : kLinTile;
-    const int cols = q.rank_pad < 128 ? q.rank_pad : 128, per = 128 / cols;
-    p.idesc = idesc_f16(dtype == SKG_IN_BF16, 128, (uint32_t)(per * cols));
+    const int cols = q.rank_pad < 128 ? q.rank_pad : 128;
     p.index = ad->index;
     p.scale = ad->scale;
     p.t = q.t;
@@ -460,14 +463,21 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     p.stages = c.stages ? c.stages : UINT32_MAX;
     p.limit = c.limit ? c.limit : kMxTimeoutNs;
     p.report = c.report;
-    // As many CTAs to the rows' k as fit the GPU at once, then clusters for more passes.
+    // As many CTAs to the rows' k as fit the GPU at once, then clusters for the adapters that
+    // the rows may have (as many as one to an SM), then adapters to a pass.
     const int64_t tiles = (m + kLinTile - 1) / kLinTile;
     p.split = 1;
     while (p.split < 8 && tiles * p.split * 2 <= 2 * c.sms && p.split * 2 <= p.ksteps) p.split *= 2;
-    const int most = ad->count < kLinTile ? ad->count : kLinTile;
-    const int passes = q.rank_pad > 128 ? most * ((q.rank_pad + 127) / 128) : (most + per - 1) / per;
-    const int64_t room = 2 * c.sms / (tiles * p.split);
-    p.groups = (int)(room < 1 ? 1 : (room < passes ? room : passes));
+    int most = ad->count < kLinTile ? ad->count : kLinTile;
+    if (m < most) most = (int)m;
+    int64_t room = c.sms / (tiles * p.split);
+    if (room < 1) room = 1;
+    const int64_t want = (most + room - 1) / room;
+    p.per = (int)(want < 128 / cols ? want : 128 / cols);
+    p.idesc = idesc_f16(dtype == SKG_IN_BF16, 128, (uint32_t)(p.per * cols));
+    const int64_t passes = q.rank_pad > 128 ? (int64_t)most * ((q.rank_pad + 127) / 128)
+                                            : (most + p.per - 1) / p.per;
+    p.groups = (int)(room < passes ? room : passes);
     CUtensorMap tx, td;
     if (!map2(&tx, dtype, X, k, m, ldx, kLinK, p.a_rows) ||
         encode_tensor_map3(&td, tma_type(dtype), 2, ad->down, (uint64_t)k, (uint64_t)ad->rank,

@@ -26,7 +26,11 @@
 
 namespace skg {
 
-constexpr int kLinThreads = 192;
+// Warps 0 and 6 load (issuing a stage takes a thread 300 to 420 cycles, more than the 256 of
+// its MMAs on a single CTA: they take every other stage), warp 1 issues the MMAs, warps 2-5
+// take the accumulators out.
+constexpr int kLinThreads = 224;
+constexpr int kLinLoader = 6;
 constexpr int kLinTile = 128;
 constexpr int kLinK = 64;                      // elements of k in a stage
 constexpr int kLinOperand = kLinTile * 128;    // bytes of an operand's 128 rows in a stage
@@ -52,7 +56,7 @@ struct LinParams {
   int lo_b;           // that operand is B, not A
   int tiles_m, tiles_n;
   int split;          // single CTAs: CTAs per tile (cluster size)
-  int direct;         // single CTAs: C is written from registers
+  int deep;           // single CTAs: one per SM, with a ring of twice the stages
   int a_rows;         // single CTAs, K-major A: rows of A's box
   uint32_t idesc;
   int act;            // kLinGated
@@ -177,26 +181,60 @@ __device__ __forceinline__ uint64_t lin_desc(uint32_t at) {
 template <bool MN>
 __host__ __device__ constexpr int lin_step() { return MN ? 2048 >> 4 : 2; }
 
-// The MMAs of one stage; those wholly past k are left out.
+// The MMAs of one stage (descriptors of its start); those wholly past k are left out.
 template <bool PAIR, bool AMN, bool BMN>
-__device__ __forceinline__ void lin_stage_mmas(uint32_t d, uint32_t a_at, uint32_t b_at,
-                                               uint32_t idesc, int left, bool first) {
-  const uint64_t a = lin_desc<AMN>(a_at), b = lin_desc<BMN>(b_at);
-  const int mmas = min(4, (left + 15) >> 4);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j >= mmas) break;
-    const uint32_t acc = (!first || j > 0) ? 1u : 0u;
+__device__ __forceinline__ void lin_stage_mmas(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               int left, bool first) {
+  auto one = [&](int j, uint32_t acc) {
     if constexpr (PAIR) umma_f16_pair(d, a + j * lin_step<AMN>(), b + j * lin_step<BMN>(), idesc, acc);
     else umma_f16(d, a + j * lin_step<AMN>(), b + j * lin_step<BMN>(), idesc, acc);
+  };
+  one(0, first ? 0u : 1u);
+  if (left > 48) {
+    one(1, 1u);
+    one(2, 1u);
+    one(3, 1u);
+  } else {
+    if (left > 16) one(1, 1u);
+    if (left > 32) one(2, 1u);
   }
 }
 
+// The MMA thread's way round the ring. The next stage is looked for before the MMAs of this
+// one are issued: a look costs some 100 cycles until its answer, which a stage of a single
+// CTA (256 cycles of MMAs) has no room for behind them.
+template <int STAGES>
+struct LinRing {
+  LinAux* aux;
+  uint64_t *full, *empty;
+  int st = 0, used = 0;
+  uint32_t phase = 0;
+  bool ready = false;
+  // The next stage's number once it is full; -1: the wait ran out.
+  __device__ __forceinline__ int take() {
+    if (!ready && !mx_wait(&full[st], phase, aux)) return -1;
+    tc_fence_after();
+    const int mine = st;
+    if (++st == STAGES) {
+      st = 0;
+      phase ^= 1u;
+    }
+    ++used;
+    ready = mbar_test_wait(&full[st], phase);
+    return mine;
+  }
+};
+
 // ------------------------------------------------------------------ adapters
-// The stages that one adapter adds to a tile. T holds a row's rp high parts, then its rp low
+// The stages that adapters add to a tile. T holds a row's rp high parts, then its rp low
 // parts (t = high + low to 16 bits of mantissa in bf16, 22 in fp16: rounding t once would add
-// as much error as the rounding of y). Up to rank 32 both lie in one stage of A; beyond,
-// stage s has the parts s & 1 of columns 64 (s / 2)...
+// as much error as the rounding of y).
+//
+// Up to rank 32 both parts lie in one stage's A, and B holds 64 / rp adapters behind one
+// another, each 128 rows of rp elements in the 32- or 64-byte swizzle (64 adapters of rank
+// 16: 16 stages instead of 64). Beyond, an adapter takes stages s = 0, 1, ... with the parts
+// s & 1 of columns 64 (s / 2)... .
+__host__ __device__ constexpr int lora_pack(int rp) { return rp <= 32 ? 64 / rp : 1; }
 __host__ __device__ constexpr int lora_stages(int rp) {
   return rp <= 32 ? 1 : 2 * ((rp + 63) / 64);
 }
@@ -204,18 +242,32 @@ __device__ __forceinline__ int lora_col_t(int rp, int s) {
   return rp <= 32 ? 0 : (s & 1) * rp + (s >> 1) * 64;
 }
 __device__ __forceinline__ int lora_col_b(int rp, int s) { return rp <= 32 ? 0 : (s >> 1) * 64; }
+// Bytes of one adapter's part of a stage's B.
+__host__ __device__ constexpr int lora_bytes(int rp) {
+  return kLinTile * 2 * (rp <= 32 ? rp : 64);
+}
 
+// B's descriptor: K-major rows of 32, 64 or 128 bytes (rank 16, 32, more) in the swizzle of
+// that width (layout 6, 4, 2 at bits 61-63), groups of eight rows behind one another.
+__device__ __forceinline__ uint64_t lora_desc(uint32_t at, int rp) {
+  const uint64_t row = rp <= 32 ? rp * 2 : 128, layout = rp == 16 ? 6 : (rp == 32 ? 4 : 2);
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((row * 8 >> 4) << 32) |
+         ((uint64_t)1 << 46) | (layout << 61);
+}
+
+// The MMAs of adapter number j of a stage (rank over 32: of its stage s), for the rows that
+// are not in `off`.
 template <bool PAIR, int W>
 __device__ __forceinline__ void lora_stage_mmas(uint32_t d, uint32_t a_at, uint32_t b_at,
-                                                uint32_t idesc, int rp, int s,
+                                                uint32_t idesc, int rp, int s, int j,
                                                 const uint32_t (&off)[W]) {
-  const uint64_t a = sdesc_sw128(a_at), b = sdesc_sw128(b_at);
+  const uint64_t a = sdesc_sw128(a_at), b = lora_desc(b_at + j * lora_bytes(rp), rp);
   const int per = (rp <= 32 ? rp : min(64, rp - (s >> 1) * 64)) >> 4;  // 16-column pieces
   const int halves = rp <= 32 ? 2 : 1;
   for (int h = 0; h < halves; ++h)
-    for (int j = 0; j < per; ++j) {
-      if constexpr (PAIR) umma_f16_rows_pair(d, a + h * (rp >> 3) + j * 2, b + j * 2, idesc, off);
-      else umma_f16_rows(d, a + h * (rp >> 3) + j * 2, b + j * 2, idesc, off);
+    for (int i = 0; i < per; ++i) {
+      if constexpr (PAIR) umma_f16_rows_pair(d, a + h * (rp >> 3) + i * 2, b + i * 2, idesc, off);
+      else umma_f16_rows(d, a + h * (rp >> 3) + i * 2, b + i * 2, idesc, off);
     }
 }
 
@@ -239,6 +291,8 @@ int lin_pair_clusters_resident();
 struct LoraParams {
   int m, k, rank, rank_pad, count;  // count: adapters in the stack
   int ksteps, split, groups, a_rows;
+  int per;             // adapters to a pass
+  int stage_bytes, ring_stages;
   uint32_t idesc;
   const int32_t* index;
   const float* scale;  // NULL = 1

@@ -111,78 +111,97 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (threadIdx.x == 0) griddep_launch_dependents();
   }
 
-  uint32_t issued = 0;  // the loading thread: stages loaded
-  if (warp == 0) {
+  uint32_t seq = 0;  // loading threads: stages gone through, every other one by this thread
+  const uint32_t me = warp == kLinLoader;
+  if (warp == 0 || warp == kLinLoader) {
     if (elect_one()) {
       int st = 0;
       uint32_t phase = 0;
       bool ok = true, waited = false;
-      // The next stage, once it is free, with its barrier (the leader's); NULL when its wait
-      // or the stages ran out.
-      uint32_t bar = 0;
-      auto next = [&]() -> uint8_t* {
-        if (issued >= p.stages) {
-          ok = false;
-          return nullptr;
+      // One stage of so many bytes in either CTA: when it is this thread's and free,
+      // load(address, the leader's barrier).
+      auto step = [&](uint32_t bytes, auto load) {
+        if ((seq & 1u) == me) {
+          if (seq >= p.stages) {
+            ok = false;
+            return;
+          }
+          if (!mx_wait(&aux->empty[st], phase ^ 1u, aux)) {
+            lin_fail(p, aux);
+            ok = false;
+            return;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&aux->full[st], 2 * bytes);
+          load(ring + st * C::STAGE_BYTES, cluster_addr(&aux->full[st], 0));
         }
-        if (!mx_wait(&aux->empty[st], phase ^ 1u, aux)) {
-          lin_fail(p, aux);
-          ok = false;
-          return nullptr;
-        }
-        uint8_t* s = ring + st * C::STAGE_BYTES;
-        bar = cluster_addr(&aux->full[st], 0);
-        if (rank == 0) mbar_arrive_expect_tx(&aux->full[st], 2 * C::STAGE_BYTES);
-        ++issued;
+        ++seq;
         if (++st == C::STAGES) {
           st = 0;
           phase ^= 1u;
         }
-        return s;
       };
+      // Four adapters of a plan from the u-th on (past their number: anything).
+      auto read = [](const LoraPlan* plan, int u, int (&id)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) id[e] = plan->id[u + e];
+      };
+      int id[4] = {0, 0, 0, 0}, count = 0;
       const int ks = p.ksteps * p.terms;
       for (int t = first; ok && t < tiles; t += stride) {
         int tm, tn;
         pair_tile(p, t, tm, tn);
         const int row = (2 * tm + rank) * kLinTile;
+        // The plan is read ahead of its use, the first entries beside their number.
+        if (waited) {
+          read(p.plan + tm, 0, id);
+          count = p.plan[tm].count;
+        }
         // Rows of B: this CTA's projection (gated), else its half of the tile's columns.
         const int col = G ? rank * p.n + tn * 128 : tn * 256 + rank * 128;
-        for (int i = 0; i < ks; ++i) {
-          const bool lo = p.terms == 2 && (i & 1);
-          const int k0 = (p.terms == 2 ? i >> 1 : i) * kLinK;
-          uint8_t* s = next();
-          if (!s) break;
-          const CUtensorMap* ma = lo && !p.lo_b ? &maps.lo : &maps.a;
-          const CUtensorMap* mb = lo && p.lo_b ? &maps.lo : &maps.b;
-          if constexpr (AMN) {
-            tma_load_2d_pair(s, ma, bar, row, k0);
-            tma_load_2d_pair(s + kLinBox, ma, bar, row + 64, k0);
-          } else {
-            tma_load_2d_pair(s, ma, bar, k0, row);
-          }
-          if constexpr (BMN) {
-            tma_load_2d_pair(s + kLinOperand, mb, bar, col, k0);
-            tma_load_2d_pair(s + kLinOperand + kLinBox, mb, bar, col + 64, k0);
-          } else {
-            tma_load_2d_pair(s + kLinOperand, mb, bar, k0, col);
-          }
-        }
+        for (int i = 0; ok && i < ks; ++i)
+          step(C::STAGE_BYTES, [&](uint8_t* s, uint32_t bar) {
+            const bool lo = p.terms == 2 && (i & 1);
+            const int k0 = (p.terms == 2 ? i >> 1 : i) * kLinK;
+            const CUtensorMap* ma = lo && !p.lo_b ? &maps.lo : &maps.a;
+            const CUtensorMap* mb = lo && p.lo_b ? &maps.lo : &maps.b;
+            if constexpr (AMN) {
+              tma_load_2d_pair(s, ma, bar, row, k0);
+              tma_load_2d_pair(s + kLinBox, ma, bar, row + 64, k0);
+            } else {
+              tma_load_2d_pair(s, ma, bar, k0, row);
+            }
+            if constexpr (BMN) {
+              tma_load_2d_pair(s + kLinOperand, mb, bar, col, k0);
+              tma_load_2d_pair(s + kLinOperand + kLinBox, mb, bar, col + 64, k0);
+            } else {
+              tma_load_2d_pair(s + kLinOperand, mb, bar, k0, col);
+            }
+          });
         if (ok && lora) {
           if (!waited) {
             griddep_wait();
             griddep_launch_dependents();
             waited = true;
+            read(p.plan + tm, 0, id);
+            count = p.plan[tm].count;
           }
-          const LoraPlan* plan = p.plan + tm;
-          const int count = plan->count, per = lora_stages(p.rank_pad);
-          for (int u = 0; ok && u < count; ++u) {
-            const int id = plan->id[u];
-            for (int j = 0; j < per; ++j) {
-              uint8_t* s = next();
-              if (!s) break;
-              tma_load_2d_pair(s, &maps.t, bar, lora_col_t(p.rank_pad, j), row);
-              tma_load_3d_pair(s + kLinOperand, &maps.up, bar, lora_col_b(p.rank_pad, j), col, id);
-            }
+          const int rp = p.rank_pad, pack = lora_pack(rp), per = lora_stages(rp);
+          const uint32_t one = (uint32_t)lora_bytes(rp);
+          for (int u = 0; ok && u < count; u += pack) {
+            const int here = min(pack, count - u);
+            int behind[4];
+            read(p.plan + tm, min(u + pack, kLoraRows - 4), behind);
+            for (int j = 0; ok && j < per; ++j)
+              step(kLinOperand + here * one, [&](uint8_t* s, uint32_t bar) {
+                tma_load_2d_pair(s, &maps.t, bar, lora_col_t(rp, j), row);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (e < here)
+                    tma_load_3d_pair(s + kLinOperand + e * one, &maps.up, bar, lora_col_b(rp, j),
+                                     col, id[e]);
+              });
+#pragma unroll
+            for (int e = 0; e < 4; ++e) id[e] = behind[e];
           }
         }
       }
@@ -192,66 +211,83 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncwarp();
   } else if (warp == 1) {
     if (elect_one() && rank == 0) {
-      int st = 0, n = 0;
-      uint32_t phase = 0, it = 0;
+      LinRing<C::STAGES> r = {aux, aux->full, aux->empty};
+      const uint64_t a0 = lin_desc<AMN>(smem_u32(ring));
+      const uint64_t b0 = lin_desc<BMN>(smem_u32(ring) + kLinOperand);
+      int n = 0;
       bool ok = true, waited = false;
-      auto stage = [&]() -> uint32_t {  // 0: the wait ran out
-        if (!mx_wait(&aux->full[st], phase, aux)) {
-          lin_fail(p, aux);
-          ok = false;
-          return 0;
-        }
-        tc_fence_after();
-        return smem_u32(ring + st * C::STAGE_BYTES);
+      // The rows to leave out for four adapters (as the loading thread reads them).
+      auto read = [](const LoraPlan* plan, int u, uint32_t (&off)[4][8]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int w = 0; w < 8; ++w) off[e][w] = ~plan->rows[u + e][w];
       };
-      auto done = [&]() {
-        umma_commit_pair(&aux->empty[st]);
-        ++it;
-        if (++st == C::STAGES) {
-          st = 0;
-          phase ^= 1u;
-        }
-      };
+      uint32_t off[4][8];
+      int count = 0;
+      const int terms = p.terms, k = p.k;
+      const uint32_t idesc = p.idesc;
       const int ks = p.ksteps * p.terms;
       for (int t = first; ok && t < tiles; t += stride, ++n) {
         // The accumulator's last tile is out of it.
         if (n > 1 && !mx_wait((n & 1) ? &aux->tempty1 : &aux->tempty, (uint32_t)((n >> 1) - 1) & 1u,
                               aux)) {
-          lin_fail(p, aux);
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (n & 1) * 256;
-        for (int i = 0; i < ks; ++i) {
-          const uint32_t s = stage();
-          if (!s) break;
-          lin_stage_mmas<true, AMN, BMN>(d, s, s + kLinOperand, p.idesc,
-                                         p.k - (p.terms == 2 ? i >> 1 : i) * kLinK, i == 0);
-          done();
-        }
-        if (ok && lora) {
-          if (!waited) griddep_wait();
-          waited = true;
+        const LoraPlan* plan = nullptr;
+        if (lora) {
           int tm, tn;
           pair_tile(p, t, tm, tn);
-          const LoraPlan* plan = p.plan + tm;
-          const int count = plan->count, per = lora_stages(p.rank_pad);
-          for (int u = 0; ok && u < count; ++u) {
-            uint32_t off[8];
-#pragma unroll
-            for (int w = 0; w < 8; ++w) off[w] = ~plan->rows[u][w];
+          plan = p.plan + tm;
+          if (waited) {
+            read(plan, 0, off);
+            count = plan->count;
+          }
+        }
+        for (int i = 0; i < ks; ++i) {
+          const int st = r.take();
+          ok = st >= 0;
+          if (!ok) break;
+          const uint64_t at = (uint64_t)((st * C::STAGE_BYTES) >> 4);
+          lin_stage_mmas<true, AMN, BMN>(d, a0 + at, b0 + at, idesc,
+                                         k - (terms == 2 ? i >> 1 : i) * kLinK, i == 0);
+          umma_commit_pair(&aux->empty[st]);
+        }
+        if (ok && lora) {
+          if (!waited) {
+            griddep_wait();
+            waited = true;
+            read(plan, 0, off);
+            count = plan->count;
+          }
+          const int rp = p.rank_pad, pack = lora_pack(rp), per = lora_stages(rp);
+          for (int u = 0; ok && u < count; u += pack) {
+            const int here = min(pack, count - u);
+            uint32_t behind[4][8];
+            read(plan, min(u + pack, kLoraRows - 4), behind);
             for (int j = 0; j < per; ++j) {
-              const uint32_t s = stage();
-              if (!s) break;
-              lora_stage_mmas<true>(d, s, s + kLinOperand, p.idesc, p.rank_pad, j, off);
-              done();
+              const int st = r.take();
+              ok = st >= 0;
+              if (!ok) break;
+              const uint32_t s = smem_u32(ring + st * C::STAGE_BYTES);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (e < here) lora_stage_mmas<true>(d, s, s + kLinOperand, idesc, rp, j, e, off[e]);
+              umma_commit_pair(&aux->empty[st]);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int w = 0; w < 8; ++w) off[e][w] = behind[e][w];
           }
         }
         if (ok) umma_commit_pair(&aux->tfull[n & 1]);
       }
-      if (it > 0) {
+      if (!ok) lin_fail(p, aux);
+      if (r.used > 0) {
         umma_commit_pair(&aux->drain);
         mx_wait(&aux->drain, 0, aux, true);
       }
@@ -341,10 +377,11 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
   // leader's last commit has reached the other CTA's barrier, and no CTA leaves while the
   // other may still signal its barriers.
   if (warp == 1 && rank == 1 && first < tiles && elect_one()) mx_wait(&aux->drain, 0, aux, true);
-  if (warp == 0 && rank == 0 && issued > 0 && mx_aborted(aux))
-    for (uint32_t i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
-      mx_wait(&aux->full[i % C::STAGES], (i / C::STAGES) & 1u, aux, true);
-  if (warp == 0 && rank == 1 && issued > 0 && mx_aborted(aux))
+  if (rank == 0 && seq > 0 && mx_aborted(aux))
+    for (uint32_t i = seq > C::STAGES ? seq - C::STAGES : 0; i < seq; ++i)
+      if ((i & 1u) == me)
+        mx_wait(&aux->full[i % C::STAGES], (i / C::STAGES) & 1u, aux, true);
+  if (rank == 1 && seq > 0 && mx_aborted(aux))
     for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) __nanosleep(1000);
   __syncwarp();
   cluster_sync();

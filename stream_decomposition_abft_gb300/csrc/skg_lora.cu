@@ -2,12 +2,13 @@
 // rows of any mixture of adapters, and the plans that the product behind it reads.
 //
 // A cluster takes 128 rows of x and finds the distinct adapters in them (the plan: one pass
-// of comparisons over 256 indices). With ranks up to 128 it works on as many adapters at
-// once as fit 128 columns of the accumulator (8 of rank 16): a stage is 64 of k of the rows
-// and of those adapters' A, one MMA forms every row's product with every one of them, and on
-// the way out each row takes the columns of its own. Infinities and NaN in other adapters
-// stay in columns that nothing reads. More adapters than that take more passes over x (in
-// L2), which `groups` clusters share; larger ranks take a pass for each 128 columns.
+// of comparisons over 256 indices). With ranks up to 128 it works on `per` adapters at once,
+// at most as many as fit 128 columns of the accumulator (8 of rank 16): a stage is 64 of k
+// of the rows and of those adapters' A, one MMA forms every row's product with every one of
+// them, and on the way out each row takes the columns of its own. Infinities and NaN in other
+// adapters stay in columns that nothing reads. More adapters than that take more passes over
+// x (in L2), which `groups` clusters share; larger ranks take a pass for each 128 columns.
+// Few rows or few adapters make small stages, and the ring holds up to 16 of them.
 //
 // The CTAs of a cluster split k; their partial sums are added in rank order through
 // distributed shared memory (no atomics, the same result every time). t is stored as the sum
@@ -27,89 +28,89 @@ namespace skg {
 namespace {
 
 constexpr int kPitch = 132;  // floats per row of the partial sums
-constexpr int kStages = 3;   // two CTAs share an SM
-constexpr int kStageBytes = 2 * kLinOperand;
+constexpr int kRing = 6 * kLinOperand;  // two CTAs share an SM
+constexpr int kMaxStages = 16;
 
+// The adapters of a tile's rows, and those of the 256 rows that the plan in global memory
+// covers.
 struct Plan {
-  int32_t ids[kLoraRows];   // adapter of each row, -1: none
-  int32_t slot[kLoraRows];  // number of that adapter in the plan
-  int32_t id[kLoraRows];    // adapters by number
-  uint32_t rows[kLoraRows][8];
-  int32_t list[kLinTile];   // the adapters (numbers) of this tile's 128 rows
-  int32_t place[kLoraRows]; // number -> place in list
-  uint32_t lead[8];
-  int32_t count, tile_count;
+  int32_t ids[kLinTile];   // adapter of each row, -1: none
+  int32_t slot[kLinTile];  // number of that adapter
+  int32_t id[kLinTile];    // adapters by number, in the order of their first rows
+  float scale[kLinTile];
+  uint32_t lead[4];        // rows that are their adapter's first
+  int32_t ids2[kLoraRows], slot2[kLoraRows];
+  uint32_t lead2[8];
 };
 
-constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + 256 + sizeof(Plan);
-static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
-static_assert(kLinTile * kPitch * 4 <= kStages * kStageBytes, "the partial sums fit the ring");
+struct LoraAux : LinAux {  // with barriers of its own for the ring
+  uint64_t ring_full[kMaxStages], ring_empty[kMaxStages];
+};
 
-// All threads. Rows row0, ... of the index; `half`: the 128 of them that are this tile's.
-__device__ void make_plan(const LoraParams& p, Plan* pl, int row0, int half) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kLoraRows; i += kLinThreads) {
-    const int id = row0 + i < p.m ? p.index[row0 + i] : -1;
-    pl->ids[i] = id >= 0 && id < p.count ? id : -1;
+constexpr uint32_t kSmem = 1024 + kRing + 512 + sizeof(Plan);
+static_assert(sizeof(LoraAux) <= 512, "aux size");
+static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+static_assert(kLinTile * kPitch * 4 <= kRing, "the partial sums fit the ring");
+
+__device__ __forceinline__ void fail(const LoraParams& p, LoraAux* aux) {
+  if (atomicExch(&aux->abort_flag, 1) == 0) {
+    atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
+    atomicAdd(&p.report->timeouts, 1u);
   }
-  for (int i = threadIdx.x; i < kLoraRows * 8; i += kLinThreads) (&pl->rows[0][0])[i] = 0;
-  __syncthreads();
-  // The first row of each row's adapter, first within its 32 rows, then before them.
-  for (int g = warp; g < 8; g += kLinThreads / 32) {
-    const int i = g * 32 + lane, id = pl->ids[i];
+}
+
+template <int THREADS>
+__device__ __forceinline__ void plan_sync() {
+  if constexpr (THREADS == kLinThreads) __syncthreads();
+  else named_bar_sync(3, THREADS);
+}
+
+// Numbers the distinct adapters of `rows` rows from row0 on in the order of their first rows
+// (THREADS threads, of which this is `tid`): ids and slot of each row, lead (the first rows);
+// emit(number, id) once for each, mask(number, word, rows of those 32). Returns their number.
+template <int THREADS, typename Emit, typename Mask>
+__device__ __forceinline__ int number_adapters(const LoraParams& p, int row0, int rows, int tid,
+                                               int32_t* ids, int32_t* slot, uint32_t* lead,
+                                               Emit emit, Mask mask) {
+  const int warp = tid >> 5, lane = tid & 31, words = (rows + 31) / 32;
+  for (int i = tid; i < words * 32; i += THREADS) {
+    const int id = i < rows ? p.index[row0 + i] : -1;
+    ids[i] = id >= 0 && id < p.count ? id : -1;
+  }
+  plan_sync<THREADS>();
+  // The first row of each row's adapter: within its 32 rows, then before them.
+  for (int g = warp; g < words; g += THREADS / 32) {
+    const int i = g * 32 + lane, id = ids[i];
     const uint32_t same = __match_any_sync(0xffffffffu, id);
     int first = g * 32 + __ffs(same) - 1;
-    if (__any_sync(0xffffffffu, id >= 0)) {
-      for (int j = g * 32 - 4; j >= 0; j -= 4) {
-        const int4 o = *reinterpret_cast<const int4*>(&pl->ids[j]);
-        first = o.w == id ? j + 3 : first;
-        first = o.z == id ? j + 2 : first;
-        first = o.y == id ? j + 1 : first;
-        first = o.x == id ? j : first;
-      }
+    for (int j = g * 32 - 4; j >= 0; j -= 4) {
+      const int4 o = *reinterpret_cast<const int4*>(&ids[j]);
+      first = o.w == id ? j + 3 : first;
+      first = o.z == id ? j + 2 : first;
+      first = o.y == id ? j + 1 : first;
+      first = o.x == id ? j : first;
     }
-    pl->slot[i] = first;  // a row's number, until all are known
-    const uint32_t lead = __ballot_sync(0xffffffffu, id >= 0 && first == i);
-    if (lane == 0) pl->lead[g] = lead;
+    slot[i] = first;  // (a row's number, until all are known)
+    const uint32_t b = __ballot_sync(0xffffffffu, id >= 0 && first == i);
+    if (lane == 0) lead[g] = b;
   }
-  __syncthreads();
-  for (int g = warp; g < 8; g += kLinThreads / 32) {
-    const int i = g * 32 + lane, id = pl->ids[i], first = pl->slot[i];
+  plan_sync<THREADS>();
+  int count = 0;
+  for (int w = 0; w < words; ++w) count += __popc(lead[w]);
+  for (int g = warp; g < words; g += THREADS / 32) {
+    const int i = g * 32 + lane, id = ids[i], first = slot[i];
     const uint32_t same = __match_any_sync(0xffffffffu, id);
     int s = 0;
-    for (int w = 0; w < 8; ++w) {
-      const uint32_t below = w < (first >> 5) ? ~0u : (w == (first >> 5) ? (1u << (first & 31)) - 1 : 0u);
-      s += __popc(pl->lead[w] & below);
-    }
-    __syncwarp();
+    for (int w = 0; w <= first >> 5; ++w)
+      s += __popc(lead[w] & (w < (first >> 5) ? ~0u : (1u << (first & 31)) - 1));
     if (id >= 0) {
-      pl->slot[i] = s;
-      if (first == i) pl->id[s] = id;
-      if (lane == __ffs(same) - 1) pl->rows[s][g] = same;
+      slot[i] = s;
+      if (first == i) emit(s, id);
+      if (lane == __ffs(same) - 1) mask(s, g, same);
     }
   }
-  __syncthreads();
-  if (warp == 0) {
-    int count = 0, mine = 0;
-    for (int w = 0; w < 8; ++w) count += __popc(pl->lead[w]);
-    for (int s = lane; s < (count + 31) / 32 * 32; s += 32) {
-      bool here = false;
-      if (s < count)
-        for (int w = 0; w < 4; ++w) here |= pl->rows[s][half * 4 + w] != 0;
-      const uint32_t b = __ballot_sync(0xffffffffu, here);
-      if (here) {
-        const int at = mine + __popc(b & ((1u << lane) - 1));
-        pl->list[at] = s;
-        pl->place[s] = at;
-      }
-      mine += __popc(b);
-    }
-    if (lane == 0) {
-      pl->count = count;
-      pl->tile_count = mine;
-    }
-  }
-  __syncthreads();
+  plan_sync<THREADS>();
+  return count;
 }
 
 template <typename T>
@@ -134,8 +135,8 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                  const LoraParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  LinAux* aux = reinterpret_cast<LinAux*>(ring + kStages * kStageBytes);
-  Plan* pl = reinterpret_cast<Plan*>(ring + kStages * kStageBytes + 256);
+  LoraAux* aux = reinterpret_cast<LoraAux*>(ring + kRing);
+  Plan* pl = reinterpret_cast<Plan*>(ring + kRing + 512);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
   const int unit = (int)blockIdx.x / p.split;
@@ -148,9 +149,9 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     prefetch_tmap(&tmA);
     aux->abort_flag = 0;
     aux->limit = p.limit;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&aux->full[i], 1);
-      mbar_init(&aux->empty[i], 1);
+    for (int i = 0; i < p.ring_stages; ++i) {
+      mbar_init(&aux->ring_full[i], 1);
+      mbar_init(&aux->ring_empty[i], 1);
     }
     mbar_init(&aux->tfull[0], 1);
     mbar_init(&aux->drain, 1);
@@ -164,87 +165,124 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = aux->tmem_slot;
-  // The product behind reads x and writes y before it waits for this kernel, so it may
-  // start only when all that ran before is complete.
   griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  make_plan(p, pl, (tm >> 1) * kLoraRows, tm & 1);
 
-  if (group == 0 && rank == 0 && (tm & 1) == 0) {
+  const int rp = p.rank_pad, cols = min(rp, 128), chunks = (rp + 127) / 128;
+  const int per = p.per, stages = p.ring_stages;
+  int seq = 0, it = 0, n = 0;
+  int load_st = 0, mma_st = 0, early = 0;
+  uint32_t load_phase = 0, mma_phase = 0;
+  bool load_ok = true, mma_ok = true;
+  const bool loader = warp == 0 || warp == kLinLoader;
+  const int me = warp == kLinLoader;  // a loading thread takes every other stage
+  // The first pass's x is under way while the plan is made.
+  if (loader && elect_one()) {
+    early = min(min(stages, kb1 - kb0), (int)min(p.stages, (uint32_t)kMaxStages));
+    for (int i = me; i < early; i += 2) {
+      mbar_expect_tx(&aux->ring_full[i], (uint32_t)p.a_rows * 128);
+      tma_load_2d(ring + i * p.stage_bytes, &tmX, &aux->ring_full[i], (kb0 + i) * kLinK,
+                  tm * kLinTile);
+    }
+  }
+  __syncwarp();
+  const int rows = min(kLinTile, p.m - tm * kLinTile);
+  const int count = number_adapters<kLinThreads>(
+      p, tm * kLinTile, rows, (int)threadIdx.x, pl->ids, pl->slot, pl->lead,
+      [&](int s, int id) {
+        pl->id[s] = id;
+        pl->scale[s] = p.scale ? p.scale[id] : 1.f;
+      },
+      [](int, int, uint32_t) {});
+  // Passes: `per` adapters each, or (rank over 128) one adapter's next 128 columns.
+  const int passes = chunks > 1 ? count * chunks : (count + per - 1) / per;
+  // The product behind reads x and writes y before it waits for this kernel: that is safe
+  // once all that ran before is complete, as it is here. But its loads of W would queue
+  // ahead of these (one token, k = 8192: 10 us for loads of 2): it may start when the last
+  // of them is on its way.
+  if (threadIdx.x == 0 && group >= passes) griddep_launch_dependents();
+
+  // The plan for the product, by the warps that wait for the accumulator anyway.
+  if (warp >= 2 && !loader && group == 0 && rank == 0 && (tm & 1) == 0) {
     LoraPlan* out = p.plan + (tm >> 1);
-    const int count = pl->count;
-    if (threadIdx.x == 0) out->count = count;
-    for (int i = threadIdx.x; i < count; i += kLinThreads) out->id[i] = pl->id[i];
-    for (int i = threadIdx.x; i < count * 8; i += kLinThreads)
-      (&out->rows[0][0])[i] = (&pl->rows[0][0])[i];
+    const int tid = (int)threadIdx.x - 64;
+    const int both = min(kLoraRows, p.m - tm * kLinTile);
+    for (int i = tid; i < (both + 31) / 32 * 32 * 2; i += 128)
+      reinterpret_cast<uint4*>(&out->rows[0][0])[i] = make_uint4(0, 0, 0, 0);
+    const int c = number_adapters<128>(
+        p, tm * kLinTile, both, tid, pl->ids2, pl->slot2, pl->lead2,
+        [&](int s, int id) { out->id[s] = id; },
+        [&](int s, int w, uint32_t m) { out->rows[s][w] = m; });
+    if (tid == 0) out->count = c;
   }
 
-  // Passes: `per` adapters each, or (rank over 128) one adapter's next 128 columns.
-  const int rp = p.rank_pad, cols = min(rp, 128), chunks = (rp + 127) / 128;
-  const int per = 128 / cols;
-  const int passes = chunks > 1 ? pl->tile_count * chunks : (pl->tile_count + per - 1) / per;
-  const int rows = min(kLinTile, p.m - tm * kLinTile);
-  int issued = 0, it = 0, n = 0;
-  bool load_ok = true, mma_ok = true;
   for (int pass = group; pass < passes; pass += p.groups, ++n) {
     const int first = chunks > 1 ? pass / chunks : pass * per;
     const int chunk = chunks > 1 ? pass % chunks : 0;
-    const int here = chunks > 1 ? 1 : min(per, pl->tile_count - first);
+    const int here = chunks > 1 ? 1 : min(per, count - first);
     bool fine = true;
-    if (warp == 0) {
+    if (loader) {
       if (elect_one()) {
+        int id[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) id[j] = j < here ? pl->id[first + j] : 0;
         for (int kb = kb0; load_ok && kb < kb1; ++kb) {
-          const int st = issued % kStages;
-          if ((uint32_t)issued >= p.stages) {
-            load_ok = false;
-            break;
-          }
-          if (!mx_wait(&aux->empty[st], (uint32_t)((issued / kStages) & 1) ^ 1u, aux)) {
-            if (atomicExch(&aux->abort_flag, 1) == 0) {
-              atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
-              atomicAdd(&p.report->timeouts, 1u);
+          if ((seq & 1) == me) {
+            if ((uint32_t)seq >= p.stages) {
+              load_ok = false;
+              break;
             }
-            load_ok = false;
-            break;
+            uint64_t* bar = &aux->ring_full[load_st];
+            if (!mx_wait(&aux->ring_empty[load_st], load_phase ^ 1u, aux)) {
+              fail(p, aux);
+              load_ok = false;
+              break;
+            }
+            uint8_t* s = ring + load_st * p.stage_bytes;
+            const uint32_t a_bytes = seq < early ? 0 : (uint32_t)p.a_rows * 128;
+            mbar_arrive_expect_tx(bar, a_bytes + (uint32_t)(here * cols) * 128);
+            if (a_bytes) tma_load_2d(s, &tmX, bar, kb * kLinK, tm * kLinTile);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < here)
+                tma_load_3d(s + (p.a_rows + j * cols) * 128, &tmA, bar, kb * kLinK, chunk * 128,
+                            id[j]);
           }
-          uint8_t* s = ring + st * kStageBytes;
-          mbar_arrive_expect_tx(&aux->full[st], (uint32_t)(p.a_rows + here * cols) * 128);
-          tma_load_2d(s, &tmX, &aux->full[st], kb * kLinK, tm * kLinTile);
-          for (int j = 0; j < here; ++j)
-            tma_load_3d(s + kLinOperand + j * cols * 128, &tmA, &aux->full[st], kb * kLinK,
-                        chunk * 128, pl->id[pl->list[first + j]]);
-          ++issued;
+          ++seq;
+          if (++load_st == stages) {
+            load_st = 0;
+            load_phase ^= 1u;
+          }
         }
+        if (pass + p.groups >= passes) griddep_launch_dependents();
       }
       __syncwarp();
     } else if (warp == 1) {
       if (elect_one()) {
         for (int kb = kb0; mma_ok && kb < kb1; ++kb) {
-          const int st = it % kStages;
-          if (!mx_wait(&aux->full[st], (uint32_t)((it / kStages) & 1), aux)) {
-            if (atomicExch(&aux->abort_flag, 1) == 0) {
-              atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
-              atomicAdd(&p.report->timeouts, 1u);
-            }
+          const int st = mma_st;
+          if (!mx_wait(&aux->ring_full[st], mma_phase, aux)) {
+            fail(p, aux);
             mma_ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t s = smem_u32(ring + st * kStageBytes);
-          lin_stage_mmas<false, false, false>(tmem, s, s + kLinOperand, p.idesc,
+          const uint32_t s = smem_u32(ring + st * p.stage_bytes);
+          lin_stage_mmas<false, false, false>(tmem, lin_desc<false>(s),
+                                              lin_desc<false>(s + p.a_rows * 128), p.idesc,
                                               p.k - kb * kLinK, kb == kb0);
-          umma_commit(&aux->empty[st]);
+          umma_commit(&aux->ring_empty[st]);
           ++it;
+          if (++mma_st == stages) {
+            mma_st = 0;
+            mma_phase ^= 1u;
+          }
         }
         if (mma_ok) umma_commit(&aux->tfull[0]);
       }
       __syncwarp();
-    } else {
+    } else {  // warps 2-5
       fine = mx_wait(&aux->tfull[0], (uint32_t)n & 1u, aux);
-      if (!fine && atomicExch(&aux->abort_flag, 1) == 0) {
-        atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
-        atomicAdd(&p.report->timeouts, 1u);
-      }
+      if (!fine) fail(p, aux);
       fine = epi_all(fine);
       tc_fence_after();
       const int q = warp & 3, r = q * 32 + lane;
@@ -274,22 +312,26 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
       const int mine = rank < rows ? (rows - rank + p.split - 1) / p.split : 0;
       for (int i = threadIdx.x; i < mine * quads; i += kLinThreads) {
         const int r = rank + (i / quads) * p.split, c = (i % quads) * 4;
-        const int row = (tm & 1) * kLinTile + r;
-        const int id = pl->ids[row];
-        if (id < 0) continue;
-        const int at = pl->place[pl->slot[row]] - first;
+        if (pl->ids[r] < 0) continue;
+        const int at = pl->slot[r] - first;
         if (at < 0 || at >= here) continue;
         const float* src = part + r * kPitch + at * cols + c;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.split; ++s) {
-          const float4 u = p.split > 1 ? ld_shared_cluster_f32x4(cluster_addr(src, (uint32_t)s))
-                                       : *reinterpret_cast<const float4*>(src);
-          v[0] += u.x;
-          v[1] += u.y;
-          v[2] += u.z;
-          v[3] += u.w;
-        }
-        const float f = p.scale ? p.scale[id] : 1.f;
+        float4 u[8];  // the loads in flight together
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < p.split)
+            u[s] = p.split > 1 ? ld_shared_cluster_f32x4(cluster_addr(src, (uint32_t)s))
+                               : *reinterpret_cast<const float4*>(src);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < p.split) {
+            v[0] += u[s].x;
+            v[1] += u[s].y;
+            v[2] += u[s].z;
+            v[3] += u[s].w;
+          }
+        const float f = pl->scale[pl->slot[r]];
         const int col = chunk * 128 + c;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = col + e < p.rank ? f * v[e] : 0.f;
@@ -298,9 +340,10 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
       }
     }
     // The ring is written by the next pass's copies, and no CTA leaves while another reads
-    // its partial sums.
+    // its partial sums (loads whose values are used by now).
     fence_proxy_async_smem();
-    if (p.split > 1) cluster_sync();
+    __syncwarp();
+    if (p.split > 1) cluster_meet();
     else __syncthreads();
   }
   if (warp == 1 && elect_one() && it > 0) {
@@ -308,9 +351,17 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     mx_wait(&aux->drain, 0, aux, true);
   }
   __syncwarp();
-  if (warp == 0 && issued > 0 && mx_aborted(aux))  // elected lane alone has issued > 0
-    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-      mx_wait(&aux->full[i % kStages], (uint32_t)((i / kStages) & 1), aux, true);
+  // Copies land before the CTA leaves: those of x for rows without any adapter (or stages not
+  // come to), whose barriers still lack the arrival, and those that no MMA waited for.
+  for (int i = 0; i < early; ++i)
+    if ((i & 1) == me && i >= seq) {
+      mbar_arrive(&aux->ring_full[i]);
+      mx_wait(&aux->ring_full[i], 0, aux, true);
+    }
+  if (seq > 0 && mx_aborted(aux))
+    for (int i = seq > stages ? seq - stages : 0; i < seq; ++i)
+      if ((i & 1) == me)
+        mx_wait(&aux->ring_full[i % stages], (uint32_t)((i / stages) & 1), aux, true);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -322,8 +373,14 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
 }
 
 template <typename T>
-cudaError_t launch(const CUtensorMap& x, const CUtensorMap& down, const LoraParams& p,
+cudaError_t launch(const CUtensorMap& x, const CUtensorMap& down, LoraParams p,
                    cudaStream_t stream) {
+  const int cols = p.rank_pad < 128 ? p.rank_pad : 128;
+  p.stage_bytes = (p.a_rows + p.per * cols) * 128;
+  // An MMA reads 128 rows from a stage's start, so as many end inside the ring.
+  const int last = p.stage_bytes > kLinOperand ? p.stage_bytes : kLinOperand;
+  const int fit = (kRing - last) / p.stage_bytes + 1;
+  p.ring_stages = fit < kMaxStages ? fit : kMaxStages;
   static std::atomic<uint64_t> done_mask{0};
   const cudaError_t e = opt_in_smem((const void*)lora_down_kernel<T>, done_mask, (int)kSmem);
   if (e != cudaSuccess) return e;
