@@ -147,7 +147,7 @@ struct Product {
   void* pre;
   int64_t ldp;
   const skg_adapters_t* adapters;
-  void* t;
+  void* t;          // with a plan: t and the plan come from skg_lora.cu's kernel
   LoraPlan* plan;
   int rank_pad;
 };
@@ -209,7 +209,51 @@ bool wants_pairs(int64_t m, int64_t tiles, int ksteps, int clusters, double sing
   return 4.2 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;
 }
 
+// How a product runs.
+struct Choice {
+  bool pair, deep;
+  int64_t tiles_m, tiles_n;
+  int split, resident;
+};
+Choice choose(const Product& q, const Common& c) {
+  const int64_t cols = q.mode == kLinGated ? 2 * q.n : q.n;  // of the accumulators
+  const int64_t tm1 = (q.m + 127) / 128, tn1 = (cols + 127) / 128;
+  const int64_t tm2 = (q.m + 255) / 256, tn2 = (cols + 255) / 256;
+  const int steps = (int)((q.k + kLinK - 1) / kLinK) * (q.a.lo || q.b.lo ? 2 : 1);
+  Choice h = {};
+  h.resident = lin_pair_clusters_resident();
+  const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms);
+  h.pair = q.out != SKG_OUT_F32 && h.resident > 0 &&
+           wants_pairs(q.m, tm2 * tn2, steps, h.resident, single.us);
+  h.tiles_m = h.pair ? tm2 : tm1;
+  h.tiles_n = h.pair ? tn2 : tn1;
+  h.split = h.pair ? 1 : single.split;
+  h.deep = !h.pair && tm1 * tn1 * h.split <= c.sms;
+  return h;
+}
+
+// Adapters that 128 rows can have.
+int most_adapters(int64_t m, const skg_adapters_t& ad) {
+  const int rows = m < kLinTile ? (int)m : kLinTile;
+  return ad.count < rows ? ad.count : rows;
+}
+
+// Whether a product with adapters is one launch (skg_lin_adapted.cu).
+bool one_launch(const Product& q, const Choice& h) {
+  return q.adapters && !h.pair && (q.m <= 16 || h.deep) &&
+         lin_adapted_fits(most_adapters(q.m, *q.adapters), q.rank_pad);
+}
+
+bool map_down(CUtensorMap* t, int dtype, const skg_adapters_t& ad, int64_t k, int box_rows) {
+  return encode_tensor_map3(t, tma_type(dtype), 2, ad.down, (uint64_t)k, (uint64_t)ad.rank,
+                            (uint64_t)ad.count, (uint64_t)ld_of(ad.ld_down, ad.rank, k),
+                            (uint64_t)ld_of(ad.stride_down, ad.count, k), kLinK,
+                            (uint32_t)box_rows, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
 skg_status_t run_product(const Product& q, const Common& c) {
+  const Choice h = choose(q, c);
+  const bool pair = h.pair, gated = q.mode == kLinGated, fused = one_launch(q, h);
   LinParams p = {};
   p.m = (int)q.m;
   p.n = (int)q.n;
@@ -227,26 +271,19 @@ skg_status_t run_product(const Product& q, const Common& c) {
   p.report = c.report;
   p.stages = c.stages ? c.stages : UINT32_MAX;
   p.limit = c.limit ? c.limit : kMxTimeoutNs;
-  const bool gated = q.mode == kLinGated;
-  const int64_t cols = gated ? 2 * q.n : q.n;  // of the accumulators
-  const int64_t tm1 = (q.m + 127) / 128, tn1 = (cols + 127) / 128;
-  const int64_t tm2 = (q.m + 255) / 256, tn2 = (cols + 255) / 256;
-  const int resident = lin_pair_clusters_resident();
-  const SinglePlan single = single_plan(q.m, tm1 * tn1, p.ksteps * p.terms, c.sms);
-  const bool pair = q.out != SKG_OUT_F32 && resident > 0 &&
-                    wants_pairs(q.m, tm2 * tn2, p.ksteps * p.terms, resident, single.us);
-  p.tiles_m = (int)(pair ? tm2 : tm1);
-  p.tiles_n = (int)(pair ? tn2 : tn1);
-  p.split = pair ? 1 : single.split;
-  p.deep = !pair && tm1 * tn1 * p.split <= c.sms;
-  if ((int64_t)p.tiles_m * p.tiles_n * p.split > INT32_MAX) return SKG_ERR_UNSUPPORTED;
+  if (h.tiles_m * h.tiles_n * h.split > INT32_MAX) return SKG_ERR_UNSUPPORTED;
+  p.tiles_m = (int)h.tiles_m;
+  p.tiles_n = (int)h.tiles_n;
+  p.split = h.split;
+  p.deep = h.deep;
   p.a_rows = !pair && q.m < kLinTile ? (p.m + 7) / 8 * 8 : kLinTile;
   const uint32_t bf16 = c.dtype == SKG_IN_BF16;
   p.idesc = idesc_f16(bf16, pair ? 256 : 128, pair ? 256 : 128) | ((uint32_t)q.a.mn << 15) |
             ((uint32_t)q.b.mn << 16);
 
-  // Rows of B's box: a tile's (K-major) columns, or one projection's share of them.
-  const int b_box = pair ? 128 : (gated ? 64 : 128);
+  // Rows of B, and of its box: a tile's (K-major) columns, or one projection's share of them.
+  const int64_t cols = gated ? 2 * q.n : q.n;
+  const int b_box = gated && !pair ? 64 : 128;
   LinMaps t;
   if (!map_operand(&t.a, c.dtype, q.a, q.a.p, q.m, q.k, p.a_rows) ||
       !map_operand(&t.b, c.dtype, q.b, q.b.p, cols, q.k, b_box))
@@ -256,16 +293,31 @@ skg_status_t run_product(const Product& q, const Common& c) {
       !(p.lo_b ? map_operand(&t.lo, c.dtype, q.b, q.b.lo, cols, q.k, b_box)
                : map_operand(&t.lo, c.dtype, q.a, q.a.lo, q.m, q.k, p.a_rows)))
     return SKG_ERR_CUDA;
-  if (q.plan) {
+  if (q.adapters) {
     const skg_adapters_t& ad = *q.adapters;
-    if (!map2(&t.t, c.dtype, q.t, 2 * q.rank_pad, q.m, 2 * q.rank_pad, 64, p.a_rows) ||
-        encode_tensor_map3(&t.up, tma_type(c.dtype), 2, ad.up, (uint64_t)ad.rank, (uint64_t)q.n,
+    if (encode_tensor_map3(&t.up, tma_type(c.dtype), 2, ad.up, (uint64_t)ad.rank, (uint64_t)q.n,
                            (uint64_t)ad.count, (uint64_t)ld_of(ad.ld_up, q.n, ad.rank),
                            (uint64_t)ld_of(ad.stride_up, ad.count, ad.rank),
                            (uint32_t)(q.rank_pad <= 32 ? q.rank_pad : 64), 128,
                            q.rank_pad == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
                            : q.rank_pad == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                               : CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+      return SKG_ERR_CUDA;
+    if (fused) {
+      AdaptedParams a = {};
+      a.index = ad.index;
+      a.scale = ad.scale;
+      a.count = ad.count;
+      a.rank = ad.rank;
+      a.most = most_adapters(q.m, ad);
+      a.idesc_up = p.idesc;
+      p.idesc = idesc_f16(bf16, 128, (uint32_t)(128 + a.most * q.rank_pad));
+      CUtensorMap down;
+      if (!map_down(&down, c.dtype, ad, q.k, q.rank_pad)) return SKG_ERR_CUDA;
+      return launch_lin_adapted(q.out, t, down, p, a, c.stream) == cudaSuccess ? SKG_OK
+                                                                               : SKG_ERR_CUDA;
+    }
+    if (!map2(&t.t, c.dtype, q.t, 2 * q.rank_pad, q.m, 2 * q.rank_pad, 64, p.a_rows))
       return SKG_ERR_CUDA;
   }
   if (pair) {
@@ -275,9 +327,9 @@ skg_status_t run_product(const Product& q, const Common& c) {
       return SKG_ERR_CUDA;
   }
   const LinVariant v = {q.mode, q.a.mn, q.b.mn, q.out};
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  const int64_t tiles = h.tiles_m * h.tiles_n;
   const cudaError_t e =
-      pair ? launch_lin_pair(v, t, p, (int)(tiles < resident ? tiles : resident), c.stream)
+      pair ? launch_lin_pair(v, t, p, (int)(tiles < h.resident ? tiles : h.resident), c.stream)
            : launch_lin_single(v, t, p, c.stream);
   return e == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
 }
@@ -444,6 +496,8 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
   if (ad) {
     q.adapters = ad;
     q.rank_pad = (ad->rank + 15) / 16 * 16;
+  }
+  if (ad && !one_launch(q, choose(q, c))) {
     q.plan = reinterpret_cast<LoraPlan*>(scratch);
     q.t = (uint8_t*)scratch +
           up256((size_t)((m + kLoraRows - 1) / kLoraRows) * sizeof(LoraPlan));
@@ -468,8 +522,7 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     const int64_t tiles = (m + kLinTile - 1) / kLinTile;
     p.split = 1;
     while (p.split < 8 && tiles * p.split * 2 <= 2 * c.sms && p.split * 2 <= p.ksteps) p.split *= 2;
-    int most = ad->count < kLinTile ? ad->count : kLinTile;
-    if (m < most) most = (int)m;
+    const int most = most_adapters(m, *ad);
     int64_t room = c.sms / (tiles * p.split);
     if (room < 1) room = 1;
     const int64_t want = (most + room - 1) / room;
@@ -479,11 +532,7 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
                                             : (most + p.per - 1) / p.per;
     p.groups = (int)(room < passes ? room : passes);
     CUtensorMap tx, td;
-    if (!map2(&tx, dtype, X, k, m, ldx, kLinK, p.a_rows) ||
-        encode_tensor_map3(&td, tma_type(dtype), 2, ad->down, (uint64_t)k, (uint64_t)ad->rank,
-                           (uint64_t)ad->count, (uint64_t)ld_of(ad->ld_down, ad->rank, k),
-                           (uint64_t)ld_of(ad->stride_down, ad->count, k), kLinK, (uint32_t)cols,
-                           CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    if (!map2(&tx, dtype, X, k, m, ldx, kLinK, p.a_rows) || !map_down(&td, dtype, *ad, k, cols))
       return SKG_ERR_CUDA;
     if (launch_lora_down(dtype, tx, td, p, c.stream) != cudaSuccess) return SKG_ERR_CUDA;
   }

@@ -34,6 +34,7 @@ constexpr int kLinLoader = 6;
 constexpr int kLinTile = 128;
 constexpr int kLinK = 64;                      // elements of k in a stage
 constexpr int kLinOperand = kLinTile * 128;    // bytes of an operand's 128 rows in a stage
+constexpr int kLinPitch = 132;                 // floats per row of a partial tile
 constexpr int kLinBox = 64 * 128;              // bytes of an MN-major box: 64 k x 64 elements
 constexpr int kLoraRows = 256;                 // rows that one adapter plan covers
 
@@ -247,6 +248,11 @@ __host__ __device__ constexpr int lora_bytes(int rp) {
   return kLinTile * 2 * (rp <= 32 ? rp : 64);
 }
 
+// Bytes of an adapter's 128 rows of B_s in shared memory, all of its pieces.
+__host__ __device__ constexpr int per_ups(int rp) {
+  return lora_bytes(rp) * (rp <= 32 ? 1 : (rp + 63) / 64);
+}
+
 // B's descriptor: K-major rows of 32, 64 or 128 bytes (rank 16, 32, more) in the swizzle of
 // that width (layout 6, 4, 2 at bits 61-63), groups of eight rows behind one another.
 __device__ __forceinline__ uint64_t lora_desc(uint32_t at, int rp) {
@@ -271,6 +277,77 @@ __device__ __forceinline__ void lora_stage_mmas(uint32_t d, uint32_t a_at, uint3
     }
 }
 
+template <int THREADS>
+__device__ __forceinline__ void plan_sync() {
+  if constexpr (THREADS == kLinThreads) __syncthreads();
+  else named_bar_sync(3, THREADS);
+}
+
+// Numbers the distinct adapters of `rows` rows from row0 on in the order of their first rows
+// (THREADS threads, of which this is `tid`): ids and slot of each row, lead (the first rows);
+// emit(number, id) once for each, mask(number, word, rows of those 32). Returns their number.
+template <int THREADS, typename Emit, typename Mask>
+__device__ __forceinline__ int number_adapters(const int32_t* index, int stack, int row0, int rows, int tid,
+                                               int32_t* ids, int32_t* slot, uint32_t* lead,
+                                               Emit emit, Mask mask) {
+  const int warp = tid >> 5, lane = tid & 31, words = (rows + 31) / 32;
+  for (int i = tid; i < words * 32; i += THREADS) {
+    const int id = i < rows ? index[row0 + i] : -1;
+    ids[i] = id >= 0 && id < stack ? id : -1;
+  }
+  plan_sync<THREADS>();
+  // The first row of each row's adapter: within its 32 rows, then before them.
+  for (int g = warp; g < words; g += THREADS / 32) {
+    const int i = g * 32 + lane, id = ids[i];
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    int first = g * 32 + __ffs(same) - 1;
+    for (int j = g * 32 - 4; j >= 0; j -= 4) {
+      const int4 o = *reinterpret_cast<const int4*>(&ids[j]);
+      first = o.w == id ? j + 3 : first;
+      first = o.z == id ? j + 2 : first;
+      first = o.y == id ? j + 1 : first;
+      first = o.x == id ? j : first;
+    }
+    slot[i] = first;  // (a row's number, until all are known)
+    const uint32_t b = __ballot_sync(0xffffffffu, id >= 0 && first == i);
+    if (lane == 0) lead[g] = b;
+  }
+  plan_sync<THREADS>();
+  int count = 0;
+  for (int w = 0; w < words; ++w) count += __popc(lead[w]);
+  for (int g = warp; g < words; g += THREADS / 32) {
+    const int i = g * 32 + lane, id = ids[i], first = slot[i];
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
+    int s = 0;
+    for (int w = 0; w <= first >> 5; ++w)
+      s += __popc(lead[w] & (w < (first >> 5) ? ~0u : (1u << (first & 31)) - 1));
+    if (id >= 0) {
+      slot[i] = s;
+      if (first == i) emit(s, id);
+      if (lane == __ffs(same) - 1) mask(s, g, same);
+    }
+  }
+  plan_sync<THREADS>();
+  return count;
+}
+
+// Four values as sums of two of T.
+template <typename T>
+__device__ __forceinline__ void store_parts(T* hi, T* lo, const float (&v)[4]) {
+  union {
+    T e[4];
+    uint2 d;
+  } h, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h.e[i] = mx_from_f32<T>(v[i]);
+    const float r = v[i] - mx_to_f32(h.e[i]);
+    l.e[i] = mx_from_f32<T>(isfinite(r) ? r : 0.f);  // an infinite or NaN t is in the high part
+  }
+  *reinterpret_cast<uint2*>(hi) = h.d;
+  *reinterpret_cast<uint2*>(lo) = l.d;
+}
+
 // ------------------------------------------------------------------ launches
 // The kernels' variants. out: skg_out_t of C (kLinPlain with N-major B: also fp32).
 struct LinVariant {
@@ -281,6 +358,21 @@ struct LinVariant {
 
 cudaError_t launch_lin_single(const LinVariant& v, const LinMaps& t, const LinParams& p,
                               cudaStream_t stream);
+// Plain, K-major operands, adapters in the same kernel (skg_lin_adapted.cu); whether that is
+// possible for so many rows and adapters of a padded rank.
+struct AdaptedParams {
+  const int32_t* index;
+  const float* scale;  // NULL = 1
+  int count;           // adapters in the stack
+  int most;            // that a tile's rows can have
+  int rank;
+  int stage_bytes, stages;
+  uint32_t idesc_up;   // of the products with B_s
+};
+constexpr bool lin_adapted_fits(int most, int rank_pad) { return most * rank_pad <= 128; }
+cudaError_t launch_lin_adapted(int out, const LinMaps& t, const CUtensorMap& down,
+                               const LinParams& p, AdaptedParams a, cudaStream_t stream);
+
 cudaError_t launch_lin_pair(const LinVariant& v, const LinMaps& t, const LinParams& p,
                             int clusters, cudaStream_t stream);
 

@@ -27,7 +27,7 @@
 namespace skg {
 namespace {
 
-constexpr int kPitch = 132;  // floats per row of the partial sums
+constexpr int kPitch = kLinPitch;
 constexpr int kRing = 6 * kLinOperand;  // two CTAs share an SM
 constexpr int kMaxStages = 16;
 
@@ -57,76 +57,6 @@ __device__ __forceinline__ void fail(const LoraParams& p, LoraAux* aux) {
     atomicOr(&p.report->status_bits, 1u << SKG_ERR_PIPELINE_TIMEOUT);
     atomicAdd(&p.report->timeouts, 1u);
   }
-}
-
-template <int THREADS>
-__device__ __forceinline__ void plan_sync() {
-  if constexpr (THREADS == kLinThreads) __syncthreads();
-  else named_bar_sync(3, THREADS);
-}
-
-// Numbers the distinct adapters of `rows` rows from row0 on in the order of their first rows
-// (THREADS threads, of which this is `tid`): ids and slot of each row, lead (the first rows);
-// emit(number, id) once for each, mask(number, word, rows of those 32). Returns their number.
-template <int THREADS, typename Emit, typename Mask>
-__device__ __forceinline__ int number_adapters(const LoraParams& p, int row0, int rows, int tid,
-                                               int32_t* ids, int32_t* slot, uint32_t* lead,
-                                               Emit emit, Mask mask) {
-  const int warp = tid >> 5, lane = tid & 31, words = (rows + 31) / 32;
-  for (int i = tid; i < words * 32; i += THREADS) {
-    const int id = i < rows ? p.index[row0 + i] : -1;
-    ids[i] = id >= 0 && id < p.count ? id : -1;
-  }
-  plan_sync<THREADS>();
-  // The first row of each row's adapter: within its 32 rows, then before them.
-  for (int g = warp; g < words; g += THREADS / 32) {
-    const int i = g * 32 + lane, id = ids[i];
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    int first = g * 32 + __ffs(same) - 1;
-    for (int j = g * 32 - 4; j >= 0; j -= 4) {
-      const int4 o = *reinterpret_cast<const int4*>(&ids[j]);
-      first = o.w == id ? j + 3 : first;
-      first = o.z == id ? j + 2 : first;
-      first = o.y == id ? j + 1 : first;
-      first = o.x == id ? j : first;
-    }
-    slot[i] = first;  // (a row's number, until all are known)
-    const uint32_t b = __ballot_sync(0xffffffffu, id >= 0 && first == i);
-    if (lane == 0) lead[g] = b;
-  }
-  plan_sync<THREADS>();
-  int count = 0;
-  for (int w = 0; w < words; ++w) count += __popc(lead[w]);
-  for (int g = warp; g < words; g += THREADS / 32) {
-    const int i = g * 32 + lane, id = ids[i], first = slot[i];
-    const uint32_t same = __match_any_sync(0xffffffffu, id);
-    int s = 0;
-    for (int w = 0; w <= first >> 5; ++w)
-      s += __popc(lead[w] & (w < (first >> 5) ? ~0u : (1u << (first & 31)) - 1));
-    if (id >= 0) {
-      slot[i] = s;
-      if (first == i) emit(s, id);
-      if (lane == __ffs(same) - 1) mask(s, g, same);
-    }
-  }
-  plan_sync<THREADS>();
-  return count;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_parts(T* hi, T* lo, const float (&v)[4]) {
-  union {
-    T e[4];
-    uint2 d;
-  } h, l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h.e[i] = mx_from_f32<T>(v[i]);
-    const float r = v[i] - mx_to_f32(h.e[i]);
-    l.e[i] = mx_from_f32<T>(isfinite(r) ? r : 0.f);  // an infinite or NaN t is in the high part
-  }
-  *reinterpret_cast<uint2*>(hi) = h.d;
-  *reinterpret_cast<uint2*>(lo) = l.d;
 }
 
 template <typename T>
@@ -165,14 +95,20 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = aux->tmem_slot;
+  // The product behind reads x and writes y before it waits for this kernel: that is safe
+  // once all that ran before is complete, as it is now. (Its loads of W queue with these; to
+  // let it start behind the last of these instead took 1 to 3 us more in all.)
   griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
 
   const int rp = p.rank_pad, cols = min(rp, 128), chunks = (rp + 127) / 128;
   const int per = p.per, stages = p.ring_stages;
   int seq = 0, it = 0, n = 0;
   int load_st = 0, mma_st = 0, early = 0;
   uint32_t load_phase = 0, mma_phase = 0;
-  bool load_ok = true, mma_ok = true;
+  bool load_ok = true, mma_ok = true, ready = false;
+  const uint64_t a0 = lin_desc<false>(smem_u32(ring));
+  const uint64_t b0 = lin_desc<false>(smem_u32(ring) + p.a_rows * 128);
   const bool loader = warp == 0 || warp == kLinLoader;
   const int me = warp == kLinLoader;  // a loading thread takes every other stage
   // The first pass's x is under way while the plan is made.
@@ -187,7 +123,7 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
   __syncwarp();
   const int rows = min(kLinTile, p.m - tm * kLinTile);
   const int count = number_adapters<kLinThreads>(
-      p, tm * kLinTile, rows, (int)threadIdx.x, pl->ids, pl->slot, pl->lead,
+      p.index, p.count, tm * kLinTile, rows, (int)threadIdx.x, pl->ids, pl->slot, pl->lead,
       [&](int s, int id) {
         pl->id[s] = id;
         pl->scale[s] = p.scale ? p.scale[id] : 1.f;
@@ -195,11 +131,6 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
       [](int, int, uint32_t) {});
   // Passes: `per` adapters each, or (rank over 128) one adapter's next 128 columns.
   const int passes = chunks > 1 ? count * chunks : (count + per - 1) / per;
-  // The product behind reads x and writes y before it waits for this kernel: that is safe
-  // once all that ran before is complete, as it is here. But its loads of W would queue
-  // ahead of these (one token, k = 8192: 10 us for loads of 2): it may start when the last
-  // of them is on its way.
-  if (threadIdx.x == 0 && group >= passes) griddep_launch_dependents();
 
   // The plan for the product, by the warps that wait for the accumulator anyway.
   if (warp >= 2 && !loader && group == 0 && rank == 0 && (tm & 1) == 0) {
@@ -209,7 +140,7 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     for (int i = tid; i < (both + 31) / 32 * 32 * 2; i += 128)
       reinterpret_cast<uint4*>(&out->rows[0][0])[i] = make_uint4(0, 0, 0, 0);
     const int c = number_adapters<128>(
-        p, tm * kLinTile, both, tid, pl->ids2, pl->slot2, pl->lead2,
+        p.index, p.count, tm * kLinTile, both, tid, pl->ids2, pl->slot2, pl->lead2,
         [&](int s, int id) { out->id[s] = id; },
         [&](int s, int w, uint32_t m) { out->rows[s][w] = m; });
     if (tid == 0) out->count = c;
@@ -253,29 +184,28 @@ lora_down_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             load_phase ^= 1u;
           }
         }
-        if (pass + p.groups >= passes) griddep_launch_dependents();
       }
       __syncwarp();
     } else if (warp == 1) {
       if (elect_one()) {
         for (int kb = kb0; mma_ok && kb < kb1; ++kb) {
           const int st = mma_st;
-          if (!mx_wait(&aux->ring_full[st], mma_phase, aux)) {
+          if (!ready && !mx_wait(&aux->ring_full[st], mma_phase, aux)) {
             fail(p, aux);
             mma_ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t s = smem_u32(ring + st * p.stage_bytes);
-          lin_stage_mmas<false, false, false>(tmem, lin_desc<false>(s),
-                                              lin_desc<false>(s + p.a_rows * 128), p.idesc,
-                                              p.k - kb * kLinK, kb == kb0);
-          umma_commit(&aux->ring_empty[st]);
-          ++it;
           if (++mma_st == stages) {
             mma_st = 0;
             mma_phase ^= 1u;
           }
+          ready = mbar_test_wait(&aux->ring_full[mma_st], mma_phase);  // (as LinRing does)
+          const uint64_t at = (uint64_t)((st * p.stage_bytes) >> 4);
+          lin_stage_mmas<false, false, false>(tmem, a0 + at, b0 + at, p.idesc, p.k - kb * kLinK,
+                                              kb == kb0);
+          umma_commit(&aux->ring_empty[st]);
+          ++it;
         }
         if (mma_ok) umma_commit(&aux->tfull[0]);
       }

@@ -126,6 +126,23 @@ def test_adapters_ranks(ws, kind, r, m, n, k):
     check(y, *ref.linear(x, w, a, b, f, i))
 
 
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("m,s,r", [(1, 16, 16), (1, 3, 128), (2, 64, 64), (8, 64, 8), (7, 8, 16),
+                                   (16, 2, 64), (16, 1, 128), (5, 4, 32), (13, 3, 40), (64, 5, 16),
+                                   (128, 1, 128), (129, 8, 16), (300, 2, 64), (300, 8, 8),
+                                   (200, 3, 40), (40, 4, 24), (333, 1, 96), (127, 2, 48)])
+@pytest.mark.parametrize("n,k", [(1000, 2200), (264, 72), (128, 8), (3000, 1032)])
+def test_adapters_few(ws, kind, m, s, r, n, k):
+    """Few adapters to a tile (one launch), k split and not, rows with none."""
+    g = gen(m + s)
+    x, w = normal(g, kind, m, k), normal(g, kind, n, k, scale=k ** -0.5)
+    a, b, f = stack(g, kind, s, r, n, k)
+    for order in ("mixed", "none", "last"):
+        i = indices(g, m, s, order)
+        y = layers.linear(x, w, layers.Adapters(a, b, f), i, workspace=ws)
+        check(y, *ref.linear(x, w, a, b, f, i), what=order)
+
+
 @pytest.mark.parametrize("m,order", [(64, "mixed"), (333, "mixed"), (2048, "segments"), (2048, "own"),
                                      (2500, "mixed")])
 def test_adapters_sizes(ws, m, order):
