@@ -86,7 +86,7 @@ __device__ __forceinline__ void store8(T* hi, T* lo, const float (&v)[8]) {
 }
 
 // Eight elements of a row per thread; reads and writes each element once, so memory bounds it.
-template <typename T, typename D>
+template <typename T, typename D, int ACT>
 __global__ void __launch_bounds__(128) dgate_kernel(const DgateParams p) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -100,11 +100,10 @@ __global__ void __launch_bounds__(128) dgate_kernel(const DgateParams p) {
     load8<T>(pre + p.f, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float da;
-      const float a = lin_act<true>(p.act, g[i], da);
-      dg[i] = d[i] * u[i] * da;
-      du[i] = d[i] * a;
-      h[i] = a * u[i];
+      const LinGrad r = lin_grad<ACT>(d[i], g[i], u[i]);
+      dg[i] = r.dg;
+      du[i] = r.du;
+      h[i] = r.h;
     }
     const int64_t at = row * 2 * p.f + col;
     T *hi = reinterpret_cast<T*>(p.dpre) + at, *lo = reinterpret_cast<T*>(p.dpre_lo);
@@ -118,14 +117,25 @@ __global__ void __launch_bounds__(128) dgate_kernel(const DgateParams p) {
   }
 }
 
-cudaError_t launch_dgate(int dtype, const DgateParams& p, cudaStream_t stream) {
+template <typename T, typename D>
+cudaError_t launch_dgate_as(const DgateParams& p, cudaStream_t stream) {
   const dim3 grid((unsigned)((p.f / 8 + 127) / 128), (unsigned)(p.m < 32768 ? p.m : 32768));
+  const dim3 block(128);
+  switch (p.act) {
+    case SKG_ACT_SILU: return launch_pdl(dgate_kernel<T, D, SKG_ACT_SILU>, grid, block, 0, stream, p);
+    case SKG_ACT_GELU: return launch_pdl(dgate_kernel<T, D, SKG_ACT_GELU>, grid, block, 0, stream, p);
+    case SKG_ACT_GELU_TANH:
+      return launch_pdl(dgate_kernel<T, D, SKG_ACT_GELU_TANH>, grid, block, 0, stream, p);
+    default: return launch_pdl(dgate_kernel<T, D, SKG_ACT_RELU>, grid, block, 0, stream, p);
+  }
+}
+
+cudaError_t launch_dgate(int dtype, const DgateParams& p, cudaStream_t stream) {
   if (dtype == SKG_IN_F16)
-    return p.f32 ? launch_pdl(dgate_kernel<__half, float>, grid, dim3(128), 0, stream, p)
-                 : launch_pdl(dgate_kernel<__half, __half>, grid, dim3(128), 0, stream, p);
-  return p.f32 ? launch_pdl(dgate_kernel<__nv_bfloat16, float>, grid, dim3(128), 0, stream, p)
-               : launch_pdl(dgate_kernel<__nv_bfloat16, __nv_bfloat16>, grid, dim3(128), 0, stream,
-                            p);
+    return p.f32 ? launch_dgate_as<__half, float>(p, stream)
+                 : launch_dgate_as<__half, __half>(p, stream);
+  return p.f32 ? launch_dgate_as<__nv_bfloat16, float>(p, stream)
+               : launch_dgate_as<__nv_bfloat16, __nv_bfloat16>(p, stream);
 }
 
 // ------------------------------------------------------------------ products
@@ -144,8 +154,10 @@ struct Product {
   int64_t ldc;
   int out;          // skg_out_t
   int act;
-  void* pre;
+  void* pre;        // kLinGated: PRE, or NULL; kLinGrad: DPRE
   int64_t ldp;
+  const void* pre_in;  // kLinGrad: PRE
+  int64_t ldp_in;
   const skg_adapters_t* adapters;
   void* t;          // with a plan: t and the plan come from skg_lora.cu's kernel
   LoraPlan* plan;
@@ -185,28 +197,41 @@ bool map_operand(CUtensorMap* t, int dtype, const Operand& o, const void* p, int
               : map2(t, dtype, p, k, rows, o.ld, kLinK, box_rows);
 }
 
-// Single CTAs: how many share a 128 x 128 tile (S), and the estimated time (us).
+// Single CTAs: how many share a 128 x 128 tile (S), and the estimated time (us). Up to 16
+// rows of A the sum over the cluster is a few rows, and S is what fits the GPU at once (1 x
+// 1024 x 8192: 27, 15, 9.1, 6.1 us with S = 1, 2, 4, 8). Else a fixed cost that grows with S,
+// and the CTA's stages of k, at 0.2 us where it has an SM to itself and 0.44 where two share
+// one (333 x 2048 x 2048: 10.4, 8.0, 10.3 with S = 1, 2, 4: 48, 96, 192 CTAs). Clusters of
+// eight find room one to an SM up to eight of them (128 x 1000 x 2200: 7.2 against 8.4 with
+// S = 4; 16 tiles, 128 x 2048 x 2048: 8.5 against 6.7).
 struct SinglePlan {
   int split;
   double us;
 };
 SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms) {
   SinglePlan best = {1, 1e30};
-  for (int s = 1; s <= (m <= 16 ? 8 : 4); s *= 2) {
+  for (int s = 1; s <= 8; s *= 2) {
     if (s > 1 && (tiles * s > 2 * sms || s > ksteps)) break;
-    const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
     const int stages = (ksteps + s - 1) / s;
-    const double us = tiles * s <= sms ? (s > 1 ? 4.2 : 3.2) + 0.36 * stages
-                                       : (s > 1 && m > 64 ? 6.5 : 5.2) + 0.48 * waves * stages;
+    const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
+    double us;
+    if (tiles * s <= sms)
+      us = (s == 1 ? 4.4 : s == 2 ? 4.9 : s == 4 ? 5.3 : tiles <= 8 ? 5.7 : 8.6) + 0.2 * stages;
+    else
+      us = (s == 1 ? 3.2 : s == 8 ? 9.0 : 6.5) + 0.436 * (double)waves * stages;
     if (m <= 16 || us < best.us) best = {s, us};
   }
   return best;
 }
 
-// Whether a product runs on CTA pairs.
+// Whether a product runs on CTA pairs, whose 256 x 256 tiles halve what each SM reads per
+// product but cannot share a tile's k. Up to 128 rows the single CTAs win at every n and k;
+// beyond, the lower estimate: 0.262 us a stage, 0.29 where the power limit lowers the clock
+// (1024 x 2048 x 2048: 12.9 us paired, 10.8 single; 1024 x 8192 x 1024: 13.8 and 19.9).
 bool wants_pairs(int64_t m, int64_t tiles, int ksteps, int clusters, double single_us) {
   if (m <= kLinTile) return false;
-  return 4.2 + 0.29 * (double)((tiles + clusters - 1) / clusters) * ksteps <= single_us;
+  const int64_t waves = (tiles + clusters - 1) / clusters;
+  return 4.2 + (waves > 1 ? 0.29 : 0.262) * (double)waves * ksteps <= single_us;
 }
 
 // How a product runs.
@@ -223,12 +248,13 @@ Choice choose(const Product& q, const Common& c) {
   Choice h = {};
   h.resident = lin_pair_clusters_resident();
   const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms);
-  h.pair = q.out != SKG_OUT_F32 && h.resident > 0 &&
+  h.pair = q.out != SKG_OUT_F32 && h.resident > 0 && q.n >= 8 &&
            wants_pairs(q.m, tm2 * tn2, steps, h.resident, single.us);
   h.tiles_m = h.pair ? tm2 : tm1;
   h.tiles_n = h.pair ? tn2 : tn1;
   h.split = h.pair ? 1 : single.split;
-  h.deep = !h.pair && tm1 * tn1 * h.split <= c.sms;
+  // (Clusters of eight do not all find eight SMs of their own in a GPC.)
+  h.deep = !h.pair && tm1 * tn1 * h.split <= (h.split < 8 ? c.sms : 64);
   return h;
 }
 
@@ -321,7 +347,11 @@ skg_status_t run_product(const Product& q, const Common& c) {
       return SKG_ERR_CUDA;
   }
   if (pair) {
-    if (!map2(&t.c, c.dtype, q.c, q.n, q.m, p.ldc, 64, 32)) return SKG_ERR_CUDA;
+    if (!map2(&t.c, c.dtype, q.c, q.n & ~7, q.m, p.ldc, 64, 32)) return SKG_ERR_CUDA;
+    if (q.mode == kLinGrad &&
+        (!map2(&t.t, c.dtype, q.pre_in, q.n, q.m, q.ldp_in, 64, 32) ||
+         !map2(&t.up, c.dtype, (const uint16_t*)q.pre_in + q.n, q.n, q.m, q.ldp_in, 64, 32)))
+      return SKG_ERR_CUDA;
     if (q.pre && (!map2(&t.gate, c.dtype, q.pre, q.n, q.m, p.ldp, 64, 32) ||
                   !map2(&t.pre_up, c.dtype, (const uint16_t*)q.pre + q.n, q.n, q.m, p.ldp, 64, 32)))
       return SKG_ERR_CUDA;
@@ -671,25 +701,38 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
     q.k = k;
     q.a = {dY, lddy, false, nullptr};
     q.b = {W_out, ldw_out, true, nullptr};
-    q.c = base + s.dh;
-    q.ldc = hidden;
-    q.out = SKG_OUT_F32;
-    st = run_product(q, c);
+    q.out = out_of(dtype);
+    q.act = act;
+    if (!two && choose(q, c).pair) {  // dH stays in the accumulator
+      q.mode = kLinGrad;
+      q.c = base + s.h;
+      q.ldc = hidden;
+      q.pre = base + s.dpre;
+      q.ldp = 2 * hidden;
+      q.pre_in = PRE;
+      q.ldp_in = ldp;
+      st = run_product(q, c);
+    } else {
+      q.c = base + s.dh;
+      q.ldc = hidden;
+      q.out = SKG_OUT_F32;
+      st = run_product(q, c);
+      DgateParams d = {};
+      d.m = m;
+      d.f = (int)hidden;
+      d.f32 = 1;
+      d.act = act;
+      d.dh = base + s.dh;
+      d.lddh = hidden;
+      d.pre = PRE;
+      d.ldp = ldp;
+      d.dpre = base + s.dpre;
+      d.dpre_lo = two ? base + s.dpre_lo : nullptr;
+      d.h = base + s.h;
+      d.h_lo = two ? base + s.h_lo : nullptr;
+      if (st == SKG_OK && launch_dgate(dtype, d, c.stream) != cudaSuccess) st = SKG_ERR_CUDA;
+    }
     if (st != SKG_OK) return st;
-    DgateParams d = {};
-    d.m = m;
-    d.f = (int)hidden;
-    d.f32 = 1;
-    d.act = act;
-    d.dh = base + s.dh;
-    d.lddh = hidden;
-    d.pre = PRE;
-    d.ldp = ldp;
-    d.dpre = base + s.dpre;
-    d.dpre_lo = two ? base + s.dpre_lo : nullptr;
-    d.h = base + s.h;
-    d.h_lo = two ? base + s.h_lo : nullptr;
-    if (launch_dgate(dtype, d, c.stream) != cudaSuccess) return SKG_ERR_CUDA;
   }
   st = in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W_in,
                     ldw_in, dX, lddx, dW_in, lddw_in, c);

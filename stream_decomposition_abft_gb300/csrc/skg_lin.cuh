@@ -13,11 +13,14 @@
 //   kLinGated   B holds two projections of n rows each; a tile takes half of its columns
 //               from either, so one thread holds gate and up of an output:
 //               H = act(gate) * up, and PRE = (gate | up) where it is asked for
+//   kLinGrad    the product is the gradient of a gated output (pairs, N-major B): with PRE,
+//               DPRE = the gradients of gate and up, and H formed again
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "skg_internal.h"
 #include "skg_mx.cuh"
@@ -38,7 +41,7 @@ constexpr int kLinPitch = 132;                 // floats per row of a partial ti
 constexpr int kLinBox = 64 * 128;              // bytes of an MN-major box: 64 k x 64 elements
 constexpr int kLoraRows = 256;                 // rows that one adapter plan covers
 
-enum LinMode { kLinPlain = 0, kLinGated = 1 };
+enum LinMode { kLinPlain = 0, kLinGated = 1, kLinGrad = 2 };
 
 // The adapters that 256 rows use, in the order of their first rows, and the rows of each
 // (word w, bit b: row 32 w + b).
@@ -77,7 +80,8 @@ struct LinMaps {
   CUtensorMap a, b;
   CUtensorMap lo;         // the two-term operand's low parts
   CUtensorMap t, up;      // adapters: scale (x A^T) in high and low parts; their B (3 dimensions)
-  CUtensorMap c, gate, pre_up;  // pairs: stores
+  CUtensorMap c, gate, pre_up;  // pairs: stores (C or H, the halves of PRE or DPRE);
+                                // kLinGrad: t and up are the halves of PRE
 };
 
 struct LinAux : MxAux {
@@ -98,32 +102,70 @@ __device__ __forceinline__ float lin_sigmoid(float x) {
   return __fdividef(1.f, 1.f + __expf(-x));  // e^-x = inf gives 0
 }
 
-template <bool GRAD>
-__device__ __forceinline__ float lin_act(int act, float g, float& d) {
-  if (act == SKG_ACT_SILU) {
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float lin_act(float g, float& d) {
+  if constexpr (ACT == SKG_ACT_SILU) {
     const float p = lin_sigmoid(g);
     if (GRAD) d = p * (1.f + g * (1.f - p));
     return g * p;
-  }
-  if (act == SKG_ACT_GELU) {
+  } else if constexpr (ACT == SKG_ACT_GELU) {
     const float p = 0.5f * erfcf(-0.70710678f * g);  // not 1 + erf, whose sum cancels for g < 0
     if (GRAD) d = p + g * (0.39894228f * __expf(-0.5f * g * g));
     return g * p;
-  }
-  if (act == SKG_ACT_GELU_TANH) {
+  } else if constexpr (ACT == SKG_ACT_GELU_TANH) {
     // (1 + tanh u) / 2 = sigmoid(2 u)
     const float p = lin_sigmoid(1.59576912f * (g + 0.044715f * g * g * g));
     const float q = p * (1.f - p);
     if (GRAD) d = q == 0.f ? p : p + g * q * (1.59576912f * (1.f + 0.134145f * g * g));
     return g * p;
+  } else {
+    if (GRAD) d = g > 0.f ? 1.f : (g == g ? 0.f : g);
+    return g > 0.f ? g : (g == g ? 0.f : g);
   }
-  if (GRAD) d = g > 0.f ? 1.f : (g == g ? 0.f : g);
-  return g > 0.f ? g : (g == g ? 0.f : g);
 }
 
-__device__ __forceinline__ float lin_gated(int act, float gate, float up) {
+// f(the activation as a constant): one copy of f's code for each, of which a launch runs one.
+// (With the choice inside, at every element, the way out of a tile took 1.5 us longer, most
+// of it waiting for instructions.)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == SKG_ACT_SILU) f(std::integral_constant<int, SKG_ACT_SILU>{});
+  else if (act == SKG_ACT_GELU) f(std::integral_constant<int, SKG_ACT_GELU>{});
+  else if (act == SKG_ACT_GELU_TANH) f(std::integral_constant<int, SKG_ACT_GELU_TANH>{});
+  else f(std::integral_constant<int, SKG_ACT_RELU>{});
+}
+
+template <int ACT>
+__device__ __forceinline__ float lin_gated(float gate, float up) {
   float d;
-  return lin_act<false>(act, gate, d) * up;
+  return lin_act<ACT, false>(gate, d) * up;
+}
+
+// Four at once; GELU's error function is long, and is called.
+static __device__ __noinline__ float4 lin_gelu4(float4 g, float4 u) {
+  return make_float4(lin_gated<SKG_ACT_GELU>(g.x, u.x), lin_gated<SKG_ACT_GELU>(g.y, u.y),
+                     lin_gated<SKG_ACT_GELU>(g.z, u.z), lin_gated<SKG_ACT_GELU>(g.w, u.w));
+}
+template <int ACT>
+__device__ __forceinline__ float4 lin_gated4(const float4& g, const float4& u) {
+  if constexpr (ACT == SKG_ACT_GELU) return lin_gelu4(g, u);
+  else
+    return make_float4(lin_gated<ACT>(g.x, u.x), lin_gated<ACT>(g.y, u.y),
+                       lin_gated<ACT>(g.z, u.z), lin_gated<ACT>(g.w, u.w));
+}
+
+// The gradients of a gated output h = act(g) u: of g and u, from dh; and h.
+struct LinGrad {
+  float dg, du, h;
+};
+template <int ACT>
+__device__ __forceinline__ LinGrad lin_grad(float dh, float g, float u) {
+  float da;
+  const float a = lin_act<ACT, true>(g, da);
+  return {dh * u * da, dh * a, a * u};
+}
+static __device__ __noinline__ LinGrad lin_grad_gelu(float dh, float g, float u) {
+  return lin_grad<SKG_ACT_GELU>(dh, g, u);
 }
 
 // ------------------------------------------------------------------ MMAs

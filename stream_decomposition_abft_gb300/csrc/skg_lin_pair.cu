@@ -15,21 +15,29 @@
 namespace skg {
 namespace {
 
+struct PairAux : LinAux {
+  uint64_t pre[4];  // kLinGrad: a warp's boxes of PRE are there
+};
+
+template <int MODE>
 struct PairCfg {
   static constexpr int STAGE_BYTES = 2 * kLinOperand;
-  static constexpr int STAGING = 4 * 8192;  // per epilogue warp: two boxes of 32 rows x 128 bytes
-  static constexpr int STAGES = 6;
+  // Per epilogue warp: two boxes of 32 rows x 128 bytes on their way out; kLinGrad: two of PRE
+  // on their way in.
+  static constexpr int WARP_STAGING = MODE == kLinGrad ? 16384 : 8192;
+  static constexpr int STAGING = 4 * WARP_STAGING;
+  static constexpr int STAGES = MODE == kLinGrad ? 5 : 6;
   static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + STAGING + 512;
   static_assert(SMEM <= kSmemLimit, "shared memory");
-  static_assert(sizeof(LinAux) <= 512, "aux size");
+  static_assert(sizeof(PairAux) <= 512, "aux size");
 };
 
 // A box of 32 rows x 128 bytes (this lane's row: the values f(0), f(1), ...) in the 128-byte
 // swizzle, and its store by TMA; two boxes per warp in turn. The engine clips what is past
-// the matrix.
+// the matrix, to whole 16 bytes; returns the box.
 template <typename T, typename F>
-__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* staging, uint32_t& box,
-                                          int lane, int col, int row, bool in, F f) {
+__device__ __forceinline__ uint8_t* store_box(const CUtensorMap* map, uint8_t* staging, uint32_t& box,
+                                          int lane, int col, int row, F f) {
   constexpr int PER = 16 / (int)sizeof(T);
   uint8_t* st = staging + (box & 1) * 4096;
   ++box;
@@ -48,8 +56,82 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* stagi
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (in) tma_store_2d(map, st, col, row);
+    tma_store_2d(map, st, col, row);
     bulk_commit();
+  }
+  return st;
+}
+
+// The columns of a box of C behind the last whole 16 bytes of a row (the map ends before them:
+// what the engine would write there is not C's), one by one.
+template <typename T>
+__device__ __noinline__ void store_rest(const LinParams& p, const uint8_t* st, int lane, int col,
+                                        int row) {
+  if (row + lane >= p.m) return;
+  for (int c = max(p.n & ~7, col); c < min(p.n, col + 64); ++c) {
+    const int i = c - col;
+    reinterpret_cast<T*>(p.c)[(int64_t)(row + lane) * p.ldc + c] = *reinterpret_cast<const T*>(
+        st + lane * 128 + (((i >> 3) ^ (lane & 7)) << 4) + (i & 7) * sizeof(T));
+  }
+}
+
+// kLinGrad: 64 columns of dH (this lane's row: v), of the gate and the other projection (g, u:
+// eight of T each) to boxes of both gradients and of H.
+template <typename T>
+__device__ __forceinline__ void grad_boxes(const LinParams& p, const LinMaps& maps,
+                                           uint8_t* staging, uint32_t& box, int lane, int col,
+                                           int row, const uint32_t (&v)[2][32], uint4 (&g)[8],
+                                           uint4 (&u)[8]) {
+  union Eight {
+    uint4 q;
+    T e[8];
+  };
+  with_act(p.act, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    uint8_t* st = staging + (box & 1) * 4096;
+    ++box;
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      Eight a, b, dg, d2, o;
+      a.q = g[j];
+      b.q = u[j];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float dh = __uint_as_float(v[j >> 2][(j & 3) * 8 + i]);
+        const LinGrad r = ACT == SKG_ACT_GELU ? lin_grad_gelu(dh, mx_to_f32(a.e[i]), mx_to_f32(b.e[i]))
+                                              : lin_grad<ACT>(dh, mx_to_f32(a.e[i]), mx_to_f32(b.e[i]));
+        dg.e[i] = mx_from_f32<T>(r.dg);
+        d2.e[i] = mx_from_f32<T>(r.du);
+        o.e[i] = mx_from_f32<T>(r.h);
+      }
+      *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = dg.q;
+      g[j] = d2.q;
+      u[j] = o.q;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&maps.gate, st, col, row);
+      bulk_commit();
+    }
+  });
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint8_t* st = staging + (box & 1) * 4096;
+    ++box;
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = k ? u[j] : g[j];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(k ? &maps.c : &maps.pre_up, st, col, row);
+      bulk_commit();
+    }
   }
 }
 
@@ -67,14 +149,14 @@ __device__ __forceinline__ void pair_tile(const LinParams& p, int t, int& tm, in
 template <int MODE, bool AMN, bool BMN, typename T>
 __global__ void __launch_bounds__(kLinThreads, 1)
 lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
-  using C = PairCfg;
+  using C = PairCfg<MODE>;
   constexpr bool G = MODE == kLinGated;
   constexpr bool LORA = MODE == kLinPlain && !AMN && !BMN;
   constexpr int TILE_N = G ? 128 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* staging = ring + C::STAGES * C::STAGE_BYTES;
-  LinAux* aux = reinterpret_cast<LinAux*>(staging + C::STAGING);
+  PairAux* aux = reinterpret_cast<PairAux*>(staging + C::STAGING);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int tiles = p.tiles_m * p.tiles_n;
@@ -96,6 +178,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     mbar_init(&aux->tempty, 8);  // the epilogue warps of both CTAs
     mbar_init(&aux->tempty1, 8);
     mbar_init(&aux->drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&aux->pre[i], 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -295,19 +378,35 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncwarp();
   } else {
     const int q = warp & 3;
-    uint8_t* mine = staging + q * 8192;
-    uint32_t box = 0;
+    uint8_t* mine = staging + q * C::WARP_STAGING;
+    uint32_t box = 0, pres = 0;
     int n = 0;
     for (int t = first; t < tiles; t += stride, ++n) {
       int tm, tn;
       pair_tile(p, t, tm, tn);
       const int row0 = (2 * tm + rank) * kLinTile + q * 32, col0 = tn * TILE_N;
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * 256;
+      const bool live = row0 < p.m;
+      // kLinGrad: PRE of 64 columns comes while the 64 before them (or the MMAs) are worked on.
+      auto fetch_pre = [&](int col) {
+        if constexpr (MODE == kLinGrad) {
+          if (live && col < p.n && lane == 0) {
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&aux->pre[q], 8192);
+            tma_load_2d(mine + 8192, &maps.t, &aux->pre[q], col, row0);
+            tma_load_2d(mine + 12288, &maps.up, &aux->pre[q], col, row0);
+          }
+        }
+      };
+      fetch_pre(col0);
       const bool got = mx_wait(&aux->tfull[n & 1], (uint32_t)(n >> 1) & 1u, aux);
       if (!got) lin_fail(p, aux);
-      if (!__all_sync(0xffffffffu, got)) break;
+      if (!__all_sync(0xffffffffu, got)) {
+        // (What fetch_pre asked for lands before the CTA leaves.)
+        if (MODE == kLinGrad && live && col0 < p.n) mx_wait(&aux->pre[q], pres & 1u, aux, true);
+        break;
+      }
       tc_fence_after();
-      const bool live = row0 < p.m;
       // Four pieces of 64 accumulator columns: 64 columns of C each; gated: the gate's 64,
       // then the other projection's 64 of the same outputs.
       uint32_t v[2][2][32];
@@ -316,54 +415,78 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) tmem_ld32_async(acc + c + i * 32, v[s & 1][i]);
       };
+      auto hand_over = [&]() {  // all of the tile is in registers
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive_remote(cluster_addr((n & 1) ? &aux->tempty1 : &aux->tempty, 0u));
+      };
+      auto value = [&](int b, int i) { return __uint_as_float(v[b][i >> 5][i & 31]); };
       fetch(0);
       fetch(1);
+      if constexpr (G) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (!G || (s & 1) == 0) {
-          // (A wait is for all loads under way.)
-          tmem_ld_wait32(v[s & 1][0]);
-          tmem_ld_wait32(v[s & 1][1]);
-        }
-        if (G) {
-          if (s & 1) continue;
-          tmem_ld_wait32(v[1][0]);
-          tmem_ld_wait32(v[1][1]);
-          const int col = col0 + (s >> 1) * 64;
-          const bool in = live && col < p.n;
-          if (s == 2) {  // all of the tile is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-              mbar_arrive_remote(cluster_addr((n & 1) ? &aux->tempty1 : &aux->tempty, 0u));
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            tmem_ld_wait32(v[b][0]);
+            tmem_ld_wait32(v[b][1]);
           }
-          if (in) {
-            store_box<T>(&maps.c, mine, box, lane, col, row0, true, [&](int i) {
-              return lin_gated(p.act, __uint_as_float(v[0][i >> 5][i & 31]),
-                               __uint_as_float(v[1][i >> 5][i & 31]));
-            });
+          if (s == 1) hand_over();
+          const int col = col0 + s * 64;
+          if (live && col < p.n) {
             if (p.pre) {
-              store_box<T>(&maps.gate, mine, box, lane, col, row0, true,
-                           [&](int i) { return __uint_as_float(v[0][i >> 5][i & 31]); });
-              store_box<T>(&maps.pre_up, mine, box, lane, col, row0, true,
-                           [&](int i) { return __uint_as_float(v[1][i >> 5][i & 31]); });
+              store_box<T>(&maps.gate, mine, box, lane, col, row0,
+                           [&](int i) { return value(0, i); });
+              store_box<T>(&maps.pre_up, mine, box, lane, col, row0,
+                           [&](int i) { return value(1, i); });
             }
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 64; i += 4) {
+                const float4 h = lin_gated4<decltype(act)::value>(
+                    make_float4(value(0, i), value(0, i + 1), value(0, i + 2), value(0, i + 3)),
+                    make_float4(value(1, i), value(1, i + 1), value(1, i + 2), value(1, i + 3)));
+                v[0][i >> 5][i & 31] = __float_as_uint(h.x);
+                v[0][i >> 5][(i & 31) + 1] = __float_as_uint(h.y);
+                v[0][i >> 5][(i & 31) + 2] = __float_as_uint(h.z);
+                v[0][i >> 5][(i & 31) + 3] = __float_as_uint(h.w);
+              }
+            });
+            store_box<T>(&maps.c, mine, box, lane, col, row0, [&](int i) { return value(0, i); });
           }
           if (s == 0) {
             fetch(2);
             fetch(3);
           }
-        } else {
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          tmem_ld_wait32(v[s & 1][0]);
+          tmem_ld_wait32(v[s & 1][1]);
           const int col = col0 + s * 64;
-          if (s == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-              mbar_arrive_remote(cluster_addr((n & 1) ? &aux->tempty1 : &aux->tempty, 0u));
+          if (s == 3) hand_over();
+          if (live && col < p.n) {
+            if constexpr (MODE == kLinGrad) {
+              uint4 g[8], u[8];
+              if (!mx_wait(&aux->pre[q], pres & 1u, aux, true)) lin_fail(p, aux);
+              ++pres;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int at = lane * 128 + ((j ^ (lane & 7)) << 4);
+                g[j] = *reinterpret_cast<const uint4*>(mine + 8192 + at);
+                u[j] = *reinterpret_cast<const uint4*>(mine + 12288 + at);
+              }
+              __syncwarp();
+              if (s < 3) fetch_pre(col + 64);
+              grad_boxes<T>(p, maps, mine, box, lane, col, row0, v[s & 1], g, u);
+            } else {
+              const uint8_t* st = store_box<T>(&maps.c, mine, box, lane, col, row0,
+                                               [&](int i) { return value(s & 1, i); });
+              if ((p.n & 7) && col + 64 > (p.n & ~7)) store_rest<T>(p, st, lane, col, row0);
+            }
           }
-          if (live && col < p.n)
-            store_box<T>(&maps.c, mine, box, lane, col, row0, true,
-                         [&](int i) { return __uint_as_float(v[s & 1][i >> 5][i & 31]); });
           if (s < 2) fetch(s + 2);
         }
       }
@@ -396,16 +519,17 @@ template <int MODE, bool AMN, bool BMN, typename T>
 cudaError_t launch(const LinMaps& t, const LinParams& p, int clusters, cudaStream_t stream) {
   auto kernel = lin_pair_kernel<MODE, AMN, BMN, T>;
   static std::atomic<uint64_t> done_mask{0};
-  const cudaError_t e = opt_in_smem((const void*)kernel, done_mask, (int)PairCfg::SMEM);
+  const cudaError_t e = opt_in_smem((const void*)kernel, done_mask, (int)PairCfg<MODE>::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kernel, dim3((unsigned)(2 * clusters)), dim3(kLinThreads),
-                            PairCfg::SMEM, stream, 2, t, p);
+                            PairCfg<MODE>::SMEM, stream, 2, t, p);
 }
 
 template <typename T>
 cudaError_t launch_type(const LinVariant& v, const LinMaps& t, const LinParams& p, int clusters,
                         cudaStream_t stream) {
   if (v.mode == kLinGated) return launch<kLinGated, false, false, T>(t, p, clusters, stream);
+  if (v.mode == kLinGrad) return launch<kLinGrad, false, true, T>(t, p, clusters, stream);
   if (v.a_mn) return launch<kLinPlain, true, true, T>(t, p, clusters, stream);
   if (v.b_mn) return launch<kLinPlain, false, true, T>(t, p, clusters, stream);
   return launch<kLinPlain, false, false, T>(t, p, clusters, stream);
@@ -428,11 +552,11 @@ int lin_pair_clusters_resident() {
   auto kernel = lin_pair_kernel<kLinGated, false, false, __nv_bfloat16>;  // all alike in resources
   int n = 0;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)PairCfg::SMEM) == cudaSuccess) {
+                           (int)PairCfg<kLinGated>::SMEM) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * 256);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = PairCfg::SMEM;
+    cfg.dynamicSmemBytes = PairCfg<kLinGated>::SMEM;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;

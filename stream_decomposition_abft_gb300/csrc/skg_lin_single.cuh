@@ -16,13 +16,13 @@ __device__ __forceinline__ void write4(T* c, const float (&v)[4], int left) {
 }
 
 // Four output columns of row r: v as the accumulator has them; gated: gate and up.
-template <int MODE, typename T>
+template <int MODE, int ACT, typename T>
 __device__ __forceinline__ void finish4(const LinParams& p, int row, int col, const float4& v,
                                         const float4& u) {
   T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
   if constexpr (MODE == kLinGated) {
-    const float h[4] = {lin_gated(p.act, v.x, u.x), lin_gated(p.act, v.y, u.y),
-                        lin_gated(p.act, v.z, u.z), lin_gated(p.act, v.w, u.w)};
+    const float4 o = lin_gated4<ACT>(v, u);
+    const float h[4] = {o.x, o.y, o.z, o.w};
     write4<T>(c, h, p.n - col);
     if (p.pre) {
       T* g = reinterpret_cast<T*>(p.pre) + (int64_t)row * p.ldp + col;
@@ -41,7 +41,7 @@ __device__ __forceinline__ void finish4(const LinParams& p, int row, int col, co
 // outputs; the loads of several rows are in flight together. Every value that is loaded is
 // used, so no load is still on its way to another CTA's shared memory when a thread comes to
 // the barrier that lets that CTA leave.
-template <int MODE, typename T, int S>
+template <int MODE, int ACT, typename T, int S>
 __device__ __forceinline__ void reduce_rows(const LinParams& p, const float* part, int w0,
                                             int warps, int lane, int first, int limit, int tm,
                                             int tn) {
@@ -93,7 +93,7 @@ __device__ __forceinline__ void reduce_rows(const LinParams& p, const float* par
           b.w += u[j][s].w;
         }
       }
-      finish4<MODE, T>(p, tm * kLinTile + r, col, a, b);
+      finish4<MODE, ACT, T>(p, tm * kLinTile + r, col, a, b);
     }
   }
 }
@@ -118,25 +118,36 @@ __device__ __forceinline__ void keep_rows(uint32_t tmem, int q, int lane, float*
 }
 
 // After each CTA's rows are in its partial tile: the sum over the cluster, and the rows out.
-template <int MODE, typename T>
-__device__ __forceinline__ void tile_out(const LinParams& p, const float* part, int warp, int lane,
+template <int MODE, int ACT, typename T>
+__device__ __forceinline__ void tile_out_as(const LinParams& p, const float* part, int warp, int lane,
                                          int rank, int tm, int tn, bool fine) {
   if (p.split == 1) {
     // A warp writes the 32 rows that its own lanes stored.
     const int q = warp & 3;
     if (warp >= 2 && warp < kLinLoader && fine)
-      reduce_rows<MODE, T, 1>(p, part, 0, 1, lane, q * 32, q * 32 + 32, tm, tn);
+      reduce_rows<MODE, ACT, T, 1>(p, part, 0, 1, lane, q * 32, q * 32 + 32, tm, tn);
     return;
   }
   cluster_sync();
   if (fine) {
     constexpr int W = kLinThreads / 32;
-    if (p.split == 2) reduce_rows<MODE, T, 2>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
-    else if (p.split == 4) reduce_rows<MODE, T, 4>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
-    else reduce_rows<MODE, T, 8>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
+    if (p.split == 2) reduce_rows<MODE, ACT, T, 2>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
+    else if (p.split == 4) reduce_rows<MODE, ACT, T, 4>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
+    else reduce_rows<MODE, ACT, T, 8>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
   }
   __syncwarp();
   cluster_meet();  // no CTA leaves while another reads its partial sums
+}
+
+template <int MODE, typename T>
+__device__ __forceinline__ void tile_out(const LinParams& p, const float* part, int warp, int lane,
+                                         int rank, int tm, int tn, bool fine) {
+  if constexpr (MODE == kLinGated)
+    with_act(p.act, [&](auto act) {
+      tile_out_as<MODE, decltype(act)::value, T>(p, part, warp, lane, rank, tm, tn, fine);
+    });
+  else
+    tile_out_as<MODE, 0, T>(p, part, warp, lane, rank, tm, tn, fine);
 }
 
 }  // namespace skg
