@@ -32,49 +32,27 @@ constexpr int64_t kMaxDim = INT32_MAX / 4;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// ------------------------------------------------------------------ dPRE and H
+// ------------------------------------------------------------------ dPRE from a given dH
 struct DgateParams {
   int64_t m;
-  int f, f32, act;
+  int f, act;
   const void* dh;
   int64_t lddh;
   const void* pre;
   int64_t ldp;
   void* dpre;     // m x 2 f
   void* dpre_lo;  // its low parts, or NULL
-  void* h;        // m x f, or NULL
-  void* h_lo;
 };
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-  union {
-    uint4 q;
-    T e[8];
-  } u;
-  u.q = *reinterpret_cast<const uint4*>(p);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = mx_to_f32(u.e[i]);
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = a.z;
-  v[3] = a.w;
-  v[4] = b.x;
-  v[5] = b.y;
-  v[6] = b.z;
-  v[7] = b.w;
-}
+union Eight {
+  uint4 q;
+  T e[8];
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* hi, T* lo, const float (&v)[8]) {
-  union {
-    uint4 q;
-    T e[8];
-  } h, l;
+  Eight<T> h, l;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     h.e[i] = mx_from_f32<T>(v[i]);
@@ -86,56 +64,49 @@ __device__ __forceinline__ void store8(T* hi, T* lo, const float (&v)[8]) {
 }
 
 // Eight elements of a row per thread; reads and writes each element once, so memory bounds it.
-template <typename T, typename D, int ACT>
+template <typename T, int ACT>
 __global__ void __launch_bounds__(128) dgate_kernel(const DgateParams p) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int col = ((int)blockIdx.x * 128 + (int)threadIdx.x) * 8;
   if (col >= p.f) return;
   for (int64_t row = blockIdx.y; row < p.m; row += gridDim.y) {
-    float d[8], g[8], u[8], dg[8], du[8], h[8];
-    load8<D>(reinterpret_cast<const D*>(p.dh) + row * p.lddh + col, d);
+    Eight<T> d, g, u;
+    d.q = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.dh) + row * p.lddh + col);
     const T* pre = reinterpret_cast<const T*>(p.pre) + row * p.ldp + col;
-    load8<T>(pre, g);
-    load8<T>(pre + p.f, u);
+    g.q = *reinterpret_cast<const uint4*>(pre);
+    u.q = *reinterpret_cast<const uint4*>(pre + p.f);
+    float dg[8], du[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const LinGrad r = lin_grad<ACT>(d[i], g[i], u[i]);
+      const LinGrad r = lin_grad<ACT>(mx_to_f32(d.e[i]), mx_to_f32(g.e[i]), mx_to_f32(u.e[i]));
       dg[i] = r.dg;
       du[i] = r.du;
-      h[i] = r.h;
     }
     const int64_t at = row * 2 * p.f + col;
     T *hi = reinterpret_cast<T*>(p.dpre) + at, *lo = reinterpret_cast<T*>(p.dpre_lo);
     lo = lo ? lo + at : lo;
     store8<T>(hi, lo, dg);
     store8<T>(hi + p.f, lo ? lo + p.f : lo, du);
-    if (p.h) {
-      T* hlo = reinterpret_cast<T*>(p.h_lo);
-      store8<T>(reinterpret_cast<T*>(p.h) + row * p.f + col, hlo ? hlo + row * p.f + col : hlo, h);
-    }
   }
 }
 
-template <typename T, typename D>
+template <typename T>
 cudaError_t launch_dgate_as(const DgateParams& p, cudaStream_t stream) {
   const dim3 grid((unsigned)((p.f / 8 + 127) / 128), (unsigned)(p.m < 32768 ? p.m : 32768));
   const dim3 block(128);
   switch (p.act) {
-    case SKG_ACT_SILU: return launch_pdl(dgate_kernel<T, D, SKG_ACT_SILU>, grid, block, 0, stream, p);
-    case SKG_ACT_GELU: return launch_pdl(dgate_kernel<T, D, SKG_ACT_GELU>, grid, block, 0, stream, p);
+    case SKG_ACT_SILU: return launch_pdl(dgate_kernel<T, SKG_ACT_SILU>, grid, block, 0, stream, p);
+    case SKG_ACT_GELU: return launch_pdl(dgate_kernel<T, SKG_ACT_GELU>, grid, block, 0, stream, p);
     case SKG_ACT_GELU_TANH:
-      return launch_pdl(dgate_kernel<T, D, SKG_ACT_GELU_TANH>, grid, block, 0, stream, p);
-    default: return launch_pdl(dgate_kernel<T, D, SKG_ACT_RELU>, grid, block, 0, stream, p);
+      return launch_pdl(dgate_kernel<T, SKG_ACT_GELU_TANH>, grid, block, 0, stream, p);
+    default: return launch_pdl(dgate_kernel<T, SKG_ACT_RELU>, grid, block, 0, stream, p);
   }
 }
 
 cudaError_t launch_dgate(int dtype, const DgateParams& p, cudaStream_t stream) {
-  if (dtype == SKG_IN_F16)
-    return p.f32 ? launch_dgate_as<__half, float>(p, stream)
-                 : launch_dgate_as<__half, __half>(p, stream);
-  return p.f32 ? launch_dgate_as<__nv_bfloat16, float>(p, stream)
-               : launch_dgate_as<__nv_bfloat16, __nv_bfloat16>(p, stream);
+  return dtype == SKG_IN_F16 ? launch_dgate_as<__half>(p, stream)
+                             : launch_dgate_as<__nv_bfloat16>(p, stream);
 }
 
 // ------------------------------------------------------------------ products
@@ -152,12 +123,13 @@ struct Product {
   Operand a, b;
   void* c;
   int64_t ldc;
-  int out;          // skg_out_t
   int act;
   void* pre;        // kLinGated: PRE, or NULL; kLinGrad: DPRE
   int64_t ldp;
   const void* pre_in;  // kLinGrad: PRE
   int64_t ldp_in;
+  void *c_lo, *pre_lo;
+  const Product* second;  // a second product of the same k (M-major A, N-major B, pairs)
   const skg_adapters_t* adapters;
   void* t;          // with a plan: t and the plan come from skg_lora.cu's kernel
   LoraPlan* plan;
@@ -200,26 +172,27 @@ bool map_operand(CUtensorMap* t, int dtype, const Operand& o, const void* p, int
 // Single CTAs: how many share a 128 x 128 tile (S), and the estimated time (us). Up to 16
 // rows of A the sum over the cluster is a few rows, and S is what fits the GPU at once (1 x
 // 1024 x 8192: 27, 15, 9.1, 6.1 us with S = 1, 2, 4, 8). Else a fixed cost that grows with S,
-// and the CTA's stages of k, at 0.2 us where it has an SM to itself and 0.44 where two share
-// one (333 x 2048 x 2048: 10.4, 8.0, 10.3 with S = 1, 2, 4: 48, 96, 192 CTAs). Clusters of
-// eight find room one to an SM up to eight of them (128 x 1000 x 2200: 7.2 against 8.4 with
-// S = 4; 16 tiles, 128 x 2048 x 2048: 8.5 against 6.7).
+// and the CTA's stages of k, at 0.2 us where all clusters find an SM for each CTA and 0.44
+// where two CTAs share one (333 x 2048 x 2048: 10.4, 8.0, 10.3 with S = 1, 2, 4: 48, 96, 192
+// CTAs). Larger clusters find less room, as a GPC's SMs do not divide by them: 128 x 2048 x
+// 2048, 16 tiles, takes 6.8, 6.5, 8.6 with S = 4, 6, 8.
 struct SinglePlan {
   int split;
+  bool deep;
   double us;
 };
 SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms) {
-  SinglePlan best = {1, 1e30};
-  for (int s = 1; s <= 8; s *= 2) {
+  constexpr double kFixed[9] = {0, 4.4, 4.9, 5.1, 5.3, 0, 5.6, 0, 5.7};
+  SinglePlan best = {1, false, 1e30};
+  for (int s : {1, 2, 3, 4, 6, 8}) {
     if (s > 1 && (tiles * s > 2 * sms || s > ksteps)) break;
+    const bool deep = s == 1 ? tiles <= sms : tiles <= lin_single_clusters(s);
+    if ((s == 3 || s == 6) && (m <= 16 || !deep)) continue;
     const int stages = (ksteps + s - 1) / s;
     const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
-    double us;
-    if (tiles * s <= sms)
-      us = (s == 1 ? 4.4 : s == 2 ? 4.9 : s == 4 ? 5.3 : tiles <= 8 ? 5.7 : 8.6) + 0.2 * stages;
-    else
-      us = (s == 1 ? 3.2 : s == 8 ? 9.0 : 6.5) + 0.436 * (double)waves * stages;
-    if (m <= 16 || us < best.us) best = {s, us};
+    const double us = deep ? kFixed[s] + 0.2 * stages
+                           : (s == 1 ? 3.2 : s == 8 ? 9.0 : 6.5) + 0.436 * (double)waves * stages;
+    if (m <= 16 || us < best.us) best = {s, deep, us};
   }
   return best;
 }
@@ -248,13 +221,13 @@ Choice choose(const Product& q, const Common& c) {
   Choice h = {};
   h.resident = lin_pair_clusters_resident();
   const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms);
-  h.pair = q.out != SKG_OUT_F32 && h.resident > 0 && q.n >= 8 &&
+  // (The low parts of H and DPRE are written by single CTAs; up to 128 rows they run.)
+  h.pair = h.resident > 0 && q.n >= 8 && !q.c_lo &&
            wants_pairs(q.m, tm2 * tn2, steps, h.resident, single.us);
   h.tiles_m = h.pair ? tm2 : tm1;
   h.tiles_n = h.pair ? tn2 : tn1;
   h.split = h.pair ? 1 : single.split;
-  // (Clusters of eight do not all find eight SMs of their own in a GPC.)
-  h.deep = !h.pair && tm1 * tn1 * h.split <= (h.split < 8 ? c.sms : 64);
+  h.deep = !h.pair && single.deep;
   return h;
 }
 
@@ -292,6 +265,10 @@ skg_status_t run_product(const Product& q, const Common& c) {
   p.ldc = ld_of(q.ldc, q.m, q.n);
   p.pre = q.pre;
   p.ldp = ld_of(q.ldp, q.m, 2 * q.n);
+  p.pre_in = q.pre_in;
+  p.ldp_in = ld_of(q.ldp_in, q.m, 2 * q.n);
+  p.c_lo = q.c_lo;
+  p.pre_lo = q.pre_lo;
   p.plan = q.plan;
   p.rank_pad = q.rank_pad;
   p.report = c.report;
@@ -340,7 +317,7 @@ skg_status_t run_product(const Product& q, const Common& c) {
       p.idesc = idesc_f16(bf16, 128, (uint32_t)(128 + a.most * q.rank_pad));
       CUtensorMap down;
       if (!map_down(&down, c.dtype, ad, q.k, q.rank_pad)) return SKG_ERR_CUDA;
-      return launch_lin_adapted(q.out, t, down, p, a, c.stream) == cudaSuccess ? SKG_OK
+      return launch_lin_adapted(out_of(c.dtype), t, down, p, a, c.stream) == cudaSuccess ? SKG_OK
                                                                                : SKG_ERR_CUDA;
     }
     if (!map2(&t.t, c.dtype, q.t, 2 * q.rank_pad, q.m, 2 * q.rank_pad, 64, p.a_rows))
@@ -349,15 +326,28 @@ skg_status_t run_product(const Product& q, const Common& c) {
   if (pair) {
     if (!map2(&t.c, c.dtype, q.c, q.n & ~7, q.m, p.ldc, 64, 32)) return SKG_ERR_CUDA;
     if (q.mode == kLinGrad &&
-        (!map2(&t.t, c.dtype, q.pre_in, q.n, q.m, q.ldp_in, 64, 32) ||
-         !map2(&t.up, c.dtype, (const uint16_t*)q.pre_in + q.n, q.n, q.m, q.ldp_in, 64, 32)))
+        (!map2(&t.t, c.dtype, q.pre_in, q.n, q.m, p.ldp_in, 64, 32) ||
+         !map2(&t.up, c.dtype, (const uint16_t*)q.pre_in + q.n, q.n, q.m, p.ldp_in, 64, 32)))
       return SKG_ERR_CUDA;
     if (q.pre && (!map2(&t.gate, c.dtype, q.pre, q.n, q.m, p.ldp, 64, 32) ||
                   !map2(&t.pre_up, c.dtype, (const uint16_t*)q.pre + q.n, q.n, q.m, p.ldp, 64, 32)))
       return SKG_ERR_CUDA;
   }
-  const LinVariant v = {q.mode, q.a.mn, q.b.mn, q.out};
-  const int64_t tiles = h.tiles_m * h.tiles_n;
+  int64_t tiles = h.tiles_m * h.tiles_n;
+  if (pair && q.second) {
+    const Product& w = *q.second;
+    p.second = {(int)w.m, (int)w.n, (int)((w.m + 255) / 256), (int)((w.n + 255) / 256),
+                w.b.lo != nullptr, w.c, ld_of(w.ldc, w.m, w.n)};
+    tiles += (int64_t)p.second.tiles_m * p.second.tiles_n;
+    if (tiles > INT32_MAX) return SKG_ERR_UNSUPPORTED;
+    if (!map_operand(&t.t, c.dtype, w.a, w.a.p, w.m, w.k, 128) ||
+        !map_operand(&t.up, c.dtype, w.b, w.b.p, w.n, w.k, 128) ||
+        !map2(&t.pre_up, c.dtype, w.c, w.n & ~7, w.m, p.second.ldc, 64, 32) ||
+        (p.terms == 2 && !map_operand(&t.gate, c.dtype, w.a.lo ? w.a : w.b, w.a.lo ? w.a.lo : w.b.lo,
+                                      w.a.lo ? w.m : w.n, w.k, 128)))
+      return SKG_ERR_CUDA;
+  }
+  const LinVariant v = {q.mode, q.a.mn, q.b.mn, out_of(c.dtype)};
   const cudaError_t e =
       pair ? launch_lin_pair(v, t, p, (int)(tiles < h.resident ? tiles : h.resident), c.stream)
            : launch_lin_single(v, t, p, c.stream);
@@ -417,7 +407,7 @@ skg_status_t common(int32_t dtype, void* workspace, void* stream, Common* c) {
 
 // Scratch of the gradients, from its start.
 struct BackwardScratch {
-  size_t dpre, dpre_lo, h, h_lo, dh, total;
+  size_t dpre, dpre_lo, h, h_lo, total;
 };
 BackwardScratch backward_scratch(int64_t m, int64_t f, bool block) {
   BackwardScratch s = {};
@@ -432,15 +422,17 @@ BackwardScratch backward_scratch(int64_t m, int64_t f, bool block) {
   s.dpre_lo = take(two * n * 4);
   s.h = take(block ? n * 2 : 0);
   s.h_lo = take(block ? two * n * 2 : 0);
-  s.dh = take(block ? n * 4 : 0);
   s.total = at;
   return s;
 }
 
-// dX = dPRE W (m x k) and dW = dPRE^T X (2 f x k).
+// dX = dPRE W (m x k), dW = dPRE^T X (2 f x k) and a second weight gradient (or NULL), which
+// shares the launch where both run on pairs (512 tokens, 1024 and 2816 wide: two launches of
+// 88 and 44 tiles on 76 pairs).
 skg_status_t in_gradients(int64_t m, int64_t f, int64_t k, const void* dpre, const void* dpre_lo,
                           const void* X, int64_t ldx, const void* W, int64_t ldw, void* dX,
-                          int64_t lddx, void* dW, int64_t lddw, const Common& c) {
+                          int64_t lddx, void* dW, int64_t lddw, const Product* other,
+                          const Common& c) {
   Product q = {};
   q.m = m;
   q.n = k;
@@ -449,7 +441,6 @@ skg_status_t in_gradients(int64_t m, int64_t f, int64_t k, const void* dpre, con
   q.b = {W, ldw, true, nullptr};
   q.c = dX;
   q.ldc = lddx;
-  q.out = out_of(c.dtype);
   skg_status_t st = product_or_zero(q, c);
   if (st != SKG_OK) return st;
   q.m = 2 * f;
@@ -458,7 +449,10 @@ skg_status_t in_gradients(int64_t m, int64_t f, int64_t k, const void* dpre, con
   q.b = {X, ldx, true, nullptr};
   q.c = dW;
   q.ldc = lddw;
-  return product_or_zero(q, c);
+  const bool both = other && m > 0 && f > 0 && choose(q, c).pair && choose(*other, c).pair;
+  if (both) q.second = other;
+  st = product_or_zero(q, c);
+  return st == SKG_OK && other && !both ? product_or_zero(*other, c) : st;
 }
 
 }  // namespace
@@ -522,7 +516,6 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
   q.b = {W, ldw, false, nullptr};
   q.c = Y;
   q.ldc = ldy;
-  q.out = out_of(dtype);
   if (ad) {
     q.adapters = ad;
     q.rank_pad = (ad->rank + 15) / 16 * 16;
@@ -601,7 +594,6 @@ skg_status_t skg_gated(int64_t m, int64_t hidden, int64_t k, const void* X, int6
   q.b = {W, ldw, false, nullptr};
   q.c = H;
   q.ldc = ldh;
-  q.out = out_of(dtype);
   q.act = act;
   q.pre = PRE;
   q.ldp = ldp;
@@ -654,7 +646,7 @@ skg_status_t skg_gated_backward(int64_t m, int64_t hidden, int64_t k, const void
     if (launch_dgate(dtype, d, c.stream) != cudaSuccess) return SKG_ERR_CUDA;
   }
   return in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W, ldw,
-                      dX, lddx, dW, lddw, c);
+                      dX, lddx, dW, lddw, nullptr, c);
 }
 
 size_t skg_scratch_size_feed_forward_backward(int64_t m, int64_t hidden) {
@@ -701,52 +693,29 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
     q.k = k;
     q.a = {dY, lddy, false, nullptr};
     q.b = {W_out, ldw_out, true, nullptr};
-    q.out = out_of(dtype);
+      q.mode = kLinGrad;  // dH stays in the accumulator
     q.act = act;
-    if (!two && choose(q, c).pair) {  // dH stays in the accumulator
-      q.mode = kLinGrad;
-      q.c = base + s.h;
-      q.ldc = hidden;
-      q.pre = base + s.dpre;
-      q.ldp = 2 * hidden;
-      q.pre_in = PRE;
-      q.ldp_in = ldp;
-      st = run_product(q, c);
-    } else {
-      q.c = base + s.dh;
-      q.ldc = hidden;
-      q.out = SKG_OUT_F32;
-      st = run_product(q, c);
-      DgateParams d = {};
-      d.m = m;
-      d.f = (int)hidden;
-      d.f32 = 1;
-      d.act = act;
-      d.dh = base + s.dh;
-      d.lddh = hidden;
-      d.pre = PRE;
-      d.ldp = ldp;
-      d.dpre = base + s.dpre;
-      d.dpre_lo = two ? base + s.dpre_lo : nullptr;
-      d.h = base + s.h;
-      d.h_lo = two ? base + s.h_lo : nullptr;
-      if (st == SKG_OK && launch_dgate(dtype, d, c.stream) != cudaSuccess) st = SKG_ERR_CUDA;
-    }
+    q.c = base + s.h;
+    q.c_lo = two ? base + s.h_lo : nullptr;
+    q.ldc = hidden;
+    q.pre = base + s.dpre;
+    q.pre_lo = two ? base + s.dpre_lo : nullptr;
+    q.ldp = 2 * hidden;
+    q.pre_in = PRE;
+    q.ldp_in = ldp;
+    st = run_product(q, c);
     if (st != SKG_OK) return st;
   }
-  st = in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W_in,
-                    ldw_in, dX, lddx, dW_in, lddw_in, c);
-  if (st != SKG_OK) return st;
-  Product q = {};
-  q.m = k;
-  q.n = hidden;
-  q.k = m;
-  q.a = {dY, lddy, true, nullptr};
-  q.b = {base + s.h, hidden, true, two ? base + s.h_lo : nullptr};
-  q.c = dW_out;
-  q.ldc = lddw_out;
-  q.out = out_of(dtype);
-  return product_or_zero(q, c);
+  Product w = {};
+  w.m = k;
+  w.n = hidden;
+  w.k = m;
+  w.a = {dY, lddy, true, nullptr};
+  w.b = {base + s.h, hidden, true, two ? base + s.h_lo : nullptr};
+  w.c = dW_out;
+  w.ldc = lddw_out;
+  return in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W_in,
+                      ldw_in, dX, lddx, dW_in, lddw_in, &w, c);
 }
 
 }  // extern "C"

@@ -13,7 +13,7 @@
 //   kLinGated   B holds two projections of n rows each; a tile takes half of its columns
 //               from either, so one thread holds gate and up of an output:
 //               H = act(gate) * up, and PRE = (gate | up) where it is asked for
-//   kLinGrad    the product is the gradient of a gated output (pairs, N-major B): with PRE,
+//   kLinGrad    the product is the gradient of a gated output (N-major B): with PRE,
 //               DPRE = the gradients of gate and up, and H formed again
 #pragma once
 #include <cuda_runtime.h>
@@ -52,6 +52,14 @@ struct LoraPlan {
   uint32_t rows[kLoraRows][8];
 };
 
+// Pairs, M-major A and N-major B: a second product of the same k in the same launch (its
+// tiles behind the first one's; tiles_m = 0: none).
+struct LinSecond {
+  int m, n, tiles_m, tiles_n, lo_b;
+  void* c;
+  int64_t ldc;
+};
+
 struct LinParams {
   int m, n, k;        // rows and columns of the result (of one projection), length of the sums
   int ksteps;         // stages of k
@@ -63,11 +71,16 @@ struct LinParams {
   int deep;           // single CTAs: one per SM, with a ring of twice the stages
   int a_rows;         // single CTAs, K-major A: rows of A's box
   uint32_t idesc;
-  int act;            // kLinGated
+  int act;            // kLinGated, kLinGrad
   void* c;
   int64_t ldc;
-  void* pre;          // kLinGated: (gate | up), or NULL
+  void* pre;          // kLinGated: PRE or NULL; kLinGrad: DPRE
   int64_t ldp;
+  const void* pre_in; // kLinGrad: PRE
+  int64_t ldp_in;
+  void* c_lo;         // kLinGrad: low parts of H and DPRE, or NULL
+  void* pre_lo;
+  LinSecond second;
   const LoraPlan* plan;  // adapters: one per 256 rows, or NULL
   int rank_pad;          // their rank, rounded up to 16
   uint32_t stages;    // a CTA loads no more stages than this (skg_layers_test_stall)
@@ -82,6 +95,7 @@ struct LinMaps {
   CUtensorMap t, up;      // adapters: scale (x A^T) in high and low parts; their B (3 dimensions)
   CUtensorMap c, gate, pre_up;  // pairs: stores (C or H, the halves of PRE or DPRE);
                                 // kLinGrad: t and up are the halves of PRE
+  // A second product's a, b, lo and c are t, up, gate and pre_up.
 };
 
 struct LinAux : MxAux {
@@ -391,7 +405,7 @@ __device__ __forceinline__ void store_parts(T* hi, T* lo, const float (&v)[4]) {
 }
 
 // ------------------------------------------------------------------ launches
-// The kernels' variants. out: skg_out_t of C (kLinPlain with N-major B: also fp32).
+// The kernels' variants. out: skg_out_t of C (fp16 or bf16).
 struct LinVariant {
   int mode;
   bool a_mn, b_mn;  // M-major A, N-major B
@@ -418,8 +432,32 @@ cudaError_t launch_lin_adapted(int out, const LinMaps& t, const CUtensorMap& dow
 cudaError_t launch_lin_pair(const LinVariant& v, const LinMaps& t, const LinParams& p,
                             int clusters, cudaStream_t stream);
 
-// CTA pairs of the pair kernel that can be resident on the current device at once.
+// CTA pairs of the pair kernel that can be resident on the current device at once, and clusters
+// of `size` of the single kernel's CTAs that have an SM each.
 int lin_pair_clusters_resident();
+int lin_single_clusters(int size);
+
+// Clusters of a kernel of this file's block size that can be resident at once (0: unknown).
+inline int clusters_resident(const void* kernel, uint32_t smem, int size) {
+  int n = 0;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) ==
+      cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(size * 256));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  return n;
+}
 
 // t = scale (x A^T) of every row's adapter, and the plans (skg_lora.cu).
 struct LoraParams {

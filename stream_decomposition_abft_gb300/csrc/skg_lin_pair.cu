@@ -65,12 +65,12 @@ __device__ __forceinline__ uint8_t* store_box(const CUtensorMap* map, uint8_t* s
 // The columns of a box of C behind the last whole 16 bytes of a row (the map ends before them:
 // what the engine would write there is not C's), one by one.
 template <typename T>
-__device__ __noinline__ void store_rest(const LinParams& p, const uint8_t* st, int lane, int col,
-                                        int row) {
-  if (row + lane >= p.m) return;
-  for (int c = max(p.n & ~7, col); c < min(p.n, col + 64); ++c) {
+__device__ __noinline__ void store_rest(void* to, int64_t ld, int m, int n, const uint8_t* st,
+                                        int lane, int col, int row) {
+  if (row + lane >= m) return;
+  for (int c = max(n & ~7, col); c < min(n, col + 64); ++c) {
     const int i = c - col;
-    reinterpret_cast<T*>(p.c)[(int64_t)(row + lane) * p.ldc + c] = *reinterpret_cast<const T*>(
+    reinterpret_cast<T*>(to)[(int64_t)(row + lane) * ld + c] = *reinterpret_cast<const T*>(
         st + lane * 128 + (((i >> 3) ^ (lane & 7)) << 4) + (i & 7) * sizeof(T));
   }
 }
@@ -137,13 +137,20 @@ __device__ __forceinline__ void grad_boxes(const LinParams& p, const LinMaps& ma
 
 // Tile t in an order that keeps the tiles in flight close together: bands of eight rows of
 // tiles, column by column within a band (2048 rows of A stay in L2 while B passes).
-__device__ __forceinline__ void pair_tile(const LinParams& p, int t, int& tm, int& tn) {
+// Returns whether it is the second product's.
+template <bool TWO>
+__device__ __forceinline__ bool pair_tile(const LinParams& p, int t, int& tm, int& tn) {
   constexpr int kBand = 8;
-  const int band = t / (kBand * p.tiles_n);
-  const int rows = min(kBand, p.tiles_m - band * kBand);
-  const int i = t - band * kBand * p.tiles_n;
+  const bool second = TWO && t >= p.tiles_m * p.tiles_n;
+  const int tiles_m = second ? p.second.tiles_m : p.tiles_m;
+  const int tiles_n = second ? p.second.tiles_n : p.tiles_n;
+  if (second) t -= p.tiles_m * p.tiles_n;
+  const int band = t / (kBand * tiles_n);
+  const int rows = min(kBand, tiles_m - band * kBand);
+  const int i = t - band * kBand * tiles_n;
   tn = i / rows;
   tm = band * kBand + i % rows;
+  return second;
 }
 
 template <int MODE, bool AMN, bool BMN, typename T>
@@ -159,7 +166,8 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
   PairAux* aux = reinterpret_cast<PairAux*>(staging + C::STAGING);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
-  const int tiles = p.tiles_m * p.tiles_n;
+  constexpr bool TWO = AMN && BMN;
+  const int tiles = p.tiles_m * p.tiles_n + (TWO ? p.second.tiles_m * p.second.tiles_n : 0);
   const int first = (int)blockIdx.x >> 1, stride = (int)gridDim.x >> 1;
   const bool lora = LORA && p.plan != nullptr;
 
@@ -232,7 +240,10 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
       const int ks = p.ksteps * p.terms;
       for (int t = first; ok && t < tiles; t += stride) {
         int tm, tn;
-        pair_tile(p, t, tm, tn);
+        const bool second = pair_tile<TWO>(p, t, tm, tn);
+        const int lo_b = second ? p.second.lo_b : p.lo_b;
+        const CUtensorMap *map_a = second ? &maps.t : &maps.a, *map_b = second ? &maps.up : &maps.b,
+                          *map_lo = second ? &maps.gate : &maps.lo;
         const int row = (2 * tm + rank) * kLinTile;
         // The plan is read ahead of its use, the first entries beside their number.
         if (waited) {
@@ -245,8 +256,8 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           step(C::STAGE_BYTES, [&](uint8_t* s, uint32_t bar) {
             const bool lo = p.terms == 2 && (i & 1);
             const int k0 = (p.terms == 2 ? i >> 1 : i) * kLinK;
-            const CUtensorMap* ma = lo && !p.lo_b ? &maps.lo : &maps.a;
-            const CUtensorMap* mb = lo && p.lo_b ? &maps.lo : &maps.b;
+            const CUtensorMap* ma = lo && !lo_b ? map_lo : map_a;
+            const CUtensorMap* mb = lo && lo_b ? map_lo : map_b;
             if constexpr (AMN) {
               tma_load_2d_pair(s, ma, bar, row, k0);
               tma_load_2d_pair(s + kLinBox, ma, bar, row + 64, k0);
@@ -323,7 +334,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         const LoraPlan* plan = nullptr;
         if (lora) {
           int tm, tn;
-          pair_tile(p, t, tm, tn);
+          pair_tile<false>(p, t, tm, tn);
           plan = p.plan + tm;
           if (waited) {
             read(plan, 0, off);
@@ -383,14 +394,15 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     int n = 0;
     for (int t = first; t < tiles; t += stride, ++n) {
       int tm, tn;
-      pair_tile(p, t, tm, tn);
+      const bool second = pair_tile<TWO>(p, t, tm, tn);
+      const int pm = second ? p.second.m : p.m, pn = second ? p.second.n : p.n;
       const int row0 = (2 * tm + rank) * kLinTile + q * 32, col0 = tn * TILE_N;
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * 256;
-      const bool live = row0 < p.m;
+      const bool live = row0 < pm;
       // kLinGrad: PRE of 64 columns comes while the 64 before them (or the MMAs) are worked on.
       auto fetch_pre = [&](int col) {
         if constexpr (MODE == kLinGrad) {
-          if (live && col < p.n && lane == 0) {
+          if (live && col < pn && lane == 0) {
             fence_proxy_async_smem();
             mbar_arrive_expect_tx(&aux->pre[q], 8192);
             tma_load_2d(mine + 8192, &maps.t, &aux->pre[q], col, row0);
@@ -403,7 +415,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
       if (!got) lin_fail(p, aux);
       if (!__all_sync(0xffffffffu, got)) {
         // (What fetch_pre asked for lands before the CTA leaves.)
-        if (MODE == kLinGrad && live && col0 < p.n) mx_wait(&aux->pre[q], pres & 1u, aux, true);
+        if (MODE == kLinGrad && live && col0 < pn) mx_wait(&aux->pre[q], pres & 1u, aux, true);
         break;
       }
       tc_fence_after();
@@ -434,7 +446,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           }
           if (s == 1) hand_over();
           const int col = col0 + s * 64;
-          if (live && col < p.n) {
+          if (live && col < pn) {
             if (p.pre) {
               store_box<T>(&maps.gate, mine, box, lane, col, row0,
                            [&](int i) { return value(0, i); });
@@ -467,7 +479,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           tmem_ld_wait32(v[s & 1][1]);
           const int col = col0 + s * 64;
           if (s == 3) hand_over();
-          if (live && col < p.n) {
+          if (live && col < pn) {
             if constexpr (MODE == kLinGrad) {
               uint4 g[8], u[8];
               if (!mx_wait(&aux->pre[q], pres & 1u, aux, true)) lin_fail(p, aux);
@@ -482,9 +494,11 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
               if (s < 3) fetch_pre(col + 64);
               grad_boxes<T>(p, maps, mine, box, lane, col, row0, v[s & 1], g, u);
             } else {
-              const uint8_t* st = store_box<T>(&maps.c, mine, box, lane, col, row0,
-                                               [&](int i) { return value(s & 1, i); });
-              if ((p.n & 7) && col + 64 > (p.n & ~7)) store_rest<T>(p, st, lane, col, row0);
+              const uint8_t* st = store_box<T>(second ? &maps.pre_up : &maps.c, mine, box, lane,
+                                               col, row0, [&](int i) { return value(s & 1, i); });
+              if ((pn & 7) && col + 64 > (pn & ~7))
+                store_rest<T>(second ? p.second.c : p.c, second ? p.second.ldc : p.ldc, pm, pn, st,
+                              lane, col, row0);
             }
           }
           if (s < 2) fetch(s + 2);
@@ -550,23 +564,7 @@ int lin_pair_clusters_resident() {
   const int have = cached[dev].load(std::memory_order_acquire);
   if (have != 0) return have > 0 ? have : 0;
   auto kernel = lin_pair_kernel<kLinGated, false, false, __nv_bfloat16>;  // all alike in resources
-  int n = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)PairCfg<kLinGated>::SMEM) == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * 256);
-    cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = PairCfg<kLinGated>::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
-  }
-  cudaGetLastError();
+  const int n = clusters_resident((const void*)kernel, PairCfg<kLinGated>::SMEM, 2);
   cached[dev].store(n > 0 ? n : -1, std::memory_order_release);
   return n;
 }

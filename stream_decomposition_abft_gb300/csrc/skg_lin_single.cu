@@ -334,6 +334,7 @@ template <typename T>
 cudaError_t launch_type(const LinVariant& v, const LinMaps& t, const LinParams& p,
                         cudaStream_t stream) {
   if (v.mode == kLinGated) return launch_ring<kLinGated, false, false, T>(t, p, stream);
+  if (v.mode == kLinGrad) return launch_ring<kLinGrad, false, true, T>(t, p, stream);
   if (v.a_mn) return launch_ring<kLinPlain, true, true, T>(t, p, stream);
   if (v.b_mn) return launch_ring<kLinPlain, false, true, T>(t, p, stream);
   return launch_ring<kLinPlain, false, false, T>(t, p, stream);
@@ -343,9 +344,20 @@ cudaError_t launch_type(const LinVariant& v, const LinMaps& t, const LinParams& 
 
 cudaError_t launch_lin_single(const LinVariant& v, const LinMaps& t, const LinParams& p,
                               cudaStream_t stream) {
-  if (v.out == SKG_OUT_F32) return launch_ring<kLinPlain, false, true, float>(t, p, stream);
   if (v.out == SKG_OUT_F16) return launch_type<__half>(v, t, p, stream);
   return launch_type<__nv_bfloat16>(v, t, p, stream);
+}
+
+int lin_single_clusters(int size) {
+  static std::atomic<int> cached[64][9];
+  int dev = 0;
+  if (size < 1 || size > 8 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  const int have = cached[dev][size].load(std::memory_order_acquire);
+  if (have != 0) return have > 0 ? have : 0;
+  auto kernel = lin_single_kernel<kLinGated, kDeep, false, false, __nv_bfloat16>;  // all alike
+  const int n = clusters_resident((const void*)kernel, SingleCfg<kDeep>::SMEM, size);
+  cached[dev][size].store(n > 0 ? n : -1, std::memory_order_release);
+  return n;
 }
 
 }  // namespace skg

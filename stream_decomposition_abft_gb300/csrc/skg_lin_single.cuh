@@ -15,10 +15,11 @@ __device__ __forceinline__ void write4(T* c, const float (&v)[4], int left) {
   }
 }
 
-// Four output columns of row r: v as the accumulator has them; gated: gate and up.
+// Four output columns of row r: v as the accumulator has them; gated: gate and up; grad: dH,
+// with g and u of PRE.
 template <int MODE, int ACT, typename T>
 __device__ __forceinline__ void finish4(const LinParams& p, int row, int col, const float4& v,
-                                        const float4& u) {
+                                        const float4& u, uint2 g_in, uint2 u_in) {
   T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
   if constexpr (MODE == kLinGated) {
     const float4 o = lin_gated4<ACT>(v, u);
@@ -29,6 +30,34 @@ __device__ __forceinline__ void finish4(const LinParams& p, int row, int col, co
       const float a[4] = {v.x, v.y, v.z, v.w}, b[4] = {u.x, u.y, u.z, u.w};
       write4<T>(g, a, p.n - col);
       write4<T>(g + p.n, b, p.n - col);
+    }
+  } else if constexpr (MODE == kLinGrad) {  // n is a multiple of 8
+    union {
+      uint2 q;
+      T e[4];
+    } g, w;
+    g.q = g_in;
+    w.q = u_in;
+    const float d[4] = {v.x, v.y, v.z, v.w};
+    float dg[4], du[4], h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = mx_to_f32(g.e[i]), b = mx_to_f32(w.e[i]);
+      const LinGrad r = ACT == SKG_ACT_GELU ? lin_grad_gelu(d[i], a, b) : lin_grad<ACT>(d[i], a, b);
+      dg[i] = r.dg;
+      du[i] = r.du;
+      h[i] = r.h;
+    }
+    T* o = reinterpret_cast<T*>(p.pre) + (int64_t)row * p.ldp + col;
+    if (p.pre_lo) {
+      T* l = reinterpret_cast<T*>(p.pre_lo) + (int64_t)row * p.ldp + col;
+      store_parts<T>(o, l, dg);
+      store_parts<T>(o + p.n, l + p.n, du);
+      store_parts<T>(c, reinterpret_cast<T*>(p.c_lo) + (int64_t)row * p.ldc + col, h);
+    } else {
+      write4<T>(o, dg, 4);
+      write4<T>(o + p.n, du, 4);
+      write4<T>(c, h, 4);
     }
   } else {
     const float a[4] = {v.x, v.y, v.z, v.w};
@@ -59,10 +88,17 @@ __device__ __forceinline__ void reduce_rows(const LinParams& p, const float* par
 #pragma unroll 1
   for (int i = w0 * R * PER; first + i * S < rows; i += warps * R * PER) {
     float4 v[R][S], u[R][S];
+    uint2 g_in[R], u_in[R];  // grad: PRE
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       const int r = first + (i + j * PER + sub) * S;
       if (r < rows && in) {
+        if constexpr (MODE == kLinGrad) {
+          const T* pre =
+              reinterpret_cast<const T*>(p.pre_in) + (int64_t)(tm * kLinTile + r) * p.ldp_in + col;
+          g_in[j] = *reinterpret_cast<const uint2*>(pre);
+          u_in[j] = *reinterpret_cast<const uint2*>(pre + p.n);
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           if constexpr (S == 1) {
@@ -93,7 +129,7 @@ __device__ __forceinline__ void reduce_rows(const LinParams& p, const float* par
           b.w += u[j][s].w;
         }
       }
-      finish4<MODE, ACT, T>(p, tm * kLinTile + r, col, a, b);
+      finish4<MODE, ACT, T>(p, tm * kLinTile + r, col, a, b, g_in[j], u_in[j]);
     }
   }
 }
@@ -132,6 +168,8 @@ __device__ __forceinline__ void tile_out_as(const LinParams& p, const float* par
   if (fine) {
     constexpr int W = kLinThreads / 32;
     if (p.split == 2) reduce_rows<MODE, ACT, T, 2>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
+    else if (p.split == 3) reduce_rows<MODE, ACT, T, 3>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
+    else if (p.split == 6) reduce_rows<MODE, ACT, T, 6>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
     else if (p.split == 4) reduce_rows<MODE, ACT, T, 4>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
     else reduce_rows<MODE, ACT, T, 8>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
   }
@@ -142,7 +180,7 @@ __device__ __forceinline__ void tile_out_as(const LinParams& p, const float* par
 template <int MODE, typename T>
 __device__ __forceinline__ void tile_out(const LinParams& p, const float* part, int warp, int lane,
                                          int rank, int tm, int tn, bool fine) {
-  if constexpr (MODE == kLinGated)
+  if constexpr (MODE != kLinPlain)
     with_act(p.act, [&](auto act) {
       tile_out_as<MODE, decltype(act)::value, T>(p, part, warp, lane, rank, tm, tn, fine);
     });
