@@ -405,6 +405,10 @@ skg_status_t common(int32_t dtype, void* workspace, void* stream, Common* c) {
   return SKG_OK;
 }
 
+// H's scratch rows start on 32-byte sectors (others: half as much again for the loads of a
+// stage).
+int64_t h_pitch(int64_t f) { return (f + 15) / 16 * 16; }
+
 // Scratch of the gradients, from its start.
 struct BackwardScratch {
   size_t dpre, dpre_lo, h, h_lo, total;
@@ -420,8 +424,9 @@ BackwardScratch backward_scratch(int64_t m, int64_t f, bool block) {
   };
   s.dpre = take(n * 4);
   s.dpre_lo = take(two * n * 4);
-  s.h = take(block ? n * 2 : 0);
-  s.h_lo = take(block ? two * n * 2 : 0);
+  const size_t nh = (size_t)m * (size_t)h_pitch(f);
+  s.h = take(block ? nh * 2 : 0);
+  s.h_lo = take(block ? two * nh * 2 : 0);
   s.total = at;
   return s;
 }
@@ -491,7 +496,7 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     if (some && (!there(ad->down, ad->rank, k, ad->ld_down) ||
                  !there(ad->up, n, ad->rank, ad->ld_up)))
       return SKG_ERR_ARG;
-    if (some && ad->count > 1 && (ad->stride_down < 0 || ad->stride_up < 0)) return SKG_ERR_ARG;
+    if (some && ad->count > 1 && (ad->stride_down <= 0 || ad->stride_up <= 0)) return SKG_ERR_ARG;
     if (ad->rank > 512 || ad->rank % 8) return SKG_ERR_UNSUPPORTED;
     if (some && (!aligned(ad->down, ad->rank, k, ad->ld_down) || !aligned(ad->up, n, ad->rank, ad->ld_up) ||
                  (ad->count > 1 && (ad->stride_down % 8 || ad->stride_up % 8)) ||
@@ -697,7 +702,7 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
     q.act = act;
     q.c = base + s.h;
     q.c_lo = two ? base + s.h_lo : nullptr;
-    q.ldc = hidden;
+    q.ldc = h_pitch(hidden);
     q.pre = base + s.dpre;
     q.pre_lo = two ? base + s.dpre_lo : nullptr;
     q.ldp = 2 * hidden;
@@ -711,7 +716,7 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
   w.n = hidden;
   w.k = m;
   w.a = {dY, lddy, true, nullptr};
-  w.b = {base + s.h, hidden, true, two ? base + s.h_lo : nullptr};
+  w.b = {base + s.h, h_pitch(hidden), true, two ? base + s.h_lo : nullptr};
   w.c = dW_out;
   w.ldc = lddw_out;
   return in_gradients(m, hidden, k, base + s.dpre, two ? base + s.dpre_lo : nullptr, X, ldx, W_in,

@@ -183,20 +183,22 @@ def test_adapters_index_out_of_the_stack_is_none(ws):
     assert torch.equal(y[none], layers.linear(x, w, workspace=ws)[none])
 
 
+@pytest.mark.parametrize("s", [5, 20])  # in one launch (but pairs), and in two
 @pytest.mark.parametrize("m,n", [(12, 256), (200, 256), (2048, 4096)])
-def test_adapters_keep_to_their_rows(ws, m, n):
+def test_adapters_keep_to_their_rows(ws, m, n, s):
     """An adapter of NaN, one of infinities, rows of NaN: others' rows are as without them."""
     g = gen(5)
-    k, s, r = 192, 5, 16
+    k, r = 192, 16
     x, w = normal(g, "bf16", m, k), normal(g, "bf16", n, k)
     a, b, f = stack(g, "bf16", s, r, n, k)
-    i = indices(g, m, s, "own")
+    i = indices(g, m, 5, "own")
     clean = layers.linear(x, w, layers.Adapters(a, b, f), i, workspace=ws)
     a[1], b[2], b[3] = float("nan"), float("nan"), float("inf")
     x[4] = float("nan")
     y = layers.linear(x, w, layers.Adapters(a, b, f), i, workspace=ws)
     kept = (i == 0) | (i == 4)
     kept[4] = False
+    assert kept.any()
     assert torch.equal(y[kept], clean[kept])
     assert y[4].isnan().all() and y[i == 1].isnan().all() and y[i == 2].isnan().all()
     assert not torch.isfinite(y[i == 3]).any()
