@@ -545,20 +545,31 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     p.stages = c.stages ? c.stages : UINT32_MAX;
     p.limit = c.limit ? c.limit : kMxTimeoutNs;
     p.report = c.report;
-    // As many CTAs to the rows' k as fit the GPU at once, then clusters for the adapters that
-    // the rows may have (as many as one to an SM), then adapters to a pass.
+    // CTAs to share the rows' k (split), clusters to share the adapters (groups), adapters to a
+    // pass: the least estimate of passes one behind another, 2.5 us and 0.25 a stage each, over
+    // what fits the GPU at once (4593 rows, k = 232, 30 adapters of rank 48: 75.8 us with k
+    // split first).
     const int64_t tiles = (m + kLinTile - 1) / kLinTile;
-    p.split = 1;
-    while (p.split < 8 && tiles * p.split * 2 <= 2 * c.sms && p.split * 2 <= p.ksteps) p.split *= 2;
-    const int most = most_adapters(m, *ad);
-    int64_t room = c.sms / (tiles * p.split);
-    if (room < 1) room = 1;
-    const int64_t want = (most + room - 1) / room;
-    p.per = (int)(want < 128 / cols ? want : 128 / cols);
+    const int most = most_adapters(m, *ad), chunks = (q.rank_pad + 127) / 128;
+    double best = 1e30;
+    for (int split = 1; split <= 8 && split <= p.ksteps; split *= 2) {
+      if (split > 1 && tiles * split > 2 * c.sms) break;
+      int64_t room = (split == 8 ? c.sms : 2 * c.sms) / (tiles * split);
+      if (room < 1) room = 1;
+      const int64_t want = (most + room - 1) / room;
+      const int per = (int)(want < 128 / cols ? want : 128 / cols);
+      const int64_t passes = chunks > 1 ? (int64_t)most * chunks : (most + per - 1) / per;
+      const int64_t groups = room < passes ? room : passes;
+      const double us = (double)((passes + groups - 1) / groups) *
+                        (2.5 + 0.25 * ((p.ksteps + split - 1) / split));
+      if (us < best) {
+        best = us;
+        p.split = split;
+        p.per = per;
+        p.groups = (int)groups;
+      }
+    }
     p.idesc = idesc_f16(dtype == SKG_IN_BF16, 128, (uint32_t)(p.per * cols));
-    const int64_t passes = q.rank_pad > 128 ? (int64_t)most * ((q.rank_pad + 127) / 128)
-                                            : (most + p.per - 1) / p.per;
-    p.groups = (int)(room < passes ? room : passes);
     CUtensorMap tx, td;
     if (!map2(&tx, dtype, X, k, m, ldx, kLinK, p.a_rows) || !map_down(&td, dtype, *ad, k, cols))
       return SKG_ERR_CUDA;

@@ -16,17 +16,17 @@ namespace skg {
 namespace {
 
 struct PairAux : LinAux {
-  uint64_t pre[4];  // kLinGrad: a warp's boxes of PRE are there
+  uint64_t pre[8];  // kLinGrad: a warp's two sets of boxes of PRE are there
 };
 
 template <int MODE>
 struct PairCfg {
   static constexpr int STAGE_BYTES = 2 * kLinOperand;
-  // Per epilogue warp: two boxes of 32 rows x 128 bytes on their way out; kLinGrad: two of PRE
-  // on their way in.
-  static constexpr int WARP_STAGING = MODE == kLinGrad ? 16384 : 8192;
+  // Boxes of 32 rows x 128 bytes for each epilogue warp: two on their way out; kLinGated: of H,
+  // gate and up; kLinGrad: two sets of gate and up, in and out, and one of H.
+  static constexpr int WARP_STAGING = 4096 * (MODE == kLinGrad ? 5 : MODE == kLinGated ? 3 : 2);
   static constexpr int STAGING = 4 * WARP_STAGING;
-  static constexpr int STAGES = MODE == kLinGrad ? 5 : 6;
+  static constexpr int STAGES = MODE == kLinGrad ? 4 : MODE == kLinGated ? 5 : 6;
   static constexpr uint32_t SMEM = 1024 + STAGES * STAGE_BYTES + STAGING + 512;
   static_assert(SMEM <= kSmemLimit, "shared memory");
   static_assert(sizeof(PairAux) <= 512, "aux size");
@@ -75,62 +75,169 @@ __device__ __noinline__ void store_rest(void* to, int64_t ld, int m, int n, cons
   }
 }
 
-// kLinGrad: 64 columns of dH (this lane's row: v), of the gate and the other projection (g, u:
-// eight of T each) to boxes of both gradients and of H.
+// 16 values of this lane's row to columns 16 c of its box.
 template <typename T>
-__device__ __forceinline__ void grad_boxes(const LinParams& p, const LinMaps& maps,
-                                           uint8_t* staging, uint32_t& box, int lane, int col,
-                                           int row, const uint32_t (&v)[2][32], uint4 (&g)[8],
-                                           uint4 (&u)[8]) {
-  union Eight {
-    uint4 q;
-    T e[8];
+__device__ __forceinline__ void box_write16(uint8_t* st, int lane, int c, const float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    union {
+      T e[8];
+      uint4 q;
+    } u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u.e[i] = mx_from_f32<T>(v[h * 8 + i]);
+    *reinterpret_cast<uint4*>(st + lane * 128 + (((2 * c + h) ^ (lane & 7)) << 4)) = u.q;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void box_read16(const uint8_t* st, int lane, int c, float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    union {
+      T e[8];
+      uint4 q;
+    } u;
+    u.q = *reinterpret_cast<const uint4*>(st + lane * 128 + (((2 * c + h) ^ (lane & 7)) << 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[h * 8 + i] = mx_to_f32(u.e[i]);
+  }
+}
+
+// The way out of a gated tile and of a gradient's, 16 columns at a time in a loop that is not
+// unrolled: the activations are long, and in straight lines of 64 columns a warp waited for
+// instructions most of the time (the gradient of a 256 x 256 tile 40 to 60 us). `done` once
+// all of the accumulator is read. cols: the tile's columns that are C's.
+template <int ACT, typename T, typename Done>
+__device__ __forceinline__ void gated_out(const LinParams& p, const LinMaps& maps, uint32_t acc,
+                                          uint8_t* mine, uint32_t& box, int lane, int col0,
+                                          int row0, int cols, Done done) {
+  const int count = (cols + 15) / 16;
+  const bool pre = p.pre != nullptr;
+  if (count == 0) {
+    done();
+    return;
+  }
+  uint32_t g[16], u[16], g2[16], u2[16];
+  auto fetch = [&](int i) {
+    const uint32_t at = acc + i * 16;
+    tmem_ld16_async(at, g2);
+    tmem_ld16_async(at + 128, u2);
   };
-  with_act(p.act, [&](auto act) {
-    constexpr int ACT = decltype(act)::value;
-    uint8_t* st = staging + (box & 1) * 4096;
-    ++box;
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
+  uint8_t* hb = mine;
+  fetch(0);
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    tmem_ld_wait16(g2);
+    tmem_ld_wait16(u2);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      Eight a, b, dg, d2, o;
-      a.q = g[j];
-      b.q = u[j];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float dh = __uint_as_float(v[j >> 2][(j & 3) * 8 + i]);
-        const LinGrad r = ACT == SKG_ACT_GELU ? lin_grad_gelu(dh, mx_to_f32(a.e[i]), mx_to_f32(b.e[i]))
-                                              : lin_grad<ACT>(dh, mx_to_f32(a.e[i]), mx_to_f32(b.e[i]));
-        dg.e[i] = mx_from_f32<T>(r.dg);
-        d2.e[i] = mx_from_f32<T>(r.du);
-        o.e[i] = mx_from_f32<T>(r.h);
+    for (int j = 0; j < 16; ++j) {
+      g[j] = g2[j];
+      u[j] = u2[j];
+    }
+    if (i + 1 < count) fetch(i + 1);
+    else done();
+    if ((i & 3) == 0) {  // boxes whose stores have read them
+      if (!pre) hb = mine + (box++ & 1) * 4096;
+      if (lane == 0) {
+        if (pre) bulk_wait_read<0>();
+        else bulk_wait_read<1>();
       }
-      *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = dg.q;
-      g[j] = d2.q;
-      u[j] = o.q;
+      __syncwarp();
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(&maps.gate, st, col, row);
-      bulk_commit();
+    float h[16], a[16], b[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      a[j] = __uint_as_float(g[j]);
+      b[j] = __uint_as_float(u[j]);
+      h[j] = lin_gated<ACT>(a[j], b[j]);
     }
-  });
+    box_write16<T>(hb, lane, i & 3, h);
+    if (pre) {
+      box_write16<T>(mine + 4096, lane, i & 3, a);
+      box_write16<T>(mine + 8192, lane, i & 3, b);
+    }
+    if ((i & 3) == 3 || i + 1 == count) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int col = col0 + (i >> 2) * 64;
+        tma_store_2d(&maps.c, hb, col, row0);
+        if (pre) {
+          tma_store_2d(&maps.gate, mine + 4096, col, row0);
+          tma_store_2d(&maps.pre_up, mine + 8192, col, row0);
+        }
+        bulk_commit();
+      }
+    }
+  }
+}
+
+// PRE of 64 columns to a warp's set number `pres` & 1 of boxes.
+__device__ __forceinline__ void fetch_pre(const LinMaps& maps, PairAux* aux, uint8_t* mine, int q,
+                                          uint32_t pres, int col, int row0) {
+  uint8_t* set = mine + (pres & 1u) * 8192;
+  uint64_t* bar = &aux->pre[q * 2 + (pres & 1u)];
+  fence_proxy_async_smem();
+  mbar_arrive_expect_tx(bar, 8192);
+  tma_load_2d(set, &maps.t, bar, col, row0);
+  tma_load_2d(set + 4096, &maps.up, bar, col, row0);
+}
+
+template <int ACT, typename T, typename Done>
+__device__ __forceinline__ void grad_out(const LinParams& p, const LinMaps& maps, PairAux* aux,
+                                         uint32_t acc, uint8_t* mine, uint32_t& pres, int q,
+                                         int lane, int col0, int row0, int cols, Done done) {
+  const int count = (cols + 15) / 16;
+  if (count == 0) {
+    done();
+    return;
+  }
+  uint32_t v[16], v2[16];
+  uint8_t* set = mine;
+  uint8_t* hb = mine + 16384;
+  tmem_ld16_async(acc, v2);
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    tmem_ld_wait16(v2);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    uint8_t* st = staging + (box & 1) * 4096;
-    ++box;
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
+    for (int j = 0; j < 16; ++j) v[j] = v2[j];
+    if (i + 1 < count) tmem_ld16_async(acc + (i + 1) * 16, v2);
+    else done();
+    if ((i & 3) == 0) {
+      if (!mx_wait(&aux->pre[q * 2 + (pres & 1u)], (pres >> 1) & 1u, aux, true)) lin_fail(p, aux);
+      set = mine + (pres & 1u) * 8192;
+      ++pres;
+      // The other set and H's box: their stores have read them. PRE of the next 64 columns
+      // comes while these are worked on.
+      if (lane == 0) {
+        bulk_wait_read<0>();
+        if (i + 4 < count) fetch_pre(maps, aux, mine, q, pres, col0 + (i >> 2) * 64 + 64, row0);
+      }
+      __syncwarp();
+    }
+    float g[16], u[16], h[16];
+    box_read16<T>(set, lane, i & 3, g);
+    box_read16<T>(set + 4096, lane, i & 3, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = k ? u[j] : g[j];
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(k ? &maps.c : &maps.pre_up, st, col, row);
-      bulk_commit();
+    for (int j = 0; j < 16; ++j) {
+      const LinGrad r = lin_grad<ACT>(__uint_as_float(v[j]), g[j], u[j]);
+      g[j] = r.dg;
+      u[j] = r.du;
+      h[j] = r.h;
+    }
+    box_write16<T>(set, lane, i & 3, g);
+    box_write16<T>(set + 4096, lane, i & 3, u);
+    box_write16<T>(hb, lane, i & 3, h);
+    if ((i & 3) == 3 || i + 1 == count) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int col = col0 + (i >> 2) * 64;
+        tma_store_2d(&maps.gate, set, col, row0);
+        tma_store_2d(&maps.pre_up, set + 4096, col, row0);
+        tma_store_2d(&maps.c, hb, col, row0);
+        bulk_commit();
+      }
     }
   }
 }
@@ -186,7 +293,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     mbar_init(&aux->tempty, 8);  // the epilogue warps of both CTAs
     mbar_init(&aux->tempty1, 8);
     mbar_init(&aux->drain, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&aux->pre[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&aux->pre[i], 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -399,80 +506,45 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
       const int row0 = (2 * tm + rank) * kLinTile + q * 32, col0 = tn * TILE_N;
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (n & 1) * 256;
       const bool live = row0 < pm;
-      // kLinGrad: PRE of 64 columns comes while the 64 before them (or the MMAs) are worked on.
-      auto fetch_pre = [&](int col) {
-        if constexpr (MODE == kLinGrad) {
-          if (live && col < pn && lane == 0) {
-            fence_proxy_async_smem();
-            mbar_arrive_expect_tx(&aux->pre[q], 8192);
-            tma_load_2d(mine + 8192, &maps.t, &aux->pre[q], col, row0);
-            tma_load_2d(mine + 12288, &maps.up, &aux->pre[q], col, row0);
-          }
-        }
-      };
-      fetch_pre(col0);
+      // (PRE's first 64 columns come while the MMAs are under way.)
+      const int cols = live ? min(TILE_N, pn - col0) : 0;
+      if (MODE == kLinGrad && cols > 0 && lane == 0)
+        fetch_pre(maps, aux, mine, q, pres, col0, row0);
+      __syncwarp();
       const bool got = mx_wait(&aux->tfull[n & 1], (uint32_t)(n >> 1) & 1u, aux);
       if (!got) lin_fail(p, aux);
       if (!__all_sync(0xffffffffu, got)) {
         // (What fetch_pre asked for lands before the CTA leaves.)
-        if (MODE == kLinGrad && live && col0 < pn) mx_wait(&aux->pre[q], pres & 1u, aux, true);
+        if (MODE == kLinGrad && cols > 0)
+          mx_wait(&aux->pre[q * 2 + (pres & 1u)], (pres >> 1) & 1u, aux, true);
         break;
       }
       tc_fence_after();
-      // Four pieces of 64 accumulator columns: 64 columns of C each; gated: the gate's 64,
-      // then the other projection's 64 of the same outputs.
-      uint32_t v[2][2][32];
-      auto fetch = [&](int s) {
-        const int c = G ? (s & 1) * 128 + (s >> 1) * 64 : s * 64;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) tmem_ld32_async(acc + c + i * 32, v[s & 1][i]);
-      };
       auto hand_over = [&]() {  // all of the tile is in registers
         tc_fence_before();
         __syncwarp();
         if (lane == 0)
           mbar_arrive_remote(cluster_addr((n & 1) ? &aux->tempty1 : &aux->tempty, 0u));
       };
-      auto value = [&](int b, int i) { return __uint_as_float(v[b][i >> 5][i & 31]); };
-      fetch(0);
-      fetch(1);
       if constexpr (G) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            tmem_ld_wait32(v[b][0]);
-            tmem_ld_wait32(v[b][1]);
-          }
-          if (s == 1) hand_over();
-          const int col = col0 + s * 64;
-          if (live && col < pn) {
-            if (p.pre) {
-              store_box<T>(&maps.gate, mine, box, lane, col, row0,
-                           [&](int i) { return value(0, i); });
-              store_box<T>(&maps.pre_up, mine, box, lane, col, row0,
-                           [&](int i) { return value(1, i); });
-            }
-            with_act(p.act, [&](auto act) {
-#pragma unroll
-              for (int i = 0; i < 64; i += 4) {
-                const float4 h = lin_gated4<decltype(act)::value>(
-                    make_float4(value(0, i), value(0, i + 1), value(0, i + 2), value(0, i + 3)),
-                    make_float4(value(1, i), value(1, i + 1), value(1, i + 2), value(1, i + 3)));
-                v[0][i >> 5][i & 31] = __float_as_uint(h.x);
-                v[0][i >> 5][(i & 31) + 1] = __float_as_uint(h.y);
-                v[0][i >> 5][(i & 31) + 2] = __float_as_uint(h.z);
-                v[0][i >> 5][(i & 31) + 3] = __float_as_uint(h.w);
-              }
-            });
-            store_box<T>(&maps.c, mine, box, lane, col, row0, [&](int i) { return value(0, i); });
-          }
-          if (s == 0) {
-            fetch(2);
-            fetch(3);
-          }
-        }
+        with_act(p.act, [&](auto act) {
+          gated_out<decltype(act)::value, T>(p, maps, acc, mine, box, lane, col0, row0, cols,
+                                             hand_over);
+        });
+      } else if constexpr (MODE == kLinGrad) {
+        with_act(p.act, [&](auto act) {
+          grad_out<decltype(act)::value, T>(p, maps, aux, acc, mine, pres, q, lane, col0, row0,
+                                            cols, hand_over);
+        });
       } else {
+        // Four pieces of 64 columns.
+        uint32_t v[2][2][32];
+        auto fetch = [&](int s) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) tmem_ld32_async(acc + s * 64 + i * 32, v[s & 1][i]);
+        };
+        fetch(0);
+        fetch(1);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           tmem_ld_wait32(v[s & 1][0]);
@@ -480,26 +552,12 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           const int col = col0 + s * 64;
           if (s == 3) hand_over();
           if (live && col < pn) {
-            if constexpr (MODE == kLinGrad) {
-              uint4 g[8], u[8];
-              if (!mx_wait(&aux->pre[q], pres & 1u, aux, true)) lin_fail(p, aux);
-              ++pres;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int at = lane * 128 + ((j ^ (lane & 7)) << 4);
-                g[j] = *reinterpret_cast<const uint4*>(mine + 8192 + at);
-                u[j] = *reinterpret_cast<const uint4*>(mine + 12288 + at);
-              }
-              __syncwarp();
-              if (s < 3) fetch_pre(col + 64);
-              grad_boxes<T>(p, maps, mine, box, lane, col, row0, v[s & 1], g, u);
-            } else {
-              const uint8_t* st = store_box<T>(second ? &maps.pre_up : &maps.c, mine, box, lane,
-                                               col, row0, [&](int i) { return value(s & 1, i); });
-              if ((pn & 7) && col + 64 > (pn & ~7))
-                store_rest<T>(second ? p.second.c : p.c, second ? p.second.ldc : p.ldc, pm, pn, st,
-                              lane, col, row0);
-            }
+            const uint8_t* st =
+                store_box<T>(second ? &maps.pre_up : &maps.c, mine, box, lane, col, row0,
+                             [&](int i) { return __uint_as_float(v[s & 1][i >> 5][i & 31]); });
+            if ((pn & 7) && col + 64 > (pn & ~7))
+              store_rest<T>(second ? p.second.c : p.c, second ? p.second.ldc : p.ldc, pm, pn, st,
+                            lane, col, row0);
           }
           if (s < 2) fetch(s + 2);
         }
