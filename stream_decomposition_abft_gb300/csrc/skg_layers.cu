@@ -175,13 +175,14 @@ bool map_operand(CUtensorMap* t, int dtype, const Operand& o, const void* p, int
 // and the CTA's stages of k, at 0.2 us where all clusters find an SM for each CTA and 0.44
 // where two CTAs share one (333 x 2048 x 2048: 10.4, 8.0, 10.3 with S = 1, 2, 4: 48, 96, 192
 // CTAs). Larger clusters find less room, as a GPC's SMs do not divide by them: 128 x 2048 x
-// 2048, 16 tiles, takes 6.8, 6.5, 8.6 with S = 4, 6, 8.
+// 2048, 16 tiles, takes 6.8, 6.5, 8.6 with S = 4, 6, 8. `out`: what the activations of a whole
+// tile take, which the CTAs of a cluster share.
 struct SinglePlan {
   int split;
   bool deep;
   double us;
 };
-SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms) {
+SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms, double out) {
   constexpr double kFixed[9] = {0, 4.4, 4.9, 5.1, 5.3, 0, 5.6, 0, 5.7};
   SinglePlan best = {1, false, 1e30};
   for (int s : {1, 2, 3, 4, 6, 8}) {
@@ -190,8 +191,9 @@ SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms) {
     if ((s == 3 || s == 6) && (m <= 16 || !deep)) continue;
     const int stages = (ksteps + s - 1) / s;
     const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
-    const double us = deep ? kFixed[s] + 0.2 * stages
-                           : (s == 1 ? 3.2 : s == 8 ? 9.0 : 6.5) + 0.436 * (double)waves * stages;
+    const double us =
+        out / s + (deep ? kFixed[s] + 0.2 * stages
+                        : (s == 1 ? 3.2 : s == 8 ? 9.0 : 6.5) + 0.436 * (double)waves * stages);
     if (m <= 16 || us < best.us) best = {s, deep, us};
   }
   return best;
@@ -201,10 +203,11 @@ SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms) {
 // product but cannot share a tile's k. Up to 128 rows the single CTAs win at every n and k;
 // beyond, the lower estimate: 0.262 us a stage, 0.29 where the power limit lowers the clock
 // (1024 x 2048 x 2048: 12.9 us paired, 10.8 single; 1024 x 8192 x 1024: 13.8 and 19.9).
-bool wants_pairs(int64_t m, int64_t tiles, int ksteps, int clusters, double single_us) {
+bool wants_pairs(int64_t m, int64_t tiles, int ksteps, int clusters, double single_us,
+                 double out) {
   if (m <= kLinTile) return false;
   const int64_t waves = (tiles + clusters - 1) / clusters;
-  return 4.2 + (waves > 1 ? 0.29 : 0.262) * (double)waves * ksteps <= single_us;
+  return 4.2 + out + (waves > 1 ? 0.29 : 0.262) * (double)waves * ksteps <= single_us;
 }
 
 // How a product runs.
@@ -220,10 +223,11 @@ Choice choose(const Product& q, const Common& c) {
   const int steps = (int)((q.k + kLinK - 1) / kLinK) * (q.a.lo || q.b.lo ? 2 : 1);
   Choice h = {};
   h.resident = lin_pair_clusters_resident();
-  const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms);
+  const double out = q.mode == kLinGrad ? 2.0 : q.mode == kLinGated ? 0.5 : 0.0;
+  const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms, out);
   // (The low parts of H and DPRE are written by single CTAs; up to 128 rows they run.)
   h.pair = h.resident > 0 && q.n >= 8 && !q.c_lo &&
-           wants_pairs(q.m, tm2 * tn2, steps, h.resident, single.us);
+           wants_pairs(q.m, tm2 * tn2, steps, h.resident, single.us, 2.0 * out);
   h.tiles_m = h.pair ? tm2 : tm1;
   h.tiles_n = h.pair ? tn2 : tn1;
   h.split = h.pair ? 1 : single.split;

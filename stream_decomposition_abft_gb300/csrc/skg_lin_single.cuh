@@ -22,8 +22,8 @@ __device__ __forceinline__ void finish4(const LinParams& p, int row, int col, co
                                         const float4& u, uint2 g_in, uint2 u_in) {
   T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
   if constexpr (MODE == kLinGated) {
-    const float4 o = lin_gated4<ACT>(v, u);
-    const float h[4] = {o.x, o.y, o.z, o.w};
+    const float h[4] = {lin_gated<ACT>(v.x, u.x), lin_gated<ACT>(v.y, u.y),
+                        lin_gated<ACT>(v.z, u.z), lin_gated<ACT>(v.w, u.w)};
     write4<T>(c, h, p.n - col);
     if (p.pre) {
       T* g = reinterpret_cast<T*>(p.pre) + (int64_t)row * p.ldp + col;
@@ -42,8 +42,7 @@ __device__ __forceinline__ void finish4(const LinParams& p, int row, int col, co
     float dg[4], du[4], h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = mx_to_f32(g.e[i]), b = mx_to_f32(w.e[i]);
-      const LinGrad r = ACT == SKG_ACT_GELU ? lin_grad_gelu(d[i], a, b) : lin_grad<ACT>(d[i], a, b);
+      const LinGrad r = lin_grad<ACT>(d[i], mx_to_f32(g.e[i]), mx_to_f32(w.e[i]));
       dg[i] = r.dg;
       du[i] = r.du;
       h[i] = r.h;
@@ -157,16 +156,22 @@ __device__ __forceinline__ void keep_rows(uint32_t tmem, int q, int lane, float*
 template <int MODE, int ACT, typename T>
 __device__ __forceinline__ void tile_out_as(const LinParams& p, const float* part, int warp, int lane,
                                          int rank, int tm, int tn, bool fine) {
+  constexpr int W = kLinThreads / 32;
   if (p.split == 1) {
-    // A warp writes the 32 rows that its own lanes stored.
-    const int q = warp & 3;
-    if (warp >= 2 && warp < kLinLoader && fine)
-      reduce_rows<MODE, ACT, T, 1>(p, part, 0, 1, lane, q * 32, q * 32 + 32, tm, tn);
+    if constexpr (MODE == kLinPlain) {
+      // A warp writes the 32 rows that its own lanes stored.
+      const int q = warp & 3;
+      if (warp >= 2 && warp < kLinLoader && fine)
+        reduce_rows<MODE, ACT, T, 1>(p, part, 0, 1, lane, q * 32, q * 32 + 32, tm, tn);
+    } else {
+      // The activations take longer than a barrier: all warps share the rows.
+      __syncthreads();
+      if (fine) reduce_rows<MODE, ACT, T, 1>(p, part, warp, W, lane, 0, kLinTile, tm, tn);
+    }
     return;
   }
   cluster_sync();
   if (fine) {
-    constexpr int W = kLinThreads / 32;
     if (p.split == 2) reduce_rows<MODE, ACT, T, 2>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
     else if (p.split == 3) reduce_rows<MODE, ACT, T, 3>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
     else if (p.split == 6) reduce_rows<MODE, ACT, T, 6>(p, part, warp, W, lane, rank, kLinTile, tm, tn);
