@@ -63,7 +63,8 @@ __device__ __forceinline__ void store8(T* hi, T* lo, const float (&v)[8]) {
   if (lo) *reinterpret_cast<uint4*>(lo) = l.q;
 }
 
-// Eight elements of a row per thread; reads and writes each element once, so memory bounds it.
+// Eight elements of a row per thread; reads and writes each element once, so memory bounds it
+// (4096 x 8192: 336 MB, 5 % of the gradient that it begins).
 template <typename T, int ACT>
 __global__ void __launch_bounds__(128) dgate_kernel(const DgateParams p) {
   griddep_wait();

@@ -8,6 +8,15 @@
 // TMEM lane, 128 columns apart. Adapters as in skg_lin_single.cu: more stages of k for each
 // adapter that the tile's 256 rows use, with the other rows left out of the MMA.
 //
+// Operands stored along k or along their rows are read in place (MN-major boxes of 64 x 64).
+// Two weight gradients of the same k share a launch.
+//
+// What bounds it: the MMAs under the power limit. 4096 x 8192 -> 28672 gated in bf16 takes
+// 1.91 to 1.99 ms in short runs and 2.19 in long ones (2.0 and 1.76 PFLOP/s); the tensor pipe
+// is busy 93 % of the time at 2048 x 8192 -> 8192 (94 to 97 % in the gradients' products,
+// 72 % with PRE, both gradients and H on the way out, whose 256 tiles take four rounds of 76
+// pairs where 3.4 would do). Few tiles: a stage of k is 0.262 us, 502 of its 512 cycles MMAs.
+//
 // What the waits' bounds and the way out share with the block-scaled product's pairs is
 // explained there (skg_mx_gemm_pair.cu).
 #include "skg_lin.cuh"

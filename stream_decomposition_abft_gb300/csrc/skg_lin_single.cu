@@ -17,6 +17,14 @@
 // (griddepcontrol.wait) and brings the tile's adapters to shared memory, so t is formed while
 // W streams.
 //
+// What bounds it: with few rows the weights' bytes (1 x 8192 -> 28672 gated, 940 MB: 135 to
+// 139 us, 6.8 to 7.0 TB/s; 1 x 8192 x 8192 23 us, 5.8 TB/s with the ramp and the tail of one
+// wave); with more rows and few tiles launch, first loads and the sum over the cluster (128 x
+// 1024 x 1024 5.6 us, of which two stages of k alone take 5.3); long k a stage's MMAs, 0.19 us
+// for 64 of k where 256 cycles would be 0.13 (both operands of an M = N = 128 MMA come from
+// shared memory; the pairs' M = N = 256 do not wait for them). Rows of k that are not whole
+// 32-byte sectors take 0.43 us a stage (k = 2200 against 2208: 16.4 and 11.3 us with 35).
+//
 // Every wait is bounded; when one runs out the CTA records SKG_ERR_PIPELINE_TIMEOUT in the
 // report, waits for its own copies and MMAs, still meets the cluster's barriers, frees its
 // TMEM and leaves.

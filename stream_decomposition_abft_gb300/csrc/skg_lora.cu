@@ -14,9 +14,11 @@
 // distributed shared memory (no atomics, the same result every time). t is stored as the sum
 // of two numbers of x's type, so that the product with B_s loses nothing to its rounding.
 //
-// What bounds it: x once from HBM for prompts (8192 x 8192: 134 MB, 20 us, under the product
-// behind it, which takes 20 times as long); a few microseconds of latency for a decode
-// batch, which pass while the product streams W (it waits for t only where it needs it).
+// What bounds it: for prompts x, once from HBM (2048 x 8192, three adapters of rank 64: 23 us
+// alone; the product behind it takes 163, and 8192 x 8192 x 8192 with eight adapters in
+// segments 609 us against 600 without); for a decode batch latency, much of which passes while
+// the product streams W, for which it waits only where it needs t (64 x 8192 x 8192, 64
+// adapters of rank 16: 37.8 us against 25.8 without any; their 34 MB alone are 5).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -300,6 +300,71 @@ def test_feed_forward_backward(ws, kind, m, f, k):
         check(t, *want[what], what=what)
 
 
+@pytest.mark.parametrize("m,f,k", [(20000, 8, 16), (5000, 8, 264), (3000, 520, 8), (300, 4096, 8),
+                                   (130, 8, 4096), (1, 8, 8192), (128, 4096, 8)])
+def test_narrow(ws, m, f, k):
+    """Sizes far apart: one column of tiles, long sums of tiny results."""
+    g = gen(m + k)
+    x, w = normal(g, "bf16", m, k), normal(g, "bf16", 2 * f, k, scale=k ** -0.5)
+    wo, dy = normal(g, "bf16", k, f, scale=f ** -0.5), normal(g, "bf16", m, k, scale=0.1)
+    h, hb, pre, pb = ref.gated(x, w, "gelu")
+    got, kept = layers.gated(x, w, "gelu", save=True, workspace=ws)
+    check(got, h, hb, "h")
+    check(kept, pre, pb, "pre")
+    want = ref.backward(x, w, kept, "gelu", dy=dy, w_out=wo)
+    for what, t in zip(("dx", "dw_in", "dw_out"),
+                       layers.feed_forward_backward(dy, x, w, wo, kept, "gelu", workspace=ws)):
+        check(t, *want[what], what=what)
+    want = ref.backward(x, w, kept, "gelu", dh=got)
+    for what, t in zip(("dx", "dw_in"), layers.gated_backward(got, x, w, kept, "gelu", workspace=ws)):
+        check(t, *want[what], what=what)
+
+
+def test_non_finite_stays_in_its_row(ws):
+    """A token of infinities or NaN: other tokens' results are as without it."""
+    for m, f, k in ((5, 64, 72), (300, 136, 200), (2048, 2048, 512)):
+        g = gen(m)
+        x, w = normal(g, "bf16", m, k), normal(g, "bf16", 2 * f, k, scale=k ** -0.5)
+        wo, dy = normal(g, "bf16", k, f, scale=f ** -0.5), normal(g, "bf16", m, k)
+        h, pre = layers.gated(x, w, save=True, workspace=ws)
+        dx = layers.feed_forward_backward(dy, x, w, wo, pre, workspace=ws)[0]
+        for bad in (float("nan"), float("inf")):
+            xb, db, pb = x.clone(), dy.clone(), pre.clone()
+            xb[3], db[2], pb[1, 0] = bad, bad, bad
+            hb = layers.gated(xb, w, workspace=ws)
+            assert torch.equal(hb[:3], h[:3]) and torch.equal(hb[4:], h[4:])
+            assert not torch.isfinite(hb[3]).any()
+            dxb = layers.feed_forward_backward(db, x, w, wo, pb, workspace=ws)[0]
+            assert torch.equal(dxb[0], dx[0]) and torch.equal(dxb[3:], dx[3:])
+            assert not torch.isfinite(dxb[1:3]).all()
+
+
+def test_single_rows_and_columns(ws):
+    """Tensors of one row with any stride, views of larger ones, expanded ones refused."""
+    from stream_decomposition_abft_gb300.skgemm import SkgError
+    g = gen(8)
+    big = normal(g, "bf16", 9, 203)
+    w = normal(g, "bf16", 16, 200)
+    x = big[0:1, :200]
+    check(layers.linear(x, w, workspace=ws), *ref.linear(x, w))
+    with pytest.raises(SkgError, match="unsupported"):
+        layers.linear(big[:, :200], w, workspace=ws)  # rows off 16-byte boundaries
+    with pytest.raises(SkgError, match="unsupported"):
+        layers.linear(big[0:1, 1:201], w, workspace=ws)
+    with pytest.raises(SkgError, match="argument"):
+        layers.linear(x.expand(4, 200), w, workspace=ws)
+    with pytest.raises(SkgError, match="unsupported"):
+        layers.gated(x, normal(g, "bf16", 24, 200), workspace=ws)  # hidden 12
+    one = normal(g, "bf16", 1, 200)
+    with pytest.raises(ValueError, match="index"):
+        layers.linear(x, w, layers.Adapters(one.expand(1, 8, 200), w[:, :8][None]),
+                      torch.zeros(1, dtype=torch.int64, device="cuda"), workspace=ws)
+    with pytest.raises(ValueError, match="belongs to adapters"):
+        layers.linear(x, w, index=torch.zeros(1, dtype=torch.int32, device="cuda"), workspace=ws)
+    with pytest.raises(ValueError, match="tensor is wanted"):
+        layers.linear(x, w, layers.Adapters(w[None, :8], w[:, :8][None]), workspace=ws)
+
+
 def test_backward_strides(ws):
     g = gen(9)
     m, f, k = 140, 72, 203
