@@ -216,6 +216,7 @@ struct Choice {
   bool pair, deep;
   int64_t tiles_m, tiles_n;
   int split, resident;
+  double us;  // single CTAs: the estimate
 };
 Choice choose(const Product& q, const Common& c) {
   const int64_t cols = q.mode == kLinGated ? 2 * q.n : q.n;  // of the accumulators
@@ -233,6 +234,7 @@ Choice choose(const Product& q, const Common& c) {
   h.tiles_n = h.pair ? tn2 : tn1;
   h.split = h.pair ? 1 : single.split;
   h.deep = !h.pair && single.deep;
+  h.us = single.us;
   return h;
 }
 
@@ -242,10 +244,54 @@ int most_adapters(int64_t m, const skg_adapters_t& ad) {
   return ad.count < rows ? ad.count : rows;
 }
 
-// Whether a product with adapters is one launch (skg_lin_adapted.cu).
+// Whether a product with adapters is one launch (skg_lin_adapted.cu). With more than 16 rows
+// the columns of x A^T cost a stage up to 0.1 us, which long ranges of k add up to more than
+// the second launch takes (64 x 8192 x 8192, adapters of rank 16: one 27.7 in one launch, 29 in
+// two; eight 37.9 and 33.1).
 bool one_launch(const Product& q, const Choice& h) {
-  return q.adapters && !h.pair && (q.m <= 16 || h.deep) &&
-         lin_adapted_fits(most_adapters(q.m, *q.adapters), q.rank_pad);
+  if (!q.adapters || h.pair) return false;
+  const int most = most_adapters(q.m, *q.adapters);
+  if (!lin_adapted_fits(most, q.rank_pad)) return false;
+  const double stages = (double)((q.k + kLinK - 1) / kLinK) / h.split;
+  return q.m <= 16 || (h.deep && 0.1 * stages * most * q.rank_pad / 128 <= 3.0);
+}
+
+// skg_lora.cu's CTAs: to share the rows' k (split), clusters to share the adapters (groups),
+// adapters to a pass: the least estimate of passes one behind another, 2.5 us and 0.25 a stage
+// each, over what fits the GPU at once (4593 rows, k = 232, 30 adapters of rank 48: 75.8 us with
+// k split first, 38 so).
+//
+// A product behind it whose CTAs take an SM each begins everywhere at once where this kernel
+// leaves it as many SMs. That pays while its few CTAs are done by half of the product's time
+// (64 x 8192 x 8192, eight adapters of rank 16: 33.1 -> 28.3 us, 25.4 without adapters; 64
+// adapters 41.6 -> 53).
+void share_out(LoraParams& p, int cols, int most, const Choice& h, int sms) {
+  const int64_t tiles = (p.m + kLinTile - 1) / kLinTile;
+  const int chunks = (p.rank_pad + 127) / 128;
+  auto least = [&](int64_t ctas) {
+    double best = 1e30;
+    for (int split = 1; split <= 8 && split <= p.ksteps; split *= 2) {
+      const int64_t most_ctas = split == 8 && ctas > sms ? sms : ctas;
+      if (split > 1 && tiles * split > most_ctas) break;
+      int64_t room = most_ctas / (tiles * split);
+      if (room < 1) room = 1;
+      const int64_t want = (most + room - 1) / room;
+      const int per = (int)(want < 128 / cols ? want : 128 / cols);
+      const int64_t passes = chunks > 1 ? (int64_t)most * chunks : (most + per - 1) / per;
+      const int64_t groups = room < passes ? room : passes;
+      const double us = (double)((passes + groups - 1) / groups) *
+                        (2.5 + 0.25 * ((p.ksteps + split - 1) / split));
+      if (us < best) {
+        best = us;
+        p.split = split;
+        p.per = per;
+        p.groups = (int)groups;
+      }
+    }
+    return best;
+  };
+  const int64_t beside = h.deep ? sms - h.tiles_m * h.tiles_n * h.split : 0;
+  if (beside < tiles || least(beside) > 0.5 * h.us) least(2 * (int64_t)sms);
 }
 
 bool map_down(CUtensorMap* t, int dtype, const skg_adapters_t& ad, int64_t k, int box_rows) {
@@ -550,30 +596,7 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     p.stages = c.stages ? c.stages : UINT32_MAX;
     p.limit = c.limit ? c.limit : kMxTimeoutNs;
     p.report = c.report;
-    // CTAs to share the rows' k (split), clusters to share the adapters (groups), adapters to a
-    // pass: the least estimate of passes one behind another, 2.5 us and 0.25 a stage each, over
-    // what fits the GPU at once (4593 rows, k = 232, 30 adapters of rank 48: 75.8 us with k
-    // split first).
-    const int64_t tiles = (m + kLinTile - 1) / kLinTile;
-    const int most = most_adapters(m, *ad), chunks = (q.rank_pad + 127) / 128;
-    double best = 1e30;
-    for (int split = 1; split <= 8 && split <= p.ksteps; split *= 2) {
-      if (split > 1 && tiles * split > 2 * c.sms) break;
-      int64_t room = (split == 8 ? c.sms : 2 * c.sms) / (tiles * split);
-      if (room < 1) room = 1;
-      const int64_t want = (most + room - 1) / room;
-      const int per = (int)(want < 128 / cols ? want : 128 / cols);
-      const int64_t passes = chunks > 1 ? (int64_t)most * chunks : (most + per - 1) / per;
-      const int64_t groups = room < passes ? room : passes;
-      const double us = (double)((passes + groups - 1) / groups) *
-                        (2.5 + 0.25 * ((p.ksteps + split - 1) / split));
-      if (us < best) {
-        best = us;
-        p.split = split;
-        p.per = per;
-        p.groups = (int)groups;
-      }
-    }
+    share_out(p, cols, most_adapters(m, *ad), choose(q, c), c.sms);
     p.idesc = idesc_f16(dtype == SKG_IN_BF16, 128, (uint32_t)(p.per * cols));
     CUtensorMap tx, td;
     if (!map2(&tx, dtype, X, k, m, ldx, kLinK, p.a_rows) || !map_down(&td, dtype, *ad, k, cols))
