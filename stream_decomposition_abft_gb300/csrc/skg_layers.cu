@@ -200,15 +200,14 @@ SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms, double out
   return best;
 }
 
-// Whether a product runs on CTA pairs, whose 256 x 256 tiles halve what each SM reads per
+// The estimate of a product on CTA pairs, whose 256 x 256 tiles halve what each SM reads per
 // product but cannot share a tile's k. Up to 128 rows the single CTAs win at every n and k;
 // beyond, the lower estimate: 0.262 us a stage, 0.29 where the power limit lowers the clock
 // (1024 x 2048 x 2048: 12.9 us paired, 10.8 single; 1024 x 8192 x 1024: 13.8 and 19.9).
-bool wants_pairs(int64_t m, int64_t tiles, int ksteps, int clusters, double single_us,
-                 double out) {
-  if (m <= kLinTile) return false;
+double pair_us(int64_t m, int64_t tiles, int ksteps, int clusters, double out) {
+  if (m <= kLinTile) return 1e30;
   const int64_t waves = (tiles + clusters - 1) / clusters;
-  return 4.2 + out + (waves > 1 ? 0.29 : 0.262) * (double)waves * ksteps <= single_us;
+  return 4.2 + out + (waves > 1 ? 0.29 : 0.262) * (double)waves * ksteps;
 }
 
 // How a product runs.
@@ -216,7 +215,7 @@ struct Choice {
   bool pair, deep;
   int64_t tiles_m, tiles_n;
   int split, resident;
-  double us;  // single CTAs: the estimate
+  double us;  // the estimate
 };
 Choice choose(const Product& q, const Common& c) {
   const int64_t cols = q.mode == kLinGated ? 2 * q.n : q.n;  // of the accumulators
@@ -228,13 +227,15 @@ Choice choose(const Product& q, const Common& c) {
   const double out = q.mode == kLinGrad ? 2.0 : q.mode == kLinGated ? 0.5 : 0.0;
   const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms, out);
   // (The low parts of H and DPRE are written by single CTAs; up to 128 rows they run.)
-  h.pair = h.resident > 0 && q.n >= 8 && !q.c_lo &&
-           wants_pairs(q.m, tm2 * tn2, steps, h.resident, single.us, 2.0 * out);
+  const double paired = h.resident > 0 && q.n >= 8 && !q.c_lo
+                            ? pair_us(q.m, tm2 * tn2, steps, h.resident, 2.0 * out)
+                            : 1e30;
+  h.pair = paired <= single.us;
   h.tiles_m = h.pair ? tm2 : tm1;
   h.tiles_n = h.pair ? tn2 : tn1;
   h.split = h.pair ? 1 : single.split;
   h.deep = !h.pair && single.deep;
-  h.us = single.us;
+  h.us = h.pair ? paired : single.us;
   return h;
 }
 
@@ -482,33 +483,125 @@ BackwardScratch backward_scratch(int64_t m, int64_t f, bool block) {
   return s;
 }
 
-// dX = dPRE W (m x k), dW = dPRE^T X (2 f x k) and a second weight gradient (or NULL), which
-// shares the launch where both run on pairs (512 tokens, 1024 and 2816 wide: two launches of
-// 88 and 44 tiles on 76 pairs).
+// Plain products with N-major B in one launch of single CTAs, the first one's tiles shared by
+// `split` CTAs each.
+skg_status_t run_group(const Product* const* jobs, int count, int split, const Common& c) {
+  LinGroup p = {};
+  LinGroupMaps t;
+  int64_t clusters = 0;
+  p.split = split;
+  for (int j = 0; j < 3; ++j) {
+    p.first[j] = (int)clusters;
+    const Product& q = *jobs[j < count ? j : 0];
+    if (j < count) {
+      LinJob& w = p.job[j];
+      w.m = (int)q.m;
+      w.n = (int)q.n;
+      w.k = (int)q.k;
+      w.ksteps = (int)((q.k + kLinK - 1) / kLinK);
+      w.terms = q.a.lo || q.b.lo ? 2 : 1;
+      w.lo_b = q.b.lo != nullptr;
+      w.a_mn = q.a.mn;
+      w.tiles_m = (int)((q.m + 127) / 128);
+      w.tiles_n = (int)((q.n + 127) / 128);
+      w.idesc = idesc_f16(c.dtype == SKG_IN_BF16, 128, 128) | ((uint32_t)q.a.mn << 15) | (1u << 16);
+      w.c = q.c;
+      w.ldc = ld_of(q.ldc, q.m, q.n);
+      const int64_t tiles = (int64_t)w.tiles_m * w.tiles_n;
+      clusters += j == 0 ? tiles : (tiles + split - 1) / split;
+    }
+    if (!map_operand(&t.a[j], c.dtype, q.a, q.a.p, q.m, q.k, 128) ||
+        !map_operand(&t.b[j], c.dtype, q.b, q.b.p, q.n, q.k, 128))
+      return SKG_ERR_CUDA;
+    t.lo[j] = t.a[j];
+    if ((q.a.lo && !map_operand(&t.lo[j], c.dtype, q.a, q.a.lo, q.m, q.k, 128)) ||
+        (q.b.lo && !map_operand(&t.lo[j], c.dtype, q.b, q.b.lo, q.n, q.k, 128)))
+      return SKG_ERR_CUDA;
+  }
+  for (int j = count; j < 3; ++j) p.first[j] = (int)clusters;
+  p.stages = c.stages ? c.stages : UINT32_MAX;
+  p.limit = c.limit ? c.limit : kMxTimeoutNs;
+  p.report = c.report;
+  return launch_lin_group(out_of(c.dtype), t, p, (int)clusters, c.stream) == cudaSuccess
+             ? SKG_OK
+             : SKG_ERR_CUDA;
+}
+
+// How many CTAs share a tile of the first product if these run in one launch, and the estimate:
+// a fixed cost, the longer of its longest CTA and all stages over all SMs, and 3 us for each
+// further round of CTAs, whose beginnings and ends nothing covers (512 x 1024 x 2816: 39.7 us
+// for the whole gradient in this way, three rounds, 37.5 apart; 323 x 520 x 256 11.9 and 21.6).
+double group_us(const Product* const* jobs, int count, const Common& c, int* split) {
+  int64_t tiles[3], steps[3], all = 0;
+  for (int j = 0; j < count; ++j) {
+    const Product& q = *jobs[j];
+    tiles[j] = ((q.m + 127) / 128) * ((q.n + 127) / 128);
+    steps[j] = (q.k + kLinK - 1) / kLinK * (q.a.lo || q.b.lo ? 2 : 1);
+    all += tiles[j] * steps[j];
+  }
+  double best = 1e30;
+  for (int s : {1, 2, 4, 8}) {
+    if (s > 1 && (s > steps[0] || tiles[0] * s > 2 * c.sms)) break;
+    int64_t ctas = tiles[0] * s, longest = (steps[0] + s - 1) / s;
+    for (int j = 1; j < count; ++j) {
+      ctas += (tiles[j] + s - 1) / s * s;
+      if (steps[j] > longest) longest = steps[j];
+    }
+    if (ctas > INT32_MAX) return 1e30;
+    const double one = (ctas <= c.sms ? 0.2 : 0.44) * (double)longest;
+    const double sum = 0.22 * (double)all / c.sms;
+    const double waves = (double)((ctas + 2 * c.sms - 1) / (2 * c.sms));
+    const double us =
+        (s == 1 ? 4.6 : s == 8 ? 6.2 : 5.5) + 3.0 * (waves - 1) + (one > sum ? one : sum);
+    if (us < best) {
+      best = us;
+      *split = s;
+    }
+  }
+  return best;
+}
+
+// dX = dPRE W (m x k), dW = dPRE^T X (2 f x k) and a second weight gradient (or NULL): in one
+// launch of single CTAs where that is estimated the shortest (a launch less is counted as 2 us),
+// else dX by itself and the weight gradients in one launch where both run on pairs.
 skg_status_t in_gradients(int64_t m, int64_t f, int64_t k, const void* dpre, const void* dpre_lo,
                           const void* X, int64_t ldx, const void* W, int64_t ldw, void* dX,
                           int64_t lddx, void* dW, int64_t lddw, const Product* other,
                           const Common& c) {
-  Product q = {};
-  q.m = m;
-  q.n = k;
-  q.k = 2 * f;
-  q.a = {dpre, 2 * f, false, dpre_lo};
-  q.b = {W, ldw, true, nullptr};
-  q.c = dX;
-  q.ldc = lddx;
-  skg_status_t st = product_or_zero(q, c);
-  if (st != SKG_OK) return st;
-  q.m = 2 * f;
-  q.k = m;
-  q.a.mn = true;
-  q.b = {X, ldx, true, nullptr};
-  q.c = dW;
-  q.ldc = lddw;
-  const bool both = other && m > 0 && f > 0 && choose(q, c).pair && choose(*other, c).pair;
-  if (both) q.second = other;
-  st = product_or_zero(q, c);
-  return st == SKG_OK && other && !both ? product_or_zero(*other, c) : st;
+  Product x = {};
+  x.m = m;
+  x.n = k;
+  x.k = 2 * f;
+  x.a = {dpre, 2 * f, false, dpre_lo};
+  x.b = {W, ldw, true, nullptr};
+  x.c = dX;
+  x.ldc = lddx;
+  Product w = {};
+  w.m = 2 * f;
+  w.n = k;
+  w.k = m;
+  w.a = {dpre, 2 * f, true, dpre_lo};
+  w.b = {X, ldx, true, nullptr};
+  w.c = dW;
+  w.ldc = lddw;
+  if (m > 0 && f > 0) {
+    const Product* jobs[3] = {&x, &w, other};
+    const int count = other ? 3 : 2;
+    const Choice hx = choose(x, c), hw = choose(w, c);
+    double apart = hx.us + hw.us - 2.0;
+    bool both = false;
+    if (other) {
+      const Choice ho = choose(*other, c);
+      both = hw.pair && ho.pair;
+      apart += both ? ho.us - 4.2 : ho.us - 2.0;
+    }
+    int split = 1;
+    if (group_us(jobs, count, c, &split) < apart) return run_group(jobs, count, split, c);
+    if (both) w.second = other;
+  }
+  skg_status_t st = product_or_zero(x, c);
+  if (st == SKG_OK) st = product_or_zero(w, c);
+  return st == SKG_OK && other && !w.second ? product_or_zero(*other, c) : st;
 }
 
 }  // namespace

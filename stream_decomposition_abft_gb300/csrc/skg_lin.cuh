@@ -6,9 +6,11 @@
 //
 //   skg_lin_single.cu  128 x 128 tiles on single CTAs, k split over a cluster where the
 //                      tiles are few
+//   skg_lin_adapted.cu such tiles with few low-rank adapters in the same launch
+//   skg_lin_group.cu   such tiles of up to three products in one launch
 //   skg_lin_pair.cu    256 x 256 tiles on CTA pairs
 //
-// with these ways out (LinMode):
+// (skg_lora.cu forms what the others take as the adapters' operand,) with these ways out (LinMode):
 //   kLinPlain   C = A B^T, and with adapters + scale_s (x A_s^T) B_s^T per row
 //   kLinGated   B holds two projections of n rows each; a tile takes half of its columns
 //               from either, so one thread holds gate and up of an output:
@@ -29,8 +31,8 @@
 
 namespace skg {
 
-// Warps 0 and 6 load (issuing a stage takes a thread 300 to 420 cycles, more than the 256 of
-// its MMAs on a single CTA: they take every other stage), warp 1 issues the MMAs, warps 2-5
+// Warps 0 and 6 load (issuing a stage takes a thread some 300 cycles, more than the 256 of its
+// MMAs on a single CTA: they take every other stage), warp 1 issues the MMAs, warps 2-5
 // take the accumulators out.
 constexpr int kLinThreads = 224;
 constexpr int kLinLoader = 6;
@@ -184,6 +186,7 @@ __device__ __forceinline__ LinGrad lin_grad(float dh, float g, float u) {
   const float a = lin_act<ACT, true>(g, da);
   return {dh * u * da, dh * a, a * u};
 }
+
 // ------------------------------------------------------------------ MMAs
 // Masked forms: rows of the accumulator (TMEM lanes) whose bit in `off` is set keep their
 // values, whatever the products for them are.
@@ -265,7 +268,7 @@ __device__ __forceinline__ void lin_stage_mmas(uint32_t d, uint64_t a, uint64_t 
 template <int STAGES>
 struct LinRing {
   LinAux* aux;
-  uint64_t *full, *empty;
+  uint64_t* full;
   int st = 0, used = 0;
   uint32_t phase = 0;
   bool ready = false;
@@ -430,6 +433,28 @@ struct AdaptedParams {
 constexpr bool lin_adapted_fits(int most, int rank_pad) { return most * rank_pad <= 128; }
 cudaError_t launch_lin_adapted(int out, const LinMaps& t, const CUtensorMap& down,
                                const LinParams& p, AdaptedParams a, cudaStream_t stream);
+
+// Up to three plain products with N-major B in one launch (skg_lin_group.cu). The tiles of the
+// first are shared by the `split` CTAs of a cluster; of the others every CTA has its own.
+struct LinJob {
+  int m, n, k, ksteps, terms, lo_b, a_mn, tiles_m, tiles_n;
+  uint32_t idesc;
+  void* c;
+  int64_t ldc;
+};
+struct LinGroup {
+  int split;
+  int first[3];  // each product's first cluster (none: past the last cluster)
+  LinJob job[3];
+  uint32_t stages;
+  uint64_t limit;
+  skg_report_t* report;
+};
+struct LinGroupMaps {
+  CUtensorMap a[3], b[3], lo[3];
+};
+cudaError_t launch_lin_group(int out, const LinGroupMaps& t, const LinGroup& p, int clusters,
+                             cudaStream_t stream);
 
 cudaError_t launch_lin_pair(const LinVariant& v, const LinMaps& t, const LinParams& p,
                             int clusters, cudaStream_t stream);

@@ -421,7 +421,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncwarp();
   } else if (warp == 1) {
     if (elect_one() && rank == 0) {
-      LinRing<C::STAGES> r = {aux, aux->full, aux->empty};
+      LinRing<C::STAGES> r = {aux, aux->full};
       const uint64_t a0 = lin_desc<AMN>(smem_u32(ring));
       const uint64_t b0 = lin_desc<BMN>(smem_u32(ring) + kLinOperand);
       int n = 0;

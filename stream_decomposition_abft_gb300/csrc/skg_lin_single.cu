@@ -240,7 +240,7 @@ lin_single_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncwarp();
   } else if (warp == 1) {
     if (elect_one()) {
-      LinRing<C::STAGES> r = {aux, aux->full, aux->empty};
+      LinRing<C::STAGES> r = {aux, aux->full};
       const uint64_t a0 = lin_desc<AMN>(smem_u32(ring));
       const uint64_t b0 = lin_desc<BMN>(smem_u32(ring) + C::B_OFF);
       bool ok = true;

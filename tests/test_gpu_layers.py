@@ -288,7 +288,8 @@ def test_gated_backward(ws, kind, m, f, k):
 
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("m,f,k", SIZES + [(2048, 1024, 512), (100, 4096, 2048), (1, 2816, 4096),
-                                           (700, 3000, 1000)])
+                                           (700, 3000, 1000), (2, 136, 528), (400, 136, 72),
+                                           (55, 5680, 72), (1000, 72, 1000), (130, 1800, 104)])
 def test_feed_forward_backward(ws, kind, m, f, k):
     g = gen(m + f)
     x, w = normal(g, kind, m, k), normal(g, kind, 2 * f, k, scale=k ** -0.5)

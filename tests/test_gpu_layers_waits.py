@@ -68,7 +68,8 @@ def test_gated(m, f, k, stages):
     runs_out(lambda: layers.gated(x, w, save=True, workspace=ws), 1, stages, ws)
 
 
-@pytest.mark.parametrize("m,f,k,stages", [(100, 264, 520, 1), (512, 2816, 1024, 3),
+@pytest.mark.parametrize("m,f,k,stages", [(100, 264, 520, 1), (323, 256, 520, 2), (300, 1800, 104, 4),
+                                          (512, 2816, 1024, 3),
                                           (2048, 2048, 1024, 9)])
 def test_gradients(m, f, k, stages):
     ws, x, wi, wo = layers.workspace(), make(m, k), make(2 * f, k, seed=1), make(k, f, seed=2)
