@@ -43,6 +43,11 @@ constexpr int kLinPitch = 132;                 // floats per row of a partial ti
 constexpr int kLinBox = 64 * 128;              // bytes of an MN-major box: 64 k x 64 elements
 constexpr int kLoraRows = 256;                 // rows that one adapter plan covers
 
+// An allocation of TMEM waits while other CTAs of the SM hold too much of it, and CTAs of a
+// cluster wait for one another: two clusters that each held what the other wants would never
+// end. It cannot come to that: every kernel here (and the block-scaled product's) takes more
+// than a third of an SM's shared memory, so two CTAs at most share one, with 256 of the 512
+// columns each at most; the pairs, with all columns, take all of the shared memory.
 enum LinMode { kLinPlain = 0, kLinGated = 1, kLinGrad = 2 };
 
 // The adapters that 256 rows use, in the order of their first rows, and the rows of each
