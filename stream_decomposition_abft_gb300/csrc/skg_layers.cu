@@ -252,9 +252,10 @@ int most_adapters(int64_t m, const skg_adapters_t& ad) {
 bool one_launch(const Product& q, const Choice& h) {
   if (!q.adapters || h.pair) return false;
   const int most = most_adapters(q.m, *q.adapters);
-  if (!lin_adapted_fits(most, q.rank_pad)) return false;
+  const int rank = q.adapters->rank;
+  if (!lin_adapted_fits(most, rank, h.split)) return false;
   const double stages = (double)((q.k + kLinK - 1) / kLinK) / h.split;
-  return q.m <= 16 || (h.deep && 0.1 * stages * most * q.rank_pad / 128 <= 3.0);
+  return q.m <= 16 || (h.deep && 0.1 * stages * most * rank / 128 <= 3.0);
 }
 
 // skg_lora.cu's CTAs: to share the rows' k (split), clusters to share the adapters (groups),
@@ -366,9 +367,9 @@ skg_status_t run_product(const Product& q, const Common& c) {
       a.rank = ad.rank;
       a.most = most_adapters(q.m, ad);
       a.idesc_up = p.idesc;
-      p.idesc = idesc_f16(bf16, 128, (uint32_t)(128 + a.most * q.rank_pad));
+      p.idesc = idesc_f16(bf16, 128, (uint32_t)(128 + (a.most * a.rank + 15) / 16 * 16));
       CUtensorMap down;
-      if (!map_down(&down, c.dtype, ad, q.k, q.rank_pad)) return SKG_ERR_CUDA;
+      if (!map_down(&down, c.dtype, ad, q.k, ad.rank)) return SKG_ERR_CUDA;
       return launch_lin_adapted(out_of(c.dtype), t, down, p, a, c.stream) == cudaSuccess ? SKG_OK
                                                                                : SKG_ERR_CUDA;
     }

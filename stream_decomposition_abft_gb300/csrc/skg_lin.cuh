@@ -425,7 +425,7 @@ struct LinVariant {
 cudaError_t launch_lin_single(const LinVariant& v, const LinMaps& t, const LinParams& p,
                               cudaStream_t stream);
 // Plain, K-major operands, adapters in the same kernel (skg_lin_adapted.cu); whether that is
-// possible for so many rows and adapters of a padded rank.
+// possible for so many adapters to a tile of a rank.
 struct AdaptedParams {
   const int32_t* index;
   const float* scale;  // NULL = 1
@@ -435,7 +435,11 @@ struct AdaptedParams {
   int stage_bytes, stages;
   uint32_t idesc_up;   // of the products with B_s
 };
-constexpr bool lin_adapted_fits(int most, int rank_pad) { return most * rank_pad <= 128; }
+constexpr int kUpsMax = 32768;  // bytes of B_s that a CTA holds: its share of the adapters
+inline bool lin_adapted_fits(int most, int rank, int split) {
+  return most * rank <= 128 &&
+         (most + split - 1) / split * per_ups((rank + 15) / 16 * 16) <= kUpsMax;
+}
 cudaError_t launch_lin_adapted(int out, const LinMaps& t, const CUtensorMap& down,
                                const LinParams& p, AdaptedParams a, cudaStream_t stream);
 

@@ -3,7 +3,8 @@
 //
 // As in skg_lin_single.cu a CTA runs a 128 x 128 tile of y over a range of k; its stages also
 // hold the rows of A_s of every adapter that the tile's rows use (at most 128 in all), behind
-// W's rows, so that the MMAs form x A^T beside x W^T: up to 128 more columns. Then
+// W's rows, so that the MMAs form x A^T beside x W^T: up to 128 more columns (16 adapters of
+// rank 8, one of 128). Then
 //   - each row keeps its own adapter's columns; the CTAs of a cluster add up their ranges of k
 //     through distributed shared memory,
 //   - t in high and low parts becomes an operand in shared memory, and one CTA of the cluster
@@ -32,7 +33,7 @@ struct AdaptedCfg {
   static constexpr int B_OFF = FEW ? 16 * 128 : kLinOperand;
   static constexpr int D_OFF = B_OFF + kLinOperand;
   static constexpr int ROWS = FEW ? 16 : kLinTile;  // of a tile
-  static constexpr int SLOTS = 8;                   // adapters of a tile (rank_pad >= 16)
+  static constexpr int SLOTS = 16;                  // adapters of a tile (their ranks: 8 at least)
   static constexpr int MAX_STAGES = 8;
   // Once the stages are idle: t's operand (up to four pieces of 128 rows x 128 bytes), then the
   // partial tile in its place; the partial sums of t.
@@ -49,9 +50,9 @@ struct AdaptedAux : LinAux {
 struct AdaptedPlan {
   int32_t ids[kLinTile], slot[kLinTile];
   uint32_t lead[4];
-  int32_t id[8];
-  float scale[8];
-  uint32_t rows[8][4];
+  int32_t id[16];
+  float scale[16];
+  uint32_t rows[16][4];
 };
 
 constexpr int kAux = 256;
@@ -60,7 +61,7 @@ constexpr int adapted_smem(int ring, int ups) {
   return 1024 + ring + ups + kAux + (int)sizeof(AdaptedPlan);
 }
 static_assert(2 * (adapted_smem(100 * 1024, 8192) + 1024) <= 233472, "two adapters of rank 16");
-static_assert(adapted_smem(184 * 1024, 32768) <= (int)kSmemLimit, "shared memory");
+static_assert(adapted_smem(184 * 1024, kUpsMax) <= (int)kSmemLimit, "shared memory");
 
 template <bool FEW, typename T>
 __global__ void __launch_bounds__(kLinThreads, FEW ? 2 : 1)
@@ -104,7 +105,7 @@ lin_adapted_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     tmem_alloc(&aux->tmem_slot, 256);
     tmem_relinquish();
   }
-  if (threadIdx.x < 32) (&pl->rows[0][0])[threadIdx.x] = 0;
+  if (threadIdx.x < 64) (&pl->rows[0][0])[threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -167,13 +168,13 @@ lin_adapted_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
             break;
           }
           mbar_arrive_expect_tx(&aux->full[st],
-                                (seq < early ? 0 : tx) + (uint32_t)(count * rp) * 128);
+                                (seq < early ? 0 : tx) + (uint32_t)(count * a.rank) * 128);
           if (seq >= early) load(seq, st);
           uint8_t* d = ring + st * a.stage_bytes + C::D_OFF;
 #pragma unroll
           for (int j = 0; j < C::SLOTS; ++j)
             if (j < count)
-              tma_load_3d(d + j * rp * 128, &tmD, &aux->full[st], (kb0 + seq) * kLinK, 0, id[j]);
+              tma_load_3d(d + j * a.rank * 128, &tmD, &aux->full[st], (kb0 + seq) * kLinK, 0, id[j]);
         }
         if (++st == stages) {
           st = 0;
@@ -219,15 +220,15 @@ lin_adapted_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__
     const int q = warp & 3, r = q * 32 + lane;
     float* tp = reinterpret_cast<float*>(ring + C::PART) + r * kLinPitch;
     if (fine && q * 32 < rows) {
-      const int from = r < rows && pl->ids[r] >= 0 ? pl->slot[r] * rp : -1;
-      for (int c = 0; c < count * rp; c += 32) {
+      const int from = r < rows && pl->ids[r] >= 0 ? pl->slot[r] * a.rank : -1;
+      for (int c = 0; c < count * a.rank; c += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + kLinTile + c, v);
 #pragma unroll
-        for (int h = 0; h < 32; h += 16)
-          if (from >= 0 && c + h >= from && c + h < from + rp) {
+        for (int h = 0; h < 32; h += 8)
+          if (from >= 0 && c + h >= from && c + h < from + a.rank) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
+            for (int i = 0; i < 8; i += 4)
               *reinterpret_cast<uint4*>(tp + c + h - from + i) =
                   make_uint4(v[h + i], v[h + i + 1], v[h + i + 2], v[h + i + 3]);
           }
@@ -342,9 +343,9 @@ cudaError_t launch(const LinMaps& t, const CUtensorMap& down, const LinParams& p
   const int smem = adapted_smem(C::RING, ups);
   static std::atomic<uint64_t> done_mask{0};
   const cudaError_t e =
-      opt_in_smem((const void*)kernel, done_mask, adapted_smem(C::RING, 32768));
+      opt_in_smem((const void*)kernel, done_mask, adapted_smem(C::RING, kUpsMax));
   if (e != cudaSuccess) return e;
-  a.stage_bytes = C::D_OFF + a.most * p.rank_pad * 128;
+  a.stage_bytes = C::D_OFF + a.most * a.rank * 128;
   a.stages = C::RING / a.stage_bytes;
   if (a.stages > C::MAX_STAGES) a.stages = C::MAX_STAGES;
   return launch_pdl_cluster(kernel, dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.split)),

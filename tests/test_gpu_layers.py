@@ -130,7 +130,9 @@ def test_adapters_ranks(ws, kind, r, m, n, k):
 @pytest.mark.parametrize("m,s,r", [(1, 16, 16), (1, 3, 128), (2, 64, 64), (8, 64, 8), (7, 8, 16),
                                    (16, 2, 64), (16, 1, 128), (5, 4, 32), (13, 3, 40), (64, 5, 16),
                                    (128, 1, 128), (129, 8, 16), (300, 2, 64), (300, 8, 8),
-                                   (200, 3, 40), (40, 4, 24), (333, 1, 96), (127, 2, 48)])
+                                   (200, 3, 40), (40, 4, 24), (333, 1, 96), (127, 2, 48),
+                                   (16, 16, 8), (140, 16, 8), (9, 16, 8), (200, 5, 24), (65, 13, 8),
+                                   (1, 5, 120)])
 @pytest.mark.parametrize("n,k", [(1000, 2200), (264, 72), (128, 8), (3000, 1032)])
 def test_adapters_few(ws, kind, m, s, r, n, k):
     """Few adapters to a tile (one launch), k split and not, rows with none."""
