@@ -210,6 +210,12 @@ double pair_us(int64_t m, int64_t tiles, int ksteps, int clusters, double out) {
   return 4.2 + out + (waves > 1 ? 0.29 : 0.262) * (double)waves * ksteps;
 }
 
+// Adapters that 128 rows can have.
+int most_adapters(int64_t m, const skg_adapters_t& ad) {
+  const int rows = m < kLinTile ? (int)m : kLinTile;
+  return ad.count < rows ? ad.count : rows;
+}
+
 // How a product runs.
 struct Choice {
   bool pair, deep;
@@ -227,9 +233,14 @@ Choice choose(const Product& q, const Common& c) {
   const double out = q.mode == kLinGrad ? 2.0 : q.mode == kLinGated ? 0.5 : 0.0;
   const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms, out);
   // (The low parts of H and DPRE are written by single CTAs; up to 128 rows they run.)
-  const double paired = h.resident > 0 && q.n >= 8 && !q.c_lo
+  double paired = h.resident > 0 && q.n >= 8 && !q.c_lo
                             ? pair_us(q.m, tm2 * tn2, steps, h.resident, 2.0 * out)
                             : 1e30;
+  // With adapters the pairs are two launches, where single CTAs may be one (1087 x 152 x 176, one
+  // adapter: 12.4 and 10.6 us).
+  if (q.adapters && (q.m <= 16 || single.deep) &&
+      lin_adapted_fits(most_adapters(q.m, *q.adapters), q.adapters->rank, single.split))
+    paired += 1.5;
   h.pair = paired <= single.us;
   h.tiles_m = h.pair ? tm2 : tm1;
   h.tiles_n = h.pair ? tn2 : tn1;
@@ -237,12 +248,6 @@ Choice choose(const Product& q, const Common& c) {
   h.deep = !h.pair && single.deep;
   h.us = h.pair ? paired : single.us;
   return h;
-}
-
-// Adapters that 128 rows can have.
-int most_adapters(int64_t m, const skg_adapters_t& ad) {
-  const int rows = m < kLinTile ? (int)m : kLinTile;
-  return ad.count < rows ? ad.count : rows;
 }
 
 // Whether a product with adapters is one launch (skg_lin_adapted.cu). With more than 16 rows
