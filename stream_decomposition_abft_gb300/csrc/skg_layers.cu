@@ -1,14 +1,16 @@
 // The entry points of a layer's projections (skgemm.h): checks, the choice of kernel, tensor
 // maps and launches; and the elementwise kernel of the gated product's gradient.
 //
-//   skg_linear                   t = scale (x A^T) (skg_lora.cu), then y = x W^T + t B^T
+//   skg_linear                   y = x W^T + t B^T, t = scale (x A^T): one launch where a tile's
+//                                rows have few adapters (skg_lin_adapted.cu), else t first
+//                                (skg_lora.cu)
 //   skg_gated                    one kernel: both projections, the activation, the product
 //   skg_gated_backward           dPRE elementwise; dX = dPRE W; dW = dPRE^T X
-//   skg_feed_forward_backward    dH = dY W_out (fp32); dPRE and H elementwise; dX; dW_in;
+//   skg_feed_forward_backward    one kernel: dH = dY W_out, dPRE and H from it; dX; dW_in;
 //                                dW_out = dY^T H
 //
 // The products run on skg_lin_single.cu's or skg_lin_pair.cu's kernels, which read operands
-// stored along either dimension in place.
+// stored along either dimension in place; small gradients' together (skg_lin_group.cu).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
