@@ -179,20 +179,20 @@ bool map_operand(CUtensorMap* t, int dtype, const Operand& o, const void* p, int
 // where two CTAs share one (333 x 2048 x 2048: 10.4, 8.0, 10.3 with S = 1, 2, 4: 48, 96, 192
 // CTAs). Larger clusters find less room, as a GPC's SMs do not divide by them: 128 x 2048 x
 // 2048, 16 tiles, takes 6.8, 6.5, 8.6 with S = 4, 6, 8. `out`: what the activations of a whole
-// tile take, which the CTAs of a cluster share.
+// tile take, which the CTAs of a cluster share; `extra`: stages behind k's, which they share too.
 struct SinglePlan {
   int split;
   bool deep;
   double us;
 };
-SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms, double out) {
+SinglePlan single_plan(int64_t m, int64_t tiles, int ksteps, int sms, double out, int extra) {
   constexpr double kFixed[9] = {0, 4.4, 4.9, 5.1, 5.3, 0, 5.6, 0, 5.7};
   SinglePlan best = {1, false, 1e30};
   for (int s : {1, 2, 3, 4, 6, 8}) {
     if (s > 1 && (tiles * s > 2 * sms || s > ksteps)) break;
     const bool deep = s == 1 ? tiles <= sms : tiles <= lin_single_clusters(s);
     if ((s == 3 || s == 6) && (m <= 16 || !deep)) continue;
-    const int stages = (ksteps + s - 1) / s;
+    const int stages = (ksteps + extra + s - 1) / s;
     const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
     const double us =
         out / s + (deep ? kFixed[s] + 0.2 * stages
@@ -233,10 +233,14 @@ Choice choose(const Product& q, const Common& c) {
   Choice h = {};
   h.resident = lin_pair_clusters_resident();
   const double out = q.mode == kLinGrad ? 2.0 : q.mode == kLinGated ? 0.5 : 0.0;
-  const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms, out);
+  // Adapters' stages: how many of the stack a tile's rows have is not known here; half.
+  const int extra = q.adapters ? (most_adapters(q.m, *q.adapters) / 2 + lora_pack(q.rank_pad) - 1) /
+                                     lora_pack(q.rank_pad) * lora_stages(q.rank_pad)
+                               : 0;
+  const SinglePlan single = single_plan(q.m, tm1 * tn1, steps, c.sms, out, extra);
   // (The low parts of H and DPRE are written by single CTAs; up to 128 rows they run.)
   double paired = h.resident > 0 && q.n >= 8 && !q.c_lo
-                            ? pair_us(q.m, tm2 * tn2, steps, h.resident, 2.0 * out)
+                            ? pair_us(q.m, tm2 * tn2, steps + extra, h.resident, 2.0 * out)
                             : 1e30;
   // With adapters the pairs are two launches, where single CTAs may be one (1087 x 152 x 176, one
   // adapter: 12.4 and 10.6 us).
