@@ -347,10 +347,11 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           phase ^= 1u;
         }
       };
-      // Four adapters of a plan from the u-th on (past their number: anything).
+      // Four adapters of a plan from the u-th on (past their number: anything; past the
+      // plan's end its last entry).
       auto read = [](const LoraPlan* plan, int u, int (&id)[4]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) id[e] = plan->id[u + e];
+        for (int e = 0; e < 4; ++e) id[e] = plan->id[min(u + e, kLoraRows - 1)];
       };
       int id[4] = {0, 0, 0, 0}, count = 0;
       const int ks = p.ksteps * p.terms;
@@ -400,7 +401,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           for (int u = 0; ok && u < count; u += pack) {
             const int here = min(pack, count - u);
             int behind[4];
-            read(p.plan + tm, min(u + pack, kLoraRows - 4), behind);
+            read(p.plan + tm, u + pack, behind);
             for (int j = 0; ok && j < per; ++j)
               step(kLinOperand + here * one, [&](uint8_t* s, uint32_t bar) {
                 tma_load_2d_pair(s, &maps.t, bar, lora_col_t(rp, j), row);
@@ -431,7 +432,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int w = 0; w < 8; ++w) off[e][w] = ~plan->rows[u + e][w];
+          for (int w = 0; w < 8; ++w) off[e][w] = ~plan->rows[min(u + e, kLoraRows - 1)][w];
       };
       uint32_t off[4][8];
       int count = 0;
@@ -477,7 +478,7 @@ lin_pair_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
           for (int u = 0; ok && u < count; u += pack) {
             const int here = min(pack, count - u);
             uint32_t behind[4][8];
-            read(plan, min(u + pack, kLoraRows - 4), behind);
+            read(plan, u + pack, behind);
             for (int j = 0; j < per; ++j) {
               const int st = r.take();
               ok = st >= 0;

@@ -1,0 +1,79 @@
+"""A layer's projections at the ends of their ranges, against the definitions in 64 bits
+(oracle/layers_ref.py, which derives the bounds)."""
+import pytest
+import torch
+
+from oracle import layers_ref as ref
+from stream_decomposition_abft_gb300 import layers
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ws():
+    w = layers.workspace()
+    yield w
+    torch.cuda.synchronize()
+    assert w.report().timeouts == 0
+
+
+def gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, *shape, scale=1.0, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=g, device="cuda").mul_(scale).to(dtype)
+
+
+def check(got, want, bound, what=""):
+    got = got.double()
+    assert got.shape == want.shape, what
+    assert torch.isfinite(got).all(), what
+    over = (got - want).abs() - bound
+    assert float(over.max()) <= 0, f"{what}: off by {float(over.max())} more than the bound"
+
+
+# ------------------------------------------------------------------ a plan with no room left
+# Each row its own adapter: 128 to a tile of single CTAs, 256 to one of the pairs, whose plan
+# then ends with the last rows. With 1100 rows x 2560 columns the pairs run (50 tiles of 76
+# pairs), with 256 and 300 rows single CTAs.
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 136, 512])
+@pytest.mark.parametrize("s", [253, 254, 255, 256, 300, 1100])
+def test_adapter_of_its_own_for_each_row_of_a_pair(ws, r, s):
+    own_rows(ws, 1100, 2560, 136, r, s)
+
+
+@pytest.mark.parametrize("r", [16, 24, 64, 136])
+@pytest.mark.parametrize("m,s", [(127, 127), (128, 128), (256, 256), (255, 300), (300, 254)])
+def test_adapter_of_its_own_for_each_row_of_a_cta(ws, m, s, r):
+    own_rows(ws, m, 264, 200, r, s)
+
+
+@pytest.mark.parametrize("m,n,k,s,r", [(256, 16384, 520, 256, 32), (512, 8192, 1032, 512, 24),
+                                       (1024, 4096, 264, 1024, 64), (770, 4096, 1032, 254, 48)])
+def test_adapter_of_its_own_for_each_row_at_serving_sizes(ws, m, n, k, s, r):
+    own_rows(ws, m, n, k, r, s)
+
+
+def own_rows(ws, m, n, k, r, s):
+    g = gen(m + r + s)
+    x, w = normal(g, m, k), normal(g, n, k, scale=k ** -0.5)
+    a, b = normal(g, s, r, k, scale=k ** -0.5), normal(g, s, n, r, scale=r ** -0.5)
+    f = 0.5 + torch.rand(s, generator=g, device="cuda")
+    i = torch.arange(m, device="cuda") % s
+    # The definition for the rows together: row i's adapter is s = i mod the stack.
+    xd, wd = x.double(), w.double()
+    y, size = xd @ wd.t(), xd.abs() @ wd.abs().t()
+    u, least, acc = ref.U[x.dtype], ref.LEAST[x.dtype], ref.acc
+    bound = acc(k) * size
+    for at in range(0, m, 128):
+        rows = torch.arange(at, min(at + 128, m), device="cuda")
+        ai, bi, fi = a[i[rows]].double(), b[i[rows]].double(), f[i[rows]].double()[:, None]
+        t = fi * torch.einsum("mk,mrk->mr", xd[rows], ai)
+        off = fi * acc(k) * torch.einsum("mk,mrk->mr", xd[rows].abs(), ai.abs()) + \
+            4 * u * u * t.abs() + least
+        y[rows] += torch.einsum("mr,mnr->mn", t, bi)
+        bound[rows] += torch.einsum("mr,mnr->mn", off, bi.abs()) + acc(k + 2 * r) * (
+            size[rows] + 2 * torch.einsum("mr,mnr->mn", t.abs(), bi.abs()))
+    got = layers.linear(x, w, layers.Adapters(a, b, f), i.int(), workspace=ws)
+    check(got, y, bound + u * (y.abs() + bound) + least)
