@@ -43,7 +43,7 @@ struct PairCfg {
 
 // A box of 32 rows x 128 bytes (this lane's row: the values f(0), f(1), ...) in the 128-byte
 // swizzle, and its store by TMA; two boxes per warp in turn. The engine clips what is past
-// the matrix, to whole 16 bytes; returns the box.
+// the matrix, to whole 16 bytes (store_rest); returns the box.
 template <typename T, typename F>
 __device__ __forceinline__ uint8_t* store_box(const CUtensorMap* map, uint8_t* staging, uint32_t& box,
                                           int lane, int col, int row, F f) {
@@ -69,19 +69,6 @@ __device__ __forceinline__ uint8_t* store_box(const CUtensorMap* map, uint8_t* s
     bulk_commit();
   }
   return st;
-}
-
-// The columns of a box of C behind the last whole 16 bytes of a row (the map ends before them:
-// what the engine would write there is not C's), one by one.
-template <typename T>
-__device__ __noinline__ void store_rest(void* to, int64_t ld, int m, int n, const uint8_t* st,
-                                        int lane, int col, int row) {
-  if (row + lane >= m) return;
-  for (int c = max(n & ~7, col); c < min(n, col + 64); ++c) {
-    const int i = c - col;
-    reinterpret_cast<T*>(to)[(int64_t)(row + lane) * ld + c] = *reinterpret_cast<const T*>(
-        st + lane * 128 + (((i >> 3) ^ (lane & 7)) << 4) + (i & 7) * sizeof(T));
-  }
 }
 
 // 16 values of this lane's row to columns 16 c of its box.

@@ -397,13 +397,15 @@ cudaError_t plan_and_launch(const void* A, int64_t lda, const void* SA, const vo
                         CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   t[4] = t[0];
+  const int es = out == SKG_OUT_F32 ? 4 : 2;
+  if (pair && p.n < 16 / es) p.c_tma = 0;  // (no whole 16 bytes to store)
   if (pair && p.c_tma) {
-    const int es = out == SKG_OUT_F32 ? 4 : 2;
     const CUtensorMapDataType dt = out == SKG_OUT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : out == SKG_OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (encode_tensor_map(&t[4], dt, es, p.c, (uint64_t)p.n, (uint64_t)p.m, (uint64_t)p.ldc,
-                          (uint32_t)(128 / es), 32, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    if (encode_tensor_map(&t[4], dt, es, p.c, (uint64_t)(p.n / (16 / es) * (16 / es)),
+                          (uint64_t)p.m, (uint64_t)p.ldc, (uint32_t)(128 / es), 32,
+                          CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
   if (pair)

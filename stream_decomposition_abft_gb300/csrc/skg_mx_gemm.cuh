@@ -26,7 +26,7 @@ struct MxParams {
   void* c;
   int64_t ldc;
   int c_vec;        // four elements of a row are aligned together
-  int c_tma;        // rows of C on 16-byte boundaries, beta = 0: pairs store it by TMA
+  int c_tma;        // rows of C on 16-byte boundaries, beta = 0: pairs store it by TMA (store_rest)
   int ksteps;       // stages of k
   int groups;       // scale tiles along k
   int tiles_m, tiles_n;
@@ -132,6 +132,22 @@ __device__ __forceinline__ void mx_write4(const MxParams& p, int row, int col, c
   T* c = reinterpret_cast<T*>(p.c) + (int64_t)row * p.ldc + col;
   if (p.c_vec && p.beta == 0.f && col + 4 <= p.n) mx_write4_plain<T>(c, v, alpha);
   else mx_write4_any<T>(c, v, alpha, p.beta, p.n - col, p.c_vec != 0);
+}
+
+// A TMA store writes whole 16 bytes: the last ones of a row that it clips at n would reach
+// what lies behind C's columns. So its map ends at the last whole 16 bytes of n, and these
+// are the columns behind, one by one from the box (32 rows x 128 bytes in the 128-byte
+// swizzle, at row `row` and column `col`), this lane's row.
+template <typename T>
+__device__ __noinline__ void store_rest(void* to, int64_t ld, int m, int n, const uint8_t* st,
+                                        int lane, int col, int row) {
+  constexpr int PER = 16 / (int)sizeof(T), COLS = 8 * PER;
+  if (row + lane >= m) return;
+  for (int c = max(n & ~(PER - 1), col); c < min(n, col + COLS); ++c) {
+    const int i = c - col;
+    reinterpret_cast<T*>(to)[(int64_t)(row + lane) * ld + c] = *reinterpret_cast<const T*>(
+        st + lane * 128 + (((i / PER) ^ (lane & 7)) << 4) + (i % PER) * sizeof(T));
+  }
 }
 
 // The MMAs of one stage (A at its start, B at B_OFF): the scales go to TMEM columns sfa,

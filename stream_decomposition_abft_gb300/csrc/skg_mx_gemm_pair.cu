@@ -70,7 +70,8 @@ __device__ __forceinline__ void pair_write_chunk(const MxParams& p, uint8_t* sta
 
 // 64 columns: scaled, rounded and stored by TMA (beta = 0, rows of C on 16-byte
 // boundaries) from boxes of 32 rows x 128 bytes in the 128-byte swizzle, two
-// boxes per warp in turn; the engine clips what is past m and n.
+// boxes per warp in turn; the engine clips what is past m and the last whole 16
+// bytes of n, and the columns behind those are stored one by one.
 template <typename T>
 __device__ __forceinline__ void pair_store_half(const MxParams& p, const CUtensorMap* tmC,
                                                 uint8_t* staging, uint32_t& box, int lane,
@@ -104,10 +105,13 @@ __device__ __forceinline__ void pair_store_half(const MxParams& p, const CUtenso
     }
     fence_proxy_async_smem();
     __syncwarp();
+    const int col = col0 + b * 32, whole = p.n & ~(PER - 1);
     if (lane == 0) {
-      if (col0 + b * 32 < p.n) tma_store_2d(tmC, st, col0 + b * 32, row0);
+      if (col < whole) tma_store_2d(tmC, st, col, row0);
       bulk_commit();
     }
+    if (whole < p.n && col + 8 * PER > whole)
+      store_rest<T>(p.c, p.ldc, p.m, p.n, st, lane, col, row0);
   }
 }
 

@@ -127,3 +127,17 @@ def test_readme_example():
         # Of the given dn: one rounding to bf16.
         got = got.double().cpu().numpy()
         assert np.linalg.norm(got - want) / np.linalg.norm(want) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("m,n", [(2048, 2041), (2048, 2042), (2048, 2045), (2300, 1923), (2300, 1990),
+                                 (40000, 3), (40000, 7), (40000, 9), (300, 2047), (5, 1003)])
+def test_product_leaves_what_is_behind_its_columns(fmt, dtype, m, n):
+    # Rows of out on 16-byte boundaries, as many columns as leave whole 16 bytes unfilled, on
+    # either kernel: the same bits as in rows of their own, and nothing behind them.
+    a, b = mx.quantize(randn(m, 512, seed=m), fmt), mx.quantize(randn(n, 512, seed=n), fmt)
+    buf = torch.full((m + 1, n // 8 * 8 + 24), 7.0, dtype=dtype, device="cuda")
+    mx.matmul(a, b, out=buf[:m, 8:8 + n])
+    assert torch.equal(buf[:m, 8:8 + n], mx.matmul(a, b, out_dtype=dtype))
+    assert bool((buf[:, :8] == 7).all() and (buf[:, 8 + n:] == 7).all() and (buf[m] == 7).all())
