@@ -306,7 +306,8 @@ skg_status_t skg_workspace_init(void* workspace, size_t bytes, void* stream);
  *      elements (>= k row-major, >= m column-major).
  *   B: device, in_dtype, stored as b_layout says (skg_b_layout_t), ldb
  *      >= k (K-major) or >= n (N-major).
- *   C: device, out_dtype, row-major m x n, ldc >= n; read only if beta != 0.
+ *   C: device, out_dtype, row-major m x n, ldc >= n; read only if beta != 0;
+ *      what lies behind the n columns of its rows stays as it was.
  *   A, B, C must be 16-byte aligned and lda, ldb, ldc must be multiples of
  *   16 bytes (the TMA engine's rule); otherwise SKG_ERR_UNSUPPORTED. An
  *   unknown layout value or a leading dimension below its minimum is

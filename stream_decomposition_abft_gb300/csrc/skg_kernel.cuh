@@ -547,6 +547,33 @@ __device__ __forceinline__ void staging_read(const uint8_t* buf, int r, uint32_t
   }
 }
 
+// A box's rows to C past the TMA engine, from column col0 to n: its store writes whole 16
+// bytes, and where n is no whole number of them the last ones of a row would reach what lies
+// behind C's columns. One lane per row.
+template <int OUT>
+__device__ __noinline__ void store_box_rows(void* c, int64_t ldc, int m, int n,
+                                            const uint8_t* buf, int lane, int row0, int col0) {
+  constexpr int BYTES = OUT == 0 ? 4 : 2;
+  if (row0 + lane >= m) return;
+  uint8_t* out = static_cast<uint8_t*>(c) + ((int64_t)(row0 + lane) * ldc + col0) * BYTES;
+  const int bytes = min((n - col0) * BYTES, 128);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    union {
+      uint4 q;
+      uint16_t h[8];
+    } u;
+    u.q = *reinterpret_cast<const uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4));
+    if (j * 16 + 16 <= bytes) {
+      *reinterpret_cast<uint4*>(out + j * 16) = u.q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j * 16 + i * 2 < bytes) *reinterpret_cast<uint16_t*>(out + j * 16 + i * 2) = u.h[i];
+    }
+  }
+}
+
 __device__ __forceinline__ float4 ld_cg_f4(const float* p) {
   return __ldcg(reinterpret_cast<const float4*>(p));
 }
@@ -2614,8 +2641,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           staging_write(buf, lane, wout);
           fence_proxy_async_smem();
           __syncwarp();
+          const bool part = (p.n & (16 / C::OUT_BYTES - 1)) != 0 && col0 + C::EPI_COLS > p.n;
+          if (part)
+            store_box_rows<C::OUT>(p.c_ptr, p.ldc, p.m, p.n, buf, lane, m0 + q * 32, col0);
           if (lane == 0) {
-            tma_store_2d(&tmC, buf, col0, m0 + q * 32);
+            if (!part) tma_store_2d(&tmC, buf, col0, m0 + q * 32);
             bulk_commit();
           }
           bsel = (bsel + 1) % C::EPI_BUFS;
