@@ -621,7 +621,8 @@ skg_status_t skg_mx_test_stall(int32_t stages, uint64_t timeout_ns);
  * base addresses 16-byte aligned (the TMA engine's rules), else
  * SKG_ERR_UNSUPPORTED. `hidden` is a multiple of 8. Products and sums are in
  * fp32 on the tensor cores; results are rounded once to dtype. The same inputs
- * give the same result every time. Outputs overlap no input and no other output.
+ * give the same result every time. Outputs share no memory with an input or another output
+ * (SKG_ERR_ARG; columns of one buffer that lie beside one another do not).
  * Sizes of zero are valid (sums over nothing are zero).
  *
  * workspace: device, 256-byte aligned, skg_workspace_size_layers bytes, zeroed

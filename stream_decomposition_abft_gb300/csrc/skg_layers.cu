@@ -443,6 +443,64 @@ bool aligned(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   return rows == 0 || cols == 0 || (((uintptr_t)p & 15) == 0 && (rows == 1 || ld % 8 == 0));
 }
 
+// Rows of `width` bytes, `pitch` bytes from one to the next (none: rows or width 0).
+struct Rows {
+  int64_t at, rows, width, pitch;
+  int64_t end() const { return at + (rows - 1) * pitch + width; }
+};
+Rows rows_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int bytes = 2) {
+  const bool some = p && rows > 0 && cols > 0;
+  return {(int64_t)(uintptr_t)p, some ? rows : 0, cols * bytes, rows > 1 ? ld * bytes : cols * bytes};
+}
+
+// Whether some byte is in both. Rows that lie between one another's (columns of one buffer)
+// are told apart.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.rows == 0 || b.rows == 0 || a.end() <= b.at || b.end() <= a.at) return false;
+  // Row i of b and row j of a meet if i b.pitch - j a.pitch is between a.at - b.at - b.width and
+  // a.at - b.at + a.width.
+  const int64_t low = a.at - b.at - b.width, high = a.at - b.at + a.width;
+  auto above = [](int64_t v, int64_t pitch) {  // the least multiple of pitch over v, in pitches
+    return v >= 0 ? v / pitch + 1 : -((-v - 1) / pitch);
+  };
+  if (a.pitch == b.pitch) {
+    int64_t t = above(low, a.pitch);
+    if (t < 1 - a.rows) t = 1 - a.rows;
+    return t < b.rows && t * a.pitch < high;
+  }
+  if (a.rows > b.rows) return overlap(b, a);
+  for (int64_t j = 0; j < a.rows; ++j) {
+    int64_t i = above(low + j * a.pitch, b.pitch);
+    if (i < 0) i = 0;
+    if (i < b.rows && i * b.pitch < high + j * a.pitch) return true;
+  }
+  return false;
+}
+
+// The matrices of a stack, `stride` elements apart.
+bool overlap_stack(const Rows& out, const void* p, int64_t count, int64_t stride, int64_t rows,
+                   int64_t cols, int64_t ld) {
+  Rows one = rows_of(p, rows, cols, ld);
+  if (count <= 0 || out.rows == 0 || one.rows == 0 || out.end() <= one.at ||
+      one.end() + (count - 1) * stride * 2 <= out.at)
+    return false;
+  for (int64_t s = 0; s < count; ++s, one.at += stride * 2)
+    if (overlap(out, one)) return true;
+  return false;
+}
+
+// Whether one of the outputs shares memory with an input or another output.
+template <int OUTS, int INS>
+bool any_overlap(const Rows (&outs)[OUTS], const Rows (&ins)[INS]) {
+  for (int i = 0; i < OUTS; ++i) {
+    for (const Rows& r : ins)
+      if (overlap(outs[i], r)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+  }
+  return false;
+}
+
 skg_status_t check_sizes(int64_t m, int64_t n, int64_t k, int32_t dtype) {
   if (m < 0 || n < 0 || k < 0 || (dtype != SKG_IN_F16 && dtype != SKG_IN_BF16)) return SKG_ERR_ARG;
   if (m > kMaxDim || n > kMaxDim / 2 || k > kMaxDim) return SKG_ERR_UNSUPPORTED;
@@ -666,6 +724,13 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
   const size_t need = ad ? skg_scratch_size_linear(m, ad->rank) : 0;
   st = check_memory(workspace, ws_bytes, scratch, scratch_bytes, need);
   if (st != SKG_OK) return st;
+  const Rows out = rows_of(Y, m, n, ldy);
+  if (overlap(out, rows_of(X, m, k, ldx)) || overlap(out, rows_of(W, n, k, ldw))) return SKG_ERR_ARG;
+  if (ad && (overlap(out, rows_of(ad->index, 1, m, m, 4)) ||
+             overlap(out, rows_of(ad->scale, 1, ad->count, ad->count, 4)) ||
+             overlap_stack(out, ad->down, ad->count, ad->stride_down, ad->rank, k, ad->ld_down) ||
+             overlap_stack(out, ad->up, ad->count, ad->stride_up, n, ad->rank, ad->ld_up)))
+    return SKG_ERR_ARG;
   Common c;
   st = common(dtype, workspace, stream, &c);
   if (st != SKG_OK) return st;
@@ -727,6 +792,9 @@ skg_status_t skg_gated(int64_t m, int64_t hidden, int64_t k, const void* X, int6
     return SKG_ERR_UNSUPPORTED;
   st = check_memory(workspace, ws_bytes, nullptr, 0, 0);
   if (st != SKG_OK) return st;
+  if (any_overlap({rows_of(H, m, hidden, ldh), rows_of(PRE, m, 2 * hidden, ldp)},
+                  {rows_of(X, m, k, ldx), rows_of(W, 2 * hidden, k, ldw)}))
+    return SKG_ERR_ARG;
   Common c;
   st = common(dtype, workspace, stream, &c);
   if (st != SKG_OK) return st;
@@ -775,6 +843,10 @@ skg_status_t skg_gated_backward(int64_t m, int64_t hidden, int64_t k, const void
   st = check_memory(workspace, ws_bytes, scratch, scratch_bytes,
                     skg_scratch_size_gated_backward(m, hidden));
   if (st != SKG_OK) return st;
+  if (any_overlap({rows_of(dX, m, k, lddx), rows_of(dW, 2 * hidden, k, lddw)},
+                  {rows_of(dH, m, hidden, lddh), rows_of(X, m, k, ldx),
+                   rows_of(W, 2 * hidden, k, ldw), rows_of(PRE, m, 2 * hidden, ldp)}))
+    return SKG_ERR_ARG;
   Common c;
   st = common(dtype, workspace, stream, &c);
   if (st != SKG_OK) return st;
@@ -829,6 +901,12 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
   st = check_memory(workspace, ws_bytes, scratch, scratch_bytes,
                     skg_scratch_size_feed_forward_backward(m, hidden));
   if (st != SKG_OK) return st;
+  if (any_overlap({rows_of(dX, m, k, lddx), rows_of(dW_in, 2 * hidden, k, lddw_in),
+                   rows_of(dW_out, k, hidden, lddw_out)},
+                  {rows_of(dY, m, k, lddy), rows_of(X, m, k, ldx),
+                   rows_of(W_in, 2 * hidden, k, ldw_in), rows_of(W_out, k, hidden, ldw_out),
+                   rows_of(PRE, m, 2 * hidden, ldp)}))
+    return SKG_ERR_ARG;
   Common c;
   st = common(dtype, workspace, stream, &c);
   if (st != SKG_OK) return st;

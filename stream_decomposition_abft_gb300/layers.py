@@ -72,8 +72,9 @@ def linear(x, w, adapters=None, index=None, out=None, workspace=None, stream=Non
     with adapter s = index[i].
 
     x (m, k), w (n, k); index: (m,) int32 on the device, in any order, a value that is
-    negative or not below S for none. ``out`` (m, n) is written in place, or allocated
-    (for n that is no multiple of 8 as a view of padded rows)."""
+    negative or not below S for none. ``out`` (m, n) is written in place (it shares no memory
+    with an input: refused), or allocated (for n that is no multiple of 8 as a view of padded
+    rows)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear(x, w, adapters, index, out, workspace)

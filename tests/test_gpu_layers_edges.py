@@ -77,3 +77,27 @@ def own_rows(ws, m, n, k, r, s):
             size[rows] + 2 * torch.einsum("mr,mnr->mn", t.abs(), bi.abs()))
     got = layers.linear(x, w, layers.Adapters(a, b, f), i.int(), workspace=ws)
     check(got, y, bound + u * (y.abs() + bound) + least)
+
+
+# ------------------------------------------------------------------ out beside its inputs
+def test_out_in_a_buffer_of_its_inputs(ws):
+    """Columns of one buffer: taken where they lie beside one another, refused where they share
+    a byte."""
+    from stream_decomposition_abft_gb300.skgemm import SkgError
+    g = gen(12)
+    m, n, k, r = 300, 72, 64, 16
+    buf = normal(g, m, k + n + 8)
+    w, i = normal(g, n, k), torch.zeros(m, dtype=torch.int32, device="cuda")
+    ad = layers.Adapters(normal(g, 1, r, k), normal(g, 1, n, r))
+    x = buf[:, :k]
+    want, plain = layers.linear(x, w, ad, i, workspace=ws), layers.linear(x, w, workspace=ws)
+    before = buf.clone()
+    assert torch.equal(layers.linear(x, w, ad, i, out=buf[:, k:k + n], workspace=ws), want)
+    assert torch.equal(layers.linear(x, w, out=buf[:, k + 8:], workspace=ws), plain)
+    assert torch.equal(x, before[:, :k]) and torch.equal(buf[:, k:k + 8], want[:, :8])
+    for out in (buf[:, k - 8:k - 8 + n], buf[:, :n]):
+        with pytest.raises(SkgError, match="argument"):
+            layers.linear(x, w, out=out, workspace=ws)
+    with pytest.raises(SkgError, match="argument"):
+        layers.linear(x[:8], w, out=torch.as_strided(w, (8, n), (n, 1)), workspace=ws)
+    assert torch.equal(x, before[:, :k])
