@@ -1,9 +1,10 @@
 // Python module _skg_torch: the microscaled entry points of libskgemm.so, and those of a
-// layer's projections in 16 bits, on torch tensors. It checks the arguments, allocates the outputs, and hands pointers,
-// strides and the current stream to the C ABI; all arithmetic runs there. (A
-// call of one token takes the GPU 3 to 4 us; the same marshalling in Python took
-// 14 to 20 us.) Functions take their arguments by position, return the library's
-// status (an int) when it refuses a call, and raise ValueError themselves.
+// layer's projections in 16 bits, on torch tensors. It checks the arguments, allocates
+// the outputs, and hands pointers, strides and the current stream to the C ABI; all
+// arithmetic runs there. (A call of one token takes the GPU 3 to 4 us; the same
+// marshalling in Python took 14 to 20 us.) Functions take their arguments by position,
+// return the library's status (an int) when it refuses a call, and raise ValueError
+// themselves.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -132,6 +133,12 @@ struct Quantized {
     scales = empty({(int64_t)skg_mx_scales_size(rows, k, fmt)}, at::kByte, d);
   }
 };
+
+// A given output is written: autograd sees it changed, as after any operation in place.
+PyObject* written(const at::Tensor& out) {
+  if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+  return THPVariable_Wrap(out);
+}
 
 PyObject* wrap_or_none(const at::Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
@@ -318,7 +325,7 @@ PyObject* matmul(PyObject* const* v, Py_ssize_t n) {
                              b.scales->data_ptr(), b.g, (float)beta, out.data_ptr(), ldc, a.fmt,
                              type_of("out", out.scalar_type(), true), ws.data_ptr(),
                              (size_t)ws.nbytes(), stream_of(d));
-  return st != SKG_OK ? PyLong_FromLong(st) : THPVariable_Wrap(out);
+  return st != SKG_OK ? PyLong_FromLong(st) : written(out);
 }
 
 // ------------------------------------------------------------------ a layer's projections
@@ -425,7 +432,7 @@ PyObject* linear(PyObject* const* v, Py_ssize_t n) {
                             adapted ? &ad : nullptr, out.data_ptr(), ldo, type, ws.data_ptr(),
                             (size_t)ws.nbytes(), bytes ? scratch.data_ptr() : nullptr, bytes,
                             stream_of(d));
-  return st != SKG_OK ? PyLong_FromLong(st) : THPVariable_Wrap(out);
+  return st != SKG_OK ? PyLong_FromLong(st) : written(out);
 }
 
 // Rows of one projection of w_in (2 hidden, k).

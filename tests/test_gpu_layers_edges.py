@@ -101,3 +101,21 @@ def test_out_in_a_buffer_of_its_inputs(ws):
     with pytest.raises(SkgError, match="argument"):
         layers.linear(x[:8], w, out=torch.as_strided(w, (8, n), (n, 1)), workspace=ws)
     assert torch.equal(x, before[:, :k])
+
+
+def test_autograd_sees_a_given_out_written(ws):
+    from stream_decomposition_abft_gb300 import mx
+    g = gen(13)
+    x, w = normal(g, 8, 64), normal(g, 16, 64)
+    a, b = mx.quantize(x, "mxfp8"), mx.quantize(w, "mxfp8")
+    for write in (lambda out: layers.linear(x, w, out=out, workspace=ws),
+                  lambda out: mx.matmul(a, b, out=out)):
+        out = normal(g, 8, 16)
+        p = torch.ones(8, 16, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+        loss = (p * out).sum()  # keeps out for p's gradient
+        assert write(out) is out
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        with torch.inference_mode():
+            kept = normal(g, 8, 16)
+        assert write(kept) is kept  # an inference tensor has no version
