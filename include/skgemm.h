@@ -703,6 +703,11 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
  * elements of k). */
 skg_status_t skg_layers_test_stall(int32_t stages, uint64_t timeout_ns);
 
+/* Testing only: a[i] = act(g[i]) and d[i] = act'(g[i]) as the kernels above form them, in
+ * fp32, on `stream` (device vectors of `count`). */
+skg_status_t skg_layers_test_activation(int32_t act, int64_t count, const float* g, float* a,
+                                        float* d, void* stream);
+
 /* Number of SMs of the current device (0 if there is no device). */
 int32_t skg_device_sm_count(void);
 

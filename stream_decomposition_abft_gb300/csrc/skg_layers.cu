@@ -112,6 +112,13 @@ cudaError_t launch_dgate(int dtype, const DgateParams& p, cudaStream_t stream) {
                              : launch_dgate_as<__nv_bfloat16>(p, stream);
 }
 
+// ------------------------------------------------------------------ the activations alone
+template <int ACT>
+__global__ void act_kernel(int64_t count, const float* g, float* a, float* d) {
+  for (int64_t i = blockIdx.x * 128ll + threadIdx.x; i < count; i += gridDim.x * 128ll)
+    a[i] = lin_act<ACT, true>(g[i], d[i]);
+}
+
 // ------------------------------------------------------------------ products
 struct Operand {
   const void* p;
@@ -686,6 +693,22 @@ skg_status_t skg_layers_test_stall(int32_t stages, uint64_t timeout_ns) {
   g_test_stages.store((uint32_t)stages, std::memory_order_relaxed);
   g_test_limit.store(timeout_ns, std::memory_order_relaxed);
   return SKG_OK;
+}
+
+skg_status_t skg_layers_test_activation(int32_t act, int64_t count, const float* g, float* a,
+                                        float* d, void* stream) {
+  if (act < SKG_ACT_SILU || act > SKG_ACT_RELU || count < 0 || (count && (!g || !a || !d)))
+    return SKG_ERR_ARG;
+  if (count == 0) return SKG_OK;
+  const int64_t blocks = (count + 127) / 128;
+  const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096)), block(128);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (act == SKG_ACT_SILU) act_kernel<SKG_ACT_SILU><<<grid, block, 0, st>>>(count, g, a, d);
+  else if (act == SKG_ACT_GELU) act_kernel<SKG_ACT_GELU><<<grid, block, 0, st>>>(count, g, a, d);
+  else if (act == SKG_ACT_GELU_TANH)
+    act_kernel<SKG_ACT_GELU_TANH><<<grid, block, 0, st>>>(count, g, a, d);
+  else act_kernel<SKG_ACT_RELU><<<grid, block, 0, st>>>(count, g, a, d);
+  return cudaGetLastError() == cudaSuccess ? SKG_OK : SKG_ERR_CUDA;
 }
 
 size_t skg_workspace_size_layers(void) { return fixed_header_bytes(); }

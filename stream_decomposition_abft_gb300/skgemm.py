@@ -109,7 +109,7 @@ SYMBOLS = ("skg_opts_default", "skg_workspace_size", "skg_workspace_init", "skg_
            "skg_workspace_size_layers", "skg_scratch_size_linear", "skg_linear", "skg_gated",
            "skg_scratch_size_gated_backward", "skg_gated_backward",
            "skg_scratch_size_feed_forward_backward", "skg_feed_forward_backward",
-           "skg_layers_test_stall")
+           "skg_layers_test_stall", "skg_layers_test_activation")
 
 _lib = None
 
@@ -224,6 +224,8 @@ def lib() -> ctypes.CDLL:
     L.skg_feed_forward_backward.restype = i32
     L.skg_layers_test_stall.argtypes = [i32, ctypes.c_uint64]
     L.skg_layers_test_stall.restype = i32
+    L.skg_layers_test_activation.argtypes = [i32, i64, vp, vp, vp, vp]
+    L.skg_layers_test_activation.restype = i32
     L.skg_device_sm_count.argtypes = []
     L.skg_device_sm_count.restype = i32
     L.skg_status_string.argtypes = [i32]
@@ -485,6 +487,10 @@ def feed_forward_backward(m, hidden, k, dY_ptr, lddy, X_ptr, ldx, Wi_ptr, ldwi, 
 
 def layers_test_stall(stages: int, timeout_ns: int = 0) -> int:
     return lib().skg_layers_test_stall(stages, timeout_ns)
+
+
+def layers_test_activation(act, count, g_ptr, a_ptr, d_ptr, stream) -> int:
+    return lib().skg_layers_test_activation(act, count, g_ptr, a_ptr, d_ptr, stream)
 
 
 def device_sm_count() -> int:
