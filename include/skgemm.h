@@ -652,8 +652,9 @@ typedef struct {
  * row i with adapter s = index[i]
  *     y_i += scale_s (x_i A_s^T) B_s^T.
  * x_i A_s^T is held in twice dtype's mantissa between the products (in fp16 up to
- * 65504, infinite beyond). An adapter's infinities and NaN reach its own rows alone.
- */
+ * 65504, infinite beyond), as a sum of two numbers of dtype: where B_s holds an infinity,
+ * their products with it may cancel, and y is NaN where the formula is infinite. An
+ * adapter's infinities and NaN reach its own rows alone. */
 size_t skg_scratch_size_linear(int64_t m, int32_t rank);
 skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
                         int64_t ldw, const skg_adapters_t* adapters, void* Y, int64_t ldy,
@@ -678,7 +679,11 @@ skg_status_t skg_gated(int64_t m, int64_t hidden, int64_t k, const void* X, int6
 
 /* Its gradients from dH: with (g | u) = PRE,
  *     dPRE = (dH * u * act'(g) | dH * act(g)), rounded to dtype (up to 128 rows held
- *     in twice its mantissa), dX = dPRE W (m x k), dW = dPRE^T X (2 hidden x k). */
+ *     in twice its mantissa), dX = dPRE W (m x k), dW = dPRE^T X (2 hidden x k).
+ * So from 129 rows on a gradient's error is about sqrt(2) times its own rounding's. In
+ * fp16 dPRE has fp16's range: below 2^-25 it is zero, beyond 65504 infinite (scale the
+ * loss). Up to 128 rows dPRE is a sum of two numbers of dtype, whose products with an
+ * infinity of W or X may cancel: NaN where the formula is infinite. */
 size_t skg_scratch_size_gated_backward(int64_t m, int64_t hidden);
 skg_status_t skg_gated_backward(int64_t m, int64_t hidden, int64_t k, const void* dH, int64_t lddh,
                                 const void* X, int64_t ldx, const void* W, int64_t ldw,
@@ -688,7 +693,8 @@ skg_status_t skg_gated_backward(int64_t m, int64_t hidden, int64_t k, const void
 
 /* The gradients of Y = H W_out^T (W_out k x hidden) with H = gated(X, W_in), from dY
  * (m x k): dH = dY W_out in fp32, dX and dW_in as above, and
- *     dW_out = dY^T H (k x hidden), H formed again from PRE and rounded as dPRE is. */
+ *     dW_out = dY^T H (k x hidden), H formed again from PRE and rounded as dPRE is (what
+ *     is said of dPRE's range and of infinities holds for H and dY too). */
 size_t skg_scratch_size_feed_forward_backward(int64_t m, int64_t hidden);
 skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, const void* dY,
                                        int64_t lddy, const void* X, int64_t ldx, const void* W_in,

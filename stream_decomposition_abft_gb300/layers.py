@@ -20,8 +20,14 @@ w_in = [W_gate; W_up] (2 hidden, k)::
 
 Tensors are fp16 or bf16, all of one type, with a contiguous last dimension, rows on
 16-byte boundaries, and a hidden size that is a multiple of 8. The functions return
-plain tensors, without autograd history: gradients are the calls above. Adapters are
-for serving: they have no gradient here.
+plain tensors, without autograd history, whether or not their inputs require a gradient:
+gradients are the calls above. Adapters are for serving: they have no gradient here.
+
+Between the gradients' products the projections' gradients (and act(gate) * up, formed
+again) are rounded to the tensors' type, from 129 rows on once, up to 128 rows to twice
+its mantissa. In fp16 they have its range: zero below 2^-25, infinite beyond 65504, so
+losses are scaled as in any fp16 training. An infinite weight gives infinities or NaN in
+the results that it reaches, not always the one that the formula has.
 
 Every function runs on the current stream of the tensors' device, or on ``stream``;
 the tensors it allocates then belong to that stream. ``workspace``:

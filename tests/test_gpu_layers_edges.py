@@ -119,3 +119,76 @@ def test_autograd_sees_a_given_out_written(ws):
         with torch.inference_mode():
             kept = normal(g, 8, 16)
         assert write(kept) is kept  # an inference tensor has no version
+
+
+# ------------------------------------------------------------------ the range of fp16
+@pytest.mark.parametrize("size", [1e-4, 1e-6, 3e-8])
+@pytest.mark.parametrize("m", [40, 129, 600])
+def test_small_gradients_in_fp16(ws, m, size):
+    """Between the products gradients are off by half a subnormal step (in the bound) at most."""
+    g = gen(m)
+    f, k = 136, 72
+    x, w = normal(g, m, k, dtype=torch.float16), normal(g, 2 * f, k, dtype=torch.float16)
+    wo, pre = normal(g, k, f, dtype=torch.float16), normal(g, m, 2 * f, dtype=torch.float16)
+    dh, dy = normal(g, m, f, scale=size, dtype=torch.float16), \
+        normal(g, m, k, scale=size, dtype=torch.float16)
+    assert dh.any()
+    want = ref.backward(x, w, pre, "silu", dh=dh)
+    for what, t in zip(("dx", "dw_in"), layers.gated_backward(dh, x, w, pre, workspace=ws)):
+        check(t, *want[what], what=what)
+    want = ref.backward(x, w, pre, "silu", dy=dy, w_out=wo)
+    for what, t in zip(("dx", "dw_in", "dw_out"),
+                       layers.feed_forward_backward(dy, x, w, wo, pre, workspace=ws)):
+        check(t, *want[what], what=what)
+
+
+@pytest.mark.parametrize("m", [40, 300])
+def test_large_gradients_in_fp16(ws, m):
+    """A projection's gradient beyond 65504 is infinite: its token's dx is not finite, and other
+    tokens' are right."""
+    g = gen(m)
+    f, k = 136, 72
+    x, w = (normal(g, r, k, scale=1e-4, dtype=torch.float16) for r in (m, 2 * f))
+    pre = normal(g, m, 2 * f, scale=4.0, dtype=torch.float16)
+    dh = normal(g, m, f, scale=1500.0, dtype=torch.float16)
+    dh[::2] *= 8
+    a, da = ref.act(pre[:, :f].double(), "silu")
+    dpre = torch.cat((dh.double() * pre[:, f:].double() * da, dh.double() * a), 1).abs()
+    most = dpre.max(1).values
+    fits, over = most < 65000, most > 66000
+    assert fits.any() and over.any()
+    dx, dw = layers.gated_backward(dh, x, w, pre, workspace=ws)
+    want = ref.backward(x, w, pre, "silu", dh=dh)
+    check(dx[fits], want["dx"][0][fits], want["dx"][1][fits])
+    assert not torch.isfinite(dx[over]).all(1).any()
+    fits, over = dpre.max(0).values < 65000, dpre.max(0).values > 66000
+    check(dw[fits], want["dw_in"][0][fits], want["dw_in"][1][fits]) if fits.any() else None
+    assert not torch.isfinite(dw[over]).all(1).any()
+
+
+# ------------------------------------------------------------------ infinite weights
+@pytest.mark.parametrize("m", [5, 40, 300])
+def test_infinite_weights_are_never_finite(ws, m):
+    """Infinities of a weight reach the results that they are a term of (as infinities or NaN:
+    the operands in two parts may cancel), and no others."""
+    g = gen(m)
+    f, k, n, r = 72, 64, 136, 16
+    x, w = normal(g, m, k), normal(g, n, k)
+    a, b = normal(g, 2, r, k), normal(g, 2, n, r)
+    i = (torch.arange(m, device="cuda") % 2).int()
+    clean = layers.linear(x, w, layers.Adapters(a, b), i, workspace=ws)
+    b[1, 7, 3] = float("inf")
+    y = layers.linear(x, w, layers.Adapters(a, b), i, workspace=ws)
+    assert not torch.isfinite(y[1::2, 7]).any()
+    y[1::2, 7] = clean[1::2, 7]
+    assert torch.equal(y, clean)
+
+    wi, wo = normal(g, 2 * f, k), normal(g, k, f)
+    pre, dy = normal(g, m, 2 * f), normal(g, m, k)
+    clean = layers.feed_forward_backward(dy, x, wi, wo, pre, "gelu", workspace=ws)
+    wi[70, 5] = float("-inf")
+    dx, dwi, dwo = layers.feed_forward_backward(dy, x, wi, wo, pre, "gelu", workspace=ws)
+    assert not torch.isfinite(dx[:, 5]).any()
+    dx[:, 5] = clean[0][:, 5]
+    for got, want in zip((dx, dwi, dwo), clean):
+        assert torch.equal(got, want)
