@@ -943,7 +943,7 @@ skg_status_t skg_feed_forward_backward(int64_t m, int64_t hidden, int64_t k, con
     q.k = k;
     q.a = {dY, lddy, false, nullptr};
     q.b = {W_out, ldw_out, true, nullptr};
-      q.mode = kLinGrad;  // dH stays in the accumulator
+    q.mode = kLinGrad;  // dH stays in the accumulator
     q.act = act;
     q.c = base + s.h;
     q.c_lo = two ? base + s.h_lo : nullptr;

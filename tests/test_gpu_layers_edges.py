@@ -192,3 +192,26 @@ def test_infinite_weights_are_never_finite(ws, m):
     dx[:, 5] = clean[0][:, 5]
     for got, want in zip((dx, dwi, dwo), clean):
         assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ far gates, few rows
+@pytest.mark.parametrize("name", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("m", [11, 16, 100, 128])
+def test_far_gates_of_few_rows(ws, name, m):
+    """All of the far gates in the path of few rows and in gradients held in two parts."""
+    far = torch.tensor([0.0, 1e-30, -1e-30, 30.0, -30.0, 100.0, -100.0, 1e4, -1e4, 1e18, -1e18],
+                       device="cuda").bfloat16()
+    k, f = 8, 16
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = far[torch.arange(m, device="cuda") % len(far)]
+    w = torch.zeros(2 * f, k, dtype=torch.bfloat16, device="cuda")
+    w[:f, 0], w[f:, 1], x[:, 1] = 1.0, 1.0, 0.5
+    h, pre = layers.gated(x, w, name, save=True, workspace=ws)
+    want, bound, wp, pb = ref.gated(x, w, name)
+    check(h, want, bound + 1e-30)
+    check(pre, wp, pb)
+    dh = torch.ones(m, f, dtype=torch.bfloat16, device="cuda")
+    grads = ref.backward(x, w, pre, name, dh=dh)
+    dx, dw = layers.gated_backward(dh, x, w, pre, name, workspace=ws)
+    check(dx, *grads["dx"])
+    check(dw, *grads["dw_in"])
