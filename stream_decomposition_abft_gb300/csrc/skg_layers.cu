@@ -449,9 +449,15 @@ bool there(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   return rows == 0 || cols == 0 || (p && (rows <= 1 || ld >= cols));
 }
 
-// The TMA engine's rules, of a matrix with elements in it.
+// The TMA engine's rules, of a matrix with elements in it: its base, the rows' distance, which
+// has 39 bits, and (of the processor's addresses) its whole extent.
+constexpr int64_t kMaxStride = ((int64_t)1 << 39) - 1;  // elements of two bytes
+bool spans(int64_t count, int64_t stride) {
+  return count <= 1 || (stride <= kMaxStride && stride <= ((int64_t)1 << 55) / count);
+}
 bool aligned(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  return rows == 0 || cols == 0 || (((uintptr_t)p & 15) == 0 && (rows == 1 || ld % 8 == 0));
+  return rows == 0 || cols == 0 ||
+         (((uintptr_t)p & 15) == 0 && (rows == 1 || ld % 8 == 0) && spans(rows, ld));
 }
 
 // Rows of `width` bytes, `pitch` bytes from one to the next (none: rows or width 0).
@@ -741,6 +747,7 @@ skg_status_t skg_linear(int64_t m, int64_t n, int64_t k, const void* X, int64_t 
     if (ad->rank > 512 || ad->rank % 8) return SKG_ERR_UNSUPPORTED;
     if (some && (!aligned(ad->down, ad->rank, k, ad->ld_down) || !aligned(ad->up, n, ad->rank, ad->ld_up) ||
                  (ad->count > 1 && (ad->stride_down % 8 || ad->stride_up % 8)) ||
+                 !spans(ad->count, ad->stride_down) || !spans(ad->count, ad->stride_up) ||
                  ((uintptr_t)ad->index & 3) || ((uintptr_t)ad->scale & 3)))
       return SKG_ERR_UNSUPPORTED;
     if (!some) ad = nullptr;
@@ -814,7 +821,7 @@ skg_status_t skg_gated(int64_t m, int64_t hidden, int64_t k, const void* X, int6
     return SKG_ERR_ARG;
   if (hidden % 8) return SKG_ERR_UNSUPPORTED;
   if (m == 0 || hidden == 0) return SKG_OK;
-  if (!aligned(X, m, k, ldx) || !aligned(W, 2, k, ldw) || !aligned(H, m, hidden, ldh) ||
+  if (!aligned(X, m, k, ldx) || !aligned(W, 2 * hidden, k, ldw) || !aligned(H, m, hidden, ldh) ||
       (PRE && !aligned(PRE, m, 2 * hidden, ldp)))
     return SKG_ERR_UNSUPPORTED;
   st = check_memory(workspace, ws_bytes, nullptr, 0, 0);

@@ -106,3 +106,19 @@ def test_against_every_byte():
         st = linear(m=m, n=n, k=k, X=X, ldx=ldx, W=2 * MB, ldw=24, Y=Y, ldy=ldy)
         assert st == (skgemm.ERR_ARG if shared else skgemm.ERR_CUDA), (m, n, k, X - MB, ldx, Y - MB, ldy)
     assert min(seen) > 500
+
+
+def test_strides_beyond_any_memory():
+    """Refused by their size, before they are multiplied."""
+    big = 1 << 61
+    for ld in (1 << 39, 1 << 45, big):
+        assert linear(ldx=ld) == linear(ldw=ld) == linear(ldy=ld) == skgemm.ERR_UNSUPPORTED
+        for name in ("ld_down", "ld_up", "stride_down", "stride_up"):
+            assert linear(ad=adapters(**{name: ld})) == skgemm.ERR_UNSUPPORTED, name
+    assert linear(m=1 << 28, ldx=1 << 30) == skgemm.ERR_UNSUPPORTED
+    assert skgemm.gated(4, 16, 64, MB, big, 2 * MB, 64, 0, 3 * MB, 16, None, 0, 0, WS, MB, None) == \
+        skgemm.ERR_UNSUPPORTED
+    assert skgemm.gated(4, 1 << 27, 64, MB, 64, 2 * MB, 1 << 34, 0, 3 * MB, 1 << 27, None, 0, 0, WS, MB,
+                        None) == skgemm.ERR_UNSUPPORTED  # 2^28 rows
+    # One row has no stride.
+    assert linear(m=1, ldx=big, Y=MB) == skgemm.ERR_ARG
